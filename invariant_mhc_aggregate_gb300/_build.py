@@ -46,6 +46,19 @@ NVCC_FLAGS = [
 ]
 
 
+#: The second library, libmhc_layer.so: the layer operators of include/mhc_layer.h
+#: (RMS norm, matrix product, rotary positions).
+LAYER_LIB_NAME = "libmhc_layer.so"
+LAYER_LIB_PATH = os.path.join(LIB_DIR, LAYER_LIB_NAME)
+LAYER_SOURCES = [os.path.join(CSRC, f) for f in
+                 ("mhc_layer.cu", "mhc_launch_norm.cu", "mhc_launch_linear.cu", "mhc_launch_rotary.cu")]
+LAYER_DEPS = LAYER_SOURCES + [os.path.join(CSRC, f) for f in
+                              ("mhc_layer_launch.cuh", "mhc_norm.cuh", "mhc_linear.cuh", "mhc_rotary.cuh",
+                               "mhc_launch.cuh", "mhc_device.cuh", "mhc_coeffs.cuh", "mhc_shift.cuh",
+                               "mhc_shift_bulk.cuh", "mhc_bulk.cuh", "fastdiv.cuh")] \
+    + [os.path.join(INCLUDE, f) for f in ("mhc_layer.h", "mhc_h_aggregate.h")]
+
+
 def nvcc_path() -> str:
     for cand in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -53,9 +66,9 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found (set NVCC or put the CUDA toolkit on PATH)")
 
 
-def _digest(extra_flags) -> str:
+def _digest(extra_flags, deps=None) -> str:
     h = hashlib.sha256()
-    for p in DEPS:
+    for p in (DEPS if deps is None else deps):
         with open(p, "rb") as f:
             h.update(f.read())
     h.update(" ".join(NVCC_FLAGS + list(extra_flags)).encode())
@@ -103,21 +116,19 @@ def kernel_digest() -> str:
     return h.hexdigest()
 
 
-def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
-    """Build the library if its sources or flags changed; return its path."""
-    digest = _digest(extra_flags)
-    stamp = LIB_PATH + ".stamp"
-    if not force and os.path.exists(LIB_PATH) and os.path.exists(stamp):
+def _build(lib_path, sources, digest, force, extra_flags, verbose) -> str:
+    stamp = lib_path + ".stamp"
+    if not force and os.path.exists(lib_path) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == digest:
-                return LIB_PATH
+                return lib_path
     os.makedirs(LIB_DIR, exist_ok=True)
     nvcc = nvcc_path()
     with tempfile.TemporaryDirectory(dir=LIB_DIR) as work:
         # one translation unit per process, in parallel
         procs = []
         objs = []
-        for src in SOURCES:
+        for src in sources:
             obj = os.path.join(work, os.path.basename(src) + ".o")
             cmd = [nvcc, *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC, "-c", "-o", obj, src]
             procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
@@ -129,17 +140,28 @@ def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
                 raise RuntimeError(f"nvcc failed ({' '.join(cmd)}):\n{err}")
             if verbose and err:
                 print(err)
-        tmp = os.path.join(work, LIB_NAME)
+        tmp = os.path.join(work, os.path.basename(lib_path))
         cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-o", tmp, *objs]
         res = subprocess.run(cmd, capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed ({' '.join(cmd)}):\n{res.stderr}")
-        os.replace(tmp, LIB_PATH)
+        os.replace(tmp, lib_path)
     with open(stamp, "w") as f:
         f.write(digest + "\n")
-    return LIB_PATH
+    return lib_path
+
+
+def build(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
+    """Build the library if its sources or flags changed; return its path."""
+    return _build(LIB_PATH, SOURCES, _digest(extra_flags), force, extra_flags, verbose)
+
+
+def build_layer(force: bool = False, extra_flags=(), verbose: bool = False) -> str:
+    """Build the layer operators' library if its sources or flags changed; return its path."""
+    return _build(LAYER_LIB_PATH, LAYER_SOURCES, _digest(extra_flags, LAYER_DEPS), force, extra_flags, verbose)
 
 
 if __name__ == "__main__":
     import sys
     print(build(force="--force" in sys.argv, verbose=True))
+    print(build_layer(force="--force" in sys.argv, verbose=True))

@@ -1,0 +1,406 @@
+// RMS norm kernels (sm_103a): forward with the residual's addition and an
+// optional 8-bit output, and backward.  Definitions in mhc_layer.h.
+//
+// HBM-bound: about 5 operations per value that is read or written once.  A
+// row is held in registers between the sum of squares and the output, so each
+// value crosses HBM once.
+//
+// Order of a row's sum (it depends on H only): the row is cut into chunks of
+// 8 values; thread j of the row's nt threads owns chunks j, j + nt, ... (at
+// most K of them), sums each as the pairwise tree ((0+1)+(2+3))+((4+5)+(6+7))
+// and adds the chunks in increasing order; a warp folds by exchanging with
+// lanes at distance 16, 8, 4, 2, 1; the warps' results are added in
+// increasing order.  nt and K follow from H (shape_of).
+//
+// Two ways to move a row, with the same sums:
+//  * VEC: 16-byte loads and stores of the thread's own chunks (H % 8 == 0 and
+//    16-byte aligned rows);
+//  * otherwise thread j moves the values j, j + nt, ... with 2-byte accesses
+//    (a warp's accesses are then contiguous whatever the row's alignment) and
+//    the products of a row's sum change hands through shared memory, where
+//    every row is aligned.
+#pragma once
+
+#include "mhc_device.cuh"
+
+namespace mhc {
+namespace norm {
+
+constexpr int kMaxH = 32768;
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxFloor = 0x1p-60f;
+
+enum Out { kOutSame = 0, kOutFp8Row = 1, kOutFp8Group = 2 };
+constexpr int kGroup = 128;
+
+struct FwdArgs {
+    const uint16_t* x;
+    const uint16_t* residual;   // null without one
+    const float* weight;
+    void* y;
+    float* scale;
+    uint16_t* total;
+    float* rstd;
+    int64_t T;
+    int64_t x_stride, residual_stride;
+    uint32_t H;
+    float eps;
+};
+
+struct BwdArgs {
+    const uint16_t* g;
+    const uint16_t* s;
+    const float* weight;
+    const float* rstd;
+    const uint16_t* grad_total;   // null without one
+    uint16_t* grad_x;
+    float* partial;               // [gridDim.x, H]
+    int64_t T;
+    int64_t g_stride, s_stride;
+    uint32_t H;
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Two E4M3 values, rounded to nearest even; past 448 they stay at 448.
+__device__ __forceinline__ uint16_t e4m3_pair(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float chunk_sum(const float* q) {
+    return __fadd_rn(__fadd_rn(__fadd_rn(q[0], q[1]), __fadd_rn(q[2], q[3])),
+                     __fadd_rn(__fadd_rn(q[4], q[5]), __fadd_rn(q[6], q[7])));
+}
+
+// Folds one value per thread over the row's threads (a warp, or the block):
+// every thread gets the result.  `shared` holds 32 floats and is free again
+// after the caller's next barrier.
+template <class Op>
+__device__ __forceinline__ float fold(float v, float* shared, Op op) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    const uint32_t warps = blockDim.x >> 5;
+    if (warps == 1) return v;
+    if ((threadIdx.x & 31u) == 0) shared[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = shared[0];
+    for (uint32_t i = 1; i < warps; ++i) v = op(v, shared[i]);
+    return v;
+}
+
+struct Add {
+    __device__ float operator()(float a, float b) const { return __fadd_rn(a, b); }
+};
+struct Max {
+    __device__ float operator()(float a, float b) const { return max_nan(a, b); }
+};
+
+// One row of a 2-byte buffer in the registers of the row's threads; values
+// past H read as +0.
+template <int DT, int K, bool VEC>
+__device__ __forceinline__ void load_row(const uint16_t* __restrict__ row, uint32_t H, float (&v)[8 * K]) {
+    const uint32_t nt = blockDim.x, j = threadIdx.x;
+    if constexpr (VEC) {
+        Words<4> w[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const uint32_t c = 8 * (j + k * nt);
+            if (c < H) {
+                w[k] = ld_stream<4>(row + c);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[k].w[i] = 0;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[8 * k + 2 * i] = Elem<DT>::lo(w[k].w[i]);
+                v[8 * k + 2 * i + 1] = Elem<DT>::hi(w[k].w[i]);
+            }
+    } else {
+        uint16_t h[8 * K];
+#pragma unroll
+        for (int m = 0; m < 8 * K; ++m) {
+            const uint32_t c = j + m * nt;
+            h[m] = c < H ? ld_stream2(row + c) : uint16_t(0);
+        }
+#pragma unroll
+        for (int m = 0; m < 8 * K; ++m) v[m] = Elem<DT>::one(h[m]);
+    }
+}
+
+template <int DT, int K, bool VEC>
+__device__ __forceinline__ void store_row(uint16_t* __restrict__ row, uint32_t H, const float (&v)[8 * K]) {
+    const uint32_t nt = blockDim.x, j = threadIdx.x;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const uint32_t c = 8 * (j + k * nt);
+            if (c < H) {
+                Words<4> w;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w.w[i] = Elem<DT>::pack(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
+                st_stream<4>(row + c, w);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < 8 * K; ++m) {
+            const uint32_t c = j + m * nt;
+            if (c < H) st_stream2(row + c, Elem<DT>::cvt(v[m]));
+        }
+    }
+}
+
+// The norm's weight at the thread's values (it stays in L1: 4 H bytes).
+template <int K, bool VEC>
+__device__ __forceinline__ void load_weight(const float* __restrict__ w, uint32_t H, float (&v)[8 * K]) {
+    const uint32_t nt = blockDim.x, j = threadIdx.x;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const uint32_t c = 8 * (j + k * nt);
+            float4 a = make_float4(0, 0, 0, 0), b = a;
+            if (c < H) {
+                a = __ldg(reinterpret_cast<const float4*>(w + c));
+                b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
+            }
+            v[8 * k] = a.x, v[8 * k + 1] = a.y, v[8 * k + 2] = a.z, v[8 * k + 3] = a.w;
+            v[8 * k + 4] = b.x, v[8 * k + 5] = b.y, v[8 * k + 6] = b.z, v[8 * k + 7] = b.w;
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < 8 * K; ++m) {
+            const uint32_t c = j + m * nt;
+            v[m] = c < H ? __ldg(w + c) : 0.0f;
+        }
+    }
+}
+
+// The row's sum of q in the order stated above.  `stage`: 8 * K * nt floats,
+// without VEC only.
+template <int K, bool VEC>
+__device__ __forceinline__ float row_sum(const float (&q)[8 * K], float* stage, float* shared) {
+    float acc = 0.0f;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) acc = __fadd_rn(acc, chunk_sum(q + 8 * k));
+    } else {
+        const uint32_t nt = blockDim.x, j = threadIdx.x;
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < 8 * K; ++m) stage[j + m * nt] = q[m];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const float4* p = reinterpret_cast<const float4*>(stage + 8 * (j + k * nt));
+            const float4 a = p[0], b = p[1];
+            const float c[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            acc = __fadd_rn(acc, chunk_sum(c));
+        }
+    }
+    return fold(acc, shared, Add());
+}
+
+// Forward: block (nt, rows); rows > 1 only with VEC and nt = 32 (a warp per
+// row, no barrier).
+template <int DT, int K, bool VEC, int OUT>
+__global__ void fwd_kernel(const FwdArgs a) {
+    pdl_enter();
+    extern __shared__ __align__(16) float stage[];
+    __shared__ float shared[2][32];
+    const int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (t >= a.T) return;
+    const uint32_t H = a.H, nt = blockDim.x, j = threadIdx.x;
+    float s[8 * K], q[8 * K];
+    load_row<DT, K, VEC>(a.x + t * a.x_stride, H, s);
+    if (a.residual != nullptr) {
+        load_row<DT, K, VEC>(a.residual + t * a.residual_stride, H, q);
+#pragma unroll
+        for (int i = 0; i < 8 * K; ++i) s[i] = __fadd_rn(s[i], q[i]);
+        store_row<DT, K, VEC>(a.total + t * int64_t(H), H, s);
+    }
+#pragma unroll
+    for (int i = 0; i < 8 * K; ++i) q[i] = __fmul_rn(s[i], s[i]);
+    const float sum = row_sum<K, VEC>(q, stage, shared[0]);
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(H)), a.eps)));
+    if (j == 0) a.rstd[t] = rstd;
+    load_weight<K, VEC>(a.weight, H, q);
+#pragma unroll
+    for (int i = 0; i < 8 * K; ++i) s[i] = __fmul_rn(__fmul_rn(s[i], rstd), q[i]);
+    if constexpr (OUT == kOutSame) {
+        store_row<DT, K, VEC>(static_cast<uint16_t*>(a.y) + t * int64_t(H), H, s);
+    } else {
+        uint8_t* y = static_cast<uint8_t*>(a.y) + t * int64_t(H);
+        const uint32_t groups = OUT == kOutFp8Row ? 1 : (H + kGroup - 1) / kGroup;
+        float inv[K];   // of the thread's chunks (VEC), or inv[0] of the row
+        if constexpr (OUT == kOutFp8Row) {
+            float m = kAmaxFloor;
+#pragma unroll
+            for (int i = 0; i < 8 * K; ++i) m = max_nan(m, fabsf(s[i]));
+            m = fold(m, shared[1], Max());
+            if (j == 0) a.scale[t] = __fdiv_rn(m, kE4m3Max);
+            const float r = __fdiv_rn(kE4m3Max, m);
+#pragma unroll
+            for (int k = 0; k < K; ++k) inv[k] = r;
+        } else {
+            // 16 chunks to a group: half a warp's chunks of the same k
+            if constexpr (!VEC) {
+                __syncthreads();
+#pragma unroll
+                for (int m = 0; m < 8 * K; ++m) stage[j + m * nt] = s[m];
+                __syncthreads();
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float m = kAmaxFloor;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(VEC ? s[8 * k + i] : stage[8 * (j + k * nt) + i]));
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+                inv[k] = __fdiv_rn(kE4m3Max, m);
+                const uint32_t c = j + k * nt;
+                if ((j & 15u) == 0 && 8 * c < H) a.scale[t * groups + c / 16] = __fdiv_rn(m, kE4m3Max);
+            }
+            if constexpr (!VEC) {   // the groups' factors, over the staged values
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if ((j & 15u) == 0) stage[(j + k * nt) / 16] = inv[k];
+                __syncthreads();
+            }
+        }
+        if constexpr (VEC) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const uint32_t c = 8 * (j + k * nt);
+                if (c < H) {
+                    uint32_t w[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float* p = s + 8 * k + 4 * i;
+                        w[i] = uint32_t(e4m3_pair(__fmul_rn(p[0], inv[k]), __fmul_rn(p[1], inv[k]))) |
+                               uint32_t(e4m3_pair(__fmul_rn(p[2], inv[k]), __fmul_rn(p[3], inv[k]))) << 16;
+                    }
+                    __stcs(reinterpret_cast<uint2*>(y + c), make_uint2(w[0], w[1]));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < 8 * K; ++m) {
+                const uint32_t c = j + m * nt;
+                if (c < H) {
+                    const float r = OUT == kOutFp8Row ? inv[0] : stage[c / kGroup];
+                    y[c] = uint8_t(e4m3_pair(__fmul_rn(s[m], r), 0.0f));
+                }
+            }
+        }
+    }
+}
+
+// Backward: block b takes rows b * rows + y, then steps of gridDim.x * rows
+// (rows = blockDim.y > 1 only with VEC and nt = 32), writes their grad_x and
+// leaves the sum of their g * n in partial[b]; the rows of one (b, y) are
+// added in increasing order, then the y in increasing order.
+template <int DT, int K, bool VEC>
+__global__ void bwd_kernel(const BwdArgs a) {
+    pdl_enter();
+    extern __shared__ __align__(16) float stage[];
+    __shared__ float shared[2][32];
+    const uint32_t H = a.H, nt = blockDim.x, j = threadIdx.x, rows = blockDim.y;
+    const int64_t step = int64_t(gridDim.x) * rows;
+    float acc[8 * K];
+#pragma unroll
+    for (int i = 0; i < 8 * K; ++i) acc[i] = 0.0f;
+    int turn = 0;
+    for (int64_t t = int64_t(blockIdx.x) * rows + threadIdx.y; t < a.T; t += step, turn ^= 1) {
+        float g[8 * K], n[8 * K], q[8 * K];
+        load_row<DT, K, VEC>(a.s + t * a.s_stride, H, n);
+        load_row<DT, K, VEC>(a.g + t * a.g_stride, H, g);
+        const float rstd = __ldg(a.rstd + t);
+        load_weight<K, VEC>(a.weight, H, q);
+#pragma unroll
+        for (int i = 0; i < 8 * K; ++i) {
+            n[i] = __fmul_rn(n[i], rstd);
+            acc[i] = __fadd_rn(acc[i], __fmul_rn(g[i], n[i]));
+            g[i] = __fmul_rn(g[i], q[i]);
+            q[i] = __fmul_rn(g[i], n[i]);
+        }
+        const float m = __fdiv_rn(row_sum<K, VEC>(q, stage, shared[turn]), float(H));
+#pragma unroll
+        for (int i = 0; i < 8 * K; ++i) g[i] = __fmul_rn(rstd, __fsub_rn(g[i], __fmul_rn(n[i], m)));
+        if (a.grad_total != nullptr) {
+            load_row<DT, K, VEC>(a.grad_total + t * int64_t(H), H, q);
+#pragma unroll
+            for (int i = 0; i < 8 * K; ++i) g[i] = __fadd_rn(g[i], q[i]);
+        }
+        store_row<DT, K, VEC>(a.grad_x + t * int64_t(H), H, g);
+    }
+    float* out = a.partial + int64_t(blockIdx.x) * H;
+    if (rows > 1) {   // the warps of a block one after the other, in shared memory
+        for (uint32_t y = 0; y < rows; ++y) {
+            if (threadIdx.y == y) {
+#pragma unroll
+                for (int i = 0; i < 8 * K; ++i) {
+                    const uint32_t at = j + i * 32;
+                    stage[at] = y == 0 ? acc[i] : __fadd_rn(stage[at], acc[i]);
+                }
+            }
+            __syncthreads();
+        }
+        if (threadIdx.y != 0) return;
+#pragma unroll
+        for (int i = 0; i < 8 * K; ++i) acc[i] = stage[j + i * 32];
+    }
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const uint32_t c = 8 * (j + k * nt);
+            if (c < H) {
+                float4* p = reinterpret_cast<float4*>(out + c);
+                p[0] = make_float4(acc[8 * k], acc[8 * k + 1], acc[8 * k + 2], acc[8 * k + 3]);
+                p[1] = make_float4(acc[8 * k + 4], acc[8 * k + 5], acc[8 * k + 6], acc[8 * k + 7]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < 8 * K; ++m) {
+            const uint32_t c = j + m * nt;
+            if (c < H) out[c] = acc[m];
+        }
+    }
+}
+
+// Column sums of partial [P,H]: block (32, 8); thread (x, y) adds the rows
+// y, y + 8, ... of column x in increasing order, then the 8 sums in
+// increasing order.  Also the bias gradient's last step.
+constexpr int kColRows = 8;
+
+static __global__ void __launch_bounds__(32 * kColRows)
+column_sum_kernel(const float* __restrict__ partial, float* __restrict__ out, uint32_t P, uint32_t H) {
+    pdl_enter();
+    __shared__ float part[kColRows][32];
+    const uint32_t c = blockIdx.x * 32 + threadIdx.x;
+    float acc = 0.0f;
+    if (c < H)
+#pragma unroll 4
+        for (uint32_t p = threadIdx.y; p < P; p += kColRows) acc = __fadd_rn(acc, partial[uint64_t(p) * H + c]);
+    part[threadIdx.y][threadIdx.x] = acc;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < H) {
+#pragma unroll
+        for (int y = 1; y < kColRows; ++y) acc = __fadd_rn(acc, part[y][threadIdx.x]);
+        out[c] = acc;
+    }
+}
+
+}  // namespace norm
+}  // namespace mhc
