@@ -21,7 +21,7 @@ from __future__ import annotations
 
 import torch
 
-from . import binding
+from . import binding, layer
 
 
 class HAggregate(torch.autograd.Function):
@@ -215,3 +215,105 @@ def mhc_post_sigmoid(x: torch.Tensor, y: torch.Tensor, mix: torch.Tensor, alpha:
                      b: torch.Tensor, res: torch.Tensor) -> torch.Tensor:
     """Differentiable mHC post with post = sigmoid(alpha * mix + b) computed in the kernel."""
     return MhcPostSigmoid.apply(x, y, mix, alpha, b, res)
+
+
+# ---------------------------------------------------------------------------
+# the layer between the aggregate and the post (the calls of .layer)
+# ---------------------------------------------------------------------------
+
+class RmsNorm(torch.autograd.Function):
+    """(y, total): total = x + residual, y its RMS norm times weight; one
+    kernel forward, two backward (the weight's gradient is summed over tokens
+    in a fixed order)."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        H = x.shape[-1]
+        xx = x.reshape(-1, H)
+        rr = None if residual is None else residual.reshape(-1, H)
+        if residual is not None and residual.shape != x.shape:
+            raise ValueError(f"shape mismatch: x {tuple(x.shape)}, residual {tuple(residual.shape)}")
+        y, total, rstd = layer.rms_norm(xx, weight.contiguous(), residual=rr, eps=eps)
+        ctx.save_for_backward(total, weight, rstd)
+        ctx.with_residual = residual is not None
+        return y.reshape(x.shape), total.reshape(x.shape) if ctx.with_residual else x.view_as(x)
+
+    @staticmethod
+    def backward(ctx, grad_y, grad_total):
+        total, weight, rstd = ctx.saved_tensors
+        H = total.shape[-1]
+        gt = grad_total.reshape(-1, H).contiguous()
+        gx, gw = layer.rms_norm_backward(grad_y.reshape(-1, H).contiguous(), total, weight.contiguous(), rstd,
+                                         grad_total=gt)
+        gx = gx.reshape(grad_y.shape)
+        return (gx if ctx.needs_input_grad[0] else None, gw if ctx.needs_input_grad[1] else None,
+                gx if ctx.with_residual and ctx.needs_input_grad[2] else None, None)
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6):
+    """Differentiable (y, total) of layer.rms_norm, for x [...,H] of any leading shape."""
+    return RmsNorm.apply(x, weight, residual, eps)
+
+
+class Linear(torch.autograd.Function):
+    """act(x weight^T + bias) + residual; one product forward (two outputs with
+    an activation: y and the pre-activation the backward reads), two backward."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, activation, residual):
+        I, O = x.shape[-1], weight.shape[0]
+        xx, ww = x.reshape(-1, I).contiguous(), weight.contiguous()
+        rr = None if residual is None else residual.reshape(-1, O)
+        if residual is not None and residual.shape != (*x.shape[:-1], O):
+            raise ValueError(f"shape mismatch: x {tuple(x.shape)}, residual {tuple(residual.shape)}")
+        z = None
+        if activation == "none":
+            y = layer.linear(xx, ww, bias=bias, activation=activation, residual=rr)
+        else:
+            y, z = layer.linear_preact(xx, ww, bias=bias, activation=activation, residual=rr)
+        ctx.save_for_backward(xx, ww, *(() if z is None else (z,)))
+        ctx.activation, ctx.lead, ctx.with_bias = activation, x.shape[:-1], bias is not None
+        return y.reshape(*x.shape[:-1], O)
+
+    @staticmethod
+    def backward(ctx, grad_y):
+        x, w, *z = ctx.saved_tensors
+        O = w.shape[0]
+        if grad_y.dtype != x.dtype:
+            raise TypeError(f"the output gradient must be {x.dtype}, got {grad_y.dtype}")
+        need = ctx.needs_input_grad
+        gx = gw = gb = None
+        if need[0] or need[1] or (need[2] and ctx.with_bias):
+            gx, gw, gb = layer.linear_backward(grad_y.reshape(-1, O).contiguous(), x, w, z=z[0] if z else None,
+                                               activation=ctx.activation, bias=need[2] and ctx.with_bias,
+                                               want=(need[0], need[1]))
+        return (None if gx is None else gx.reshape(*ctx.lead, x.shape[-1]), gw, gb, None,
+                grad_y if need[4] else None)
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, activation: str = "none",
+           residual: torch.Tensor | None = None) -> torch.Tensor:
+    """Differentiable layer.linear, for x [...,I] of any leading shape."""
+    return Linear.apply(x, weight, bias, activation, residual)
+
+
+class Rotary(torch.autograd.Function):
+    """layer.rotary; the gradient is the rotation by the opposite angle."""
+
+    @staticmethod
+    def forward(ctx, x, positions, frequencies, interleaved, scale):
+        ctx.save_for_backward(positions, frequencies)
+        ctx.interleaved, ctx.scale = interleaved, scale
+        return layer.rotary(x, positions, frequencies, interleaved=interleaved, scale=scale)
+
+    @staticmethod
+    def backward(ctx, grad):
+        positions, frequencies = ctx.saved_tensors
+        return (layer.rotary(grad.contiguous(), positions, frequencies, interleaved=ctx.interleaved, scale=ctx.scale,
+                             inverse=True), None, None, None, None)
+
+
+def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, interleaved: bool = False,
+           scale: float = 1.0) -> torch.Tensor:
+    """Differentiable layer.rotary of x [T,heads,D]."""
+    return Rotary.apply(x, positions, frequencies, interleaved, scale)

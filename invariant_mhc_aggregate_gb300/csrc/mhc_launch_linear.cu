@@ -1,4 +1,6 @@
 // Launch shapes of the matrix product.
+#include <cudaTypedefs.h>
+
 #include "mhc_layer_launch.cuh"
 
 namespace mhc {
@@ -6,13 +8,214 @@ namespace layer {
 
 using namespace linear;
 
+namespace {
+
+// Set to 1 when a bounded wait runs out (see mhc_bulk.cuh); one per device.
+__device__ unsigned int g_timeouts;
+
+cudaError_t timeouts_ptr(unsigned int** p) {
+    static std::atomic<unsigned int*> cached[kMaxDevices];
+    const int dev = current_device();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    unsigned int* q = cached[dev].load(std::memory_order_acquire);
+    if (q == nullptr) {
+        const cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(&q), g_timeouts);
+        if (e != cudaSuccess) return e;
+        cached[dev].store(q, std::memory_order_release);
+    }
+    *p = q;
+    return cudaSuccess;
+}
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point (the
+// library does not link the driver library itself); resolved once.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static std::atomic<void*> fn{nullptr};
+    void* p = fn.load(std::memory_order_acquire);
+    if (p == nullptr) {
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn.store(p, std::memory_order_release);
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+}
+
+// Rows of `length` elements of `size` bytes, box 128 bytes x box_rows, 128-byte swizzle.
+cudaError_t encode(CUtensorMap* map, const void* base, int64_t rows, int64_t length, int64_t stride, int64_t size,
+                   uint32_t box_rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 f = tensor_map_encoder();
+    if (f == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {cuuint64_t(length), cuuint64_t(rows)};
+    // one row has no stride; any multiple of 16 does
+    const cuuint64_t strides[1] = {cuuint64_t((rows > 1 ? stride : (length + 15) / 16 * 16) * size)};
+    const cuuint32_t box[2] = {cuuint32_t(128 / size), box_rows};
+    const cuuint32_t step[2] = {1, 1};
+    const CUresult r = f(map, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                         const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Shared memory of a ring of stages: 7 stages of the pair kernel's widest
+// tile, next to the barriers and the 1024 bytes of alignment in the 227 KB.
+constexpr uint32_t kRingBytes = 224 * 1024;
+
+// Parts of K: as many (1, 2, 4 or 8) as the GPU's 152 SMs can take at once
+// when the call has few rows, with at least 8 blocks of K a part.  It
+// follows from N and K alone, so that a row's sum does not depend on how many
+// rows the call has.
+uint32_t splits_of(int64_t N, int64_t kb) {
+    const int64_t tiles = (N + kLanesP - 1) / kLanesP;
+    uint32_t s = 1;
+    while (s < 8 && tiles * s * 2 <= 152 && kb >= int64_t(s) * 16) s *= 2;
+    return s;
+}
+
+template <typename Kernel>
+cudaError_t launch_tiles(Kernel kernel, std::atomic<uint64_t>& allowed, dim3 grid, uint32_t threads, uint32_t smem,
+                         uint32_t cluster, cudaStream_t stream, const CUtensorMap& mp, const CUtensorMap& mq,
+                         const TileArgs& a) {
+    cudaError_t e = allow_smem(kernel, kRingBytes + 1024, allowed);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, mp, mq, a);
+}
+
+template <bool FP8, int OUT, int LAYOUT>
+cudaError_t launch_split(TileArgs a, CUtensorMap& mp, CUtensorMap& mq, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed{0};
+    a.stage_bytes = kBytesP + a.width * 128;
+    const uint32_t budget = kRingBytes;
+    a.stages = budget / a.stage_bytes < kMaxStages ? budget / a.stage_bytes : kMaxStages;
+    const uint32_t parts = a.splits > 1 ? a.width * kLanesP * 4 : 0;
+    const uint32_t ring = a.stages * a.stage_bytes;
+    return launch_tiles(split_kernel<FP8, OUT, LAYOUT>, allowed, dim3(a.p_tiles * a.splits, a.q_tiles), kSplitThreads,
+                        (ring > parts ? ring : parts) + 1024, a.splits, stream, mp, mq, a);
+}
+
+template <bool FP8, int OUT, int LAYOUT>
+cudaError_t launch_pair(TileArgs a, CUtensorMap& mp, CUtensorMap& mq, cudaStream_t stream) {
+    a.stage_bytes = kBytesP + a.width / 2 * 128;
+    const uint32_t budget = kRingBytes;
+    a.stages = budget / a.stage_bytes < kMaxStages ? budget / a.stage_bytes : kMaxStages;
+    const uint32_t tiles = a.p_tiles * a.q_tiles, pairs = uint32_t(num_sms()) / 2;
+    const dim3 grid(2 * (tiles < pairs ? tiles : pairs));
+    const uint32_t smem = a.stages * a.stage_bytes + 1024;
+    if (a.splits > 1) {
+        static std::atomic<uint64_t> allowed{0};
+        return launch_tiles(pair_kernel<FP8, OUT, LAYOUT, true>, allowed, grid, kPairThreads, smem, 2, stream, mp, mq, a);
+    }
+    static std::atomic<uint64_t> allowed{0};
+    return launch_tiles(pair_kernel<FP8, OUT, LAYOUT, false>, allowed, grid, kPairThreads, smem, 2, stream, mp, mq, a);
+}
+
+template <bool FP8, int OUT, int LAYOUT>
+cudaError_t launch_tile(bool pair, const TileArgs& a, CUtensorMap& mp, CUtensorMap& mq, cudaStream_t stream) {
+    return pair ? launch_pair<FP8, OUT, LAYOUT>(a, mp, mq, stream) : launch_split<FP8, OUT, LAYOUT>(a, mp, mq, stream);
+}
+
+template <int OUT>
+cudaError_t launch_layout(bool pair, const TileArgs& a, CUtensorMap& mp, CUtensorMap& mq, bool p_mn, bool q_mn,
+                          cudaStream_t stream) {
+    if (!p_mn) return launch_tile<false, OUT, kBothK>(pair, a, mp, mq, stream);
+    return q_mn ? launch_tile<false, OUT, kBothMn>(pair, a, mp, mq, stream)
+                : launch_tile<false, OUT, kPMnQK>(pair, a, mp, mq, stream);
+}
+
+// The pair kernel's tile width: the one in steps of 32 rows (128 where Q is
+// MN-major: whole panels for each CTA) whose rounds of tiles over the pairs
+// of SMs take the least time, a round costing its width and, as measured,
+// about 16 rows' worth for its start and end.
+uint32_t pair_width(int64_t N, int64_t M, bool q_mn) {
+    const int64_t p_tiles = (N + 255) / 256, pairs = num_sms() / 2;
+    uint32_t best = 256;
+    int64_t least = INT64_MAX;
+    for (uint32_t w = 256; w >= 128; w -= q_mn ? 128 : 32) {
+        const int64_t rounds = (p_tiles * ((M + w - 1) / w) + pairs - 1) / pairs;
+        if (rounds * (w + 16) < least) least = rounds * (w + 16), best = w;
+    }
+    return best;
+}
+
+}  // namespace
+
+int64_t take_wait_timeouts() {
+    unsigned int n = 0;
+    const unsigned int zero = 0;
+    if (cudaDeviceSynchronize() != cudaSuccess) return -1;
+    if (cudaMemcpyFromSymbol(&n, g_timeouts, sizeof(n)) != cudaSuccess) return -1;
+    if (n != 0 && cudaMemcpyToSymbol(g_timeouts, &zero, sizeof(zero)) != cudaSuccess) return -1;
+    return int64_t(n);
+}
+
 cudaError_t product(const Product& p, int in, int out, cudaStream_t stream) {
-    const dim3 grid(uint32_t((p.N + 63) / 64), uint32_t((p.M + 63) / 64));
-    if (in == kE4m3)
-        return out == kBF16 ? launch2d(simple_kernel<kE4m3, kBF16>, grid, 256, stream, p)
-                            : launch2d(simple_kernel<kE4m3, kF16>, grid, 256, stream, p);
-    return in == kBF16 ? launch2d(simple_kernel<kBF16, kBF16>, grid, 256, stream, p)
-                       : launch2d(simple_kernel<kF16, kF16>, grid, 256, stream, p);
+    const bool fp8 = in == kE4m3;
+    const int64_t size = fp8 ? 1 : 2;
+    TileArgs a;
+    a.e = p.e;
+    a.N = p.N;
+    a.rows = uint32_t(p.M);
+    a.kb = uint32_t((p.K * size + 127) / 128);
+    a.splits = splits_of(p.N, a.kb);
+    const bool p_mn = p.b_mn, q_mn = p.a_mn;
+    cudaError_t e = timeouts_ptr(&a.timeouts);
+    if (e != cudaSuccess) return e;
+    const int64_t big_tiles = (p.N + 255) / 256 * ((p.M + 255) / 256);
+    const bool pair = p.M > 256 && big_tiles * 2 >= num_sms() / 2;
+    uint32_t box_q;
+    if (pair) {
+        a.width = pair_width(p.N, p.M, q_mn);
+        a.p_tiles = uint32_t((p.N + 255) / 256);
+        a.q_tiles = uint32_t((p.M + a.width - 1) / a.width);
+        a.idesc = umma::instr_desc(in == kBF16 ? 1 : 0, p_mn, q_mn, 2 * kLanesP, a.width);
+        box_q = a.width / 2;
+    } else {
+        // tiles of equal width, in steps of 16 rows (64 where Q is MN-major)
+        const int64_t step = q_mn ? 64 : 16;
+        a.q_tiles = uint32_t((p.M + 255) / 256);
+        a.width = uint32_t(((p.M + a.q_tiles - 1) / a.q_tiles + step - 1) / step * step);
+        a.p_tiles = uint32_t((p.N + kLanesP - 1) / kLanesP);
+        a.idesc = umma::instr_desc(in == kBF16 ? 1 : 0, p_mn, q_mn, kLanesP, a.width);
+        box_q = a.width;
+    }
+    CUtensorMap mp, mq;
+    e = p_mn ? encode(&mp, p.b, p.K, p.N, p.b_stride, size, 64) : encode(&mp, p.b, p.N, p.K, p.b_stride, size, kLanesP);
+    if (e != cudaSuccess) return e;
+    e = q_mn ? encode(&mq, p.a, p.K, p.M, p.a_stride, size, 64) : encode(&mq, p.a, p.M, p.K, p.a_stride, size, box_q);
+    if (e != cudaSuccess) return e;
+    if (fp8)
+        return out == kBF16 ? launch_tile<true, kBF16, kBothK>(pair, a, mp, mq, stream)
+                            : launch_tile<true, kF16, kBothK>(pair, a, mp, mq, stream);
+    return out == kBF16 ? launch_layout<kBF16>(pair, a, mp, mq, p_mn, q_mn, stream)
+                        : launch_layout<kF16>(pair, a, mp, mq, p_mn, q_mn, stream);
+}
+
+cudaError_t repack(const void* src, void* dst, int64_t rows, int64_t length, int64_t stride, int64_t pitch,
+                   int64_t size, cudaStream_t stream) {
+    const int64_t vectors = rows * (pitch * size / 16);
+    const uint32_t blocks = grid_for(uint64_t(vectors), 256, uint64_t(num_sms()) * 32);
+    if (size == 1)
+        return launch(repack_kernel<uint8_t>, blocks, 256, stream, static_cast<const uint8_t*>(src),
+                      static_cast<uint8_t*>(dst), vectors, length, stride, pitch);
+    return launch(repack_kernel<uint16_t>, blocks, 256, stream, static_cast<const uint16_t*>(src),
+                  static_cast<uint16_t*>(dst), vectors, length, stride, pitch);
 }
 
 // Runs of rows whose column sums are added up one after the other: 64 rows
@@ -24,10 +227,10 @@ int64_t slope_partials(int64_t T) {
 }
 
 cudaError_t slope(const uint16_t* g, const uint16_t* preact, uint16_t* u, float* grad_bias, float* partial, int64_t T,
-                  int64_t O, int act, int dtype, cudaStream_t stream) {
+                  int64_t O, int64_t pitch, int act, int dtype, cudaStream_t stream) {
     const int64_t runs = slope_partials(T), rows = (T + runs - 1) / runs;
     float* sums = grad_bias == nullptr ? nullptr : runs > 1 ? partial : grad_bias;
-    const bool vec = O % 8 == 0 && aligned(g, 16) && aligned(preact, 16) && aligned(u, 16);   // null is aligned
+    const bool vec = O % 8 == 0 && pitch % 8 == 0 && aligned(g, 16) && aligned(preact, 16) && aligned(u, 16);   // null is aligned
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(uint32_t((O + (vec ? 255 : 31)) / (vec ? 256 : 32)), uint32_t(runs));
     cfg.blockDim = dim3(32, kSlopeRows);
@@ -39,7 +242,7 @@ cudaError_t slope(const uint16_t* g, const uint16_t* preact, uint16_t* u, float*
     cfg.numAttrs = 1;
     auto* kernel = dtype == kBF16 ? (vec ? slope_kernel<kBF16, 8> : slope_kernel<kBF16, 1>)
                                   : (vec ? slope_kernel<kF16, 8> : slope_kernel<kF16, 1>);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, g, preact, u, sums, T, O, rows, act);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, g, preact, u, sums, T, O, pitch, rows, act);
     if (e != cudaSuccess || grad_bias == nullptr || runs == 1) return e;
     return column_sum(partial, grad_bias, uint32_t(runs), O, stream);
 }

@@ -37,9 +37,8 @@ constexpr int kAbiVersion = 1;
 
 thread_local int32_t g_last_cuda_error = 0;
 
-mhc_status_t finish(cudaError_t launch_error) {
-    cudaError_t e = launch_error;
-    if (e == cudaSuccess) e = cudaGetLastError();
+mhc_status_t finish(cudaError_t e) {
+    if (e != cudaSuccess) cudaGetLastError();   // reported here, not by the next call
     g_last_cuda_error = int32_t(e);
     return e == cudaSuccess ? MHC_OK : MHC_ERR_CUDA;
 }
@@ -171,6 +170,29 @@ mhc_status_t norm_bwd(const void* g, const void* s, const float* weight, const f
 
 constexpr int64_t kMaxSide = int64_t(1) << 30;   // coordinates are 32-bit
 
+inline int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+
+// An operand [rows, length] as the product reads it: in place where its rows
+// start on 16-byte boundaries, else copied to such rows in the workspace.
+struct Operand {
+    const void* p;
+    int64_t rows, length, stride, size;
+    bool in_place;
+
+    Operand(const void* ptr, int64_t r, int64_t l, int64_t s, int64_t sz, bool ptr_aligned)
+        : p(ptr), rows(r), length(l), stride(s), size(sz), in_place(ptr_aligned && (s * sz % 16 == 0 || r <= 1)) {}
+    int64_t pitch() const { return round16(length * size) / size; }
+    int64_t bytes() const { return in_place ? 0 : rows * pitch() * size; }
+    // Lays the operand out at `at` if need be, and moves `at` past it.
+    cudaError_t place(char*& at, cudaStream_t stream) {
+        if (in_place) return cudaSuccess;
+        const cudaError_t e = mhc::layer::repack(p, at, rows, length, stride, pitch(), size, stream);
+        p = at, stride = pitch();
+        at += rows * pitch() * size;
+        return e;
+    }
+};
+
 inline bool act_ok(int32_t a) { return a >= MHC_ACT_NONE && a <= MHC_ACT_GELU; }
 
 mhc_status_t linear_fwd(const void* x, const float* x_scale, const void* w, const float* w_scale, const float* bias,
@@ -181,17 +203,21 @@ mhc_status_t linear_fwd(const void* x, const float* x_scale, const void* w, cons
     if (T > kMaxSide || I > kMaxSide || O > kMaxSide) return MHC_ERR_UNSUPPORTED;
     if (T == 0) return MHC_OK;
     const int64_t size = fp8 ? 1 : 2;
-    const int64_t need = mhc_linear_workspace(T, I, O, x_stride, w_stride, int32_t(size),
-                                              aligned(x, 16) && aligned(w, 16));
+    Operand a(x, T, I, x_stride, size, aligned(x, 16)), b(w, O, I, w_stride, size, aligned(w, 16));
+    const int64_t need = a.bytes() + b.bytes();
     const Buffer outs[3] = {dense(y, T, O, 2), dense(preact, T, O, 2, true),
                             workspace_of(workspace, workspace_bytes, need)};
     const Buffer ins[6] = {rows(x, T, I, x_stride, size), rows(w, O, I, w_stride, size),
                            dense(x_scale, T, 1, 4, !fp8), dense(w_scale, O, 1, 4, !fp8), dense(bias, O, 1, 4, true),
                            rows(residual, T, O, residual_stride, 2, true)};
     if (!valid(outs, ins)) return MHC_ERR_INVALID_ARG;
+    char* at = static_cast<char*>(workspace);
+    cudaError_t e = a.place(at, cu(stream));
+    if (e == cudaSuccess) e = b.place(at, cu(stream));
+    if (e != cudaSuccess) return finish(e);
     mhc::linear::Product p;
-    p.a = x, p.b = w;
-    p.a_m = x_stride, p.a_k = 1, p.b_n = w_stride, p.b_k = 1;
+    p.a = a.p, p.b = b.p;
+    p.a_stride = a.stride, p.a_mn = false, p.b_stride = b.stride, p.b_mn = false;
     p.M = T, p.N = O, p.K = I;
     p.e = {fp8 ? x_scale : nullptr, fp8 ? w_scale : nullptr, bias, static_cast<const uint16_t*>(residual),
            static_cast<uint16_t*>(y), static_cast<uint16_t*>(preact), residual_stride, int(act)};
@@ -205,6 +231,8 @@ extern "C" {
 int32_t mhc_layer_abi_version(void) { return kAbiVersion; }
 
 int32_t mhc_layer_last_cuda_error(void) { return g_last_cuda_error; }
+
+int64_t mhc_layer_wait_timeouts(void) { return mhc::layer::take_wait_timeouts(); }
 
 mhc_status_t mhc_rms_norm_fwd(const void* x, const void* residual, const float* weight, void* y, void* total,
                               float* rstd, int64_t T, int64_t H, int64_t x_stride, int64_t residual_stride, float eps,
@@ -237,8 +265,9 @@ mhc_status_t mhc_rms_norm_bwd(const void* g, const void* s, const float* weight,
 
 int64_t mhc_linear_workspace(int64_t T, int64_t I, int64_t O, int64_t x_stride, int64_t w_stride, int32_t itemsize,
                              int32_t aligned) {
-    (void)T, (void)I, (void)O, (void)x_stride, (void)w_stride, (void)itemsize, (void)aligned;
-    return 0;
+    if (T <= 0 || I <= 0 || O <= 0 || (itemsize != 1 && itemsize != 2)) return 0;
+    return Operand(nullptr, T, I, x_stride, itemsize, aligned != 0).bytes() +
+           Operand(nullptr, O, I, w_stride, itemsize, aligned != 0).bytes();
 }
 
 mhc_status_t mhc_linear_fwd(const void* x, const void* w, const float* bias, const void* residual, void* y,
@@ -258,17 +287,25 @@ mhc_status_t mhc_linear_fp8_fwd(const void* x8, const float* x_scale, const void
                       x_stride, w_stride, residual_stride, act, true, dtype, stream);
 }
 
-// The workspace of the backward: u [T,O] where it is not g itself, then the
-// column sums of the bias gradient.
-static int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+// The workspace of the backward: u with rows on 16-byte boundaries, where it
+// is not g itself, the column sums of the bias gradient, then the operands
+// that have to be laid out again.
+static int64_t bwd_workspace(int64_t T, int64_t I, int64_t O, int32_t act, bool want_x, bool want_w, bool want_bias,
+                             bool g_aligned, bool x_aligned, bool w_aligned) {
+    const bool want_u = want_x || want_w;
+    const int64_t runs = mhc::layer::slope_partials(T);
+    int64_t n = want_bias && runs > 1 ? round16(runs * O * 4) : 0;
+    if (want_u) n += Operand(nullptr, T, O, O, 2, g_aligned && act == MHC_ACT_NONE).bytes();
+    if (want_w) n += Operand(nullptr, T, I, I, 2, x_aligned).bytes();
+    if (want_x) n += Operand(nullptr, O, I, I, 2, w_aligned).bytes();
+    return n;
+}
 
 int64_t mhc_linear_bwd_workspace(int64_t T, int64_t I, int64_t O, mhc_activation_t act, int32_t want_x, int32_t want_w,
                                  int32_t want_bias, int32_t aligned) {
-    (void)I, (void)aligned;
-    if (T <= 0 || O <= 0) return 0;
-    const bool own_u = act != MHC_ACT_NONE && (want_x || want_w);
-    const int64_t runs = mhc::layer::slope_partials(T);
-    return (own_u ? round16(T * O * 2) : 0) + (want_bias && runs > 1 ? runs * O * 4 : 0);
+    if (T <= 0 || I <= 0 || O <= 0) return 0;
+    const bool al = aligned != 0;
+    return bwd_workspace(T, I, O, act, want_x != 0, want_w != 0, want_bias != 0, al, al, al);
 }
 
 mhc_status_t mhc_linear_bwd(const void* g, const void* x, const void* w, const void* preact, void* grad_x,
@@ -284,39 +321,55 @@ mhc_status_t mhc_linear_bwd(const void* g, const void* x, const void* w, const v
         if (e == cudaSuccess && grad_bias != nullptr) e = cudaMemsetAsync(grad_bias, 0, size_t(O) * 4, cu(stream));
         return finish(e);
     }
-    const int64_t need = mhc_linear_bwd_workspace(T, I, O, act, grad_x != nullptr, grad_w != nullptr,
-                                                  grad_bias != nullptr, aligned(g, 16) && aligned(x, 16) && aligned(w, 16));
+    const bool want_x = grad_x != nullptr, want_w = grad_w != nullptr;
+    const int64_t need = bwd_workspace(T, I, O, act, want_x, want_w, grad_bias != nullptr, aligned(g, 16), aligned(x, 16),
+                                       aligned(w, 16));
     const Buffer outs[4] = {dense(grad_x, T, I, 2, true), dense(grad_w, O, I, 2, true), dense(grad_bias, O, 1, 4, true),
                             workspace_of(workspace, workspace_bytes, need)};
-    const Buffer ins[4] = {dense(g, T, O, 2), dense(x, T, I, 2, grad_w == nullptr), dense(w, O, I, 2, grad_x == nullptr),
+    const Buffer ins[4] = {dense(g, T, O, 2), dense(x, T, I, 2, !want_w), dense(w, O, I, 2, !want_x),
                            dense(preact, T, O, 2, act == MHC_ACT_NONE)};
     if (!valid(outs, ins)) return MHC_ERR_INVALID_ARG;
-    const bool own_u = act != MHC_ACT_NONE && (grad_x != nullptr || grad_w != nullptr);
-    char* ws = static_cast<char*>(workspace);
-    const void* u = own_u ? ws : g;
-    if (own_u || grad_bias != nullptr) {
-        const cudaError_t e = mhc::layer::slope(
-            static_cast<const uint16_t*>(g), act == MHC_ACT_NONE ? nullptr : static_cast<const uint16_t*>(preact),
-            own_u ? reinterpret_cast<uint16_t*>(ws) : nullptr, grad_bias,
-            reinterpret_cast<float*>(ws + (own_u ? round16(T * O * 2) : 0)), T, O, int(act), dtype, cu(stream));
+    char* at = static_cast<char*>(workspace);
+    float* partial = reinterpret_cast<float*>(at);
+    const int64_t runs = mhc::layer::slope_partials(T);
+    if (grad_bias != nullptr && runs > 1) at += round16(runs * O * 4);
+    cudaError_t e = cudaSuccess;
+    Operand u(g, T, O, O, 2, aligned(g, 16) && act == MHC_ACT_NONE);
+    if (act != MHC_ACT_NONE || grad_bias != nullptr) {
+        uint16_t* own = act != MHC_ACT_NONE && (want_x || want_w) ? reinterpret_cast<uint16_t*>(at) : nullptr;
+        e = mhc::layer::slope(static_cast<const uint16_t*>(g),
+                              act == MHC_ACT_NONE ? nullptr : static_cast<const uint16_t*>(preact), own, grad_bias,
+                              partial, T, O, u.pitch(), int(act), dtype, cu(stream));
         if (e != cudaSuccess) return finish(e);
+        if (own != nullptr) {
+            u.p = own, u.stride = u.pitch(), at += u.bytes(), u.in_place = true;
+        }
     }
+    if (!want_x && !want_w) return finish(cudaSuccess);
+    e = u.place(at, cu(stream));
+    if (e != cudaSuccess) return finish(e);
     mhc::linear::Product p;
     p.e = {nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, mhc::linear::kActNone};
-    if (grad_x != nullptr) {   // [T,I] = u [T,O] . w [O,I]
-        p.a = u, p.a_m = O, p.a_k = 1;
-        p.b = w, p.b_n = 1, p.b_k = I;
+    if (want_x) {   // [T,I] = u [T,O] . w [O,I]
+        Operand b(w, O, I, I, 2, aligned(w, 16));
+        e = b.place(at, cu(stream));
+        if (e != cudaSuccess) return finish(e);
+        p.a = u.p, p.a_stride = u.stride, p.a_mn = false;
+        p.b = b.p, p.b_stride = b.stride, p.b_mn = true;
         p.M = T, p.N = I, p.K = O;
         p.e.y = static_cast<uint16_t*>(grad_x);
-        const cudaError_t e = mhc::layer::product(p, dtype, dtype, cu(stream));
+        e = mhc::layer::product(p, dtype, dtype, cu(stream));
         if (e != cudaSuccess) return finish(e);
     }
-    if (grad_w != nullptr) {   // [O,I] = u^T [O,T] . x [T,I]
-        p.a = u, p.a_m = 1, p.a_k = O;
-        p.b = x, p.b_n = 1, p.b_k = I;
+    if (want_w) {   // [O,I] = u^T [O,T] . x [T,I]
+        Operand b(x, T, I, I, 2, aligned(x, 16));
+        e = b.place(at, cu(stream));
+        if (e != cudaSuccess) return finish(e);
+        p.a = u.p, p.a_stride = u.stride, p.a_mn = true;
+        p.b = b.p, p.b_stride = b.stride, p.b_mn = true;
         p.M = O, p.N = I, p.K = T;
         p.e.y = static_cast<uint16_t*>(grad_w);
-        const cudaError_t e = mhc::layer::product(p, dtype, dtype, cu(stream));
+        e = mhc::layer::product(p, dtype, dtype, cu(stream));
         if (e != cudaSuccess) return finish(e);
     }
     return finish(cudaSuccess);

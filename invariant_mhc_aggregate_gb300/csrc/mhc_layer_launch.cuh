@@ -38,13 +38,21 @@ cudaError_t rotary(const RotaryCall& c);
 // Column sums of partial [P,H] into out [H] (mhc_launch_norm.cu).
 cudaError_t column_sum(const float* partial, float* out, uint32_t P, int64_t H, cudaStream_t stream);
 
-// Matrix product (mhc_launch_linear.cu).  in, out: kBF16, kF16; in also kE4m3.
+// Matrix product (mhc_launch_linear.cu).  in, out: kBF16, kF16; in also
+// kE4m3.  Every operand's rows start on 16-byte boundaries.
 cudaError_t product(const linear::Product& p, int in, int out, cudaStream_t stream);
-// u = g * act'(preact) (u null: not stored) and, with grad_bias, its column
-// sums through `partial` (slope_partials(T) * O floats).
+// Rows of `length` elements of `size` bytes copied from `stride` to `pitch`.
+cudaError_t repack(const void* src, void* dst, int64_t rows, int64_t length, int64_t stride, int64_t pitch,
+                   int64_t size, cudaStream_t stream);
+// u = g * act'(preact) (u, of row pitch `pitch`, null: not stored) and, with
+// grad_bias, its column sums through `partial` (slope_partials(T) * O floats).
 cudaError_t slope(const uint16_t* g, const uint16_t* preact, uint16_t* u, float* grad_bias, float* partial, int64_t T,
-                  int64_t O, int act, int dtype, cudaStream_t stream);
+                  int64_t O, int64_t pitch, int act, int dtype, cudaStream_t stream);
 int64_t slope_partials(int64_t T);
+// 1 if a bounded wait of the product ran out on the current device since the
+// last call, else 0 (clears the record; synchronizes the device); -1 on a
+// CUDA error.
+int64_t take_wait_timeouts();
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 

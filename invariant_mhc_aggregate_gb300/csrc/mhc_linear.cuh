@@ -4,9 +4,8 @@
 // (t, o, i), grad_x (t, i, o) and grad_w (o, i, t).
 #pragma once
 
-#include <cuda_fp8.h>
-
 #include "mhc_device.cuh"
+#include "mhc_umma.cuh"
 
 namespace mhc {
 namespace linear {
@@ -15,13 +14,30 @@ constexpr int kE4m3 = 2;   // operand type, beside kBF16 and kF16
 
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
 
-__device__ __forceinline__ float activation(float z, int act) {
-    switch (act) {
-        case kActRelu: return z * (z > 0.0f ? 1.0f : 0.0f);
-        case kActSilu: return __fdividef(z, 1.0f + __expf(-z));
-        case kActGelu: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-        default: return z;
-    }
+// The normal distribution, from erfc(x) = t (a1 + t (a2 + t (a3 + t (a4 + t
+// a5)))) exp(-x^2), t = 1 / (1 + p x), x >= 0 (Abramowitz and Stegun, Handbook
+// of Mathematical Functions, 7.1.26: within 1.5e-7), without a branch that
+// the lanes of a warp would take apart.
+__device__ __forceinline__ float normal_cdf(float z) {
+    const float x = fabsf(z) * 0.70710678f;
+    const float t = __fdividef(1.0f, __fmaf_rn(0.3275911f, x, 1.0f));
+    float q = __fmaf_rn(t, 1.061405429f, -1.453152027f);
+    q = __fmaf_rn(t, q, 1.421413741f);
+    q = __fmaf_rn(t, q, -0.284496736f);
+    q = __fmaf_rn(t, q, 0.254829592f);
+    const float tail = 0.5f * q * t * __expf(-x * x);
+    return z < 0.0f ? tail : 1.0f - tail;
+}
+
+// The forward's exponential is the hardware's (ex2.approx through __expf,
+// within a few units of the last FP32 place): the result is rounded to 11
+// bits or fewer.
+template <int ACT>
+__device__ __forceinline__ float activation(float z) {
+    if constexpr (ACT == kActRelu) return z * (z > 0.0f ? 1.0f : 0.0f);
+    if constexpr (ACT == kActSilu) return __fdividef(z, 1.0f + __expf(-z));
+    if constexpr (ACT == kActGelu) return z * normal_cdf(z);
+    return z;
 }
 
 __device__ __forceinline__ float slope(float z, int act) {
@@ -50,66 +66,532 @@ struct Epilogue {
 struct Product {
     const void* a;
     const void* b;
-    int64_t a_m, a_k, b_n, b_k;   // strides in elements; one of each pair is 1
+    int64_t a_stride, b_stride;   // of their rows, in elements
+    bool a_mn, b_mn;              // rows run along m (n), one for each k; else along k.  b_mn where a_mn.
     int64_t M, N, K;
     Epilogue e;
 };
 
-template <int IN>
-__device__ __forceinline__ float operand(const void* p, int64_t i) {
-    if constexpr (IN == kE4m3) {
-        const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(p)[i], __NV_E4M3);
-        return __half2float(__half(h));
+// How the operands P and Q lie in memory: rows along K, or (2-byte types)
+// rows along their lanes or columns ("MN-major").
+enum Layout { kBothK = 0, kPMnQK = 1, kBothMn = 2 };   // forward, grad_x, grad_w
+
+// How a tile lies: the output's contiguous index n on the lanes of tensor
+// memory (operand P = B, 128 lanes a CTA) and its rows m on the columns
+// (operand Q = A).  A warp then holds 32 consecutive n of one row, so every
+// access of the epilogue is a contiguous 64 bytes whatever the alignment of
+// the output, and bias and column scale are one register.
+struct TileArgs {
+    Epilogue e;
+    int64_t N;               // output columns
+    uint32_t rows;           // output rows
+    uint32_t kb;             // blocks of 128 bytes of K
+    uint32_t splits;         // of K; split s takes the blocks [s kb / splits, (s + 1) kb / splits)
+    uint32_t width;          // output rows of a tile
+    uint32_t stages, stage_bytes;
+    uint32_t idesc;
+    uint32_t p_tiles, q_tiles;
+    unsigned int* timeouts;
+};
+
+constexpr uint32_t kLanesP = 128;                    // lanes of a CTA
+constexpr uint32_t kBytesP = kLanesP * 128;          // of one block of K
+constexpr uint32_t kPanel = 64 * 128;                // 64 lanes or columns x 64 K, MN-major
+constexpr uint32_t kMaxStages = 12;
+constexpr uint32_t kKPerBlock = 4;                   // MMAs (32 bytes of K each) of one block
+
+// The residual at rows m0, m0 + step, ... (C of them) of output column n;
+// 0 where it is not read.
+template <int C>
+__device__ __forceinline__ void load_residual(const Epilogue& e, bool n_ok, int64_t n, uint32_t m0, uint32_t step,
+                                              uint32_t rows, uint16_t (&r)[C]) {
+    if (e.residual == nullptr) return;
+    const uint16_t* p = e.residual + int64_t(m0) * e.residual_stride + n;
+    const int64_t stride = int64_t(step) * e.residual_stride;
+#pragma unroll
+    for (int c = 0; c < C; ++c) r[c] = n_ok && m0 + c * step < rows ? ld_stream2(p + c * stride) : uint16_t(0);
+}
+
+// From the FP32 sums v of those rows to y (and preact).  ALL: every row and
+// the column exist; else rows at or past `rows` (the end of the output, or of
+// the caller's tile) and, with n_ok false, the whole column are not touched.
+template <int OUT, int C, bool ALL>
+__device__ __forceinline__ void emit_rows(const Epilogue& e, int64_t N, bool n_ok, int64_t n, uint32_t m0, uint32_t step,
+                                          uint32_t rows, float (&v)[C], const uint16_t (&r)[C], float bias,
+                                          float col_scale) {
+    auto there = [&](int c) { return ALL || (n_ok && m0 + c * step < rows); };
+    if (e.row_scale != nullptr) {
+        const float* p = e.row_scale + m0;
+#pragma unroll
+        for (int c = 0; c < C; ++c, p += step)
+            if (there(c)) v[c] = __fmul_rn(__fmul_rn(v[c], __ldg(p)), col_scale);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) v[c] = __fadd_rn(v[c], bias);
+    const int64_t stride = int64_t(step) * N;
+    if (e.preact != nullptr) {
+        uint16_t* p = e.preact + int64_t(m0) * N + n;
+#pragma unroll
+        for (int c = 0; c < C; ++c, p += stride)
+            if (there(c)) *p = Elem<OUT>::cvt(v[c]);
+    }
+    switch (e.act) {
+        case kActRelu:
+#pragma unroll
+            for (int c = 0; c < C; ++c) v[c] = activation<kActRelu>(v[c]);
+            break;
+        case kActSilu:
+#pragma unroll
+            for (int c = 0; c < C; ++c) v[c] = activation<kActSilu>(v[c]);
+            break;
+        case kActGelu:
+#pragma unroll
+            for (int c = 0; c < C; ++c) v[c] = activation<kActGelu>(v[c]);
+            break;
+        default: break;
+    }
+    if (e.residual != nullptr) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] = __fadd_rn(v[c], Elem<OUT>::one(r[c]));
+    }
+    uint16_t* p = e.y + int64_t(m0) * N + n;
+#pragma unroll
+    for (int c = 0; c < C; ++c, p += stride)
+        if (there(c)) *p = Elem<OUT>::cvt(v[c]);
+}
+
+template <int OUT, int C>
+__device__ __forceinline__ void emit(const Epilogue& e, int64_t N, bool n_ok, int64_t n, uint32_t m0, uint32_t step,
+                                     uint32_t rows, float (&v)[C], const uint16_t (&r)[C], float bias, float col_scale) {
+    if (__all_sync(0xFFFFFFFFu, n_ok) && m0 + (C - 1) * step < rows)
+        emit_rows<OUT, C, true>(e, N, n_ok, n, m0, step, rows, v, r, bias, col_scale);
+    else
+        emit_rows<OUT, C, false>(e, N, n_ok, n, m0, step, rows, v, r, bias, col_scale);
+}
+
+__device__ __forceinline__ uint32_t split_begin(const TileArgs& a, uint32_t s) {
+    return uint32_t(uint64_t(a.kb) * s / a.splits);
+}
+
+// One block of K of P (128 lanes from p0) and of Q (`columns` from q0) into a stage.
+template <int CG, bool FP8, int LAYOUT>
+__device__ __forceinline__ void load_p(uint32_t stage, const CUtensorMap* mp, uint32_t k, int p0, uint32_t bar) {
+    const int k0 = int(k * (FP8 ? 128u : 64u));
+    if constexpr (LAYOUT == kBothK) {
+        umma::tensor_copy_2d<CG>(stage, mp, k0, p0, bar);
     } else {
-        return Elem<IN>::one(static_cast<const uint16_t*>(p)[i]);
+        umma::tensor_copy_2d<CG>(stage, mp, p0, k0, bar);
+        umma::tensor_copy_2d<CG>(stage + kPanel, mp, p0 + 64, k0, bar);
     }
 }
 
-template <int OUT>
-__device__ __forceinline__ void finish(const Epilogue& e, int64_t N, int64_t m, int64_t n, float sum) {
-    float z = sum;
-    if (e.row_scale != nullptr) z = z * e.row_scale[m] * e.col_scale[n];
-    if (e.bias != nullptr) z += e.bias[n];
-    if (e.preact != nullptr) e.preact[m * N + n] = Elem<OUT>::cvt(z);
-    z = activation(z, e.act);
-    if (e.residual != nullptr) z += Elem<OUT>::one(e.residual[m * e.residual_stride + n]);
-    e.y[m * N + n] = Elem<OUT>::cvt(z);
+template <int CG, bool FP8, int LAYOUT>
+__device__ __forceinline__ void load_q(uint32_t stage, const CUtensorMap* mq, uint32_t k, int q0, uint32_t columns,
+                                       uint32_t bar) {
+    const int k0 = int(k * (FP8 ? 128u : 64u));
+    if constexpr (LAYOUT != kBothMn) {
+        umma::tensor_copy_2d<CG>(stage + kBytesP, mq, k0, q0, bar);
+    } else {
+        for (uint32_t j = 0; j < columns; j += 64)
+            umma::tensor_copy_2d<CG>(stage + kBytesP + j / 64 * kPanel, mq, q0 + int(j), k0, bar);
+    }
 }
 
-// 64 x 64 tiles, 16 of k at a time through shared memory, 4 x 4 sums a thread.
-template <int IN, int OUT>
-__global__ void __launch_bounds__(256) simple_kernel(const Product p) {
+// Operand descriptors of stage 0; a stage further on adds its bytes / 16.  The
+// next 32 bytes of K lie 32 bytes on within the swizzled rows, or, MN-major,
+// 16 rows of 128 bytes on (addresses count 16 bytes).
+struct Descs {
+    uint64_t p, q;
+};
+
+template <int LAYOUT>
+__device__ __forceinline__ Descs descs(uint32_t stages) {
+    return {umma::smem_desc(stages, LAYOUT == kBothK ? 16 : kPanel),
+            umma::smem_desc(stages + kBytesP, LAYOUT == kBothMn ? kPanel : 16)};
+}
+
+template <int CG, bool FP8, int LAYOUT>
+__device__ __forceinline__ void multiply_block(const Descs& d, uint32_t offset, uint32_t idesc, uint32_t tmem, bool first) {
+    constexpr uint32_t kP = LAYOUT == kBothK ? 2 : 128, kQ = LAYOUT == kBothMn ? 128 : 2;
+    const uint64_t p = d.p + (offset >> 4), q = d.q + (offset >> 4);
+#pragma unroll
+    for (uint32_t i = 0; i < kKPerBlock; ++i)
+        umma::mma<CG, FP8>(tmem, p + i * kP, q + i * kQ, idesc, !(first && i == 0));
+}
+
+// The end of a producer, which is at the stage after its last: waits until no
+// copy and no completion signal of the last `issued` stages is in flight (for
+// their copies alone after a wait that ran out).
+__device__ __forceinline__ void drain(bool& ok, uint32_t issued, umma::Ring at, uint32_t count, uint32_t bar_empty,
+                                      uint32_t bar_full) {
+    for (uint32_t i = 0; i < issued; ++i) {
+        if (at.stage == 0) at.stage = count, at.parity ^= 1;
+        --at.stage;
+        ok = umma::wait((ok ? bar_empty : bar_full) + 8 * at.stage, at.parity) && ok;
+    }
+}
+
+__device__ __forceinline__ void timed_out(const TileArgs& a) { *a.timeouts = 1u; }
+
+// --------------------------------------------------------------------------
+// Few tiles: one tile of 128 lanes x `width` columns a cluster of `splits`
+// CTAs, each of which sums its part of K; the parts meet in shared memory and
+// are added in increasing order, the columns shared out among the CTAs.
+//
+// Warps 0-3 read tensor memory, one thread of warp 4 issues copies, one of
+// warp 5 multiplies.
+// --------------------------------------------------------------------------
+constexpr uint32_t kSplitThreads = 192;
+
+template <bool FP8, int OUT, int LAYOUT>
+__global__ void __launch_bounds__(kSplitThreads, 1)
+split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUtensorMap mq,
+             const __grid_constant__ TileArgs a) {
+    extern __shared__ char raw[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done;
+    __shared__ uint32_t tmem_base;
+    char* stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = a.splits > 1 ? umma::cluster_rank() : 0;
+    const int64_t n0 = int64_t(blockIdx.x / a.splits) * kLanesP;
+    const uint32_t m0 = blockIdx.y * a.width;
+    uint32_t columns = 32;
+    while (columns < a.width) columns *= 2;
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < a.stages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        mbar_init(&done, 1);
+        mbar_init_fence();
+    }
+    if (warp == 4) {
+        umma::tmem_alloc<1>(&tmem_base, columns);
+        if (lane == 0) {
+            umma::prefetch_map(&mp);
+            umma::prefetch_map(&mq);
+        }
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = tmem_base;
+    const uint32_t k0 = split_begin(a, rank), k1 = split_begin(a, rank + 1);
     pdl_enter();
-    __shared__ float sa[16][65], sb[16][65];
-    const int64_t m0 = int64_t(blockIdx.y) * 64, n0 = int64_t(blockIdx.x) * 64;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < p.K; k0 += 16) {
-        for (int i = threadIdx.x; i < 1024; i += 256) {
-            const int ka = p.a_k == 1 ? i % 16 : i / 64, ma = p.a_k == 1 ? i / 16 : i % 64;
-            sa[ka][ma] = k0 + ka < p.K && m0 + ma < p.M ? operand<IN>(p.a, (m0 + ma) * p.a_m + (k0 + ka) * p.a_k) : 0.0f;
-            const int kb = p.b_k == 1 ? i % 16 : i / 64, nb = p.b_k == 1 ? i / 16 : i % 64;
-            sb[kb][nb] = k0 + kb < p.K && n0 + nb < p.N ? operand<IN>(p.b, (n0 + nb) * p.b_n + (k0 + kb) * p.b_k) : 0.0f;
+    const uint32_t ring = smem_addr(stages), bar_full = smem_addr(full), bar_empty = smem_addr(empty);
+    const uint32_t count = a.stages, bytes = a.stage_bytes;
+    if (warp == 4) {
+        if (lane == 0) {
+            umma::Ring at;
+            bool ok = true;
+            uint32_t k = k0;
+            for (; k < k1; ++k, at.next(count)) {
+                // (the first round finds every stage free: the phase before a new barrier's first one)
+                if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
+                umma::expect_tx(bar_full + 8 * at.stage, bytes);
+                load_p<1, FP8, LAYOUT>(ring + at.stage * bytes, &mp, k, int(n0), bar_full + 8 * at.stage);
+                load_q<1, FP8, LAYOUT>(ring + at.stage * bytes, &mq, k, int(m0), a.width, bar_full + 8 * at.stage);
+            }
+            drain(ok, min(k - k0, count), at, count, bar_empty, bar_full);
+            if (!ok) timed_out(a);
         }
-        __syncthreads();
+    } else if (warp == 5) {
+        if (lane == 0) {
+            const Descs d = descs<LAYOUT>(ring);
+            umma::Ring at;
+            for (uint32_t k = k0; k < k1; ++k, at.next(count)) {
+                if (!umma::wait(bar_full + 8 * at.stage, at.parity)) {
+                    timed_out(a);
+                    break;
+                }
+                umma::fence_after_sync();
+                multiply_block<1, FP8, LAYOUT>(d, at.stage * bytes, a.idesc, tmem, k == k0);
+                umma::commit<1>(bar_empty + 8 * at.stage);
+            }
+            umma::commit<1>(smem_addr(&done));
+        }
+    } else {
+        if (!umma::wait(smem_addr(&done), 0)) timed_out(a);
+        umma::fence_after_sync();
+        const int64_t n = n0 + threadIdx.x;
+        const bool n_ok = n < a.N;
+        const uint32_t tw = tmem + (warp * 32u << 16);
+        const uint32_t valid = min(a.width, a.rows - m0);
+        const float bias = a.e.bias != nullptr && n < a.N ? __ldg(a.e.bias + n) : 0.0f;
+        const float cs = a.e.col_scale != nullptr && n < a.N ? __ldg(a.e.col_scale + n) : 1.0f;
+        float* part = reinterpret_cast<float*>(stages);   // [column][lane]: every copy has landed and been read
+        for (uint32_t c = 0; c < valid; c += 16) {
+            float v[16];
+            umma::tmem_ld(tw + c, v);
+            umma::tmem_wait_ld();
+            if (a.splits == 1) {
+                uint16_t r[16];
+                load_residual<16>(a.e, n_ok, n, m0 + c, 1, a.rows, r);
+                emit<OUT, 16>(a.e, a.N, n_ok, n, m0 + c, 1, a.rows, v, r, bias, cs);
+            } else {
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
+                for (int i = 0; i < 16; ++i) part[(c + i) * kLanesP + threadIdx.x] = v[i];
+            }
+        }
+        umma::fence_before_sync();
+    }
+    __syncwarp();
+    if (a.splits > 1) {
+        umma::cluster_sync();
+        if (warp < 4) {
+            const int64_t n = n0 + threadIdx.x;
+            const uint32_t valid = min(a.width, a.rows - m0);
+            const float bias = a.e.bias != nullptr && n < a.N ? __ldg(a.e.bias + n) : 0.0f;
+            const float cs = a.e.col_scale != nullptr && n < a.N ? __ldg(a.e.col_scale + n) : 1.0f;
+            // 8 columns at a time, their loads issued together
+            const uint32_t at = smem_addr(stages) + threadIdx.x * 4;
+            for (uint32_t c = rank; c < valid; c += 8 * a.splits) {
+                uint16_t res[8];
+                load_residual<8>(a.e, n < a.N, n, m0 + c, a.splits, m0 + valid, res);
+                float v[8];
+                for (uint32_t r = 0; r < a.splits; ++r) {
+                    const uint32_t peer = umma::map_rank(at, r);
+                    float w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                    for (uint32_t i = 0; i < 8; ++i) {
+                        const uint32_t col = c + i * a.splits;
+                        w[i] = col < valid ? umma::ld_cluster(peer + col * (kLanesP * 4)) : 0.0f;
+                    }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += sa[k][ty + 16 * i] * sb[k][tx + 16 * j];
+                    for (uint32_t i = 0; i < 8; ++i) v[i] = r == 0 ? w[i] : __fadd_rn(v[i], w[i]);
+                }
+                emit<OUT, 8>(a.e, a.N, n < a.N, n, m0 + c, a.splits, m0 + valid, v, res, bias, cs);
+            }
+        }
+        umma::cluster_sync();   // no CTA leaves while another reads its part
+    } else {
         __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m < p.M && n < p.N) finish<OUT>(p.e, p.N, m, n, acc[i][j]);
-        }
+    umma::fence_after_sync();
+    if (warp == 4) umma::tmem_free<1>(tmem, columns);
 }
 
-// u = g * act'(preact) over [T,O], rounded to u (null: not stored), and the
+// --------------------------------------------------------------------------
+// Many tiles: a pair of CTAs on two SMs computes tiles of 256 lanes x `width`
+// columns (each holds half the lanes of P and half the columns of Q in its
+// shared memory, and half the lanes of the sums), one after the other, the
+// copies running ahead across tiles.  Two accumulators of `width` columns
+// alternate, so the epilogue of one tile runs under the multiplication of the
+// next.  The parts of K that split_kernel gives to different CTAs are summed
+// apart here too and added in the same order, so that both kernels give the
+// same bits.
+//
+// Warps 0-15 read tensor memory (four warps for each quarter of the lanes, a
+// quarter of the columns each, so that the parts' sums of 64 columns fit a
+// thread's registers).  One thread of warp 16 copies P, one of warp 18 copies
+// Q (a copy takes its thread well over 100 cycles, and a block of K has 512),
+// one of warp 17 (of the first CTA) multiplies.
+// --------------------------------------------------------------------------
+constexpr uint32_t kPairEpilogueWarps = 16;
+constexpr uint32_t kPairThreads = 32 * (kPairEpilogueWarps + 3);
+constexpr uint32_t kCopyP = kPairEpilogueWarps, kMultiply = kCopyP + 1, kCopyQ = kCopyP + 2;   // warps
+constexpr int kChunk = 8;   // columns that a warp takes out of tensor memory at a time
+constexpr uint32_t kTmemColumns = 512;
+
+// Tile i of the order: bands of kBand p tiles, in each band q tile by q tile,
+// so that the tiles in flight share their operands in L2.
+constexpr uint32_t kBand = 8;
+
+
+__device__ __forceinline__ void tile_at(const TileArgs& a, uint32_t i, uint32_t& p, uint32_t& q) {
+    const uint32_t band = i / (kBand * a.q_tiles);
+    const uint32_t first = band * kBand;
+    const uint32_t height = min(kBand, a.p_tiles - first);
+    const uint32_t j = i - first * a.q_tiles;
+    q = j / height;
+    p = first + (j - q * height);
+}
+
+template <bool FP8, int OUT, int LAYOUT, bool PARTS>
+__global__ void __launch_bounds__(kPairThreads, 1)
+pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUtensorMap mq,
+            const __grid_constant__ TileArgs a) {
+    extern __shared__ char raw[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sum_full[2], sum_empty[2];
+    __shared__ uint32_t tmem_base;
+    char* stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = umma::cluster_rank();
+    const uint32_t half = a.width / 2;
+    const uint32_t tiles = a.p_tiles * a.q_tiles, step = gridDim.x / 2;
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < a.stages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(sum_full + b, 1);
+            mbar_init(sum_empty + b, 2 * kPairEpilogueWarps);
+        }
+        mbar_init_fence();
+    }
+    if (warp == kCopyP) {
+        umma::tmem_alloc<2>(&tmem_base, kTmemColumns);
+        if (lane == 0) {
+            umma::prefetch_map(&mp);
+            umma::prefetch_map(&mq);
+        }
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::cluster_sync();   // the other CTA's barriers are ready too
+    umma::fence_after_sync();
+    const uint32_t tmem = tmem_base;
+    pdl_enter();
+    const uint32_t ring = smem_addr(stages), bar_full = smem_addr(full), bar_empty = smem_addr(empty);
+    const uint32_t bar_sum = smem_addr(sum_full), bar_free = smem_addr(sum_empty);
+    const uint32_t count = a.stages, bytes = a.stage_bytes, kb = a.kb;
+    if (warp == kCopyP || warp == kCopyQ) {
+        if (lane == 0) {
+            // both CTAs' copies count on the first one's barrier; its phase cannot end
+            // before that CTA's arrival, whichever copy lands first
+            const uint32_t bar_pair = umma::map_rank(bar_full, 0);
+            umma::Ring at;
+            bool ok = true;
+            uint32_t issued = 0;
+            for (uint32_t i = blockIdx.x / 2; i < tiles && ok; i += step) {
+                uint32_t pt, qt;
+                tile_at(a, i, pt, qt);
+                const int p0 = int(pt * 2 * kLanesP + rank * kLanesP), q0 = int(qt * a.width + rank * half);
+                for (uint32_t k = 0; k < kb; ++k, ++issued, at.next(count)) {
+                    if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
+                    if (warp == kCopyP) {
+                        if (rank == 0) umma::expect_tx(bar_full + 8 * at.stage, 2 * bytes);
+                        load_p<2, FP8, LAYOUT>(ring + at.stage * bytes, &mp, k, p0, bar_pair + 8 * at.stage);
+                    } else {
+                        load_q<2, FP8, LAYOUT>(ring + at.stage * bytes, &mq, k, q0, half, bar_pair + 8 * at.stage);
+                    }
+                }
+            }
+            drain(ok, min(issued, count), at, count, bar_empty, rank == 0 ? bar_full : bar_empty);
+            if (!ok) timed_out(a);
+        }
+    } else if (warp == kMultiply) {
+        if (lane == 0 && rank == 0) {
+            const Descs d = descs<LAYOUT>(ring);
+            const uint32_t idesc = a.idesc;
+            umma::Ring at, sum;
+            bool ok = true;
+            for (uint32_t i = blockIdx.x / 2; i < tiles && ok; i += step) {
+                uint32_t k = 0;
+                for (uint32_t part = 0; part < a.splits && ok; ++part, sum.next(2)) {
+                    if (!(ok = umma::wait(bar_free + 8 * sum.stage, sum.parity ^ 1))) break;
+                    umma::fence_after_sync();
+                    const uint32_t to = tmem + sum.stage * 256, k1 = split_begin(a, part + 1);
+                    bool first = true;
+                    for (; k < k1; ++k, at.next(count)) {
+                        if (!(ok = umma::wait(bar_full + 8 * at.stage, at.parity))) break;
+                        umma::fence_after_sync();
+                        multiply_block<2, FP8, LAYOUT>(d, at.stage * bytes, idesc, to, first);
+                        umma::commit<2>(bar_empty + 8 * at.stage);
+                        first = false;
+                    }
+                    umma::commit<2>(bar_sum + 8 * sum.stage);
+                }
+            }
+            if (!ok) timed_out(a);
+        }
+    } else {
+        const uint32_t quarter = warp % 4, mine = a.width / 4, c0 = warp / 4 * mine;   // its columns: c0 .. c0 + mine
+        const uint32_t tw = tmem + (quarter * 32u << 16) + c0;
+        const uint32_t signal = umma::map_rank(bar_free, 0);
+        umma::Ring sum;
+        bool ok = true;
+        for (uint32_t i = blockIdx.x / 2; i < tiles && ok; i += step) {
+            uint32_t pt, qt;
+            tile_at(a, i, pt, qt);
+            const int64_t col = int64_t(pt) * 2 * kLanesP + rank * kLanesP + quarter * 32 + lane;
+            const uint32_t m0 = qt * a.width + c0;
+            const bool n_ok = col < a.N;
+            const float bias = a.e.bias != nullptr && col < a.N ? __ldg(a.e.bias + col) : 0.0f;
+            const float cs = a.e.col_scale != nullptr && col < a.N ? __ldg(a.e.col_scale + col) : 1.0f;
+            if constexpr (PARTS) {
+                // the parts are added up in registers, and their sum goes back to the
+                // last part's columns, from where both forms take it
+                float acc[8][kChunk];
+                for (uint32_t part = 0; part < a.splits; ++part) {
+                    if (!(ok = umma::wait(bar_sum + 8 * sum.stage, sum.parity))) break;
+                    umma::fence_after_sync();
+#pragma unroll
+                    for (uint32_t j = 0; j < 8; ++j) {
+                        if (j * kChunk < mine) {
+                            float v[kChunk];
+                            umma::tmem_ld(tw + sum.stage * 256 + j * kChunk, v);
+                            umma::tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < kChunk; ++c) acc[j][c] = part == 0 ? v[c] : __fadd_rn(acc[j][c], v[c]);
+                        }
+                    }
+                    if (part + 1 < a.splits) {
+                        umma::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) umma::arrive_cluster(signal + 8 * sum.stage);
+                        sum.next(2);
+                    }
+                }
+                if (!ok) break;
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j)
+                    if (j * kChunk < mine) umma::tmem_st(tw + sum.stage * 256 + j * kChunk, acc[j]);
+                umma::tmem_wait_st();
+            } else {
+                if (!(ok = umma::wait(bar_sum + 8 * sum.stage, sum.parity))) break;
+                umma::fence_after_sync();
+            }
+            const uint32_t from = tw + sum.stage * 256;
+            uint16_t r[kChunk];   // a chunk's residual arrives while the chunk before it is worked on
+            load_residual<kChunk>(a.e, n_ok, col, m0, 1, a.rows, r);
+#pragma unroll 1
+            for (uint32_t c = 0; c < mine; c += kChunk) {
+                float v[kChunk];
+                umma::tmem_ld(from + c, v);
+                uint16_t now[kChunk];
+#pragma unroll
+                for (int k = 0; k < kChunk; ++k) now[k] = r[k];
+                if (c + kChunk < mine) load_residual<kChunk>(a.e, n_ok, col, m0 + c + kChunk, 1, a.rows, r);
+                umma::tmem_wait_ld();
+                emit<OUT, kChunk>(a.e, a.N, n_ok, col, m0 + c, 1, a.rows, v, now, bias, cs);
+            }
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) umma::arrive_cluster(signal + 8 * sum.stage);
+            sum.next(2);
+        }
+        if (!ok) timed_out(a);
+        umma::fence_before_sync();
+    }
+    __syncwarp();
+    umma::cluster_sync();   // neither CTA leaves while the other may still signal it
+    umma::fence_after_sync();
+    if (warp == kCopyP) umma::tmem_free<2>(tmem, kTmemColumns);
+}
+
+// Rows of `length` values copied to a row pitch that starts every row on 16
+// bytes, for operands that the tensor copies cannot read in place.  A thread
+// writes one 16-byte vector.
+template <class V>
+__global__ void __launch_bounds__(256)
+repack_kernel(const V* __restrict__ src, V* __restrict__ dst, int64_t vectors, int64_t length, int64_t stride,
+              int64_t pitch) {
+    pdl_enter();
+    constexpr int W = 16 / sizeof(V);
+    const int64_t per_row = pitch / W;
+    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < vectors; i += int64_t(gridDim.x) * 256) {
+        const int64_t row = i / per_row, c = (i - row * per_row) * W;
+        const V* p = src + row * stride + c;
+        alignas(16) V v[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) v[j] = c + j < length ? p[j] : V(0);
+        *reinterpret_cast<uint4*>(dst + row * pitch + c) = *reinterpret_cast<const uint4*>(v);
+    }
+}
+
+// u = g * act'(preact) over [T,O], rounded to u (row pitch `pitch`; null: not stored), and the
 // column sums of the unrounded u over each of gridDim.y runs of `rows` rows
 // in partial [gridDim.y, O] (null: not wanted).  Block (32, 8): 32 W columns,
 // 8 rows at a time.
@@ -118,7 +600,7 @@ constexpr int kSlopeRows = 8;
 template <int DT, int W>
 __global__ void __launch_bounds__(32 * kSlopeRows)
 slope_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ preact, uint16_t* __restrict__ u,
-             float* __restrict__ partial, int64_t T, int64_t O, int64_t rows, int act) {
+             float* __restrict__ partial, int64_t T, int64_t O, int64_t pitch, int64_t rows, int act) {
     pdl_enter();
     __shared__ float part[kSlopeRows][32 * W];
     const int64_t c = (int64_t(blockIdx.x) * 32 + threadIdx.x) * W;
@@ -147,12 +629,12 @@ slope_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ preact
                     Words<4> o;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o.w[i] = Elem<DT>::pack(v[2 * i], v[2 * i + 1]);
-                    *reinterpret_cast<Words<4>*>(u + at) = o;
+                    *reinterpret_cast<Words<4>*>(u + t * pitch + c) = o;
                 }
             } else {
                 v[0] = Elem<DT>::one(g[at]);
                 if (act != kActNone) v[0] *= slope(Elem<DT>::one(preact[at]), act);
-                if (u != nullptr) u[at] = Elem<DT>::cvt(v[0]);
+                if (u != nullptr) u[t * pitch + c] = Elem<DT>::cvt(v[0]);
             }
 #pragma unroll
             for (int i = 0; i < W; ++i) acc[i] = __fadd_rn(acc[i], v[i]);

@@ -48,6 +48,7 @@ EXPORTS = (
     "mhc_linear_bwd_workspace",
     "mhc_rotary",
     "mhc_layer_last_cuda_error",
+    "mhc_layer_wait_timeouts",
 )
 
 _STATUS = {1: "MHC_ERR_INVALID_ARG", 2: "MHC_ERR_UNSUPPORTED", 3: "MHC_ERR_CUDA"}
@@ -92,11 +93,19 @@ def load():
                 ("mhc_linear_workspace", i64, [i64] * 5 + [i32, i32]),
                 ("mhc_linear_bwd_workspace", i64, [i64] * 3 + [i32] * 5),
                 ("mhc_rotary", i32, [p] * 4 + [i64] * 8 + [f32, i32, i32, i32, p]),
-                ("mhc_layer_last_cuda_error", i32, [])):
+                ("mhc_layer_last_cuda_error", i32, []),
+                ("mhc_layer_wait_timeouts", i64, [])):
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = res, args
         _lib = lib
         return lib
+
+
+def wait_timeouts() -> int:
+    """1 if a bounded wait of the product's kernels ran out on the current
+    device since the last call, else 0 (clears it; synchronizes the device);
+    -1 on a CUDA error."""
+    return int(load().mhc_layer_wait_timeouts())
 
 
 _DTYPES = {torch.bfloat16: MHC_DTYPE_BF16, torch.float16: MHC_DTYPE_F16}
