@@ -10,7 +10,7 @@ namespace {
 
 // Threads of a row and chunks of a thread: they fix the order of the row's
 // sum, so they follow from H alone.  Up to 1024 values a warp holds the row;
-// longer rows take 4 chunks a thread.
+// longer rows take 2 chunks a thread, past 8192 values 4, past 16384 values 8.
 struct Shape {
     uint32_t nt;
     int K;
@@ -21,18 +21,23 @@ Shape shape_of(uint32_t H) {
     if (chunks <= 32) return {32, 1};
     if (chunks <= 64) return {32, 2};
     if (chunks <= 128) return {32, 4};
-    return {(chunks + 127) / 128 * 32, 4};
+    if (chunks <= 1024) return {(chunks + 63) / 64 * 32, 2};
+    if (chunks <= 2048) return {(chunks + 127) / 128 * 32, 4};
+    return {kMaxThreads, 8};
 }
 
 constexpr uint32_t kWarpRows = 4;   // rows of a block where a warp holds a row
 
+// Shared memory of one SM that the blocks of these kernels share out.
+constexpr uint32_t kRowSmem = 216 * 1024;
+
 uint32_t stage_bytes(Shape s) { return 8u * uint32_t(s.K) * s.nt * 4u; }
 
-template <typename Args>
-cudaError_t launch_rows(void (*kernel)(Args), uint32_t grid, uint32_t nt, uint32_t rows, uint32_t smem,
-                        std::atomic<uint64_t>& allowed, cudaStream_t stream, const Args& a) {
+template <typename... Params, typename... Args>
+cudaError_t launch_rows(void (*kernel)(Params...), uint32_t grid, uint32_t nt, uint32_t rows, uint32_t smem,
+                        std::atomic<uint64_t>& allowed, cudaStream_t stream, Args... args) {
     if (smem > 48 * 1024) {
-        const cudaError_t e = allow_smem(kernel, 8 * 4 * 1024 * 4, allowed);
+        const cudaError_t e = allow_smem(kernel, kRowSmem, allowed);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -45,7 +50,23 @@ cudaError_t launch_rows(void (*kernel)(Args), uint32_t grid, uint32_t nt, uint32
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+// The ring kernels' shape: blocks of an SM and stages of a block, so that the
+// ring of each SM holds most of its shared memory.
+struct RingShape {
+    uint32_t blocks, stages;   // blocks: of one SM
+};
+
+// `most`: blocks of an SM that the kernel's registers allow.
+RingShape ring_shape(uint32_t row_bytes, uint32_t most) {
+    const uint32_t fit = kRowSmem / (2 * row_bytes + 1024);   // with two stages each
+    RingShape r;
+    r.blocks = fit < 1 ? 1 : fit < most ? fit : most;
+    r.stages = kRowSmem / r.blocks / row_bytes;
+    if (r.stages > kRingStages) r.stages = kRingStages;
+    return r;
 }
 
 template <int DT, int K, bool VEC, int OUT>
@@ -72,8 +93,28 @@ cudaError_t fwd_launch(const FwdArgs& args, Shape s, cudaStream_t stream) {
     return cudaSuccess;
 }
 
+template <int DT, int K, int OUT>
+cudaError_t fwd_ring(const FwdArgs& a, Shape s, RingShape ring, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed{0}, narrow{0};
+    RingRows r = {{a.x, a.residual, nullptr}, {a.x_stride, a.residual_stride, 0}, a.residual != nullptr ? 2u : 1u};
+    const uint32_t grid = uint32_t(num_sms()) * ring.blocks, smem = ring.stages * r.arrays * a.H * 2;
+    if (K == 2 && s.nt <= 448)
+        return launch_rows(fwd_ring_kernel<DT, K, OUT, 448>, grid, s.nt, 1, smem, narrow, stream, a, r, ring.stages);
+    return launch_rows(fwd_ring_kernel<DT, K, OUT, 512>, grid, s.nt, 1, smem, allowed, stream, a, r, ring.stages);
+}
+
 template <int DT, int K, bool VEC>
 cudaError_t fwd_out(const FwdArgs& a, Shape s, int out, cudaStream_t stream) {
+    if constexpr (VEC && (K == 2 || K == 4)) {
+        const uint32_t row = a.H * 2 * (a.residual != nullptr ? 2 : 1);
+        const RingShape ring = ring_shape(row, K == 2 ? 65536 / (s.nt * (s.nt <= 448 ? 72 : 64)) : 1);
+        // (not for rows of one warp, nor where a block would have no second row)
+        if (s.nt > 32 && ring.stages >= 2 && a.T > int64_t(num_sms()) * ring.blocks) switch (out) {
+            case kOutSame: return fwd_ring<DT, K, kOutSame>(a, s, ring, stream);
+            case kOutFp8Row: return fwd_ring<DT, K, kOutFp8Row>(a, s, ring, stream);
+            default: return fwd_ring<DT, K, kOutFp8Group>(a, s, ring, stream);
+        }
+    }
     switch (out) {
         case kOutSame: return fwd_launch<DT, K, VEC, kOutSame>(a, s, stream);
         case kOutFp8Row: return fwd_launch<DT, K, VEC, kOutFp8Row>(a, s, stream);
@@ -87,7 +128,8 @@ cudaError_t fwd_shape(const FwdArgs& a, int out, cudaStream_t stream) {
     switch (s.K) {
         case 1: return fwd_out<DT, 1, VEC>(a, s, out, stream);
         case 2: return fwd_out<DT, 2, VEC>(a, s, out, stream);
-        default: return fwd_out<DT, 4, VEC>(a, s, out, stream);
+        case 4: return fwd_out<DT, 4, VEC>(a, s, out, stream);
+        default: return fwd_out<DT, 8, VEC>(a, s, out, stream);
     }
 }
 
@@ -95,6 +137,18 @@ template <int DT, int K, bool VEC>
 cudaError_t bwd_launch(const BwdArgs& a, Shape s, uint32_t blocks, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
     const uint32_t rows = VEC && s.nt == 32 ? kWarpRows : 1;
+    if constexpr (VEC && (K == 2 || K == 4)) {
+        const RingRows r = {{a.g, a.s, a.grad_total}, {a.g_stride, a.s_stride, int64_t(a.H)}, a.grad_total != nullptr ? 3u : 2u};
+        const uint32_t row = a.H * 2 * r.arrays;
+        RingShape ring = ring_shape(row, (blocks + uint32_t(num_sms()) - 1) / uint32_t(num_sms()));
+        if (rows == 1 && ring.stages >= 2 && a.T > int64_t(blocks)) {
+            static std::atomic<uint64_t> ring_allowed{0}, narrow{0};
+            const uint32_t smem = ring.stages * row;
+            if (K == 2 && s.nt <= 448)
+                return launch_rows(bwd_ring_kernel<DT, K, 448>, blocks, s.nt, 1, smem, narrow, stream, a, r, ring.stages);
+            return launch_rows(bwd_ring_kernel<DT, K, 512>, blocks, s.nt, 1, smem, ring_allowed, stream, a, r, ring.stages);
+        }
+    }
     return launch_rows(bwd_kernel<DT, K, VEC>, blocks, s.nt, rows, VEC && rows == 1 ? 0 : stage_bytes(s), allowed,
                        stream, a);
 }
@@ -105,7 +159,8 @@ cudaError_t bwd_shape(const BwdArgs& a, uint32_t blocks, cudaStream_t stream) {
     switch (s.K) {
         case 1: return bwd_launch<DT, 1, VEC>(a, s, blocks, stream);
         case 2: return bwd_launch<DT, 2, VEC>(a, s, blocks, stream);
-        default: return bwd_launch<DT, 4, VEC>(a, s, blocks, stream);
+        case 4: return bwd_launch<DT, 4, VEC>(a, s, blocks, stream);
+        default: return bwd_launch<DT, 8, VEC>(a, s, blocks, stream);
     }
 }
 
@@ -120,12 +175,13 @@ cudaError_t norm_fwd(const FwdArgs& a, int dtype, int out, cudaStream_t stream) 
     return vec ? fwd_shape<kF16, true>(a, out, stream) : fwd_shape<kF16, false>(a, out, stream);
 }
 
-// Blocks of the backward, each with a partial sum of grad_weight: two for
-// each of the 152 SMs, a constant so that the sum's order does not depend on
-// the device.
+// Blocks of the backward, each with a partial sum of grad_weight: for each of
+// 152 SMs as many as have 1024 threads (a constant, so that the sum's order
+// does not depend on the device), at most one for each row.
 uint32_t norm_bwd_partials(int64_t T, int64_t H) {
-    (void)H;
-    return uint32_t(T < 304 ? T : 304);
+    const Shape s = shape_of(uint32_t(H));
+    const int64_t most = 152 * (1024 / s.nt < 8 ? 1024 / s.nt : 8);
+    return uint32_t(T < most ? T : most);
 }
 
 cudaError_t norm_bwd(BwdArgs a, float* grad_weight, float* workspace, int dtype, cudaStream_t stream) {

@@ -12,21 +12,27 @@
 // lanes at distance 16, 8, 4, 2, 1; the warps' results are added in
 // increasing order.  nt and K follow from H (shape_of).
 //
-// Two ways to move a row, with the same sums:
-//  * VEC: 16-byte loads and stores of the thread's own chunks (H % 8 == 0 and
-//    16-byte aligned rows);
+// Three ways to move a row, with the same sums:
+//  * ring: rows of 16-byte aligned values (H % 8 == 0) longer than a warp
+//    holds, more of them than there are blocks: bulk copies bring a block's
+//    next rows to shared memory while it works on one, so that the loads of
+//    a row do not wait for its sum; the norm's weight stays in registers;
+//  * VEC: 16-byte loads and stores of the thread's own chunks, for the other
+//    aligned rows;
 //  * otherwise thread j moves the values j, j + nt, ... with 2-byte accesses
 //    (a warp's accesses are then contiguous whatever the row's alignment) and
 //    the products of a row's sum change hands through shared memory, where
 //    every row is aligned.
 #pragma once
 
+#include "mhc_bulk.cuh"
 #include "mhc_device.cuh"
 
 namespace mhc {
 namespace norm {
 
 constexpr int kMaxH = 32768;
+constexpr int kMaxThreads = 512;   // of a row
 constexpr float kE4m3Max = 448.0f;
 constexpr float kAmaxFloor = 0x1p-60f;
 
@@ -41,6 +47,7 @@ struct FwdArgs {
     float* scale;
     uint16_t* total;
     float* rstd;
+    unsigned int* timeouts;     // ring kernels only
     int64_t T;
     int64_t x_stride, residual_stride;
     uint32_t H;
@@ -55,6 +62,7 @@ struct BwdArgs {
     const uint16_t* grad_total;   // null without one
     uint16_t* grad_x;
     float* partial;               // [gridDim.x, H]
+    unsigned int* timeouts;       // ring kernels only
     int64_t T;
     int64_t g_stride, s_stride;
     uint32_t H;
@@ -210,32 +218,10 @@ __device__ __forceinline__ float row_sum(const float (&q)[8 * K], float* stage, 
     return fold(acc, shared, Add());
 }
 
-// Forward: block (nt, rows); rows > 1 only with VEC and nt = 32 (a warp per
-// row, no barrier).
+// The row's output from v: 16-bit values, or E4M3 values and their scales.
 template <int DT, int K, bool VEC, int OUT>
-__global__ void fwd_kernel(const FwdArgs a) {
-    pdl_enter();
-    extern __shared__ __align__(16) float stage[];
-    __shared__ float shared[2][32];
-    const int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
-    if (t >= a.T) return;
+__device__ __forceinline__ void store_y(const FwdArgs& a, int64_t t, float (&s)[8 * K], float* stage, float* shared) {
     const uint32_t H = a.H, nt = blockDim.x, j = threadIdx.x;
-    float s[8 * K], q[8 * K];
-    load_row<DT, K, VEC>(a.x + t * a.x_stride, H, s);
-    if (a.residual != nullptr) {
-        load_row<DT, K, VEC>(a.residual + t * a.residual_stride, H, q);
-#pragma unroll
-        for (int i = 0; i < 8 * K; ++i) s[i] = __fadd_rn(s[i], q[i]);
-        store_row<DT, K, VEC>(a.total + t * int64_t(H), H, s);
-    }
-#pragma unroll
-    for (int i = 0; i < 8 * K; ++i) q[i] = __fmul_rn(s[i], s[i]);
-    const float sum = row_sum<K, VEC>(q, stage, shared[0]);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(H)), a.eps)));
-    if (j == 0) a.rstd[t] = rstd;
-    load_weight<K, VEC>(a.weight, H, q);
-#pragma unroll
-    for (int i = 0; i < 8 * K; ++i) s[i] = __fmul_rn(__fmul_rn(s[i], rstd), q[i]);
     if constexpr (OUT == kOutSame) {
         store_row<DT, K, VEC>(static_cast<uint16_t*>(a.y) + t * int64_t(H), H, s);
     } else {
@@ -246,7 +232,7 @@ __global__ void fwd_kernel(const FwdArgs a) {
             float m = kAmaxFloor;
 #pragma unroll
             for (int i = 0; i < 8 * K; ++i) m = max_nan(m, fabsf(s[i]));
-            m = fold(m, shared[1], Max());
+            m = fold(m, shared, Max());
             if (j == 0) a.scale[t] = __fdiv_rn(m, kE4m3Max);
             const float r = __fdiv_rn(kE4m3Max, m);
 #pragma unroll
@@ -306,12 +292,63 @@ __global__ void fwd_kernel(const FwdArgs a) {
     }
 }
 
+// Forward: block (nt, rows); rows > 1 only with VEC and nt = 32 (a warp per
+// row, no barrier).
+template <int DT, int K, bool VEC, int OUT>
+__global__ void __launch_bounds__(kMaxThreads, 1) fwd_kernel(const FwdArgs a) {
+    pdl_enter();
+    extern __shared__ __align__(16) float stage[];
+    __shared__ float shared[2][32];
+    const int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (t >= a.T) return;
+    const uint32_t H = a.H, j = threadIdx.x;
+    float s[8 * K], q[8 * K];
+    load_row<DT, K, VEC>(a.x + t * a.x_stride, H, s);
+    if (a.residual != nullptr) {
+        load_row<DT, K, VEC>(a.residual + t * a.residual_stride, H, q);
+#pragma unroll
+        for (int i = 0; i < 8 * K; ++i) s[i] = __fadd_rn(s[i], q[i]);
+        store_row<DT, K, VEC>(a.total + t * int64_t(H), H, s);
+    }
+#pragma unroll
+    for (int i = 0; i < 8 * K; ++i) q[i] = __fmul_rn(s[i], s[i]);
+    const float sum = row_sum<K, VEC>(q, stage, shared[0]);
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(H)), a.eps)));
+    if (j == 0) a.rstd[t] = rstd;
+    load_weight<K, VEC>(a.weight, H, q);
+#pragma unroll
+    for (int i = 0; i < 8 * K; ++i) s[i] = __fmul_rn(__fmul_rn(s[i], rstd), q[i]);
+    store_y<DT, K, VEC, OUT>(a, t, s, stage, shared[1]);
+}
+
+template <int K, bool VEC>
+__device__ __forceinline__ void store_partial(float* __restrict__ out, uint32_t H, const float (&acc)[8 * K]) {
+    const uint32_t nt = blockDim.x, j = threadIdx.x;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const uint32_t c = 8 * (j + k * nt);
+            if (c < H) {
+                float4* p = reinterpret_cast<float4*>(out + c);
+                p[0] = make_float4(acc[8 * k], acc[8 * k + 1], acc[8 * k + 2], acc[8 * k + 3]);
+                p[1] = make_float4(acc[8 * k + 4], acc[8 * k + 5], acc[8 * k + 6], acc[8 * k + 7]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < 8 * K; ++m) {
+            const uint32_t c = j + m * nt;
+            if (c < H) out[c] = acc[m];
+        }
+    }
+}
+
 // Backward: block b takes rows b * rows + y, then steps of gridDim.x * rows
 // (rows = blockDim.y > 1 only with VEC and nt = 32), writes their grad_x and
 // leaves the sum of their g * n in partial[b]; the rows of one (b, y) are
 // added in increasing order, then the y in increasing order.
 template <int DT, int K, bool VEC>
-__global__ void bwd_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 1) bwd_kernel(const BwdArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float stage[];
     __shared__ float shared[2][32];
@@ -344,7 +381,6 @@ __global__ void bwd_kernel(const BwdArgs a) {
         }
         store_row<DT, K, VEC>(a.grad_x + t * int64_t(H), H, g);
     }
-    float* out = a.partial + int64_t(blockIdx.x) * H;
     if (rows > 1) {   // the warps of a block one after the other, in shared memory
         for (uint32_t y = 0; y < rows; ++y) {
             if (threadIdx.y == y) {
@@ -360,29 +396,193 @@ __global__ void bwd_kernel(const BwdArgs a) {
 #pragma unroll
         for (int i = 0; i < 8 * K; ++i) acc[i] = stage[j + i * 32];
     }
-    if constexpr (VEC) {
+    store_partial<K, VEC>(a.partial + int64_t(blockIdx.x) * H, H, acc);
+}
+
+// The ring of a block: kept rows of `arrays` buffers, bulk-copied by thread 0.
+// Stage i of the ring holds the block's rows i, i + stages, ...; its buffers
+// lie one after the other.  A stage is free again after the barrier inside
+// the row's sum: by then every thread has its values in registers.
+struct RingRows {
+    const uint16_t* from[3];
+    int64_t stride[3];
+    uint32_t arrays;
+};
+
+__device__ __forceinline__ void ring_copy(char* stage, const RingRows& r, int64_t t, uint32_t bytes, uint64_t* full) {
+    mbar_arrive_expect_tx(full, r.arrays * bytes);
+    for (uint32_t i = 0; i < r.arrays; ++i) bulk_copy_g2s(stage + i * bytes, r.from[i] + t * r.stride[i], bytes, full);
+}
+
+template <int DT, int K>
+__device__ __forceinline__ void stage_words(const char* row, uint32_t H, Words<4> (&w)[K]) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const uint32_t c = 8 * (j + k * nt);
-            if (c < H) {
-                float4* p = reinterpret_cast<float4*>(out + c);
-                p[0] = make_float4(acc[8 * k], acc[8 * k + 1], acc[8 * k + 2], acc[8 * k + 3]);
-                p[1] = make_float4(acc[8 * k + 4], acc[8 * k + 5], acc[8 * k + 6], acc[8 * k + 7]);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int m = 0; m < 8 * K; ++m) {
-            const uint32_t c = j + m * nt;
-            if (c < H) out[c] = acc[m];
-        }
+    for (int k = 0; k < K; ++k) {
+        const uint32_t c = 8 * (threadIdx.x + k * blockDim.x);
+        const uint4 v = c < H ? *reinterpret_cast<const uint4*>(row + 2 * c) : make_uint4(0, 0, 0, 0);
+        w[k].w[0] = v.x, w[k].w[1] = v.y, w[k].w[2] = v.z, w[k].w[3] = v.w;
     }
 }
 
-// Column sums of partial [P,H]: block (32, 8); thread (x, y) adds the rows
-// y, y + 8, ... of column x in increasing order, then the 8 sums in
+template <int DT>
+__device__ __forceinline__ void chunk_values(const Words<4>& w, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = Elem<DT>::lo(w.w[i]), v[2 * i + 1] = Elem<DT>::hi(w.w[i]);
+}
+
+constexpr uint32_t kRingStages = 4;   // at most
+
+template <int DT, int K, int OUT, int MAXT>
+__global__ void __launch_bounds__(MAXT, K == 2 ? 2 : 1)
+fwd_ring_kernel(const FwdArgs a, const RingRows r, uint32_t stages) {
+    extern __shared__ __align__(16) char ring[];
+    __shared__ float shared[2][2][32];
+    __shared__ uint64_t full[kRingStages];
+    const uint32_t H = a.H, j = threadIdx.x, bytes = 2 * H;
+    if (j == 0) {
+        for (uint32_t s = 0; s < stages; ++s) mbar_init(full + s, 1);
+        mbar_init_fence();
+    }
+    __syncthreads();
+    pdl_enter();
+    const int64_t step = gridDim.x;
+    if (j == 0)
+        for (uint32_t s = 0; s < stages; ++s)
+            if (blockIdx.x + s * step < a.T) ring_copy(ring + s * r.arrays * bytes, r, blockIdx.x + s * step, bytes, full + s);
+    float w[8 * K];
+    load_weight<K, true>(a.weight, H, w);
+    uint32_t stage = 0, parity = 0;
+    int turn = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < a.T; t += step, turn ^= 1) {
+        ok = mbar_wait_fast(full + stage, parity) && ok;
+        const char* row = ring + stage * r.arrays * bytes;
+        Words<4> raw[K];
+        float s[8 * K];
+        stage_words<DT, K>(row, H, raw);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float v[8];
+            chunk_values<DT>(raw[k], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[8 * k + i] = v[i];
+        }
+        if (r.arrays > 1) {
+            stage_words<DT, K>(row + bytes, H, raw);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float v[8];
+                chunk_values<DT>(raw[k], v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[8 * k + i] = __fadd_rn(s[8 * k + i], v[i]);
+            }
+            store_row<DT, K, true>(a.total + t * int64_t(H), H, s);
+        }
+        float acc = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(s[8 * k + i], s[8 * k + i]);
+            acc = __fadd_rn(acc, chunk_sum(q));
+        }
+        const float sum = fold(acc, shared[turn][0], Add());
+        if (j == 0 && t + stages * step < a.T && ok) {
+            fence_proxy_async_shared();
+            ring_copy(ring + stage * r.arrays * bytes, r, t + stages * step, bytes, full + stage);
+        }
+        if (++stage == stages) stage = 0, parity ^= 1;
+        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(H)), a.eps)));
+        if (j == 0) a.rstd[t] = rstd;
+#pragma unroll
+        for (int i = 0; i < 8 * K; ++i) s[i] = __fmul_rn(__fmul_rn(s[i], rstd), w[i]);
+        store_y<DT, K, true, OUT>(a, t, s, nullptr, shared[turn][1]);
+    }
+    if (!ok && a.timeouts != nullptr) *a.timeouts = 1u;
+}
+
+template <int DT, int K, int MAXT>
+__global__ void __launch_bounds__(MAXT, K == 2 ? 2 : 1)
+bwd_ring_kernel(const BwdArgs a, const RingRows r, uint32_t stages) {
+    extern __shared__ __align__(16) char ring[];
+    __shared__ float shared[2][32];
+    __shared__ uint64_t full[kRingStages];
+    const uint32_t H = a.H, j = threadIdx.x, bytes = 2 * H;
+    if (j == 0) {
+        for (uint32_t s = 0; s < stages; ++s) mbar_init(full + s, 1);
+        mbar_init_fence();
+    }
+    __syncthreads();
+    pdl_enter();
+    const int64_t step = gridDim.x;
+    if (j == 0)
+        for (uint32_t s = 0; s < stages; ++s)
+            if (blockIdx.x + s * step < a.T) ring_copy(ring + s * r.arrays * bytes, r, blockIdx.x + s * step, bytes, full + s);
+    float w[8 * K], acc[8 * K];
+    load_weight<K, true>(a.weight, H, w);
+#pragma unroll
+    for (int i = 0; i < 8 * K; ++i) acc[i] = 0.0f;
+    uint32_t stage = 0, parity = 0;
+    int turn = 0;
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < a.T; t += step, turn ^= 1) {
+        const float rstd = __ldg(a.rstd + t);
+        ok = mbar_wait_fast(full + stage, parity) && ok;
+        const char* row = ring + stage * r.arrays * bytes;
+        Words<4> g[K], n[K], more[K];
+        stage_words<DT, K>(row, H, g);
+        stage_words<DT, K>(row + bytes, H, n);
+        if (r.arrays > 2) stage_words<DT, K>(row + 2 * bytes, H, more);
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            float gv[8], nv[8], q[8];
+            chunk_values<DT>(g[k], gv);
+            chunk_values<DT>(n[k], nv);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                nv[i] = __fmul_rn(nv[i], rstd);
+                acc[8 * k + i] = __fadd_rn(acc[8 * k + i], __fmul_rn(gv[i], nv[i]));
+                q[i] = __fmul_rn(__fmul_rn(gv[i], w[8 * k + i]), nv[i]);
+            }
+            sum = __fadd_rn(sum, chunk_sum(q));
+        }
+        const float m = __fdiv_rn(fold(sum, shared[turn], Add()), float(H));
+        if (j == 0 && t + stages * step < a.T && ok) {
+            fence_proxy_async_shared();
+            ring_copy(ring + stage * r.arrays * bytes, r, t + stages * step, bytes, full + stage);
+        }
+        if (++stage == stages) stage = 0, parity ^= 1;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const uint32_t c = 8 * (j + k * blockDim.x);
+            if (c < H) {
+                float gv[8], nv[8], tv[8];
+                chunk_values<DT>(g[k], gv);
+                chunk_values<DT>(n[k], nv);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    gv[i] = __fmul_rn(rstd, __fsub_rn(__fmul_rn(gv[i], w[8 * k + i]), __fmul_rn(__fmul_rn(nv[i], rstd), m)));
+                if (r.arrays > 2) {
+                    chunk_values<DT>(more[k], tv);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) gv[i] = __fadd_rn(gv[i], tv[i]);
+                }
+                Words<4> o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o.w[i] = Elem<DT>::pack(gv[2 * i], gv[2 * i + 1]);
+                st_stream<4>(a.grad_x + t * int64_t(H) + c, o);
+            }
+        }
+    }
+    store_partial<K, true>(a.partial + int64_t(blockIdx.x) * H, H, acc);
+    if (!ok && a.timeouts != nullptr) *a.timeouts = 1u;
+}
+
+// Column sums of partial [P,H]: block (32, 32); thread (x, y) adds the rows
+// y, y + 32, ... of column x in increasing order, then the 32 sums in
 // increasing order.  Also the bias gradient's last step.
-constexpr int kColRows = 8;
+constexpr int kColRows = 32;
 
 static __global__ void __launch_bounds__(32 * kColRows)
 column_sum_kernel(const float* __restrict__ partial, float* __restrict__ out, uint32_t P, uint32_t H) {
@@ -391,7 +591,7 @@ column_sum_kernel(const float* __restrict__ partial, float* __restrict__ out, ui
     const uint32_t c = blockIdx.x * 32 + threadIdx.x;
     float acc = 0.0f;
     if (c < H)
-#pragma unroll 4
+#pragma unroll 8
         for (uint32_t p = threadIdx.y; p < P; p += kColRows) acc = __fadd_rn(acc, partial[uint64_t(p) * H + c]);
     part[threadIdx.y][threadIdx.x] = acc;
     __syncthreads();
