@@ -11,7 +11,8 @@ template <int DT, int W>
 cudaError_t launch_width(const RotaryCall& c) {
     const bool one_piece = c.interleaved && W > 1;
     const uint32_t rot_units = uint32_t(one_piece ? c.R / W : c.R / (2 * W));
-    const uint32_t units = rot_units + uint32_t((c.D - c.R) / W);
+    const uint32_t copied = uint32_t((c.D - c.R) / W), copy_units = one_piece ? copied : (copied + 1) / 2;
+    const uint32_t units = rot_units + copy_units;
     // Heads of one thread: 8 share a thread's cosines and sines (their cost
     // is then below that of the values' own arithmetic); fewer where the call
     // would not give each SM 1024 threads.
@@ -31,7 +32,8 @@ cudaError_t launch_width(const RotaryCall& c) {
         a.frequencies = c.frequencies;
         a.x_token = c.x_token, a.x_head = c.x_head, a.out_token = c.out_token, a.out_head = c.out_head;
         a.work = uint64_t(nt) * per_token;
-        a.heads = uint32_t(c.heads), a.rotated = uint32_t(c.R);
+        a.heads = uint32_t(c.heads), a.D = uint32_t(c.D), a.R = uint32_t(c.R);
+        a.copy_gap = copy_units * W;
         a.lead = c.interleaved ? 2 : W;
         a.gap = c.interleaved ? 1 : uint32_t(c.R / 2);
         a.run = uint32_t(run);

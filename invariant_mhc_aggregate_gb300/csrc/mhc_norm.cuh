@@ -501,8 +501,8 @@ fwd_ring_kernel(const FwdArgs a, const RingRows r, uint32_t stages) {
     if (!ok && a.timeouts != nullptr) *a.timeouts = 1u;
 }
 
-template <int DT, int K, int MAXT>
-__global__ void __launch_bounds__(MAXT, K == 2 ? 2 : 1)
+template <int DT, int K>
+__global__ void __launch_bounds__(kMaxThreads, 1)
 bwd_ring_kernel(const BwdArgs a, const RingRows r, uint32_t stages) {
     extern __shared__ __align__(16) char ring[];
     __shared__ float shared[2][32];
