@@ -65,11 +65,8 @@ cudaError_t encode(CUtensorMap* map, const void* base, int64_t rows, int64_t len
 constexpr uint32_t kRingBytes = 224 * 1024;
 
 // Parts of K: as many (1, 2, 4 or 8) as the GPU's 152 SMs can take at once
-// when the call has few rows, with at least 8 blocks of K a part.  It
-// follows from N and K alone, so that a row's sum does not depend on how many
-// rows the call has.
-uint32_t splits_of(int64_t N, int64_t kb) {
-    const int64_t tiles = (N + kLanesP - 1) / kLanesP;
+// when the call has `tiles` tiles of 128 lanes, with at least 8 blocks of K a part.
+uint32_t splits_of(int64_t tiles, int64_t kb) {
     uint32_t s = 1;
     while (s < 8 && tiles * s * 2 <= 152 && kb >= int64_t(s) * 16) s *= 2;
     return s;
@@ -173,12 +170,15 @@ cudaError_t product(const Product& p, int in, int out, cudaStream_t stream) {
     a.N = p.N;
     a.rows = uint32_t(p.M);
     a.kb = uint32_t((p.K * size + 127) / 128);
-    a.splits = splits_of(p.N, a.kb);
     const bool p_mn = p.b_mn, q_mn = p.a_mn;
     cudaError_t e = timeouts_ptr(&a.timeouts);
     if (e != cudaSuccess) return e;
     const int64_t big_tiles = (p.N + 255) / 256 * ((p.M + 255) / 256);
     const bool pair = p.M > 256 && big_tiles * 2 >= num_sms() / 2;
+    // Where a row's sum must not depend on how many rows the call has, the parts
+    // follow from N and K alone: those of a call with few rows.
+    const int64_t p_tiles = (p.N + kLanesP - 1) / kLanesP;
+    a.splits = p.by_row ? splits_of(p_tiles, a.kb) : pair ? 1 : splits_of(p_tiles * ((p.M + 255) / 256), a.kb);
     uint32_t box_q;
     if (pair) {
         a.width = pair_width(p.N, p.M, q_mn);

@@ -218,6 +218,7 @@ mhc_status_t linear_fwd(const void* x, const float* x_scale, const void* w, cons
     mhc::linear::Product p;
     p.a = a.p, p.b = b.p;
     p.a_stride = a.stride, p.a_mn = false, p.b_stride = b.stride, p.b_mn = false;
+    p.by_row = true;
     p.M = T, p.N = O, p.K = I;
     p.e = {fp8 ? x_scale : nullptr, fp8 ? w_scale : nullptr, bias, static_cast<const uint16_t*>(residual),
            static_cast<uint16_t*>(y), static_cast<uint16_t*>(preact), residual_stride, int(act)};
@@ -356,7 +357,7 @@ mhc_status_t mhc_linear_bwd(const void* g, const void* x, const void* w, const v
         if (e != cudaSuccess) return finish(e);
         p.a = u.p, p.a_stride = u.stride, p.a_mn = false;
         p.b = b.p, p.b_stride = b.stride, p.b_mn = true;
-        p.M = T, p.N = I, p.K = O;
+        p.M = T, p.N = I, p.K = O, p.by_row = true;
         p.e.y = static_cast<uint16_t*>(grad_x);
         e = mhc::layer::product(p, dtype, dtype, cu(stream));
         if (e != cudaSuccess) return finish(e);
@@ -367,7 +368,7 @@ mhc_status_t mhc_linear_bwd(const void* g, const void* x, const void* w, const v
         if (e != cudaSuccess) return finish(e);
         p.a = u.p, p.a_stride = u.stride, p.a_mn = true;
         p.b = b.p, p.b_stride = b.stride, p.b_mn = true;
-        p.M = O, p.N = I, p.K = T;
+        p.M = O, p.N = I, p.K = T, p.by_row = false;
         p.e.y = static_cast<uint16_t*>(grad_w);
         e = mhc::layer::product(p, dtype, dtype, cu(stream));
         if (e != cudaSuccess) return finish(e);

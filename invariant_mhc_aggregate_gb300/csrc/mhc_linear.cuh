@@ -68,6 +68,7 @@ struct Product {
     const void* b;
     int64_t a_stride, b_stride;   // of their rows, in elements
     bool a_mn, b_mn;              // rows run along m (n), one for each k; else along k.  b_mn where a_mn.
+    bool by_row;                  // a row's sums must not depend on M (its tokens): the forward and grad_x
     int64_t M, N, K;
     Epilogue e;
 };
@@ -379,11 +380,12 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
 // alternate, so the epilogue of one tile runs under the multiplication of the
 // next.  The parts of K that split_kernel gives to different CTAs are summed
 // apart here too and added in the same order, so that both kernels give the
-// same bits.
+// same bits (PARTS): the second part's accumulator takes the others' sums in,
+// the first one holds every other part.  (Sums in registers instead, 64 or
+// 128 columns a thread, spilled: T = 4096, 7168 x 7168 269 to 330 us.)
 //
 // Warps 0-15 read tensor memory (four warps for each quarter of the lanes, a
-// quarter of the columns each, so that the parts' sums of 64 columns fit a
-// thread's registers).  One thread of warp 16 copies P, one of warp 18 copies
+// quarter of the columns each).  One thread of warp 16 copies P, one of warp 18 copies
 // Q (a copy takes its thread well over 100 cycles, and a block of K has 512),
 // one of warp 17 (of the first CTA) multiplies.
 // --------------------------------------------------------------------------
@@ -406,6 +408,20 @@ __device__ __forceinline__ void tile_at(const TileArgs& a, uint32_t i, uint32_t&
     q = j / height;
     p = first + (j - q * height);
 }
+
+// The accumulator of each part of each tile in turn, and the parity of its
+// round: as many rounds as it was taken before.
+struct Sums {
+    uint32_t taken[2] = {0, 0}, last = 1;
+    // (PARTS: the second part's is the second one, every other part's the first)
+    template <bool PARTS>
+    __device__ __forceinline__ uint32_t take(uint32_t part) {
+        last = PARTS ? uint32_t(part == 1) : last ^ 1;
+        ++taken[last];
+        return last;
+    }
+    __device__ __forceinline__ uint32_t parity(uint32_t b) const { return (taken[b] - 1) & 1; }
+};
 
 template <bool FP8, int OUT, int LAYOUT, bool PARTS>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -475,14 +491,16 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
         if (lane == 0 && rank == 0) {
             const Descs d = descs<LAYOUT>(ring);
             const uint32_t idesc = a.idesc;
-            umma::Ring at, sum;
+            umma::Ring at;
+            Sums sums;
             bool ok = true;
             for (uint32_t i = blockIdx.x / 2; i < tiles && ok; i += step) {
                 uint32_t k = 0;
-                for (uint32_t part = 0; part < a.splits && ok; ++part, sum.next(2)) {
-                    if (!(ok = umma::wait(bar_free + 8 * sum.stage, sum.parity ^ 1))) break;
+                for (uint32_t part = 0; part < a.splits && ok; ++part) {
+                    const uint32_t b = sums.take<PARTS>(part);
+                    if (!(ok = umma::wait(bar_free + 8 * b, sums.parity(b) ^ 1))) break;
                     umma::fence_after_sync();
-                    const uint32_t to = tmem + sum.stage * 256, k1 = split_begin(a, part + 1);
+                    const uint32_t to = tmem + b * 256, k1 = split_begin(a, part + 1);
                     bool first = true;
                     for (; k < k1; ++k, at.next(count)) {
                         if (!(ok = umma::wait(bar_full + 8 * at.stage, at.parity))) break;
@@ -491,7 +509,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                         umma::commit<2>(bar_empty + 8 * at.stage);
                         first = false;
                     }
-                    umma::commit<2>(bar_sum + 8 * sum.stage);
+                    umma::commit<2>(bar_sum + 8 * b);
                 }
             }
             if (!ok) timed_out(a);
@@ -500,7 +518,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
         const uint32_t quarter = warp % 4, mine = a.width / 4, c0 = warp / 4 * mine;   // its columns: c0 .. c0 + mine
         const uint32_t tw = tmem + (quarter * 32u << 16) + c0;
         const uint32_t signal = umma::map_rank(bar_free, 0);
-        umma::Ring sum;
+        Sums sums;
         bool ok = true;
         for (uint32_t i = blockIdx.x / 2; i < tiles && ok; i += step) {
             uint32_t pt, qt;
@@ -510,40 +528,32 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             const bool n_ok = col < a.N;
             const float bias = a.e.bias != nullptr && col < a.N ? __ldg(a.e.bias + col) : 0.0f;
             const float cs = a.e.col_scale != nullptr && col < a.N ? __ldg(a.e.col_scale + col) : 1.0f;
-            if constexpr (PARTS) {
-                // the parts are added up in registers, and their sum goes back to the
-                // last part's columns, from where both forms take it
-                float acc[8][kChunk];
-                for (uint32_t part = 0; part < a.splits; ++part) {
-                    if (!(ok = umma::wait(bar_sum + 8 * sum.stage, sum.parity))) break;
-                    umma::fence_after_sync();
-#pragma unroll
-                    for (uint32_t j = 0; j < 8; ++j) {
-                        if (j * kChunk < mine) {
-                            float v[kChunk];
-                            umma::tmem_ld(tw + sum.stage * 256 + j * kChunk, v);
-                            umma::tmem_wait_ld();
-#pragma unroll
-                            for (int c = 0; c < kChunk; ++c) acc[j][c] = part == 0 ? v[c] : __fadd_rn(acc[j][c], v[c]);
-                        }
-                    }
-                    if (part + 1 < a.splits) {
-                        umma::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) umma::arrive_cluster(signal + 8 * sum.stage);
-                        sum.next(2);
-                    }
-                }
-                if (!ok) break;
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j)
-                    if (j * kChunk < mine) umma::tmem_st(tw + sum.stage * 256 + j * kChunk, acc[j]);
-                umma::tmem_wait_st();
-            } else {
-                if (!(ok = umma::wait(bar_sum + 8 * sum.stage, sum.parity))) break;
+            uint32_t b = 0;
+            for (uint32_t part = 0; part < a.splits; ++part) {
+                b = sums.take<PARTS>(part);
+                if (!(ok = umma::wait(bar_sum + 8 * b, sums.parity(b)))) break;
                 umma::fence_after_sync();
+                if (!PARTS || part == 0) continue;
+                // the second accumulator becomes the sum of the parts so far
+#pragma unroll 2
+                for (uint32_t c = 0; c < mine; c += kChunk) {
+                    float v[kChunk], w[kChunk];
+                    umma::tmem_ld(tw + c, v);
+                    umma::tmem_ld(tw + 256 + c, w);
+                    umma::tmem_wait_ld();
+                    // (the second part arrives where the sum goes)
+#pragma unroll
+                    for (int i = 0; i < kChunk; ++i) v[i] = __fadd_rn(v[i], w[i]);
+                    umma::tmem_st(tw + 256 + c, v);
+                }
+                umma::tmem_wait_st();
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) umma::arrive_cluster(signal);
+                b = 1;
             }
-            const uint32_t from = tw + sum.stage * 256;
+            if (!ok) break;
+            const uint32_t from = tw + b * 256;
             uint16_t r[kChunk];   // a chunk's residual arrives while the chunk before it is worked on
             load_residual<kChunk>(a.e, n_ok, col, m0, 1, a.rows, r);
 #pragma unroll 1
@@ -559,8 +569,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             }
             umma::fence_before_sync();
             __syncwarp();
-            if (lane == 0) umma::arrive_cluster(signal + 8 * sum.stage);
-            sum.next(2);
+            if (lane == 0) umma::arrive_cluster(signal + 8 * b);
         }
         if (!ok) timed_out(a);
         umma::fence_before_sync();
