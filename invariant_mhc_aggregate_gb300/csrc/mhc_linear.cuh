@@ -239,8 +239,7 @@ __device__ __forceinline__ void timed_out(const TileArgs& a) { *a.timeouts = 1u;
 // CTAs, each of which sums its part of K; the parts meet in shared memory and
 // are added in increasing order, the columns shared out among the CTAs.
 //
-// Warps 0-3 read tensor memory, one thread of warp 4 issues copies, one of
-// warp 5 multiplies.
+// Warps 0-3 read tensor memory, warp 4 copies, warp 5 multiplies.
 // --------------------------------------------------------------------------
 constexpr uint32_t kSplitThreads = 192;
 
@@ -282,34 +281,37 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     const uint32_t ring = smem_addr(stages), bar_full = smem_addr(full), bar_empty = smem_addr(empty);
     const uint32_t count = a.stages, bytes = a.stage_bytes;
     if (warp == 4) {
-        if (lane == 0) {
-            umma::Ring at;
-            bool ok = true;
-            uint32_t k = k0;
-            for (; k < k1; ++k, at.next(count)) {
-                // (the first round finds every stage free: the phase before a new barrier's first one)
-                if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
+        umma::Ring at;
+        bool ok = true;
+        uint32_t k = k0;
+        for (; k < k1; ++k, at.next(count)) {
+            // (the first round finds every stage free: the phase before a new barrier's first one)
+            if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
+            if (umma::elect()) {
                 umma::expect_tx(bar_full + 8 * at.stage, bytes);
                 load_p<1, FP8, LAYOUT>(ring + at.stage * bytes, &mp, k, int(n0), bar_full + 8 * at.stage);
                 load_q<1, FP8, LAYOUT>(ring + at.stage * bytes, &mq, k, int(m0), a.width, bar_full + 8 * at.stage);
             }
-            drain(ok, min(k - k0, count), at, count, bar_empty, bar_full);
-            if (!ok) timed_out(a);
+            __syncwarp();
         }
+        drain(ok, min(k - k0, count), at, count, bar_empty, bar_full);
+        if (!ok) timed_out(a);
     } else if (warp == 5) {
-        if (lane == 0) {
-            const Descs d = descs<LAYOUT>(ring);
-            umma::Ring at;
-            for (uint32_t k = k0; k < k1; ++k, at.next(count)) {
-                if (!umma::wait(bar_full + 8 * at.stage, at.parity)) {
-                    timed_out(a);
-                    break;
-                }
-                umma::fence_after_sync();
-                multiply_block<1, FP8, LAYOUT>(d, at.stage * bytes, a.idesc, tmem, k == k0);
-                umma::commit<1>(bar_empty + 8 * at.stage);
+        const Descs d = descs<LAYOUT>(ring);
+        const uint32_t idesc = a.idesc;
+        umma::Ring at;
+        for (uint32_t k = k0; k < k1; ++k, at.next(count)) {
+            if (!umma::wait(bar_full + 8 * at.stage, at.parity)) {
+                timed_out(a);
+                break;
             }
-            umma::commit<1>(smem_addr(&done));
+            umma::fence_after_sync();
+            if (umma::elect()) {
+                multiply_block<1, FP8, LAYOUT>(d, at.stage * bytes, idesc, tmem, k == k0);
+                umma::commit<1>(bar_empty + 8 * at.stage);
+                if (k + 1 == k1) umma::commit<1>(smem_addr(&done));
+            }
+            __syncwarp();
         }
     } else {
         if (!umma::wait(smem_addr(&done), 0)) timed_out(a);
@@ -385,9 +387,9 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
 // 128 columns a thread, spilled: T = 4096, 7168 x 7168 269 to 330 us.)
 //
 // Warps 0-15 read tensor memory (four warps for each quarter of the lanes, a
-// quarter of the columns each).  One thread of warp 16 copies P, one of warp 18 copies
-// Q (a copy takes its thread well over 100 cycles, and a block of K has 512),
-// one of warp 17 (of the first CTA) multiplies.
+// quarter of the columns each).  Warp 16 copies P, warp 18 copies Q (a block of K
+// has 512 cycles, of which a copy and its wait take well over 100), warp 17 (of
+// the first CTA) multiplies.
 // --------------------------------------------------------------------------
 constexpr uint32_t kPairEpilogueWarps = 16;
 constexpr uint32_t kPairThreads = 32 * (kPairEpilogueWarps + 3);
@@ -463,19 +465,19 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
     const uint32_t bar_sum = smem_addr(sum_full), bar_free = smem_addr(sum_empty);
     const uint32_t count = a.stages, bytes = a.stage_bytes, kb = a.kb;
     if (warp == kCopyP || warp == kCopyQ) {
-        if (lane == 0) {
-            // both CTAs' copies count on the first one's barrier; its phase cannot end
-            // before that CTA's arrival, whichever copy lands first
-            const uint32_t bar_pair = umma::map_rank(bar_full, 0);
-            umma::Ring at;
-            bool ok = true;
-            uint32_t issued = 0;
-            for (uint32_t i = blockIdx.x / 2; i < tiles && ok; i += step) {
-                uint32_t pt, qt;
-                tile_at(a, i, pt, qt);
-                const int p0 = int(pt * 2 * kLanesP + rank * kLanesP), q0 = int(qt * a.width + rank * half);
-                for (uint32_t k = 0; k < kb; ++k, ++issued, at.next(count)) {
-                    if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
+        // both CTAs' copies count on the first one's barrier; its phase cannot end
+        // before that CTA's arrival, whichever copy lands first
+        const uint32_t bar_pair = umma::map_rank(bar_full, 0);
+        umma::Ring at;
+        bool ok = true;
+        uint32_t issued = 0;
+        for (uint32_t i = blockIdx.x / 2; i < tiles && ok; i += step) {
+            uint32_t pt, qt;
+            tile_at(a, i, pt, qt);
+            const int p0 = int(pt * 2 * kLanesP + rank * kLanesP), q0 = int(qt * a.width + rank * half);
+            for (uint32_t k = 0; k < kb; ++k, ++issued, at.next(count)) {
+                if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
+                if (umma::elect()) {
                     if (warp == kCopyP) {
                         if (rank == 0) umma::expect_tx(bar_full + 8 * at.stage, 2 * bytes);
                         load_p<2, FP8, LAYOUT>(ring + at.stage * bytes, &mp, k, p0, bar_pair + 8 * at.stage);
@@ -483,12 +485,13 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                         load_q<2, FP8, LAYOUT>(ring + at.stage * bytes, &mq, k, q0, half, bar_pair + 8 * at.stage);
                     }
                 }
+                __syncwarp();
             }
-            drain(ok, min(issued, count), at, count, bar_empty, rank == 0 ? bar_full : bar_empty);
-            if (!ok) timed_out(a);
         }
+        drain(ok, min(issued, count), at, count, bar_empty, rank == 0 ? bar_full : bar_empty);
+        if (!ok) timed_out(a);
     } else if (warp == kMultiply) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             const Descs d = descs<LAYOUT>(ring);
             const uint32_t idesc = a.idesc;
             umma::Ring at;
@@ -500,16 +503,17 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                     const uint32_t b = sums.take<PARTS>(part);
                     if (!(ok = umma::wait(bar_free + 8 * b, sums.parity(b) ^ 1))) break;
                     umma::fence_after_sync();
-                    const uint32_t to = tmem + b * 256, k1 = split_begin(a, part + 1);
-                    bool first = true;
+                    const uint32_t to = tmem + b * 256, k0 = k, k1 = split_begin(a, part + 1);
                     for (; k < k1; ++k, at.next(count)) {
                         if (!(ok = umma::wait(bar_full + 8 * at.stage, at.parity))) break;
                         umma::fence_after_sync();
-                        multiply_block<2, FP8, LAYOUT>(d, at.stage * bytes, idesc, to, first);
-                        umma::commit<2>(bar_empty + 8 * at.stage);
-                        first = false;
+                        if (umma::elect()) {
+                            multiply_block<2, FP8, LAYOUT>(d, at.stage * bytes, idesc, to, k == k0);
+                            umma::commit<2>(bar_empty + 8 * at.stage);
+                            if (k + 1 == k1) umma::commit<2>(bar_sum + 8 * b);
+                        }
+                        __syncwarp();
                     }
-                    umma::commit<2>(bar_sum + 8 * b);
                 }
             }
             if (!ok) timed_out(a);

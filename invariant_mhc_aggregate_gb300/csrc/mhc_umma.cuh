@@ -172,6 +172,23 @@ __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" : : "r"(bar), "r"(bytes) : "memory");
 }
 
+// One lane of a converged warp.  The loops around copies and multiplications
+// run in the whole warp and only these instructions in one lane: their
+// operands then stay in the registers that a warp's lanes share, which such
+// instructions read (in a loop of one lane each is moved there first, at
+// twice the time).
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "}"
+        : "=r"(one));
+    return one != 0;
+}
+
 // A ring of stages: one that a thread is at, and the parity of its round.
 struct Ring {
     uint32_t stage = 0, parity = 0;
