@@ -59,6 +59,11 @@ LAYER_DEPS = LAYER_SOURCES + [os.path.join(CSRC, f) for f in
     + [os.path.join(INCLUDE, f) for f in ("mhc_layer.h", "mhc_h_aggregate.h")]
 
 
+#: The layer operators' calls from PyTorch (a CPython extension over libmhc_layer.so).
+TORCH_LIB_PATH = os.path.join(LIB_DIR, "mhc_layer_torch.so")
+TORCH_SOURCE = os.path.join(CSRC, "mhc_layer_torch.cpp")
+
+
 def nvcc_path() -> str:
     for cand in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -161,7 +166,41 @@ def build_layer(force: bool = False, extra_flags=(), verbose: bool = False) -> s
     return _build(LAYER_LIB_PATH, LAYER_SOURCES, _digest(extra_flags, LAYER_DEPS), force, extra_flags, verbose)
 
 
+def build_torch(force: bool = False) -> str:
+    """Build the CPython extension if its source, the header or the PyTorch it is
+    built against changed; return its path.  Needs libmhc_layer.so (build_layer)."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(home, "include"), "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], "-I", INCLUDE]
+    libs = ["-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
+            "-L", LIB_DIR, f"-l:{LAYER_LIB_NAME}", "-Wl,-rpath,$ORIGIN"]
+    deps = [TORCH_SOURCE] + [p for p in LAYER_DEPS if p.startswith(INCLUDE)]
+    digest = _digest(cmd + libs + [torch.__version__], deps)
+    stamp = TORCH_LIB_PATH + ".stamp"
+    if not force and os.path.exists(TORCH_LIB_PATH) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read().strip() == digest:
+                return TORCH_LIB_PATH
+    os.makedirs(LIB_DIR, exist_ok=True)
+    with tempfile.TemporaryDirectory(dir=LIB_DIR) as work:
+        tmp = os.path.join(work, os.path.basename(TORCH_LIB_PATH))
+        res = subprocess.run([*cmd, "-o", tmp, TORCH_SOURCE, *libs], capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"g++ failed ({' '.join(cmd)}):\n{res.stderr}")
+        os.replace(tmp, TORCH_LIB_PATH)
+    with open(stamp, "w") as f:
+        f.write(digest + "\n")
+    return TORCH_LIB_PATH
+
+
 if __name__ == "__main__":
     import sys
     print(build(force="--force" in sys.argv, verbose=True))
     print(build_layer(force="--force" in sys.argv, verbose=True))
+    print(build_torch(force="--force" in sys.argv))

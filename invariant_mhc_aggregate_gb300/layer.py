@@ -15,7 +15,9 @@ what stands between the mHC aggregate and the mHC post.
 As in :mod:`.binding`, this is argument marshalling only: every step runs in
 the sm_103a kernels of ``libmhc_layer.so``, there is no fallback, and calls
 are asynchronous on ``stream`` (default: the current PyTorch stream of the
-tensors' device).  Outputs and workspaces are allocated here, on the current
+tensors' device).  On the current stream the marshalling of valid arguments is
+compiled too (``mhc_layer_torch``); the functions here check and name what it
+does not take.  Outputs and workspaces are allocated here, on the current
 stream; a caller who passes another stream orders the two as with any PyTorch
 tensor.  The differentiable forms are in :mod:`.autograd`.
 """
@@ -23,6 +25,7 @@ tensor.  The differentiable forms are in :mod:`.autograd`.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import threading
@@ -101,6 +104,22 @@ def load():
         return lib
 
 
+_fast = None
+
+
+def _compiled():
+    """The compiled marshalling (raises if it has not been built)."""
+    global _fast
+    if _fast is None:
+        path = _build.TORCH_LIB_PATH
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
+        spec = importlib.util.spec_from_file_location("mhc_layer_torch", path)
+        _fast = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_fast)
+    return _fast
+
+
 def wait_timeouts() -> int:
     """1 if a bounded wait of the product's kernels ran out on the current
     device since the last call, else 0 (clears it; synchronizes the device);
@@ -169,6 +188,14 @@ def _two(t: torch.Tensor, name: str):
     return t.shape
 
 
+def _call(device, name: str, *args) -> None:
+    """The C entry point `name` with its device current; raises unless it returns MHC_OK."""
+    with torch.cuda.device(device):
+        st = getattr(load(), name)(*args)
+    if st != MHC_OK:
+        raise LayerError(st, name)
+
+
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -182,6 +209,10 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     """(y, total, rstd): total = x + residual (x itself without one), y its RMS
     norm times weight (FP32 [H]), rstd FP32 [T].  x and residual [T,H], bf16 or
     f16, with any row stride."""
+    if stream is None:
+        out = (_fast or _compiled()).rms_norm(x, weight, residual, eps, -1)
+        if out is not None:
+            return out[0], out[2], out[3]
     T, H = _two(x, "x")
     dt, dev = _storage(x, "x"), x.device
     xs = _rows(x, "x", x.dtype, x.shape, dev)
@@ -190,10 +221,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     y = torch.empty((T, H), dtype=x.dtype, device=dev)
     total = None if residual is None else torch.empty((T, H), dtype=x.dtype, device=dev)
     rstd = torch.empty(T, dtype=torch.float32, device=dev)
-    st = load().mhc_rms_norm_fwd(x.data_ptr(), _ptr(residual), weight.data_ptr(), y.data_ptr(), _ptr(total),
-                                 rstd.data_ptr(), T, H, xs, rs, eps, dt, _stream_handle(stream, dev))
-    if st != MHC_OK:
-        raise LayerError(st, "mhc_rms_norm_fwd")
+    _call(dev, "mhc_rms_norm_fwd", x.data_ptr(), _ptr(residual), weight.data_ptr(), y.data_ptr(), _ptr(total),
+          rstd.data_ptr(), T, H, xs, rs, eps, dt, _stream_handle(stream, dev))
     return y, (x if total is None else total), rstd
 
 
@@ -202,6 +231,10 @@ def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     """(y8, scale, total, rstd): as rms_norm, with y in E4M3 and FP32 scales,
     one per row (group = 0: [T,1]) or per 128 channels (group = 128:
     [T,ceil(H/128)]); y is about y8 * scale."""
+    if stream is None and (group == 0 or group == 128):
+        out = (_fast or _compiled()).rms_norm(x, weight, residual, eps, group)
+        if out is not None:
+            return out
     T, H = _two(x, "x")
     dt, dev = _storage(x, "x"), x.device
     xs = _rows(x, "x", x.dtype, x.shape, dev)
@@ -211,11 +244,8 @@ def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     scale = torch.empty((T, 1 if group == 0 else -(-H // 128)), dtype=torch.float32, device=dev)
     total = None if residual is None else torch.empty((T, H), dtype=x.dtype, device=dev)
     rstd = torch.empty(T, dtype=torch.float32, device=dev)
-    st = load().mhc_rms_norm_fp8_fwd(x.data_ptr(), _ptr(residual), weight.data_ptr(), y.data_ptr(), scale.data_ptr(),
-                                     _ptr(total), rstd.data_ptr(), T, H, xs, rs, eps, group, dt,
-                                     _stream_handle(stream, dev))
-    if st != MHC_OK:
-        raise LayerError(st, "mhc_rms_norm_fp8_fwd")
+    _call(dev, "mhc_rms_norm_fp8_fwd", x.data_ptr(), _ptr(residual), weight.data_ptr(), y.data_ptr(), scale.data_ptr(),
+          _ptr(total), rstd.data_ptr(), T, H, xs, rs, eps, group, dt, _stream_handle(stream, dev))
     return y, scale, (x if total is None else total), rstd
 
 
@@ -224,6 +254,10 @@ def rms_norm_backward(grad_y: torch.Tensor, total: torch.Tensor, weight: torch.T
     """(grad_x, grad_weight): the gradients from the gradient of y, the
     forward's total and rstd, and optionally the gradient of total itself.
     grad_x is the gradient of x and of the residual; grad_weight is FP32."""
+    if stream is None:
+        out = (_fast or _compiled()).rms_norm_backward(grad_y, total, weight, rstd, grad_total)
+        if out is not None:
+            return out
     T, H = _two(total, "total")
     dt, dev = _storage(total, "total"), total.device
     ss = _rows(total, "total", total.dtype, total.shape, dev)
@@ -237,11 +271,9 @@ def rms_norm_backward(grad_y: torch.Tensor, total: torch.Tensor, weight: torch.T
     grad_w = torch.empty(H, dtype=torch.float32, device=dev)
     need = lib.mhc_rms_norm_bwd_workspace(T, H)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    st = lib.mhc_rms_norm_bwd(grad_y.data_ptr(), total.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
-                              _ptr(grad_total), grad_x.data_ptr(), grad_w.data_ptr(), _ptr(ws), need, T, H, gs, ss, dt,
-                              _stream_handle(stream, dev))
-    if st != MHC_OK:
-        raise LayerError(st, "mhc_rms_norm_bwd")
+    _call(dev, "mhc_rms_norm_bwd", grad_y.data_ptr(), total.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
+          _ptr(grad_total), grad_x.data_ptr(), grad_w.data_ptr(), _ptr(ws), need, T, H, gs, ss, dt,
+          _stream_handle(stream, dev))
     return grad_x, grad_w
 
 
@@ -283,13 +315,11 @@ def _linear(x, x_scale, w, w_scale, bias, activation, residual, out_dtype, keep,
     work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     sh = _stream_handle(stream, dev)
     if fp8:
-        st = lib.mhc_linear_fp8_fwd(xp, x_scale.data_ptr(), wp, w_scale.data_ptr(), _ptr(bias), _ptr(residual),
-                                    y.data_ptr(), _ptr(z), _ptr(work), need, T, I, O, xs, ws, rs, act, dt, sh)
+        _call(dev, "mhc_linear_fp8_fwd", xp, x_scale.data_ptr(), wp, w_scale.data_ptr(), _ptr(bias), _ptr(residual),
+              y.data_ptr(), _ptr(z), _ptr(work), need, T, I, O, xs, ws, rs, act, dt, sh)
     else:
-        st = lib.mhc_linear_fwd(xp, wp, _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(z), _ptr(work), need, T, I, O,
-                                xs, ws, rs, act, dt, sh)
-    if st != MHC_OK:
-        raise LayerError(st, "mhc_linear_fp8_fwd" if fp8 else "mhc_linear_fwd")
+        _call(dev, "mhc_linear_fwd", xp, wp, _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(z), _ptr(work), need, T, I, O,
+              xs, ws, rs, act, dt, sh)
     return y, z
 
 
@@ -298,12 +328,20 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     """act(x weight^T + bias) + residual: x [T,I], weight [O,I], residual and
     the result [T,O], all bf16 or all f16 (x, weight and residual with any row
     stride); bias FP32 [O]; activation "none", "relu", "silu" or "gelu"."""
+    if stream is None and activation in ACTIVATIONS:
+        out = (_fast or _compiled()).linear(x, None, weight, None, bias, ACTIVATIONS[activation], residual, -1, False)
+        if out is not None:
+            return out[0]
     return _linear(x, None, weight, None, bias, activation, residual, x.dtype, False, stream)[0]
 
 
 def linear_preact(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, activation: str = "none",
                   residual: torch.Tensor | None = None, stream=None):
     """(y, z): as linear, and the pre-activation z = x weight^T + bias that linear_backward reads."""
+    if stream is None and activation in ACTIVATIONS:
+        out = (_fast or _compiled()).linear(x, None, weight, None, bias, ACTIVATIONS[activation], residual, -1, True)
+        if out is not None:
+            return out
     return _linear(x, None, weight, None, bias, activation, residual, x.dtype, True, stream)
 
 
@@ -313,6 +351,11 @@ def linear_fp8(x8: torch.Tensor, x_scale: torch.Tensor, w8: torch.Tensor, w_scal
     """The product of E4M3 operands x8 [T,I] and w8 [O,I] with one FP32 scale
     per row of each (x_scale [T] or [T,1], w_scale [O] or [O,1]); residual and
     the result are of `dtype`."""
+    if stream is None and activation in ACTIVATIONS and dtype in _DTYPES and x_scale is not None:
+        out = (_fast or _compiled()).linear(x8, x_scale, w8, w_scale, bias, ACTIVATIONS[activation], residual,
+                                            _DTYPES[dtype], False)
+        if out is not None:
+            return out[0]
     if not isinstance(x_scale, torch.Tensor) or not isinstance(w_scale, torch.Tensor):
         raise TypeError("x_scale and w_scale must be torch.Tensors")
     return _linear(x8, x_scale, w8, w_scale, bias, activation, residual, dtype, False, stream)[0]
@@ -323,6 +366,10 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     """(grad_x, grad_weight, grad_bias) of linear, from the gradient of y and,
     with an activation, the forward's z.  grad_bias is FP32, None when `bias`
     is false; `want` says which of grad_x and grad_weight to compute."""
+    if stream is None and activation in ACTIVATIONS:
+        out = (_fast or _compiled()).linear_backward(grad_y, x, weight, z, ACTIVATIONS[activation], bias, want[0], want[1])
+        if out is not None:
+            return out
     T, I = _two(x, "x")
     O, _ = _two(weight, "weight")
     dt, dev = _storage(x, "x"), x.device
@@ -342,10 +389,8 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     need = lib.mhc_linear_bwd_workspace(T, I, O, act, int(want[0]), int(want[1]), int(bias),
                                         0 if (gp | xp | wp) & 15 else 1)
     work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    st = lib.mhc_linear_bwd(gp, xp, wp, _ptr(z if act else None), _ptr(grad_x), _ptr(grad_w), _ptr(grad_b), _ptr(work),
-                            need, T, I, O, act, dt, _stream_handle(stream, dev))
-    if st != MHC_OK:
-        raise LayerError(st, "mhc_linear_bwd")
+    _call(dev, "mhc_linear_bwd", gp, xp, wp, _ptr(z if act else None), _ptr(grad_x), _ptr(grad_w), _ptr(grad_b),
+          _ptr(work), need, T, I, O, act, dt, _stream_handle(stream, dev))
     return grad_x, grad_w, grad_b
 
 
@@ -384,6 +429,10 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
     frequencies[j] and multiplied by `scale`; pairs are (j, j + R/2), or
     (2j, 2j + 1) when interleaved.  positions int64 [T].  inverse rotates back
     (the gradient).  `out` may be x itself."""
+    if stream is None and out is None:
+        done = (_fast or _compiled()).rotary(x, positions, frequencies, interleaved, float(scale), inverse)
+        if done is not None:
+            return done[0]
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     if x.dim() != 3:
@@ -407,9 +456,6 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
             raise ValueError(f"{name}'s heads must be contiguous, got strides {t.stride()}")
         head = head if heads > 1 else D
         strides += [token if T > 1 else max(heads - 1, 0) * head + D, head]
-    st = load().mhc_rotary(x.data_ptr(), positions.data_ptr(), frequencies.data_ptr(), out.data_ptr(), T, heads, D,
-                           2 * frequencies.shape[0], *strides, scale, int(interleaved), int(inverse), dt,
-                           _stream_handle(stream, dev))
-    if st != MHC_OK:
-        raise LayerError(st, "mhc_rotary")
+    _call(dev, "mhc_rotary", x.data_ptr(), positions.data_ptr(), frequencies.data_ptr(), out.data_ptr(), T, heads, D,
+          2 * frequencies.shape[0], *strides, scale, int(interleaved), int(inverse), dt, _stream_handle(stream, dev))
     return out
