@@ -136,17 +136,46 @@ cudaError_t launch_layout(bool pair, const TileArgs& a, CUtensorMap& mp, CUtenso
                 : launch_tile<false, OUT, kPMnQK>(pair, a, mp, mq, stream);
 }
 
-// The pair kernel's tile width: the one in steps of 32 rows (128 where Q is
-// MN-major: whole panels for each CTA) whose rounds of tiles over the pairs
-// of SMs take the least time, a round costing its width and, as measured,
-// about 16 rows' worth for its start and end.
-uint32_t pair_width(int64_t N, int64_t M, bool q_mn) {
-    const int64_t p_tiles = (N + 255) / 256, pairs = num_sms() / 2;
-    uint32_t best = 256;
+// Which kernel a product takes, with tiles of which width (output rows).
+struct Plan {
+    bool pair;
+    uint32_t width, splits;
+};
+
+// The cheapest plan by an estimate in SM cycles, from runs of M = 32 .. 4096
+// rows at (N, K) = (7168, 7168), (14336, 4096), (4096, 4096), (4096, 1280),
+// (2048, 2048), (1024, 1024), (1024, 7168), (520, 2048), which it orders as the
+// measurement does where the kernels differ by more than a tenth:
+//  * split_kernel: each round of its CTAs over the SMs takes 9000 + 32 width
+//    for its start and its epilogue, and 350 + 1.5 width a block of K;
+//  * pair_kernel: 10000 + 8 width once, each round max(400, 2.1 width) a block
+//    of K and 1500 a part.
+// For instance M = 256 at 4096 x 4096: split 15.5 us, pairs 21.6; M = 512: 29.9
+// and 22.2; M = 1024 at 7168 x 7168: pairs of width 224 65.5 us, 256 71.0, split
+// 92.3.
+Plan plan_of(int64_t N, int64_t M, int64_t kb, bool q_mn, bool by_row) {
+    const int64_t sms = num_sms(), p128 = (N + 127) / 128, p256 = (N + 255) / 256;
+    Plan best = {false, 256, 1};
     int64_t least = INT64_MAX;
-    for (uint32_t w = 256; w >= 128; w -= q_mn ? 128 : 32) {
-        const int64_t rounds = (p_tiles * ((M + w - 1) / w) + pairs - 1) / pairs;
-        if (rounds * (w + 16) < least) least = rounds * (w + 16), best = w;
+    // where a row's sum must not depend on how many rows the call has, the parts
+    // follow from N and K alone: those of a call with few rows
+    const uint32_t row_parts = splits_of(p128, kb);
+    const int64_t step = q_mn ? 64 : 16, q0 = (M + 255) / 256;
+    for (int64_t q = q0; q <= 8 * q0 && q <= 65535; q *= 2) {   // (its grid's second dimension)
+        const int64_t w = ((M + q - 1) / q + step - 1) / step * step;
+        const int64_t tiles = p128 * ((M + w - 1) / w);
+        const uint32_t parts = by_row ? row_parts : splits_of(tiles, kb);
+        const int64_t rounds = (tiles * parts + sms - 1) / sms;
+        const int64_t cost = rounds * (9000 + 32 * w + (kb + parts - 1) / parts * (350 + 3 * w / 2));
+        if (cost < least) least = cost, best = {false, uint32_t(w), parts};
+        if (w <= 32) break;
+    }
+    const uint32_t parts = by_row ? row_parts : 1;
+    for (int64_t w = 128; w <= 256; w += q_mn ? 128 : 32) {
+        const int64_t rounds = (p256 * ((M + w - 1) / w) + sms / 2 - 1) / (sms / 2);
+        const int64_t block = 21 * w / 10 > 400 ? 21 * w / 10 : 400;
+        const int64_t cost = 10000 + 8 * w + rounds * (kb * block + (parts > 1 ? 1500 * parts : 0));
+        if (cost < least) least = cost, best = {true, uint32_t(w), parts};
     }
     return best;
 }
@@ -173,28 +202,13 @@ cudaError_t product(const Product& p, int in, int out, cudaStream_t stream) {
     const bool p_mn = p.b_mn, q_mn = p.a_mn;
     cudaError_t e = timeouts_ptr(&a.timeouts);
     if (e != cudaSuccess) return e;
-    const int64_t big_tiles = (p.N + 255) / 256 * ((p.M + 255) / 256);
-    const bool pair = p.M > 256 && big_tiles * 2 >= num_sms() / 2;
-    // Where a row's sum must not depend on how many rows the call has, the parts
-    // follow from N and K alone: those of a call with few rows.
-    const int64_t p_tiles = (p.N + kLanesP - 1) / kLanesP;
-    a.splits = p.by_row ? splits_of(p_tiles, a.kb) : pair ? 1 : splits_of(p_tiles * ((p.M + 255) / 256), a.kb);
-    uint32_t box_q;
-    if (pair) {
-        a.width = pair_width(p.N, p.M, q_mn);
-        a.p_tiles = uint32_t((p.N + 255) / 256);
-        a.q_tiles = uint32_t((p.M + a.width - 1) / a.width);
-        a.idesc = umma::instr_desc(in == kBF16 ? 1 : 0, p_mn, q_mn, 2 * kLanesP, a.width);
-        box_q = a.width / 2;
-    } else {
-        // tiles of equal width, in steps of 16 rows (64 where Q is MN-major)
-        const int64_t step = q_mn ? 64 : 16;
-        a.q_tiles = uint32_t((p.M + 255) / 256);
-        a.width = uint32_t(((p.M + a.q_tiles - 1) / a.q_tiles + step - 1) / step * step);
-        a.p_tiles = uint32_t((p.N + kLanesP - 1) / kLanesP);
-        a.idesc = umma::instr_desc(in == kBF16 ? 1 : 0, p_mn, q_mn, kLanesP, a.width);
-        box_q = a.width;
-    }
+    const Plan plan = plan_of(p.N, p.M, a.kb, q_mn, p.by_row);
+    const bool pair = plan.pair;
+    const uint32_t lanes = pair ? 2 * kLanesP : kLanesP, box_q = pair ? plan.width / 2 : plan.width;
+    a.width = plan.width, a.splits = plan.splits;
+    a.p_tiles = uint32_t((p.N + lanes - 1) / lanes);
+    a.q_tiles = uint32_t((p.M + a.width - 1) / a.width);
+    a.idesc = umma::instr_desc(in == kBF16 ? 1 : 0, p_mn, q_mn, lanes, a.width);
     CUtensorMap mp, mq;
     e = p_mn ? encode(&mp, p.b, p.K, p.N, p.b_stride, size, 64) : encode(&mp, p.b, p.N, p.K, p.b_stride, size, kLanesP);
     if (e != cudaSuccess) return e;
@@ -207,16 +221,37 @@ cudaError_t product(const Product& p, int in, int out, cudaStream_t stream) {
                         : launch_layout<kF16>(pair, a, mp, mq, p_mn, q_mn, stream);
 }
 
-cudaError_t repack(const void* src, void* dst, int64_t rows, int64_t length, int64_t stride, int64_t pitch,
-                   int64_t size, cudaStream_t stream) {
-    const int64_t vectors = rows * (pitch * size / 16);
-    const uint32_t blocks = grid_for(uint64_t(vectors), 256, uint64_t(num_sms()) * 32);
-    if (size == 1)
-        return launch(repack_kernel<uint8_t>, blocks, 256, stream, static_cast<const uint8_t*>(src),
-                      static_cast<uint8_t*>(dst), vectors, length, stride, pitch);
-    return launch(repack_kernel<uint16_t>, blocks, 256, stream, static_cast<const uint16_t*>(src),
-                  static_cast<uint16_t*>(dst), vectors, length, stride, pitch);
+cudaError_t repack(const RepackCall* calls, int count, cudaStream_t stream) {
+    Repack r[2] = {};
+    uint64_t blocks[2] = {0, 0};
+    for (int i = 0; i < count; ++i) {
+        const RepackCall& c = calls[i];
+        r[i].src = static_cast<const char*>(c.src);
+        r[i].dst = static_cast<char*>(c.dst);
+        r[i].per_row = uint32_t(c.pitch / 16);
+        r[i].vectors = uint64_t(c.rows) * r[i].per_row;
+        r[i].by_row = make_fastdiv_u32(r[i].per_row);
+        r[i].length = uint64_t(c.length), r[i].stride = uint64_t(c.stride);
+        r[i].bytes = uint64_t(c.rows - 1) * r[i].stride + r[i].length;
+        blocks[i] = (r[i].vectors + kRepackThreads - 1) / kRepackThreads;
+    }
+    if (blocks[0] + blocks[1] > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+    return launch(repack_kernel, uint32_t(blocks[0] + blocks[1]), kRepackThreads, stream, r[0], r[1], uint32_t(blocks[0]));
 }
+
+namespace {
+
+template <int DT, int W>
+auto slope_kernel_of(int act) {
+    switch (act) {
+        case kActRelu: return slope_kernel<DT, W, kActRelu>;
+        case kActSilu: return slope_kernel<DT, W, kActSilu>;
+        case kActGelu: return slope_kernel<DT, W, kActGelu>;
+        default: return slope_kernel<DT, W, kActNone>;
+    }
+}
+
+}  // namespace
 
 // Runs of rows whose column sums are added up one after the other: 64 rows
 // or more each, at most 64 runs (a constant, so that the order of the sum
@@ -240,9 +275,9 @@ cudaError_t slope(const uint16_t* g, const uint16_t* preact, uint16_t* u, float*
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto* kernel = dtype == kBF16 ? (vec ? slope_kernel<kBF16, 8> : slope_kernel<kBF16, 1>)
-                                  : (vec ? slope_kernel<kF16, 8> : slope_kernel<kF16, 1>);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, g, preact, u, sums, T, O, pitch, rows, act);
+    auto* kernel = dtype == kBF16 ? (vec ? slope_kernel_of<kBF16, 8>(act) : slope_kernel_of<kBF16, 1>(act))
+                                  : (vec ? slope_kernel_of<kF16, 8>(act) : slope_kernel_of<kF16, 1>(act));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, g, preact, u, sums, T, O, pitch, rows);
     if (e != cudaSuccess || grad_bias == nullptr || runs == 1) return e;
     return column_sum(partial, grad_bias, uint32_t(runs), O, stream);
 }

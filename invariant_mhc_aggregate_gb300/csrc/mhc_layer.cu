@@ -183,13 +183,12 @@ struct Operand {
         : p(ptr), rows(r), length(l), stride(s), size(sz), in_place(ptr_aligned && (s * sz % 16 == 0 || r <= 1)) {}
     int64_t pitch() const { return round16(length * size) / size; }
     int64_t bytes() const { return in_place ? 0 : rows * pitch() * size; }
-    // Lays the operand out at `at` if need be, and moves `at` past it.
-    cudaError_t place(char*& at, cudaStream_t stream) {
-        if (in_place) return cudaSuccess;
-        const cudaError_t e = mhc::layer::repack(p, at, rows, length, stride, pitch(), size, stream);
-        p = at, stride = pitch();
-        at += rows * pitch() * size;
-        return e;
+    // Gives the operand its place at `at` if it needs one, and moves `at` past it.
+    void place(char*& at, mhc::layer::RepackCall* calls, int& count) {
+        if (in_place) return;
+        calls[count++] = {p, at, rows, length * size, stride * size, pitch() * size};
+        p = at, stride = pitch(), in_place = true;
+        at += rows * stride * size;
     }
 };
 
@@ -212,9 +211,14 @@ mhc_status_t linear_fwd(const void* x, const float* x_scale, const void* w, cons
                            rows(residual, T, O, residual_stride, 2, true)};
     if (!valid(outs, ins)) return MHC_ERR_INVALID_ARG;
     char* at = static_cast<char*>(workspace);
-    cudaError_t e = a.place(at, cu(stream));
-    if (e == cudaSuccess) e = b.place(at, cu(stream));
-    if (e != cudaSuccess) return finish(e);
+    mhc::layer::RepackCall calls[2];
+    int count = 0;
+    a.place(at, calls, count);
+    b.place(at, calls, count);
+    if (count > 0) {
+        const cudaError_t e = mhc::layer::repack(calls, count, cu(stream));
+        if (e != cudaSuccess) return finish(e);
+    }
     mhc::linear::Product p;
     p.a = a.p, p.b = b.p;
     p.a_stride = a.stride, p.a_mn = false, p.b_stride = b.stride, p.b_mn = false;
@@ -347,27 +351,29 @@ mhc_status_t mhc_linear_bwd(const void* g, const void* x, const void* w, const v
         }
     }
     if (!want_x && !want_w) return finish(cudaSuccess);
-    e = u.place(at, cu(stream));
-    if (e != cudaSuccess) return finish(e);
+    Operand xo(x, T, I, I, 2, aligned(x, 16)), wo(w, O, I, I, 2, aligned(w, 16));
+    mhc::layer::RepackCall calls[3];
+    int count = 0;
+    u.place(at, calls, count);
+    if (want_w) xo.place(at, calls, count);
+    if (want_x) wo.place(at, calls, count);
+    for (int i = 0; i < count; i += 2) {
+        e = mhc::layer::repack(calls + i, count - i < 2 ? 1 : 2, cu(stream));
+        if (e != cudaSuccess) return finish(e);
+    }
     mhc::linear::Product p;
     p.e = {nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, mhc::linear::kActNone};
     if (want_x) {   // [T,I] = u [T,O] . w [O,I]
-        Operand b(w, O, I, I, 2, aligned(w, 16));
-        e = b.place(at, cu(stream));
-        if (e != cudaSuccess) return finish(e);
         p.a = u.p, p.a_stride = u.stride, p.a_mn = false;
-        p.b = b.p, p.b_stride = b.stride, p.b_mn = true;
+        p.b = wo.p, p.b_stride = wo.stride, p.b_mn = true;
         p.M = T, p.N = I, p.K = O, p.by_row = true;
         p.e.y = static_cast<uint16_t*>(grad_x);
         e = mhc::layer::product(p, dtype, dtype, cu(stream));
         if (e != cudaSuccess) return finish(e);
     }
     if (want_w) {   // [O,I] = u^T [O,T] . x [T,I]
-        Operand b(x, T, I, I, 2, aligned(x, 16));
-        e = b.place(at, cu(stream));
-        if (e != cudaSuccess) return finish(e);
         p.a = u.p, p.a_stride = u.stride, p.a_mn = true;
-        p.b = b.p, p.b_stride = b.stride, p.b_mn = true;
+        p.b = xo.p, p.b_stride = xo.stride, p.b_mn = true;
         p.M = O, p.N = I, p.K = T, p.by_row = false;
         p.e.y = static_cast<uint16_t*>(grad_w);
         e = mhc::layer::product(p, dtype, dtype, cu(stream));

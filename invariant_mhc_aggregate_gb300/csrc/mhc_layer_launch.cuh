@@ -41,9 +41,14 @@ cudaError_t column_sum(const float* partial, float* out, uint32_t P, int64_t H, 
 // Matrix product (mhc_launch_linear.cu).  in, out: kBF16, kF16; in also
 // kE4m3.  Every operand's rows start on 16-byte boundaries.
 cudaError_t product(const linear::Product& p, int in, int out, cudaStream_t stream);
-// Rows of `length` elements of `size` bytes copied from `stride` to `pitch`.
-cudaError_t repack(const void* src, void* dst, int64_t rows, int64_t length, int64_t stride, int64_t pitch,
-                   int64_t size, cudaStream_t stream);
+// An operand whose rows (`length` bytes, `stride` bytes apart) are copied to
+// rows of `pitch` bytes (a multiple of 16).
+struct RepackCall {
+    const void* src;
+    void* dst;
+    int64_t rows, length, stride, pitch;
+};
+cudaError_t repack(const RepackCall* calls, int count, cudaStream_t stream);   // count 1 or 2
 // u = g * act'(preact) (u, of row pitch `pitch`, null: not stored) and, with
 // grad_bias, its column sums through `partial` (slope_partials(T) * O floats).
 cudaError_t slope(const uint16_t* g, const uint16_t* preact, uint16_t* u, float* grad_bias, float* partial, int64_t T,

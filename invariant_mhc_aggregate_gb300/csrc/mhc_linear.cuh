@@ -40,16 +40,16 @@ __device__ __forceinline__ float activation(float z) {
     return z;
 }
 
-__device__ __forceinline__ float slope(float z, int act) {
-    switch (act) {
-        case kActRelu: return z > 0.0f ? 1.0f : 0.0f;
-        case kActSilu: {
-            const float p = 1.0f / (1.0f + expf(-z));
-            return p * (1.0f + z * (1.0f - p));
-        }
-        case kActGelu: return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * expf(-0.5f * z * z) * 0.39894228f;
-        default: return 1.0f;
+// The derivatives, with the same exponential: within 2^-20 of the exact ones.
+template <int ACT>
+__device__ __forceinline__ float slope(float z) {
+    if constexpr (ACT == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
+    if constexpr (ACT == kActSilu) {
+        const float p = __fdividef(1.0f, 1.0f + __expf(-z));
+        return p * __fmaf_rn(z, 1.0f - p, 1.0f);
     }
+    if constexpr (ACT == kActGelu) return __fmaf_rn(z * 0.39894228f, __expf(-0.5f * z * z), normal_cdf(z));
+    return 1.0f;
 }
 
 struct Epilogue {
@@ -239,9 +239,14 @@ __device__ __forceinline__ void timed_out(const TileArgs& a) { *a.timeouts = 1u;
 // CTAs, each of which sums its part of K; the parts meet in shared memory and
 // are added in increasing order, the columns shared out among the CTAs.
 //
-// Warps 0-3 read tensor memory, warp 4 copies, warp 5 multiplies.
+// Warps 0-15 read tensor memory (four for each quarter of the lanes: 4 warps
+// alone took 35 ns a column, 14 us for a 256-row call of 1024 x 1024), warp 16
+// copies, warp 17 multiplies.
 // --------------------------------------------------------------------------
-constexpr uint32_t kSplitThreads = 192;
+constexpr uint32_t kEpilogueWarps = 16;
+constexpr int kChunk = 8;   // columns that a warp takes out of tensor memory at a time
+constexpr uint32_t kSplitThreads = 32 * (kEpilogueWarps + 2);
+constexpr uint32_t kSplitCopy = kEpilogueWarps, kSplitMultiply = kSplitCopy + 1;   // warps
 
 template <bool FP8, int OUT, int LAYOUT>
 __global__ void __launch_bounds__(kSplitThreads, 1)
@@ -265,7 +270,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
         mbar_init(&done, 1);
         mbar_init_fence();
     }
-    if (warp == 4) {
+    if (warp == kSplitCopy) {
         umma::tmem_alloc<1>(&tmem_base, columns);
         if (lane == 0) {
             umma::prefetch_map(&mp);
@@ -277,10 +282,19 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     umma::fence_after_sync();
     const uint32_t tmem = tmem_base;
     const uint32_t k0 = split_begin(a, rank), k1 = split_begin(a, rank + 1);
+    const uint32_t quarter = warp % 4, group = warp / 4;
+    const uint32_t valid = min(a.width, a.rows - m0);
+    const int64_t n = n0 + quarter * 32 + lane;
+    const bool n_ok = n < a.N;
+    // the thread's place in the parts, [column][lane], that take the stages' place
+    // once every copy has landed and been read
+    float* part = reinterpret_cast<float*>(stages) + quarter * 32 + lane;
     pdl_enter();
+    const float bias = a.e.bias != nullptr && n_ok ? __ldg(a.e.bias + n) : 0.0f;
+    const float cs = a.e.col_scale != nullptr && n_ok ? __ldg(a.e.col_scale + n) : 1.0f;
     const uint32_t ring = smem_addr(stages), bar_full = smem_addr(full), bar_empty = smem_addr(empty);
     const uint32_t count = a.stages, bytes = a.stage_bytes;
-    if (warp == 4) {
+    if (warp == kSplitCopy) {
         umma::Ring at;
         bool ok = true;
         uint32_t k = k0;
@@ -296,7 +310,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
         }
         drain(ok, min(k - k0, count), at, count, bar_empty, bar_full);
         if (!ok) timed_out(a);
-    } else if (warp == 5) {
+    } else if (warp == kSplitMultiply) {
         const Descs d = descs<LAYOUT>(ring);
         const uint32_t idesc = a.idesc;
         umma::Ring at;
@@ -316,24 +330,18 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     } else {
         if (!umma::wait(smem_addr(&done), 0)) timed_out(a);
         umma::fence_after_sync();
-        const int64_t n = n0 + threadIdx.x;
-        const bool n_ok = n < a.N;
-        const uint32_t tw = tmem + (warp * 32u << 16);
-        const uint32_t valid = min(a.width, a.rows - m0);
-        const float bias = a.e.bias != nullptr && n < a.N ? __ldg(a.e.bias + n) : 0.0f;
-        const float cs = a.e.col_scale != nullptr && n < a.N ? __ldg(a.e.col_scale + n) : 1.0f;
-        float* part = reinterpret_cast<float*>(stages);   // [column][lane]: every copy has landed and been read
-        for (uint32_t c = 0; c < valid; c += 16) {
-            float v[16];
-            umma::tmem_ld(tw + c, v);
+        // group g of four warps takes the chunks g, g + 4, ... of the columns
+        for (uint32_t c = group * kChunk; c < valid; c += 4 * kChunk) {
+            float v[kChunk];
+            umma::tmem_ld(tmem + (quarter * 32u << 16) + c, v);
+            uint16_t r[kChunk];
+            if (a.splits == 1) load_residual<kChunk>(a.e, n_ok, n, m0 + c, 1, m0 + valid, r);
             umma::tmem_wait_ld();
             if (a.splits == 1) {
-                uint16_t r[16];
-                load_residual<16>(a.e, n_ok, n, m0 + c, 1, a.rows, r);
-                emit<OUT, 16>(a.e, a.N, n_ok, n, m0 + c, 1, a.rows, v, r, bias, cs);
+                emit<OUT, kChunk>(a.e, a.N, n_ok, n, m0 + c, 1, m0 + valid, v, r, bias, cs);
             } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) part[(c + i) * kLanesP + threadIdx.x] = v[i];
+                for (int i = 0; i < kChunk; ++i) part[(c + i) * kLanesP] = v[i];
             }
         }
         umma::fence_before_sync();
@@ -341,29 +349,26 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     __syncwarp();
     if (a.splits > 1) {
         umma::cluster_sync();
-        if (warp < 4) {
-            const int64_t n = n0 + threadIdx.x;
-            const uint32_t valid = min(a.width, a.rows - m0);
-            const float bias = a.e.bias != nullptr && n < a.N ? __ldg(a.e.bias + n) : 0.0f;
-            const float cs = a.e.col_scale != nullptr && n < a.N ? __ldg(a.e.col_scale + n) : 1.0f;
-            // 8 columns at a time, their loads issued together
-            const uint32_t at = smem_addr(stages) + threadIdx.x * 4;
-            for (uint32_t c = rank; c < valid; c += 8 * a.splits) {
-                uint16_t res[8];
-                load_residual<8>(a.e, n < a.N, n, m0 + c, a.splits, m0 + valid, res);
-                float v[8];
+        if (warp < kEpilogueWarps) {
+            // this CTA's columns are rank, rank + splits, ...; a group takes 8 of
+            // them at a time, their loads issued together
+            const uint32_t at = smem_addr(part);
+            for (uint32_t c = rank + group * kChunk * a.splits; c < valid; c += 4 * kChunk * a.splits) {
+                uint16_t res[kChunk];
+                load_residual<kChunk>(a.e, n_ok, n, m0 + c, a.splits, m0 + valid, res);
+                float v[kChunk];
                 for (uint32_t r = 0; r < a.splits; ++r) {
                     const uint32_t peer = umma::map_rank(at, r);
-                    float w[8];
+                    float w[kChunk];
 #pragma unroll
-                    for (uint32_t i = 0; i < 8; ++i) {
+                    for (uint32_t i = 0; i < kChunk; ++i) {
                         const uint32_t col = c + i * a.splits;
                         w[i] = col < valid ? umma::ld_cluster(peer + col * (kLanesP * 4)) : 0.0f;
                     }
 #pragma unroll
-                    for (uint32_t i = 0; i < 8; ++i) v[i] = r == 0 ? w[i] : __fadd_rn(v[i], w[i]);
+                    for (uint32_t i = 0; i < kChunk; ++i) v[i] = r == 0 ? w[i] : __fadd_rn(v[i], w[i]);
                 }
-                emit<OUT, 8>(a.e, a.N, n < a.N, n, m0 + c, a.splits, m0 + valid, v, res, bias, cs);
+                emit<OUT, kChunk>(a.e, a.N, n_ok, n, m0 + c, a.splits, m0 + valid, v, res, bias, cs);
             }
         }
         umma::cluster_sync();   // no CTA leaves while another reads its part
@@ -371,7 +376,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
         __syncthreads();
     }
     umma::fence_after_sync();
-    if (warp == 4) umma::tmem_free<1>(tmem, columns);
+    if (warp == kSplitCopy) umma::tmem_free<1>(tmem, columns);
 }
 
 // --------------------------------------------------------------------------
@@ -391,10 +396,8 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
 // has 512 cycles, of which a copy and its wait take well over 100), warp 17 (of
 // the first CTA) multiplies.
 // --------------------------------------------------------------------------
-constexpr uint32_t kPairEpilogueWarps = 16;
-constexpr uint32_t kPairThreads = 32 * (kPairEpilogueWarps + 3);
-constexpr uint32_t kCopyP = kPairEpilogueWarps, kMultiply = kCopyP + 1, kCopyQ = kCopyP + 2;   // warps
-constexpr int kChunk = 8;   // columns that a warp takes out of tensor memory at a time
+constexpr uint32_t kPairThreads = 32 * (kEpilogueWarps + 3);
+constexpr uint32_t kCopyP = kEpilogueWarps, kMultiply = kCopyP + 1, kCopyQ = kCopyP + 2;   // warps
 constexpr uint32_t kTmemColumns = 512;
 
 // Tile i of the order: bands of kBand p tiles, in each band q tile by q tile,
@@ -444,7 +447,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(sum_full + b, 1);
-            mbar_init(sum_empty + b, 2 * kPairEpilogueWarps);
+            mbar_init(sum_empty + b, 2 * kEpilogueWarps);
         }
         mbar_init_fence();
     }
@@ -532,6 +535,13 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             const bool n_ok = col < a.N;
             const float bias = a.e.bias != nullptr && col < a.N ? __ldg(a.e.bias + col) : 0.0f;
             const float cs = a.e.col_scale != nullptr && col < a.N ? __ldg(a.e.col_scale + col) : 1.0f;
+            // the warp's residual (64 bytes of each row) to L2, under the multiplication:
+            // a chunk at a time from memory took 2400 cycles each
+            if (a.e.residual != nullptr) {
+                const int64_t col0 = col - lane;
+                for (uint32_t c = lane; c < mine; c += 32)
+                    if (m0 + c < a.rows && col0 < a.N) umma::prefetch_l2(a.e.residual + int64_t(m0 + c) * a.e.residual_stride + col0);
+            }
             uint32_t b = 0;
             for (uint32_t part = 0; part < a.splits; ++part) {
                 b = sums.take<PARTS>(part);
@@ -584,24 +594,57 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
     if (warp == kCopyP) umma::tmem_free<2>(tmem, kTmemColumns);
 }
 
-// Rows of `length` values copied to a row pitch that starts every row on 16
-// bytes, for operands that the tensor copies cannot read in place.  A thread
-// writes one 16-byte vector.
-template <class V>
-__global__ void __launch_bounds__(256)
-repack_kernel(const V* __restrict__ src, V* __restrict__ dst, int64_t vectors, int64_t length, int64_t stride,
-              int64_t pitch) {
+// Rows of values copied to a row pitch that starts every row on 16 bytes, for
+// operands that the tensor copies cannot read in place: up to two of them in
+// one launch.  A thread writes one 16-byte vector from the two aligned ones
+// that hold its bytes (one by one where those reach outside the source).
+struct Repack {
+    const char* src;
+    char* dst;
+    uint64_t vectors;            // of all rows
+    uint32_t per_row;            // vectors of a row at dst
+    FastDivU32 by_row;
+    uint64_t length, stride;     // bytes of a row and between rows
+    uint64_t bytes;              // of src, from the first row's start to the last one's end
+};
+
+constexpr uint32_t kRepackThreads = 256;
+
+static __global__ void __launch_bounds__(kRepackThreads) repack_kernel(const Repack first, const Repack second, uint32_t blocks) {
     pdl_enter();
-    constexpr int W = 16 / sizeof(V);
-    const int64_t per_row = pitch / W;
-    for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < vectors; i += int64_t(gridDim.x) * 256) {
-        const int64_t row = i / per_row, c = (i - row * per_row) * W;
-        const V* p = src + row * stride + c;
-        alignas(16) V v[W];
+    const bool one = blockIdx.x < blocks;
+    const Repack& r = one ? first : second;
+    const uint64_t i = uint64_t(one ? blockIdx.x : blockIdx.x - blocks) * kRepackThreads + threadIdx.x;
+    if (i >= r.vectors) return;
+    const uint64_t row = r.vectors <= 0xFFFFFFFFull ? fastdiv_u32(uint32_t(i), r.by_row) : i / r.per_row;
+    const uint64_t c = (i - row * r.per_row) * 16;         // byte within the row
+    const char* p = r.src + row * r.stride + c;
+    const uint32_t shift = uint32_t(reinterpret_cast<uintptr_t>(p) & 15u);
+    const char* base = p - shift;
+    uint32_t w[8];
+    if (base >= r.src && base + 32 <= r.src + r.bytes) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(base)), b = __ldg(reinterpret_cast<const uint4*>(base) + 1);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        // whole words first, then the rest of the shift
 #pragma unroll
-        for (int j = 0; j < W; ++j) v[j] = c + j < length ? p[j] : V(0);
-        *reinterpret_cast<uint4*>(dst + row * pitch + c) = *reinterpret_cast<const uint4*>(v);
+        for (int s = 2; s > 0; s >>= 1)
+            if ((shift / 4) & s) {
+#pragma unroll
+                for (int k = 0; k + s < 8; ++k) w[k] = w[k + s];
+            }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 8 * (shift & 3u));
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            w[k] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + 4 * k + j < r.length) w[k] |= uint32_t(static_cast<uint8_t>(__ldg(p + 4 * k + j))) << (8 * j);
+        }
     }
+    // (bytes past the row's end are read by nobody: the tensor map ends with the row)
+    *reinterpret_cast<uint4*>(r.dst + i * 16) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // u = g * act'(preact) over [T,O], rounded to u (row pitch `pitch`; null: not stored), and the
@@ -610,10 +653,10 @@ repack_kernel(const V* __restrict__ src, V* __restrict__ dst, int64_t vectors, i
 // 8 rows at a time.
 constexpr int kSlopeRows = 8;
 
-template <int DT, int W>
+template <int DT, int W, int ACT>
 __global__ void __launch_bounds__(32 * kSlopeRows)
 slope_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ preact, uint16_t* __restrict__ u,
-             float* __restrict__ partial, int64_t T, int64_t O, int64_t pitch, int64_t rows, int act) {
+             float* __restrict__ partial, int64_t T, int64_t O, int64_t pitch, int64_t rows) {
     pdl_enter();
     __shared__ float part[kSlopeRows][32 * W];
     const int64_t c = (int64_t(blockIdx.x) * 32 + threadIdx.x) * W;
@@ -629,13 +672,13 @@ slope_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ preact
             if constexpr (W == 8) {
                 const Words<4> gw = ld_stream<4>(g + at);
                 Words<4> zw;
-                if (act != kActNone) zw = ld_stream<4>(preact + at);
+                if (ACT != kActNone) zw = ld_stream<4>(preact + at);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     v[2 * i] = Elem<DT>::lo(gw.w[i]), v[2 * i + 1] = Elem<DT>::hi(gw.w[i]);
-                    if (act != kActNone) {
-                        v[2 * i] *= slope(Elem<DT>::lo(zw.w[i]), act);
-                        v[2 * i + 1] *= slope(Elem<DT>::hi(zw.w[i]), act);
+                    if (ACT != kActNone) {
+                        v[2 * i] *= slope<ACT>(Elem<DT>::lo(zw.w[i]));
+                        v[2 * i + 1] *= slope<ACT>(Elem<DT>::hi(zw.w[i]));
                     }
                 }
                 if (u != nullptr) {
@@ -646,7 +689,7 @@ slope_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ preact
                 }
             } else {
                 v[0] = Elem<DT>::one(g[at]);
-                if (act != kActNone) v[0] *= slope(Elem<DT>::one(preact[at]), act);
+                if (ACT != kActNone) v[0] *= slope<ACT>(Elem<DT>::one(preact[at]));
                 if (u != nullptr) u[t * pitch + c] = Elem<DT>::cvt(v[0]);
             }
 #pragma unroll

@@ -226,10 +226,7 @@ __device__ __forceinline__ void tensor_copy_2d(uint32_t dst, const CUtensorMap* 
             : "memory");
 }
 
-// The same box into L2 only.
-__device__ __forceinline__ void tensor_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" : : "l"(map), "r"(c0), "r"(c1) : "memory");
-}
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" : : "l"(p)); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
