@@ -191,12 +191,13 @@ MHC_API mhc_status_t mhc_rotary(const void* x, const int64_t* positions, const f
  * calling thread. */
 MHC_API int32_t mhc_layer_last_cuda_error(void);
 
-/* The product's kernels bound every wait for a copy, a free stage or a
- * finished multiplication (1 s of the GPU's global timer), so no wait can hang
+/* The kernels that wait for copies of their own (the product's, and the
+ * norm's for many rows of more than 1024 values) bound every wait for a copy,
+ * a free stage or a finished multiplication (1 s of the GPU's global timer), so no wait can hang
  * the GPU.  This returns 1 if a wait ran out on the current device since the
  * previous call, else 0, and clears the record; -1 if a CUDA call fails.  It
  * synchronizes the device.  A return of 1 means that the outputs of every
- * product on the device since the previous call are invalid. */
+ * such call on the device since the previous call are invalid. */
 MHC_API int64_t mhc_layer_wait_timeouts(void);
 
 #ifdef __cplusplus

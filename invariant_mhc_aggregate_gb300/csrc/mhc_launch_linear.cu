@@ -13,6 +13,8 @@ namespace {
 // Set to 1 when a bounded wait runs out (see mhc_bulk.cuh); one per device.
 __device__ unsigned int g_timeouts;
 
+}  // namespace
+
 cudaError_t timeouts_ptr(unsigned int** p) {
     static std::atomic<unsigned int*> cached[kMaxDevices];
     const int dev = current_device();
@@ -26,6 +28,8 @@ cudaError_t timeouts_ptr(unsigned int** p) {
     *p = q;
     return cudaSuccess;
 }
+
+namespace {
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (the
 // library does not link the driver library itself); resolved once.

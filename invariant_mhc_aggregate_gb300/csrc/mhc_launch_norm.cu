@@ -94,8 +94,10 @@ cudaError_t fwd_launch(const FwdArgs& args, Shape s, cudaStream_t stream) {
 }
 
 template <int DT, int K, int OUT>
-cudaError_t fwd_ring(const FwdArgs& a, Shape s, RingShape ring, cudaStream_t stream) {
+cudaError_t fwd_ring(FwdArgs a, Shape s, RingShape ring, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0}, narrow{0};
+    const cudaError_t e = timeouts_ptr(&a.timeouts);
+    if (e != cudaSuccess) return e;
     RingRows r = {{a.x, a.residual, nullptr}, {a.x_stride, a.residual_stride, 0}, a.residual != nullptr ? 2u : 1u};
     // four times the blocks that run at once: as they end one by one, the next
     // ones start under the others' rows, and the last rows spread out (T = 4096,
@@ -138,7 +140,7 @@ cudaError_t fwd_shape(const FwdArgs& a, int out, cudaStream_t stream) {
 }
 
 template <int DT, int K, bool VEC>
-cudaError_t bwd_launch(const BwdArgs& a, Shape s, uint32_t blocks, cudaStream_t stream) {
+cudaError_t bwd_launch(BwdArgs a, Shape s, uint32_t blocks, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
     const uint32_t rows = VEC && s.nt == 32 ? kWarpRows : 1;
     if constexpr (VEC && (K == 2 || K == 4)) {
@@ -147,6 +149,8 @@ cudaError_t bwd_launch(const BwdArgs& a, Shape s, uint32_t blocks, cudaStream_t 
         RingShape ring = ring_shape(row, (blocks + uint32_t(num_sms()) - 1) / uint32_t(num_sms()));
         if (rows == 1 && ring.stages >= 2 && a.T > int64_t(blocks)) {
             static std::atomic<uint64_t> ring_allowed{0};
+            const cudaError_t e = timeouts_ptr(&a.timeouts);
+            if (e != cudaSuccess) return e;
             return launch_rows(bwd_ring_kernel<DT, K>, blocks, s.nt, 1, ring.stages * row, ring_allowed, stream, a, r,
                                ring.stages);
         }

@@ -129,6 +129,7 @@ mhc_status_t norm_fwd(const void* x, const void* residual, const float* weight, 
     a.scale = scale;
     a.total = static_cast<uint16_t*>(total);
     a.rstd = rstd;
+    a.timeouts = nullptr;
     a.T = T;
     a.x_stride = x_stride, a.residual_stride = residual_stride;
     a.H = uint32_t(H);
@@ -160,6 +161,7 @@ mhc_status_t norm_bwd(const void* g, const void* s, const float* weight, const f
     a.grad_total = static_cast<const uint16_t*>(grad_total);
     a.grad_x = static_cast<uint16_t*>(grad_x);
     a.partial = nullptr;
+    a.timeouts = nullptr;
     a.T = T;
     a.g_stride = g_stride, a.s_stride = s_stride;
     a.H = uint32_t(H);

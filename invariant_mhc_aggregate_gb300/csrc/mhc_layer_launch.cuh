@@ -54,7 +54,10 @@ cudaError_t repack(const RepackCall* calls, int count, cudaStream_t stream);   /
 cudaError_t slope(const uint16_t* g, const uint16_t* preact, uint16_t* u, float* grad_bias, float* partial, int64_t T,
                   int64_t O, int64_t pitch, int act, int dtype, cudaStream_t stream);
 int64_t slope_partials(int64_t T);
-// 1 if a bounded wait of the product ran out on the current device since the
+// The device address of the flag that these kernels set when a bounded wait
+// runs out, for the current device.
+cudaError_t timeouts_ptr(unsigned int** p);
+// 1 if a bounded wait of these kernels ran out on the current device since the
 // last call, else 0 (clears the record; synchronizes the device); -1 on a
 // CUDA error.
 int64_t take_wait_timeouts();

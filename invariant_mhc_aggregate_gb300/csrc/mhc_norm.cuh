@@ -414,6 +414,13 @@ __device__ __forceinline__ void ring_copy(char* stage, const RingRows& r, int64_
     for (uint32_t i = 0; i < r.arrays; ++i) bulk_copy_g2s(stage + i * bytes, r.from[i] + t * r.stride[i], bytes, full);
 }
 
+// Thread 0's end after a wait that ran out: records it and waits (again
+// bounded) for the copies in flight.
+static __device__ __noinline__ void ring_late(uint64_t* full, uint32_t issued, uint32_t stages, unsigned int* timeouts) {
+    *timeouts = 1u;
+    for (uint32_t i = issued > stages ? issued - stages : 0; i < issued; ++i) mbar_wait(full + i % stages, (i / stages) & 1);
+}
+
 template <int DT, int K>
 __device__ __forceinline__ void stage_words(const char* row, uint32_t H, Words<4> (&w)[K]) {
 #pragma unroll
@@ -438,24 +445,26 @@ fwd_ring_kernel(const FwdArgs a, const RingRows r, uint32_t stages) {
     extern __shared__ __align__(16) char ring[];
     __shared__ float shared[2][2][32];
     __shared__ uint64_t full[kRingStages];
+    __shared__ volatile int late;   // a wait ran out: no further copy, no further wait
     const uint32_t H = a.H, j = threadIdx.x, bytes = 2 * H;
     if (j == 0) {
         for (uint32_t s = 0; s < stages; ++s) mbar_init(full + s, 1);
         mbar_init_fence();
+        late = 0;
     }
     __syncthreads();
     pdl_enter();
     const int64_t step = gridDim.x;
+    uint32_t issued = 0;   // of thread 0
     if (j == 0)
-        for (uint32_t s = 0; s < stages; ++s)
-            if (blockIdx.x + s * step < a.T) ring_copy(ring + s * r.arrays * bytes, r, blockIdx.x + s * step, bytes, full + s);
+        for (; issued < stages && blockIdx.x + issued * step < a.T; ++issued)
+            ring_copy(ring + issued * r.arrays * bytes, r, blockIdx.x + issued * step, bytes, full + issued);
     float w[8 * K];
     load_weight<K, true>(a.weight, H, w);
     uint32_t stage = 0, parity = 0;
     int turn = 0;
-    bool ok = true;
     for (int64_t t = blockIdx.x; t < a.T; t += step, turn ^= 1) {
-        ok = mbar_wait_fast(full + stage, parity) && ok;
+        if (!late && !mbar_wait_fast(full + stage, parity)) late = 1;
         const char* row = ring + stage * r.arrays * bytes;
         Words<4> raw[K];
         float s[8 * K];
@@ -487,9 +496,10 @@ fwd_ring_kernel(const FwdArgs a, const RingRows r, uint32_t stages) {
             acc = __fadd_rn(acc, chunk_sum(q));
         }
         const float sum = fold(acc, shared[turn][0], Add());
-        if (j == 0 && t + stages * step < a.T && ok) {
+        if (j == 0 && t + stages * step < a.T && !late) {
             fence_proxy_async_shared();
             ring_copy(ring + stage * r.arrays * bytes, r, t + stages * step, bytes, full + stage);
+            ++issued;
         }
         if (++stage == stages) stage = 0, parity ^= 1;
         const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(H)), a.eps)));
@@ -498,7 +508,7 @@ fwd_ring_kernel(const FwdArgs a, const RingRows r, uint32_t stages) {
         for (int i = 0; i < 8 * K; ++i) s[i] = __fmul_rn(__fmul_rn(s[i], rstd), w[i]);
         store_y<DT, K, true, OUT>(a, t, s, nullptr, shared[turn][1]);
     }
-    if (!ok && a.timeouts != nullptr) *a.timeouts = 1u;
+    if (j == 0 && late) ring_late(full, issued, stages, a.timeouts);
 }
 
 template <int DT, int K>
@@ -507,27 +517,29 @@ bwd_ring_kernel(const BwdArgs a, const RingRows r, uint32_t stages) {
     extern __shared__ __align__(16) char ring[];
     __shared__ float shared[2][32];
     __shared__ uint64_t full[kRingStages];
+    __shared__ volatile int late;   // a wait ran out: no further copy, no further wait
     const uint32_t H = a.H, j = threadIdx.x, bytes = 2 * H;
     if (j == 0) {
         for (uint32_t s = 0; s < stages; ++s) mbar_init(full + s, 1);
         mbar_init_fence();
+        late = 0;
     }
     __syncthreads();
     pdl_enter();
     const int64_t step = gridDim.x;
+    uint32_t issued = 0;   // of thread 0
     if (j == 0)
-        for (uint32_t s = 0; s < stages; ++s)
-            if (blockIdx.x + s * step < a.T) ring_copy(ring + s * r.arrays * bytes, r, blockIdx.x + s * step, bytes, full + s);
+        for (; issued < stages && blockIdx.x + issued * step < a.T; ++issued)
+            ring_copy(ring + issued * r.arrays * bytes, r, blockIdx.x + issued * step, bytes, full + issued);
     float w[8 * K], acc[8 * K];
     load_weight<K, true>(a.weight, H, w);
 #pragma unroll
     for (int i = 0; i < 8 * K; ++i) acc[i] = 0.0f;
     uint32_t stage = 0, parity = 0;
     int turn = 0;
-    bool ok = true;
     for (int64_t t = blockIdx.x; t < a.T; t += step, turn ^= 1) {
         const float rstd = __ldg(a.rstd + t);
-        ok = mbar_wait_fast(full + stage, parity) && ok;
+        if (!late && !mbar_wait_fast(full + stage, parity)) late = 1;
         const char* row = ring + stage * r.arrays * bytes;
         Words<4> g[K], n[K], more[K];
         stage_words<DT, K>(row, H, g);
@@ -548,9 +560,10 @@ bwd_ring_kernel(const BwdArgs a, const RingRows r, uint32_t stages) {
             sum = __fadd_rn(sum, chunk_sum(q));
         }
         const float m = __fdiv_rn(fold(sum, shared[turn], Add()), float(H));
-        if (j == 0 && t + stages * step < a.T && ok) {
+        if (j == 0 && t + stages * step < a.T && !late) {
             fence_proxy_async_shared();
             ring_copy(ring + stage * r.arrays * bytes, r, t + stages * step, bytes, full + stage);
+            ++issued;
         }
         if (++stage == stages) stage = 0, parity ^= 1;
 #pragma unroll
@@ -576,7 +589,7 @@ bwd_ring_kernel(const BwdArgs a, const RingRows r, uint32_t stages) {
         }
     }
     store_partial<K, true>(a.partial + int64_t(blockIdx.x) * H, H, acc);
-    if (!ok && a.timeouts != nullptr) *a.timeouts = 1u;
+    if (j == 0 && late) ring_late(full, issued, stages, a.timeouts);
 }
 
 // Column sums of partial [P,H]: block (32, 32); thread (x, y) adds the rows

@@ -121,7 +121,7 @@ def _compiled():
 
 
 def wait_timeouts() -> int:
-    """1 if a bounded wait of the product's kernels ran out on the current
+    """1 if a bounded wait of the library's kernels ran out on the current
     device since the last call, else 0 (clears it; synchronizes the device);
     -1 on a CUDA error."""
     return int(load().mhc_layer_wait_timeouts())

@@ -645,3 +645,41 @@ def test_refusals():
                 lambda: layer.rotary(x.view(4, 1, 64), pos, f, out=x.view(-1)[:1].expand(4, 1, 64).contiguous().as_strided((4, 1, 64), (0, 64, 1)))):
         with pytest.raises(layer.LayerError):
             bad()
+
+
+# ---------------------------------------------------------------------------
+# offsets past 32 bits
+# ---------------------------------------------------------------------------
+
+def test_norm_past_32_bits():
+    T, H = 300000, 7168                                       # 2.15e9 values
+    g = gen(41)
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, T // 2, T - 1], device="cuda")
+    x[rows] = normal(g, 3, H, dtype=torch.bfloat16)
+    w = 1 + normal(g, H, spread=0.2)
+    y, _, rstd = layer.rms_norm(x, w)
+    _, ref, v = norm_ref(x[rows], None, w, 1e-6)
+    within(y[rows], v, v.abs() * (U[torch.bfloat16] + 80 * E) + TINY[torch.bfloat16], "y")
+    assert int((rstd < 999).sum()) == 3
+    grad, grad_w = layer.rms_norm_backward(x, x, w, rstd)
+    r = rstd[rows].double()[:, None]
+    n, u = x[rows].double() * r, x[rows].double() * w.double()
+    m = (u * n).mean(-1, keepdim=True)
+    want = r * (u - n * m)
+    size = r * (u.abs() + n.abs() * (u * n).abs().mean(-1, keepdim=True))
+    within(grad[rows], want, U[torch.bfloat16] * want.abs() + 96 * E * size + TINY[torch.bfloat16], "grad_x")
+    within(grad_w, (x[rows].double() * n).sum(0), 1200 * E * (x[rows].double() * n).abs().sum(0) + 1e-40, "grad_w")
+
+
+def test_rotary_past_32_bits():
+    T, heads, D = 2200000, 8, 128                             # 2.25e9 values
+    g = gen(42)
+    x = torch.zeros(T, heads, D, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, T // 2, T - 1], device="cuda")
+    x[rows] = normal(g, 3, heads, D, dtype=torch.bfloat16)
+    pos = torch.arange(T, device="cuda")
+    f = layer.rotary_frequencies(D)
+    got = layer.rotary(x, pos, f)
+    check_rotary(got[rows], x[rows], pos[rows], f, False, 1.0, False)
+    assert int((got != 0).flatten(1).any(-1).sum()) == 3
