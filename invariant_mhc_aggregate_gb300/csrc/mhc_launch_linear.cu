@@ -283,7 +283,7 @@ cudaError_t slope(const uint16_t* g, const uint16_t* preact, uint16_t* u, float*
                                   : (vec ? slope_kernel_of<kF16, 8>(act) : slope_kernel_of<kF16, 1>(act));
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, g, preact, u, sums, T, O, pitch, rows);
     if (e != cudaSuccess || grad_bias == nullptr || runs == 1) return e;
-    return column_sum(partial, grad_bias, uint32_t(runs), O, stream);
+    return column_sum(partial, grad_bias, uint32_t(runs), O, O, stream);
 }
 
 }  // namespace layer

@@ -31,8 +31,6 @@ constexpr uint32_t kWarpRows = 4;   // rows of a block where a warp holds a row
 // Shared memory of one SM that the blocks of these kernels share out.
 constexpr uint32_t kRowSmem = 216 * 1024;
 
-uint32_t stage_bytes(Shape s) { return 8u * uint32_t(s.K) * s.nt * 4u; }
-
 template <typename... Params, typename... Args>
 cudaError_t launch_rows(void (*kernel)(Params...), uint32_t grid, uint32_t nt, uint32_t rows, uint32_t smem,
                         std::atomic<uint64_t>& allowed, cudaStream_t stream, Args... args) {
@@ -72,8 +70,7 @@ RingShape ring_shape(uint32_t row_bytes, uint32_t most) {
 template <int DT, int K, bool VEC, int OUT>
 cudaError_t fwd_launch(const FwdArgs& args, Shape s, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    const uint32_t rows = VEC && s.nt == 32 ? kWarpRows : 1;
-    const uint32_t smem = VEC ? 0 : stage_bytes(s);
+    const uint32_t rows = s.nt == 32 ? kWarpRows : 1;
     const int64_t most = int64_t(0x7FFFFFFF) * rows;   // rows of one launch
     for (int64_t t0 = 0; t0 < args.T; t0 += most) {
         FwdArgs a = args;
@@ -86,8 +83,8 @@ cudaError_t fwd_launch(const FwdArgs& args, Shape s, cudaStream_t stream) {
         a.y = static_cast<char*>(a.y) + t0 * int64_t(a.H) * (OUT == kOutSame ? 2 : 1);
         a.rstd += t0;
         if (OUT != kOutSame) a.scale += t0 * (OUT == kOutFp8Row ? 1 : (int64_t(a.H) + kGroup - 1) / kGroup);
-        const cudaError_t e = launch_rows(fwd_kernel<DT, K, VEC, OUT>, uint32_t((a.T + rows - 1) / rows), s.nt, rows,
-                                          smem, allowed, stream, a);
+        const cudaError_t e = launch_rows(fwd_kernel<DT, K, VEC, OUT>, uint32_t((a.T + rows - 1) / rows), s.nt, rows, 0,
+                                          allowed, stream, a);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -142,7 +139,7 @@ cudaError_t fwd_shape(const FwdArgs& a, int out, cudaStream_t stream) {
 template <int DT, int K, bool VEC>
 cudaError_t bwd_launch(BwdArgs a, Shape s, uint32_t blocks, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    const uint32_t rows = VEC && s.nt == 32 ? kWarpRows : 1;
+    const uint32_t rows = s.nt == 32 ? kWarpRows : 1;
     if constexpr (VEC && (K == 2 || K == 4)) {
         const RingRows r = {{a.g, a.s, a.grad_total}, {a.g_stride, a.s_stride, int64_t(a.H)}, a.grad_total != nullptr ? 3u : 2u};
         const uint32_t row = a.H * 2 * r.arrays;
@@ -155,7 +152,7 @@ cudaError_t bwd_launch(BwdArgs a, Shape s, uint32_t blocks, cudaStream_t stream)
                                ring.stages);
         }
     }
-    return launch_rows(bwd_kernel<DT, K, VEC>, blocks, s.nt, rows, VEC && rows == 1 ? 0 : stage_bytes(s), allowed,
+    return launch_rows(bwd_kernel<DT, K, VEC>, blocks, s.nt, rows, rows == 1 ? 0 : 8u * K * 32 * 4, allowed,
                        stream, a);
 }
 
@@ -183,16 +180,18 @@ cudaError_t norm_fwd(const FwdArgs& a, int dtype, int out, cudaStream_t stream) 
 
 // Blocks of the backward, each with a partial sum of grad_weight: for each of
 // 152 SMs as many as have 1024 threads (a constant, so that the sum's order
-// does not depend on the device), at most one for each row.
+// does not depend on the device), and no more than have rows.
 uint32_t norm_bwd_partials(int64_t T, int64_t H) {
     const Shape s = shape_of(uint32_t(H));
     const int64_t most = 152 * (1024 / s.nt < 8 ? 1024 / s.nt : 8);
-    return uint32_t(T < most ? T : most);
+    const int64_t blocks = s.nt == 32 ? (T + kWarpRows - 1) / kWarpRows : T;
+    return uint32_t(blocks < most ? blocks : most);
 }
 
 cudaError_t norm_bwd(BwdArgs a, float* grad_weight, float* workspace, int dtype, cudaStream_t stream) {
     const uint32_t P = norm_bwd_partials(a.T, a.H);
     a.partial = P > 1 ? workspace : grad_weight;
+    a.pitch = (a.H + 7) / 8 * 8;   // whole chunks
     const bool vec = a.H % 8 == 0 && rows16(a.g, a.g_stride) && rows16(a.s, a.s_stride) && aligned(a.weight, 16) &&
                      aligned(a.grad_x, 16) && aligned(a.partial, 16) &&
                      (a.grad_total == nullptr || aligned(a.grad_total, 16));
@@ -200,10 +199,10 @@ cudaError_t norm_bwd(BwdArgs a, float* grad_weight, float* workspace, int dtype,
     if (dtype == kBF16) e = vec ? bwd_shape<kBF16, true>(a, P, stream) : bwd_shape<kBF16, false>(a, P, stream);
     else e = vec ? bwd_shape<kF16, true>(a, P, stream) : bwd_shape<kF16, false>(a, P, stream);
     if (e != cudaSuccess || P <= 1) return e;
-    return column_sum(workspace, grad_weight, P, a.H, stream);
+    return column_sum(workspace, grad_weight, P, a.H, a.pitch, stream);
 }
 
-cudaError_t column_sum(const float* partial, float* out, uint32_t P, int64_t H, cudaStream_t stream) {
+cudaError_t column_sum(const float* partial, float* out, uint32_t P, int64_t H, int64_t pitch, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(uint32_t((H + 31) / 32));
     cfg.blockDim = dim3(32, kColRows);
@@ -213,7 +212,7 @@ cudaError_t column_sum(const float* partial, float* out, uint32_t P, int64_t H, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, column_sum_kernel, partial, out, P, uint32_t(H));
+    return cudaLaunchKernelEx(&cfg, column_sum_kernel, partial, out, P, uint32_t(H), uint32_t(pitch));
 }
 
 }  // namespace layer

@@ -258,8 +258,8 @@ mhc_status_t mhc_rms_norm_fp8_fwd(const void* x, const void* residual, const flo
 }
 
 int64_t mhc_rms_norm_bwd_workspace(int64_t T, int64_t H) {
-    if (T <= 1 || H <= 0 || H > mhc::norm::kMaxH) return 0;
-    return int64_t(mhc::layer::norm_bwd_partials(T, H)) * H * 4;
+    if (T <= 0 || H <= 0 || H > mhc::norm::kMaxH || mhc::layer::norm_bwd_partials(T, H) <= 1) return 0;
+    return int64_t(mhc::layer::norm_bwd_partials(T, H)) * ((H + 7) / 8 * 8) * 4;
 }
 
 mhc_status_t mhc_rms_norm_bwd(const void* g, const void* s, const float* weight, const float* rstd,

@@ -35,8 +35,8 @@ struct RotaryCall {
 };
 cudaError_t rotary(const RotaryCall& c);
 
-// Column sums of partial [P,H] into out [H] (mhc_launch_norm.cu).
-cudaError_t column_sum(const float* partial, float* out, uint32_t P, int64_t H, cudaStream_t stream);
+// Column sums of partial [P,H] (row pitch `pitch`) into out [H] (mhc_launch_norm.cu).
+cudaError_t column_sum(const float* partial, float* out, uint32_t P, int64_t H, int64_t pitch, cudaStream_t stream);
 
 // Matrix product (mhc_launch_linear.cu).  in, out: kBF16, kF16; in also
 // kE4m3.  Every operand's rows start on 16-byte boundaries.

@@ -19,10 +19,12 @@
 //    a row do not wait for its sum; the norm's weight stays in registers;
 //  * VEC: 16-byte loads and stores of the thread's own chunks, for the other
 //    aligned rows;
-//  * otherwise thread j moves the values j, j + nt, ... with 2-byte accesses
-//    (a warp's accesses are then contiguous whatever the row's alignment) and
-//    the products of a row's sum change hands through shared memory, where
-//    every row is aligned.
+//  * otherwise (odd H, strides or pointers off 16 bytes) the same chunks, each
+//    from the two aligned vectors that hold it, and to aligned vectors put
+//    together from two neighbouring lanes' chunks; the ends of a warp's run of
+//    chunks go value by value.  (Moving single values, a thread taking j, j +
+//    nt, ..., and exchanging the sums' terms through shared memory: T = 20000,
+//    H = 1279 109 us, backward 113.)
 #pragma once
 
 #include "mhc_bulk.cuh"
@@ -61,7 +63,8 @@ struct BwdArgs {
     const float* rstd;
     const uint16_t* grad_total;   // null without one
     uint16_t* grad_x;
-    float* partial;               // [gridDim.x, H]
+    float* partial;               // [gridDim.x, pitch]
+    uint32_t pitch;
     unsigned int* timeouts;       // ring kernels only
     int64_t T;
     int64_t g_stride, s_stride;
@@ -109,13 +112,38 @@ struct Max {
     __device__ float operator()(float a, float b) const { return max_nan(a, b); }
 };
 
-// One row of a 2-byte buffer in the registers of the row's threads; values
-// past H read as +0.
-template <int DT, int K, bool VEC>
-__device__ __forceinline__ void load_row(const uint16_t* __restrict__ row, uint32_t H, float (&v)[8 * K]) {
+// The bytes `shift` .. shift + 4 N - 1 of the 8 N bytes in w, to its first N words.
+template <int N>
+__device__ __forceinline__ void shift_bytes(uint32_t (&w)[2 * N], uint32_t shift) {
+    const uint32_t words = shift / 4;
+#pragma unroll
+    for (int s = N; s > 0; s >>= 1)
+        if (words & s) {
+#pragma unroll
+            for (int k = 0; k + s < 2 * N; ++k) w[k] = w[k + s];
+        }
+#pragma unroll
+    for (int k = 0; k < N; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 8 * (shift & 3u));
+}
+
+// An input of 2-byte rows, and where its first row starts and its last ends.
+struct Input {
+    const uint16_t* p;
+    int64_t stride;
+    const char *lo, *hi;
+    __device__ __forceinline__ Input(const uint16_t* ptr, int64_t row_stride, int64_t T, uint32_t H)
+        : p(ptr),
+          stride(row_stride),
+          lo(reinterpret_cast<const char*>(ptr)),
+          hi(reinterpret_cast<const char*>(ptr + (T - 1) * row_stride + H)) {}
+};
+
+// One row in the registers of the row's threads; values past H read as +0.
+template <int K, bool VEC>
+__device__ __forceinline__ void load_words(const Input& in, int64_t t, uint32_t H, Words<4> (&w)[K]) {
+    const uint16_t* row = in.p + t * in.stride;
     const uint32_t nt = blockDim.x, j = threadIdx.x;
     if constexpr (VEC) {
-        Words<4> w[K];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const uint32_t c = 8 * (j + k * nt);
@@ -126,44 +154,131 @@ __device__ __forceinline__ void load_row(const uint16_t* __restrict__ row, uint3
                 for (int i = 0; i < 4; ++i) w[k].w[i] = 0;
             }
         }
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[8 * k + 2 * i] = Elem<DT>::lo(w[k].w[i]);
-                v[8 * k + 2 * i + 1] = Elem<DT>::hi(w[k].w[i]);
-            }
     } else {
-        uint16_t h[8 * K];
+        const uint32_t shift = uint32_t(reinterpret_cast<uintptr_t>(row) & 15u);
+        const char* base = reinterpret_cast<const char*>(row) - shift;
+        uint32_t v[K][8];
 #pragma unroll
-        for (int m = 0; m < 8 * K; ++m) {
-            const uint32_t c = j + m * nt;
-            h[m] = c < H ? ld_stream2(row + c) : uint16_t(0);
+        for (int k = 0; k < K; ++k) {
+            const uint32_t c = 8 * (j + k * nt);
+            const char* q = base + 2 * c;
+            if (c < H && q >= in.lo && q + 32 <= in.hi) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4*>(q)), y = __ldg(reinterpret_cast<const uint4*>(q) + 1);
+                v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+                v[k][4] = y.x, v[k][5] = y.y, v[k][6] = y.z, v[k][7] = y.w;
+            } else {   // past the row, or a vector that is not all inside the input: at the shift's place
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k][i] = 0;
+                if (c < H) {
+                    uint32_t one[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c + i < H) one[i / 2] |= uint32_t(__ldg(row + c + i)) << (16 * (i & 1));
+                    // (shift_bytes below moves them back down)
+                    uint32_t up[8] = {0, 0, 0, 0, one[0], one[1], one[2], one[3]};
+                    shift_bytes<4>(up, 16 - shift);
+                    uint32_t high[8] = {one[0], one[1], one[2], one[3], 0, 0, 0, 0};
+                    shift_bytes<4>(high, 16 - shift);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[k][i] = up[i], v[k][4 + i] = high[i];
+                }
+            }
         }
 #pragma unroll
-        for (int m = 0; m < 8 * K; ++m) v[m] = Elem<DT>::one(h[m]);
+        for (int k = 0; k < K; ++k) {
+            shift_bytes<4>(v[k], shift);
+            const uint32_t c = 8 * (j + k * nt);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (c + 2 * i + 1 >= H) v[k][i] &= c + 2 * i >= H ? 0u : 0xFFFFu;
+                w[k].w[i] = v[k][i];
+            }
+        }
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void chunk_values(const Words<4>& w, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = Elem<DT>::lo(w.w[i]), v[2 * i + 1] = Elem<DT>::hi(w.w[i]);
+}
+
+template <int DT, int K, bool VEC>
+__device__ __forceinline__ void load_row(const Input& in, int64_t t, uint32_t H, float (&v)[8 * K]) {
+    Words<4> w[K];
+    load_words<K, VEC>(in, t, H, w);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        float x[8];
+        chunk_values<DT>(w[k], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * k + i] = x[i];
+    }
+}
+
+// The row's chunk c (its first value), 8 values of SIZE bytes in 2 SIZE words,
+// without 16-byte alignment (4 SIZE bytes).  Every lane of the warp calls,
+// lanes in the order of their chunks.  The aligned vector that the chunk's
+// first values lie in begins with the previous lane's last `off`.
+template <int SIZE>
+__device__ __forceinline__ void store_unaligned(char* row, uint32_t H, uint32_t c, const uint32_t (&w)[2 * SIZE]) {
+    constexpr int N = 2 * SIZE;
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(row) & (8 * SIZE - 1)) / SIZE;   // values
+    uint32_t v[2 * N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = __shfl_up_sync(0xFFFFFFFFu, w[i], 1);
+        v[N + i] = w[i];
+    }
+    shift_bytes<N>(v, 8 * SIZE - off * SIZE);
+    const auto value = [&](int i) {   // of the lane's own chunk
+        return SIZE == 2 ? w[i / 2] >> (16 * (i & 1)) : w[i / 4] >> (8 * (i & 3));
+    };
+    const auto put = [&](int i) {
+        if constexpr (SIZE == 2) st_stream2(row + 2 * (c + i), uint16_t(value(i)));
+        else row[c + i] = char(value(i));
+    };
+    // its vector holds the values c - off .. c - off + 7
+    const bool whole = (lane > 0 || off == 0) && c + 7 < H + off;
+    if (whole) {
+        char* at = row + int64_t(c) * SIZE - int64_t(off) * SIZE;
+        if constexpr (SIZE == 2) {
+            __stcs(reinterpret_cast<uint4*>(at), make_uint4(v[0], v[1], v[2], v[3]));
+        } else {
+            __stcs(reinterpret_cast<uint2*>(at), make_uint2(v[0], v[1]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < 8 - off && c + i < H) put(i);
+    }
+    // the chunk's last `off` values, where the next lane does not take them
+    if (lane == 31 || c + 8 + 7 >= H + off) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i >= 8 - off && c + i < H) put(i);
     }
 }
 
 template <int DT, int K, bool VEC>
 __device__ __forceinline__ void store_row(uint16_t* __restrict__ row, uint32_t H, const float (&v)[8 * K]) {
     const uint32_t nt = blockDim.x, j = threadIdx.x;
-    if constexpr (VEC) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const uint32_t c = 8 * (j + k * nt);
+    for (int k = 0; k < K; ++k) {
+        const uint32_t c = 8 * (j + k * nt);
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = Elem<DT>::pack(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
+        if constexpr (VEC) {
             if (c < H) {
-                Words<4> w;
+                Words<4> o;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w.w[i] = Elem<DT>::pack(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
-                st_stream<4>(row + c, w);
+                for (int i = 0; i < 4; ++i) o.w[i] = w[i];
+                st_stream<4>(row + c, o);
             }
-        }
-    } else {
-#pragma unroll
-        for (int m = 0; m < 8 * K; ++m) {
-            const uint32_t c = j + m * nt;
-            if (c < H) st_stream2(row + c, Elem<DT>::cvt(v[m]));
+        } else {
+            store_unaligned<2>(reinterpret_cast<char*>(row), H, c, w);
         }
     }
 }
@@ -172,62 +287,39 @@ __device__ __forceinline__ void store_row(uint16_t* __restrict__ row, uint32_t H
 template <int K, bool VEC>
 __device__ __forceinline__ void load_weight(const float* __restrict__ w, uint32_t H, float (&v)[8 * K]) {
     const uint32_t nt = blockDim.x, j = threadIdx.x;
-    if constexpr (VEC) {
+    const bool vectors = VEC || (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const uint32_t c = 8 * (j + k * nt);
-            float4 a = make_float4(0, 0, 0, 0), b = a;
-            if (c < H) {
-                a = __ldg(reinterpret_cast<const float4*>(w + c));
-                b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
-            }
+    for (int k = 0; k < K; ++k) {
+        const uint32_t c = 8 * (j + k * nt);
+        if (vectors && c + (VEC ? 0 : 7) < H) {
+            const float4 a = __ldg(reinterpret_cast<const float4*>(w + c)), b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
             v[8 * k] = a.x, v[8 * k + 1] = a.y, v[8 * k + 2] = a.z, v[8 * k + 3] = a.w;
             v[8 * k + 4] = b.x, v[8 * k + 5] = b.y, v[8 * k + 6] = b.z, v[8 * k + 7] = b.w;
-        }
-    } else {
+        } else {
 #pragma unroll
-        for (int m = 0; m < 8 * K; ++m) {
-            const uint32_t c = j + m * nt;
-            v[m] = c < H ? __ldg(w + c) : 0.0f;
+            for (int i = 0; i < 8; ++i) v[8 * k + i] = !VEC && c + i < H ? __ldg(w + c + i) : 0.0f;
         }
     }
 }
 
-// The row's sum of q in the order stated above.  `stage`: 8 * K * nt floats,
-// without VEC only.
-template <int K, bool VEC>
-__device__ __forceinline__ float row_sum(const float (&q)[8 * K], float* stage, float* shared) {
+// The row's sum of q in the order stated above.
+template <int K>
+__device__ __forceinline__ float row_sum(const float (&q)[8 * K], float* shared) {
     float acc = 0.0f;
-    if constexpr (VEC) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) acc = __fadd_rn(acc, chunk_sum(q + 8 * k));
-    } else {
-        const uint32_t nt = blockDim.x, j = threadIdx.x;
-        __syncthreads();
-#pragma unroll
-        for (int m = 0; m < 8 * K; ++m) stage[j + m * nt] = q[m];
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const float4* p = reinterpret_cast<const float4*>(stage + 8 * (j + k * nt));
-            const float4 a = p[0], b = p[1];
-            const float c[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            acc = __fadd_rn(acc, chunk_sum(c));
-        }
-    }
+    for (int k = 0; k < K; ++k) acc = __fadd_rn(acc, chunk_sum(q + 8 * k));
     return fold(acc, shared, Add());
 }
 
 // The row's output from v: 16-bit values, or E4M3 values and their scales.
 template <int DT, int K, bool VEC, int OUT>
-__device__ __forceinline__ void store_y(const FwdArgs& a, int64_t t, float (&s)[8 * K], float* stage, float* shared) {
+__device__ __forceinline__ void store_y(const FwdArgs& a, int64_t t, float (&s)[8 * K], float* shared) {
     const uint32_t H = a.H, nt = blockDim.x, j = threadIdx.x;
     if constexpr (OUT == kOutSame) {
         store_row<DT, K, VEC>(static_cast<uint16_t*>(a.y) + t * int64_t(H), H, s);
     } else {
         uint8_t* y = static_cast<uint8_t*>(a.y) + t * int64_t(H);
-        const uint32_t groups = OUT == kOutFp8Row ? 1 : (H + kGroup - 1) / kGroup;
-        float inv[K];   // of the thread's chunks (VEC), or inv[0] of the row
+        float inv[K];   // of the thread's chunks
         if constexpr (OUT == kOutFp8Row) {
             float m = kAmaxFloor;
 #pragma unroll
@@ -239,147 +331,152 @@ __device__ __forceinline__ void store_y(const FwdArgs& a, int64_t t, float (&s)[
             for (int k = 0; k < K; ++k) inv[k] = r;
         } else {
             // 16 chunks to a group: half a warp's chunks of the same k
-            if constexpr (!VEC) {
-                __syncthreads();
-#pragma unroll
-                for (int m = 0; m < 8 * K; ++m) stage[j + m * nt] = s[m];
-                __syncthreads();
-            }
+            const uint32_t groups = (H + kGroup - 1) / kGroup;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 float m = kAmaxFloor;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(VEC ? s[8 * k + i] : stage[8 * (j + k * nt) + i]));
+                for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(s[8 * k + i]));
 #pragma unroll
                 for (int d = 8; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
                 inv[k] = __fdiv_rn(kE4m3Max, m);
                 const uint32_t c = j + k * nt;
                 if ((j & 15u) == 0 && 8 * c < H) a.scale[t * groups + c / 16] = __fdiv_rn(m, kE4m3Max);
             }
-            if constexpr (!VEC) {   // the groups' factors, over the staged values
-                __syncthreads();
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if ((j & 15u) == 0) stage[(j + k * nt) / 16] = inv[k];
-                __syncthreads();
-            }
         }
-        if constexpr (VEC) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const uint32_t c = 8 * (j + k * nt);
-                if (c < H) {
-                    uint32_t w[2];
+        for (int k = 0; k < K; ++k) {
+            const uint32_t c = 8 * (j + k * nt);
+            uint32_t w[2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float* p = s + 8 * k + 4 * i;
-                        w[i] = uint32_t(e4m3_pair(__fmul_rn(p[0], inv[k]), __fmul_rn(p[1], inv[k]))) |
-                               uint32_t(e4m3_pair(__fmul_rn(p[2], inv[k]), __fmul_rn(p[3], inv[k]))) << 16;
-                    }
-                    __stcs(reinterpret_cast<uint2*>(y + c), make_uint2(w[0], w[1]));
-                }
+            for (int i = 0; i < 2; ++i) {
+                const float* p = s + 8 * k + 4 * i;
+                w[i] = uint32_t(e4m3_pair(__fmul_rn(p[0], inv[k]), __fmul_rn(p[1], inv[k]))) |
+                       uint32_t(e4m3_pair(__fmul_rn(p[2], inv[k]), __fmul_rn(p[3], inv[k]))) << 16;
             }
-        } else {
-#pragma unroll
-            for (int m = 0; m < 8 * K; ++m) {
-                const uint32_t c = j + m * nt;
-                if (c < H) {
-                    const float r = OUT == kOutFp8Row ? inv[0] : stage[c / kGroup];
-                    y[c] = uint8_t(e4m3_pair(__fmul_rn(s[m], r), 0.0f));
-                }
+            if constexpr (VEC) {
+                if (c < H) __stcs(reinterpret_cast<uint2*>(y + c), make_uint2(w[0], w[1]));
+            } else {
+                store_unaligned<1>(reinterpret_cast<char*>(y), H, c, w);
             }
         }
     }
 }
 
-// Forward: block (nt, rows); rows > 1 only with VEC and nt = 32 (a warp per
-// row, no barrier).
+// Forward: block (nt, rows); rows > 1 only with nt = 32 (a warp per row, no barrier).
 template <int DT, int K, bool VEC, int OUT>
 __global__ void __launch_bounds__(kMaxThreads, 1) fwd_kernel(const FwdArgs a) {
     pdl_enter();
-    extern __shared__ __align__(16) float stage[];
     __shared__ float shared[2][32];
     const int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= a.T) return;
     const uint32_t H = a.H, j = threadIdx.x;
     float s[8 * K], q[8 * K];
-    load_row<DT, K, VEC>(a.x + t * a.x_stride, H, s);
+    load_row<DT, K, VEC>(Input(a.x, a.x_stride, a.T, H), t, H, s);
     if (a.residual != nullptr) {
-        load_row<DT, K, VEC>(a.residual + t * a.residual_stride, H, q);
+        load_row<DT, K, VEC>(Input(a.residual, a.residual_stride, a.T, H), t, H, q);
 #pragma unroll
         for (int i = 0; i < 8 * K; ++i) s[i] = __fadd_rn(s[i], q[i]);
         store_row<DT, K, VEC>(a.total + t * int64_t(H), H, s);
     }
 #pragma unroll
     for (int i = 0; i < 8 * K; ++i) q[i] = __fmul_rn(s[i], s[i]);
-    const float sum = row_sum<K, VEC>(q, stage, shared[0]);
+    const float sum = row_sum<K>(q, shared[0]);
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(H)), a.eps)));
     if (j == 0) a.rstd[t] = rstd;
     load_weight<K, VEC>(a.weight, H, q);
 #pragma unroll
     for (int i = 0; i < 8 * K; ++i) s[i] = __fmul_rn(__fmul_rn(s[i], rstd), q[i]);
-    store_y<DT, K, VEC, OUT>(a, t, s, stage, shared[1]);
+    store_y<DT, K, VEC, OUT>(a, t, s, shared[1]);
 }
 
-template <int K, bool VEC>
-__device__ __forceinline__ void store_partial(float* __restrict__ out, uint32_t H, const float (&acc)[8 * K]) {
-    const uint32_t nt = blockDim.x, j = threadIdx.x;
-    if constexpr (VEC) {
+// A chunk of the backward's first pass: adds g * n to acc and gives the
+// chunk's part of the sum of u * n.
+template <int DT>
+__device__ __forceinline__ float backward_terms(const Words<4>& g, const Words<4>& s, float rstd, const float* w, float* acc) {
+    float gv[8], nv[8], q[8];
+    chunk_values<DT>(g, gv);
+    chunk_values<DT>(s, nv);
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const uint32_t c = 8 * (j + k * nt);
+    for (int i = 0; i < 8; ++i) {
+        nv[i] = __fmul_rn(nv[i], rstd);
+        acc[i] = __fadd_rn(acc[i], __fmul_rn(gv[i], nv[i]));
+        q[i] = __fmul_rn(__fmul_rn(gv[i], w[i]), nv[i]);
+    }
+    return chunk_sum(q);
+}
+
+// And of the second: grad_x.
+template <int DT>
+__device__ __forceinline__ void backward_values(const Words<4>& g, const Words<4>& s, const Words<4>& more, bool with_more,
+                                                float rstd, float m, const float* w, float* v) {
+    float gv[8], nv[8];
+    chunk_values<DT>(g, gv);
+    chunk_values<DT>(s, nv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = __fmul_rn(rstd, __fsub_rn(__fmul_rn(gv[i], w[i]), __fmul_rn(__fmul_rn(nv[i], rstd), m)));
+    if (with_more) {
+        float tv[8];
+        chunk_values<DT>(more, tv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(v[i], tv[i]);
+    }
+}
+
+// A block's sums of grad_weight: to its row of the workspace, whose rows are
+// of whole chunks, or (`last`: the only block) to grad_weight itself.
+template <int K, bool VEC>
+__device__ __forceinline__ void store_partial(float* __restrict__ out, uint32_t H, bool last, const float (&acc)[8 * K]) {
+    const uint32_t nt = blockDim.x, j = threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const uint32_t c = 8 * (j + k * nt);
+        if (VEC || !last) {
             if (c < H) {
                 float4* p = reinterpret_cast<float4*>(out + c);
                 p[0] = make_float4(acc[8 * k], acc[8 * k + 1], acc[8 * k + 2], acc[8 * k + 3]);
                 p[1] = make_float4(acc[8 * k + 4], acc[8 * k + 5], acc[8 * k + 6], acc[8 * k + 7]);
             }
-        }
-    } else {
+        } else {
 #pragma unroll
-        for (int m = 0; m < 8 * K; ++m) {
-            const uint32_t c = j + m * nt;
-            if (c < H) out[c] = acc[m];
+            for (int i = 0; i < 8; ++i)
+                if (c + i < H) out[c + i] = acc[8 * k + i];
         }
     }
 }
 
 // Backward: block b takes rows b * rows + y, then steps of gridDim.x * rows
-// (rows = blockDim.y > 1 only with VEC and nt = 32), writes their grad_x and
-// leaves the sum of their g * n in partial[b]; the rows of one (b, y) are
-// added in increasing order, then the y in increasing order.
+// (rows = blockDim.y > 1 only with nt = 32), writes their grad_x and leaves
+// the sum of their g * n in partial[b]; the rows of one (b, y) are added in
+// increasing order, then the y in increasing order.
 template <int DT, int K, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads, 1) bwd_kernel(const BwdArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float stage[];
     __shared__ float shared[2][32];
-    const uint32_t H = a.H, nt = blockDim.x, j = threadIdx.x, rows = blockDim.y;
+    const uint32_t H = a.H, j = threadIdx.x, rows = blockDim.y;
     const int64_t step = int64_t(gridDim.x) * rows;
+    const Input in_s(a.s, a.s_stride, a.T, H), in_g(a.g, a.g_stride, a.T, H), in_t(a.grad_total, H, a.T, H);
     float acc[8 * K];
 #pragma unroll
     for (int i = 0; i < 8 * K; ++i) acc[i] = 0.0f;
     int turn = 0;
     for (int64_t t = int64_t(blockIdx.x) * rows + threadIdx.y; t < a.T; t += step, turn ^= 1) {
-        float g[8 * K], n[8 * K], q[8 * K];
-        load_row<DT, K, VEC>(a.s + t * a.s_stride, H, n);
-        load_row<DT, K, VEC>(a.g + t * a.g_stride, H, g);
+        Words<4> g[K], n[K], more[K];
+        load_words<K, VEC>(in_s, t, H, n);
+        load_words<K, VEC>(in_g, t, H, g);
+        if (a.grad_total != nullptr) load_words<K, VEC>(in_t, t, H, more);
         const float rstd = __ldg(a.rstd + t);
-        load_weight<K, VEC>(a.weight, H, q);
+        float w[8 * K], sum = 0.0f;
+        load_weight<K, VEC>(a.weight, H, w);
 #pragma unroll
-        for (int i = 0; i < 8 * K; ++i) {
-            n[i] = __fmul_rn(n[i], rstd);
-            acc[i] = __fadd_rn(acc[i], __fmul_rn(g[i], n[i]));
-            g[i] = __fmul_rn(g[i], q[i]);
-            q[i] = __fmul_rn(g[i], n[i]);
-        }
-        const float m = __fdiv_rn(row_sum<K, VEC>(q, stage, shared[turn]), float(H));
+        for (int k = 0; k < K; ++k) sum = __fadd_rn(sum, backward_terms<DT>(g[k], n[k], rstd, w + 8 * k, acc + 8 * k));
+        const float m = __fdiv_rn(fold(sum, shared[turn], Add()), float(H));
+        float v[8 * K];
 #pragma unroll
-        for (int i = 0; i < 8 * K; ++i) g[i] = __fmul_rn(rstd, __fsub_rn(g[i], __fmul_rn(n[i], m)));
-        if (a.grad_total != nullptr) {
-            load_row<DT, K, VEC>(a.grad_total + t * int64_t(H), H, q);
-#pragma unroll
-            for (int i = 0; i < 8 * K; ++i) g[i] = __fadd_rn(g[i], q[i]);
-        }
-        store_row<DT, K, VEC>(a.grad_x + t * int64_t(H), H, g);
+        for (int k = 0; k < K; ++k) backward_values<DT>(g[k], n[k], more[k], a.grad_total != nullptr, rstd, m, w + 8 * k, v + 8 * k);
+        store_row<DT, K, VEC>(a.grad_x + t * int64_t(H), H, v);
     }
     if (rows > 1) {   // the warps of a block one after the other, in shared memory
         for (uint32_t y = 0; y < rows; ++y) {
@@ -396,7 +493,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) bwd_kernel(const BwdArgs a) {
 #pragma unroll
         for (int i = 0; i < 8 * K; ++i) acc[i] = stage[j + i * 32];
     }
-    store_partial<K, VEC>(a.partial + int64_t(blockIdx.x) * H, H, acc);
+    store_partial<K, VEC>(a.partial + int64_t(blockIdx.x) * a.pitch, H, gridDim.x == 1, acc);
 }
 
 // The ring of a block: kept rows of `arrays` buffers, bulk-copied by thread 0.
@@ -429,12 +526,6 @@ __device__ __forceinline__ void stage_words(const char* row, uint32_t H, Words<4
         const uint4 v = c < H ? *reinterpret_cast<const uint4*>(row + 2 * c) : make_uint4(0, 0, 0, 0);
         w[k].w[0] = v.x, w[k].w[1] = v.y, w[k].w[2] = v.z, w[k].w[3] = v.w;
     }
-}
-
-template <int DT>
-__device__ __forceinline__ void chunk_values(const Words<4>& w, float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = Elem<DT>::lo(w.w[i]), v[2 * i + 1] = Elem<DT>::hi(w.w[i]);
 }
 
 constexpr uint32_t kRingStages = 4;   // at most
@@ -506,7 +597,7 @@ fwd_ring_kernel(const FwdArgs a, const RingRows r, uint32_t stages) {
         if (j == 0) a.rstd[t] = rstd;
 #pragma unroll
         for (int i = 0; i < 8 * K; ++i) s[i] = __fmul_rn(__fmul_rn(s[i], rstd), w[i]);
-        store_y<DT, K, true, OUT>(a, t, s, nullptr, shared[turn][1]);
+        store_y<DT, K, true, OUT>(a, t, s, shared[turn][1]);
     }
     if (j == 0 && late) ring_late(full, issued, stages, a.timeouts);
 }
@@ -547,18 +638,7 @@ bwd_ring_kernel(const BwdArgs a, const RingRows r, uint32_t stages) {
         if (r.arrays > 2) stage_words<DT, K>(row + 2 * bytes, H, more);
         float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float gv[8], nv[8], q[8];
-            chunk_values<DT>(g[k], gv);
-            chunk_values<DT>(n[k], nv);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                nv[i] = __fmul_rn(nv[i], rstd);
-                acc[8 * k + i] = __fadd_rn(acc[8 * k + i], __fmul_rn(gv[i], nv[i]));
-                q[i] = __fmul_rn(__fmul_rn(gv[i], w[8 * k + i]), nv[i]);
-            }
-            sum = __fadd_rn(sum, chunk_sum(q));
-        }
+        for (int k = 0; k < K; ++k) sum = __fadd_rn(sum, backward_terms<DT>(g[k], n[k], rstd, w + 8 * k, acc + 8 * k));
         const float m = __fdiv_rn(fold(sum, shared[turn], Add()), float(H));
         if (j == 0 && t + stages * step < a.T && !late) {
             fence_proxy_async_shared();
@@ -566,46 +646,29 @@ bwd_ring_kernel(const BwdArgs a, const RingRows r, uint32_t stages) {
             ++issued;
         }
         if (++stage == stages) stage = 0, parity ^= 1;
+        float v[8 * K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const uint32_t c = 8 * (j + k * blockDim.x);
-            if (c < H) {
-                float gv[8], nv[8], tv[8];
-                chunk_values<DT>(g[k], gv);
-                chunk_values<DT>(n[k], nv);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    gv[i] = __fmul_rn(rstd, __fsub_rn(__fmul_rn(gv[i], w[8 * k + i]), __fmul_rn(__fmul_rn(nv[i], rstd), m)));
-                if (r.arrays > 2) {
-                    chunk_values<DT>(more[k], tv);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) gv[i] = __fadd_rn(gv[i], tv[i]);
-                }
-                Words<4> o;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o.w[i] = Elem<DT>::pack(gv[2 * i], gv[2 * i + 1]);
-                st_stream<4>(a.grad_x + t * int64_t(H) + c, o);
-            }
-        }
+        for (int k = 0; k < K; ++k) backward_values<DT>(g[k], n[k], more[k], r.arrays > 2, rstd, m, w + 8 * k, v + 8 * k);
+        store_row<DT, K, true>(a.grad_x + t * int64_t(H), H, v);
     }
-    store_partial<K, true>(a.partial + int64_t(blockIdx.x) * H, H, acc);
+    store_partial<K, true>(a.partial + int64_t(blockIdx.x) * a.pitch, H, false, acc);
     if (j == 0 && late) ring_late(full, issued, stages, a.timeouts);
 }
 
-// Column sums of partial [P,H]: block (32, 32); thread (x, y) adds the rows
+// Column sums of partial [P,H] (row pitch `pitch`): block (32, 32); thread (x, y) adds the rows
 // y, y + 32, ... of column x in increasing order, then the 32 sums in
 // increasing order.  Also the bias gradient's last step.
 constexpr int kColRows = 32;
 
 static __global__ void __launch_bounds__(32 * kColRows)
-column_sum_kernel(const float* __restrict__ partial, float* __restrict__ out, uint32_t P, uint32_t H) {
+column_sum_kernel(const float* __restrict__ partial, float* __restrict__ out, uint32_t P, uint32_t H, uint32_t pitch) {
     pdl_enter();
     __shared__ float part[kColRows][32];
     const uint32_t c = blockIdx.x * 32 + threadIdx.x;
     float acc = 0.0f;
     if (c < H)
 #pragma unroll 8
-        for (uint32_t p = threadIdx.y; p < P; p += kColRows) acc = __fadd_rn(acc, partial[uint64_t(p) * H + c]);
+        for (uint32_t p = threadIdx.y; p < P; p += kColRows) acc = __fadd_rn(acc, partial[uint64_t(p) * pitch + c]);
     part[threadIdx.y][threadIdx.x] = acc;
     __syncthreads();
     if (threadIdx.y == 0 && c < H) {
