@@ -21,8 +21,7 @@
 //    aligned rows;
 //  * otherwise (odd H, strides or pointers off 16 bytes) the same chunks, each
 //    from the two aligned vectors that hold it, and to aligned vectors put
-//    together from two neighbouring lanes' chunks; the ends of a warp's run of
-//    chunks go value by value.  (Moving single values, a thread taking j, j +
+//    together from two neighbouring lanes' chunks; the row's ends go value by value.  (Moving single values, a thread taking j, j +
 //    nt, ..., and exchanging the sums' terms through shared memory: T = 20000,
 //    H = 1279 109 us, backward 113.)
 #pragma once
@@ -216,70 +215,111 @@ __device__ __forceinline__ void load_row(const Input& in, int64_t t, uint32_t H,
     }
 }
 
-// The row's chunk c (its first value), 8 values of SIZE bytes in 2 SIZE words,
-// without 16-byte alignment (4 SIZE bytes).  Every lane of the warp calls,
-// lanes in the order of their chunks.  The aligned vector that the chunk's
-// first values lie in begins with the previous lane's last `off`.
+// The values lo .. hi - 1 of the 8 that v would put at the aligned address `at`.
 template <int SIZE>
-__device__ __forceinline__ void store_unaligned(char* row, uint32_t H, uint32_t c, const uint32_t (&w)[2 * SIZE]) {
-    constexpr int N = 2 * SIZE;
-    const uint32_t lane = threadIdx.x & 31u;
-    const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(row) & (8 * SIZE - 1)) / SIZE;   // values
-    uint32_t v[2 * N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        v[i] = __shfl_up_sync(0xFFFFFFFFu, w[i], 1);
-        v[N + i] = w[i];
-    }
-    shift_bytes<N>(v, 8 * SIZE - off * SIZE);
-    const auto value = [&](int i) {   // of the lane's own chunk
-        return SIZE == 2 ? w[i / 2] >> (16 * (i & 1)) : w[i / 4] >> (8 * (i & 3));
-    };
-    const auto put = [&](int i) {
-        if constexpr (SIZE == 2) st_stream2(row + 2 * (c + i), uint16_t(value(i)));
-        else row[c + i] = char(value(i));
-    };
-    // its vector holds the values c - off .. c - off + 7
-    const bool whole = (lane > 0 || off == 0) && c + 7 < H + off;
-    if (whole) {
-        char* at = row + int64_t(c) * SIZE - int64_t(off) * SIZE;
+__device__ __forceinline__ void put_some(char* at, const uint32_t* v, uint32_t lo, uint32_t hi) {
+    for (uint32_t i = lo; i < hi; ++i) {
         if constexpr (SIZE == 2) {
-            __stcs(reinterpret_cast<uint4*>(at), make_uint4(v[0], v[1], v[2], v[3]));
+            const uint32_t x = i & 4 ? (i & 2 ? v[3] : v[2]) : (i & 2 ? v[1] : v[0]);
+            st_stream2(at + 2 * i, uint16_t(i & 1 ? x >> 16 : x));
         } else {
-            __stcs(reinterpret_cast<uint2*>(at), make_uint2(v[0], v[1]));
+            at[i] = char((i & 4 ? v[1] : v[0]) >> (8 * (i & 3)));
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < 8 - off && c + i < H) put(i);
-    }
-    // the chunk's last `off` values, where the next lane does not take them
-    if (lane == 31 || c + 8 + 7 >= H + off) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i >= 8 - off && c + i < H) put(i);
     }
 }
 
-template <int DT, int K, bool VEC>
-__device__ __forceinline__ void store_row(uint16_t* __restrict__ row, uint32_t H, const float (&v)[8 * K]) {
-    const uint32_t nt = blockDim.x, j = threadIdx.x;
+// The words of a row's last lanes' chunks, for the first lanes of the warps
+// after them: written before a barrier, read after it.
+constexpr int kEdges = kMaxThreads / 32 * 8;   // warps x chunks, at most
+
+template <int N, int K>
+__device__ __forceinline__ void publish_edges(uint4* edge, const uint32_t (&w)[K][N]) {
+    if (blockDim.x == 32 || (threadIdx.x & 31u) != 31) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        edge[k * (blockDim.x >> 5) + (threadIdx.x >> 5)] = make_uint4(w[k][0], w[k][1], N > 2 ? w[k][N - 2] : 0, N > 2 ? w[k][N - 1] : 0);
+}
+
+// A row whose chunks (8 values of SIZE bytes in N = 2 SIZE words) need not be
+// aligned.  The aligned vector that a chunk's first values lie in begins with
+// the last `off` values of the chunk before it: the previous lane's, for a
+// warp's first lane the previous warp's (edge) or its own last lane's.  A
+// vector that the row's start or end cuts is written value by value.
+template <int SIZE, int K>
+__device__ __forceinline__ void store_unaligned(char* row, uint32_t H, const uint32_t (&w)[K][2 * SIZE], const uint4* edge) {
+    constexpr int N = 2 * SIZE;
+    const uint32_t lane = threadIdx.x & 31u, warps = blockDim.x >> 5;
+    const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(row) & (8 * SIZE - 1)) / SIZE;   // values
+    char* base = row - off * SIZE;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const uint32_t c = 8 * (j + k * nt);
-        uint32_t w[4];
+        const uint32_t c = 8 * (threadIdx.x + k * blockDim.x);
+        uint32_t v[2 * N];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = Elem<DT>::pack(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
-        if constexpr (VEC) {
-            if (c < H) {
-                Words<4> o;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o.w[i] = w[i];
-                st_stream<4>(row + c, o);
+        for (int i = 0; i < N; ++i) {
+            v[i] = __shfl_up_sync(0xFFFFFFFFu, w[k][i], 1);
+            v[N + i] = w[k][i];
+            if (warps == 1 && k > 0) {
+                const uint32_t last = __shfl_sync(0xFFFFFFFFu, w[k > 0 ? k - 1 : 0][i], 31);
+                if (lane == 0) v[i] = last;
             }
-        } else {
-            store_unaligned<2>(reinterpret_cast<char*>(row), H, c, w);
         }
+        if (warps > 1 && lane == 0 && c > 0) {
+            const uint4 x = edge[k * warps + (threadIdx.x >> 5) - 1];
+            v[0] = x.x, v[1] = x.y;
+            if constexpr (N > 2) v[2] = x.z, v[3] = x.w;
+        }
+        shift_bytes<N>(v, 8 * SIZE - off * SIZE);
+        char* at = base + uint64_t(c) * SIZE;
+        if (c < H + off) {
+            const uint32_t lo = c == 0 ? off : 0, hi = min(8u, H + off - c);
+            if (hi - lo == 8) {
+                if constexpr (SIZE == 2) __stcs(reinterpret_cast<uint4*>(at), make_uint4(v[0], v[1], v[2], v[3]));
+                else __stcs(reinterpret_cast<uint2*>(at), make_uint2(v[0], v[1]));
+            } else {
+                put_some<SIZE>(at, v, lo, hi);
+            }
+        }
+    }
+    // past the last thread's last chunk
+    const uint32_t c = 8 * blockDim.x * K;
+    if (threadIdx.x + 1 == blockDim.x && c < H + off) {
+        uint32_t v[2 * N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = w[K - 1][i], v[N + i] = 0;
+        shift_bytes<N>(v, 8 * SIZE - off * SIZE);
+        put_some<SIZE>(base + uint64_t(c) * SIZE, v, 0, H + off - c);
+    }
+}
+
+template <int DT, int K>
+__device__ __forceinline__ void pack_row(const float (&v)[8 * K], uint32_t (&w)[K][4]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[k][i] = Elem<DT>::pack(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
+}
+
+template <int K>
+__device__ __forceinline__ void store_aligned(uint16_t* __restrict__ row, uint32_t H, const uint32_t (&w)[K][4]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const uint32_t c = 8 * (threadIdx.x + k * blockDim.x);
+        if (c < H) __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]));
+    }
+}
+
+// (without VEC with a barrier inside, for rows of more than one warp)
+template <int DT, int K, bool VEC>
+__device__ __forceinline__ void store_row(uint16_t* __restrict__ row, uint32_t H, const float (&v)[8 * K], uint4* edge) {
+    uint32_t w[K][4];
+    pack_row<DT, K>(v, w);
+    if constexpr (VEC) {
+        store_aligned<K>(row, H, w);
+    } else {
+        publish_edges<4, K>(edge, w);
+        if (blockDim.x > 32) __syncthreads();
+        store_unaligned<2, K>(reinterpret_cast<char*>(row), H, w, edge);
     }
 }
 
@@ -313,10 +353,10 @@ __device__ __forceinline__ float row_sum(const float (&q)[8 * K], float* shared)
 
 // The row's output from v: 16-bit values, or E4M3 values and their scales.
 template <int DT, int K, bool VEC, int OUT>
-__device__ __forceinline__ void store_y(const FwdArgs& a, int64_t t, float (&s)[8 * K], float* shared) {
+__device__ __forceinline__ void store_y(const FwdArgs& a, int64_t t, float (&s)[8 * K], float* shared, uint4* edge) {
     const uint32_t H = a.H, nt = blockDim.x, j = threadIdx.x;
     if constexpr (OUT == kOutSame) {
-        store_row<DT, K, VEC>(static_cast<uint16_t*>(a.y) + t * int64_t(H), H, s);
+        store_row<DT, K, VEC>(static_cast<uint16_t*>(a.y) + t * int64_t(H), H, s, edge);
     } else {
         uint8_t* y = static_cast<uint8_t*>(a.y) + t * int64_t(H);
         float inv[K];   // of the thread's chunks
@@ -344,50 +384,60 @@ __device__ __forceinline__ void store_y(const FwdArgs& a, int64_t t, float (&s)[
                 if ((j & 15u) == 0 && 8 * c < H) a.scale[t * groups + c / 16] = __fdiv_rn(m, kE4m3Max);
             }
         }
+        uint32_t w[K][2];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const uint32_t c = 8 * (j + k * nt);
-            uint32_t w[2];
+        for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float* p = s + 8 * k + 4 * i;
-                w[i] = uint32_t(e4m3_pair(__fmul_rn(p[0], inv[k]), __fmul_rn(p[1], inv[k]))) |
-                       uint32_t(e4m3_pair(__fmul_rn(p[2], inv[k]), __fmul_rn(p[3], inv[k]))) << 16;
+                w[k][i] = uint32_t(e4m3_pair(__fmul_rn(p[0], inv[k]), __fmul_rn(p[1], inv[k]))) |
+                          uint32_t(e4m3_pair(__fmul_rn(p[2], inv[k]), __fmul_rn(p[3], inv[k]))) << 16;
             }
-            if constexpr (VEC) {
-                if (c < H) __stcs(reinterpret_cast<uint2*>(y + c), make_uint2(w[0], w[1]));
-            } else {
-                store_unaligned<1>(reinterpret_cast<char*>(y), H, c, w);
+        if constexpr (VEC) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const uint32_t c = 8 * (j + k * nt);
+                if (c < H) __stcs(reinterpret_cast<uint2*>(y + c), make_uint2(w[k][0], w[k][1]));
             }
+        } else {
+            publish_edges<2, K>(edge, w);
+            if (nt > 32) __syncthreads();
+            store_unaligned<1, K>(reinterpret_cast<char*>(y), H, w, edge);
         }
     }
 }
 
 // Forward: block (nt, rows); rows > 1 only with nt = 32 (a warp per row, no barrier).
 template <int DT, int K, bool VEC, int OUT>
-__global__ void __launch_bounds__(kMaxThreads, 1) fwd_kernel(const FwdArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, K <= 2 ? 2 : 1) fwd_kernel(const FwdArgs a) {
     pdl_enter();
     __shared__ float shared[2][32];
+    __shared__ uint4 edge[VEC ? 1 : 2][VEC ? 1 : kEdges];
     const int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= a.T) return;
     const uint32_t H = a.H, j = threadIdx.x;
     float s[8 * K], q[8 * K];
+    uint32_t total[K][4];
     load_row<DT, K, VEC>(Input(a.x, a.x_stride, a.T, H), t, H, s);
     if (a.residual != nullptr) {
         load_row<DT, K, VEC>(Input(a.residual, a.residual_stride, a.T, H), t, H, q);
 #pragma unroll
         for (int i = 0; i < 8 * K; ++i) s[i] = __fadd_rn(s[i], q[i]);
-        store_row<DT, K, VEC>(a.total + t * int64_t(H), H, s);
+        pack_row<DT, K>(s, total);
+        if constexpr (VEC) store_aligned<K>(a.total + t * int64_t(H), H, total);
+        else publish_edges<4, K>(edge[0], total);
     }
 #pragma unroll
     for (int i = 0; i < 8 * K; ++i) q[i] = __fmul_rn(s[i], s[i]);
-    const float sum = row_sum<K>(q, shared[0]);
+    const float sum = row_sum<K>(q, shared[0]);   // (a barrier, where a row has more than one warp)
+    if constexpr (!VEC)
+        if (a.residual != nullptr) store_unaligned<2, K>(reinterpret_cast<char*>(a.total + t * int64_t(H)), H, total, edge[0]);
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(H)), a.eps)));
     if (j == 0) a.rstd[t] = rstd;
     load_weight<K, VEC>(a.weight, H, q);
 #pragma unroll
     for (int i = 0; i < 8 * K; ++i) s[i] = __fmul_rn(__fmul_rn(s[i], rstd), q[i]);
-    store_y<DT, K, VEC, OUT>(a, t, s, shared[1]);
+    store_y<DT, K, VEC, OUT>(a, t, s, shared[1], edge[VEC ? 0 : 1]);
 }
 
 // A chunk of the backward's first pass: adds g * n to acc and gives the
@@ -455,6 +505,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) bwd_kernel(const BwdArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float stage[];
     __shared__ float shared[2][32];
+    __shared__ uint4 edge[VEC ? 1 : 2][VEC ? 1 : kEdges];
     const uint32_t H = a.H, j = threadIdx.x, rows = blockDim.y;
     const int64_t step = int64_t(gridDim.x) * rows;
     const Input in_s(a.s, a.s_stride, a.T, H), in_g(a.g, a.g_stride, a.T, H), in_t(a.grad_total, H, a.T, H);
@@ -476,7 +527,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) bwd_kernel(const BwdArgs a) {
         float v[8 * K];
 #pragma unroll
         for (int k = 0; k < K; ++k) backward_values<DT>(g[k], n[k], more[k], a.grad_total != nullptr, rstd, m, w + 8 * k, v + 8 * k);
-        store_row<DT, K, VEC>(a.grad_x + t * int64_t(H), H, v);
+        store_row<DT, K, VEC>(a.grad_x + t * int64_t(H), H, v, edge[VEC ? 0 : turn]);
     }
     if (rows > 1) {   // the warps of a block one after the other, in shared memory
         for (uint32_t y = 0; y < rows; ++y) {
@@ -576,7 +627,7 @@ fwd_ring_kernel(const FwdArgs a, const RingRows r, uint32_t stages) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) s[8 * k + i] = __fadd_rn(s[8 * k + i], v[i]);
             }
-            store_row<DT, K, true>(a.total + t * int64_t(H), H, s);
+            store_row<DT, K, true>(a.total + t * int64_t(H), H, s, nullptr);
         }
         float acc = 0.0f;
 #pragma unroll
@@ -597,7 +648,7 @@ fwd_ring_kernel(const FwdArgs a, const RingRows r, uint32_t stages) {
         if (j == 0) a.rstd[t] = rstd;
 #pragma unroll
         for (int i = 0; i < 8 * K; ++i) s[i] = __fmul_rn(__fmul_rn(s[i], rstd), w[i]);
-        store_y<DT, K, true, OUT>(a, t, s, shared[turn][1]);
+        store_y<DT, K, true, OUT>(a, t, s, shared[turn][1], nullptr);
     }
     if (j == 0 && late) ring_late(full, issued, stages, a.timeouts);
 }
@@ -649,7 +700,7 @@ bwd_ring_kernel(const BwdArgs a, const RingRows r, uint32_t stages) {
         float v[8 * K];
 #pragma unroll
         for (int k = 0; k < K; ++k) backward_values<DT>(g[k], n[k], more[k], r.arrays > 2, rstd, m, w + 8 * k, v + 8 * k);
-        store_row<DT, K, true>(a.grad_x + t * int64_t(H), H, v);
+        store_row<DT, K, true>(a.grad_x + t * int64_t(H), H, v, nullptr);
     }
     store_partial<K, true>(a.partial + int64_t(blockIdx.x) * a.pitch, H, false, acc);
     if (j == 0 && late) ring_late(full, issued, stages, a.timeouts);
