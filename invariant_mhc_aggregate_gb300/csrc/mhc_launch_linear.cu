@@ -68,11 +68,18 @@ cudaError_t encode(CUtensorMap* map, const void* base, int64_t rows, int64_t len
 // tile, next to the barriers and the 1024 bytes of alignment in the 227 KB.
 constexpr uint32_t kRingBytes = 224 * 1024;
 
-// Parts of K: as many (1, 2, 4 or 8) as the GPU's 152 SMs can take at once
-// when the call has `tiles` tiles of 128 lanes, with at least 8 blocks of K a part.
+// Clusters of 1, 2, 4 and 8 CTAs (one an SM) that GB300 runs at once: its
+// SMs come in groups that a cluster does not cross.
+constexpr int64_t kClustersAtOnce[4] = {152, 76, 36, 15};
+
+// Parts of K: as many (1, 2, 4 or 8) as run at once when the call has `tiles`
+// tiles of 128 lanes, with at least 8 blocks of K a part.  Joining parts takes
+// about 1.9 us, as long as 10 blocks: fewer than 24 blocks stay in one part.
+// Returns the logarithm.
 uint32_t splits_of(int64_t tiles, int64_t kb) {
-    uint32_t s = 1;
-    while (s < 8 && tiles * s * 2 <= 152 && kb >= int64_t(s) * 16) s *= 2;
+    uint32_t s = 0;
+    if (kb < 24) return s;
+    while (s < 3 && tiles <= kClustersAtOnce[s + 1] && kb >= (16 << s)) ++s;
     return s;
 }
 
@@ -99,12 +106,21 @@ cudaError_t launch_tiles(Kernel kernel, std::atomic<uint64_t>& allowed, dim3 gri
     return cudaLaunchKernelEx(&cfg, kernel, mp, mq, a);
 }
 
+// The ring's stages.  Two blocks of K a stage halve the waits and signals of
+// a block, which take longer than the multiplications of narrow tiles (M = 512
+// at 4096 x 4096 32.4 -> 20.8 us, one row at 7168 x 7168 21.7 -> 19.6), where
+// three such stages fit: all but split_kernel's widest tiles.
+void set_ring(TileArgs& a, uint32_t block_bytes) {
+    a.block_bytes = block_bytes;
+    a.unit = kRingBytes / (2 * block_bytes) >= 3 ? 2 : 1;
+    a.stage_bytes = a.unit * block_bytes;
+    a.stages = kRingBytes / a.stage_bytes < kMaxStages ? kRingBytes / a.stage_bytes : kMaxStages;
+}
+
 template <bool FP8, int OUT, int LAYOUT>
 cudaError_t launch_split(TileArgs a, CUtensorMap& mp, CUtensorMap& mq, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    a.stage_bytes = kBytesP + a.width * 128;
-    const uint32_t budget = kRingBytes;
-    a.stages = budget / a.stage_bytes < kMaxStages ? budget / a.stage_bytes : kMaxStages;
+    set_ring(a, kBytesP + a.width * 128);
     const uint32_t parts = a.splits > 1 ? a.width * kLanesP * 4 : 0;
     const uint32_t ring = a.stages * a.stage_bytes;
     return launch_tiles(split_kernel<FP8, OUT, LAYOUT>, allowed, dim3(a.p_tiles * a.splits, a.q_tiles), kSplitThreads,
@@ -113,9 +129,7 @@ cudaError_t launch_split(TileArgs a, CUtensorMap& mp, CUtensorMap& mq, cudaStrea
 
 template <bool FP8, int OUT, int LAYOUT>
 cudaError_t launch_pair(TileArgs a, CUtensorMap& mp, CUtensorMap& mq, cudaStream_t stream) {
-    a.stage_bytes = kBytesP + a.width / 2 * 128;
-    const uint32_t budget = kRingBytes;
-    a.stages = budget / a.stage_bytes < kMaxStages ? budget / a.stage_bytes : kMaxStages;
+    set_ring(a, kBytesP + a.width / 2 * 128);
     const uint32_t tiles = a.p_tiles * a.q_tiles, pairs = uint32_t(num_sms()) / 2;
     const dim3 grid(2 * (tiles < pairs ? tiles : pairs));
     const uint32_t smem = a.stages * a.stage_bytes + 1024;
@@ -146,39 +160,40 @@ struct Plan {
     uint32_t width, splits;
 };
 
-// The cheapest plan by an estimate in SM cycles, from runs of M = 32 .. 4096
-// rows at (N, K) = (7168, 7168), (14336, 4096), (4096, 4096), (4096, 1280),
-// (2048, 2048), (1024, 1024), (1024, 7168), (520, 2048), which it orders as the
-// measurement does where the kernels differ by more than a tenth:
-//  * split_kernel: each round of its CTAs over the SMs takes 9000 + 32 width
-//    for its start and its epilogue, and 350 + 1.5 width a block of K;
-//  * pair_kernel: 10000 + 8 width once, each round max(400, 2.1 width) a block
+// The cheapest plan by an estimate in SM cycles, fitted to runs of M = 16 ..
+// 2048 rows at (N, K) = (7168, 7168), (14336, 4096), (4096, 4096), (4096, 1280),
+// (2048, 2048), (1024, 1024), (1024, 7168), (520, 2048), (640, 512):
+//  * split_kernel: each round of the clusters that run at once takes 4500 + 24
+//    width for its start and epilogue, 3600 to join parts, and 260 + width a
+//    block of K;
+//  * pair_kernel: 6000 + 21 width once, each round max(300, 2.05 width) a block
 //    of K and 1500 a part.
-// For instance M = 256 at 4096 x 4096: split 15.5 us, pairs 21.6; M = 512: 29.9
-// and 22.2; M = 1024 at 7168 x 7168: pairs of width 224 65.5 us, 256 71.0, split
-// 92.3.
+// For instance M = 256 at 4096 x 4096: split 16.0 us, pairs 20.2; M = 512: 31.1
+// and 20.8; M = 1024 at 1024 x 1024: split 6.2 us in tiles of 64 rows, 10.1 in
+// tiles of 256, pairs 7.3; M = 2048 at 7168 x 7168: pairs of width 256 115.7 us,
+// 128 138.8, split 188.
 Plan plan_of(int64_t N, int64_t M, int64_t kb, bool q_mn, bool by_row) {
     const int64_t sms = num_sms(), p128 = (N + 127) / 128, p256 = (N + 255) / 256;
     Plan best = {false, 256, 1};
     int64_t least = INT64_MAX;
     // where a row's sum must not depend on how many rows the call has, the parts
     // follow from N and K alone: those of a call with few rows
-    const uint32_t row_parts = splits_of(p128, kb);
+    const uint32_t row_log = splits_of(p128, kb);
     const int64_t step = q_mn ? 64 : 16, q0 = (M + 255) / 256;
     for (int64_t q = q0; q <= 8 * q0 && q <= 65535; q *= 2) {   // (its grid's second dimension)
         const int64_t w = ((M + q - 1) / q + step - 1) / step * step;
         const int64_t tiles = p128 * ((M + w - 1) / w);
-        const uint32_t parts = by_row ? row_parts : splits_of(tiles, kb);
-        const int64_t rounds = (tiles * parts + sms - 1) / sms;
-        const int64_t cost = rounds * (9000 + 32 * w + (kb + parts - 1) / parts * (350 + 3 * w / 2));
+        const uint32_t log = by_row ? row_log : splits_of(tiles, kb), parts = 1u << log;
+        const int64_t rounds = (tiles + kClustersAtOnce[log] - 1) / kClustersAtOnce[log];
+        const int64_t cost = rounds * (4500 + 24 * w + (parts > 1 ? 3600 : 0) + (kb + parts - 1) / parts * (260 + w));
         if (cost < least) least = cost, best = {false, uint32_t(w), parts};
         if (w <= 32) break;
     }
-    const uint32_t parts = by_row ? row_parts : 1;
+    const uint32_t parts = by_row ? 1u << row_log : 1;
     for (int64_t w = 128; w <= 256; w += q_mn ? 128 : 32) {
         const int64_t rounds = (p256 * ((M + w - 1) / w) + sms / 2 - 1) / (sms / 2);
-        const int64_t block = 21 * w / 10 > 400 ? 21 * w / 10 : 400;
-        const int64_t cost = 10000 + 8 * w + rounds * (kb * block + (parts > 1 ? 1500 * parts : 0));
+        const int64_t block = 41 * w / 20 > 300 ? 41 * w / 20 : 300;
+        const int64_t cost = 6000 + 21 * w + rounds * (kb * block + (parts > 1 ? 1500 * parts : 0));
         if (cost < least) least = cost, best = {true, uint32_t(w), parts};
     }
     return best;

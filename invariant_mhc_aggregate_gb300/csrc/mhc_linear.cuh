@@ -90,6 +90,7 @@ struct TileArgs {
     uint32_t splits;         // of K; split s takes the blocks [s kb / splits, (s + 1) kb / splits)
     uint32_t width;          // output rows of a tile
     uint32_t stages, stage_bytes;
+    uint32_t unit, block_bytes;   // blocks of K of a stage, and bytes of each
     uint32_t idesc;
     uint32_t p_tiles, q_tiles;
     unsigned int* timeouts;
@@ -293,37 +294,43 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     const float bias = a.e.bias != nullptr && n_ok ? __ldg(a.e.bias + n) : 0.0f;
     const float cs = a.e.col_scale != nullptr && n_ok ? __ldg(a.e.col_scale + n) : 1.0f;
     const uint32_t ring = smem_addr(stages), bar_full = smem_addr(full), bar_empty = smem_addr(empty);
-    const uint32_t count = a.stages, bytes = a.stage_bytes;
+    const uint32_t count = a.stages, bytes = a.stage_bytes, unit = a.unit;
     if (warp == kSplitCopy) {
         umma::Ring at;
         bool ok = true;
-        uint32_t k = k0;
-        for (; k < k1; ++k, at.next(count)) {
+        uint32_t k = k0, issued = 0;
+        for (; k < k1; k += unit, ++issued, at.next(count)) {
             // (the first round finds every stage free: the phase before a new barrier's first one)
             if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
+            const uint32_t n = min(unit, k1 - k);
             if (umma::elect()) {
-                umma::expect_tx(bar_full + 8 * at.stage, bytes);
-                load_p<1, FP8, LAYOUT>(ring + at.stage * bytes, &mp, k, int(n0), bar_full + 8 * at.stage);
-                load_q<1, FP8, LAYOUT>(ring + at.stage * bytes, &mq, k, int(m0), a.width, bar_full + 8 * at.stage);
+                umma::expect_tx(bar_full + 8 * at.stage, n * a.block_bytes);
+                for (uint32_t u = 0; u < n; ++u) {
+                    const uint32_t to = ring + at.stage * bytes + u * a.block_bytes;
+                    load_p<1, FP8, LAYOUT>(to, &mp, k + u, int(n0), bar_full + 8 * at.stage);
+                    load_q<1, FP8, LAYOUT>(to, &mq, k + u, int(m0), a.width, bar_full + 8 * at.stage);
+                }
             }
             __syncwarp();
         }
-        drain(ok, min(k - k0, count), at, count, bar_empty, bar_full);
+        drain(ok, min(issued, count), at, count, bar_empty, bar_full);
         if (!ok) timed_out(a);
     } else if (warp == kSplitMultiply) {
         const Descs d = descs<LAYOUT>(ring);
         const uint32_t idesc = a.idesc;
         umma::Ring at;
-        for (uint32_t k = k0; k < k1; ++k, at.next(count)) {
+        for (uint32_t k = k0; k < k1; k += unit, at.next(count)) {
             if (!umma::wait(bar_full + 8 * at.stage, at.parity)) {
                 timed_out(a);
                 break;
             }
             umma::fence_after_sync();
+            const uint32_t n = min(unit, k1 - k);
             if (umma::elect()) {
-                multiply_block<1, FP8, LAYOUT>(d, at.stage * bytes, idesc, tmem, k == k0);
+                for (uint32_t u = 0; u < n; ++u)
+                    multiply_block<1, FP8, LAYOUT>(d, at.stage * bytes + u * a.block_bytes, idesc, tmem, k + u == k0);
                 umma::commit<1>(bar_empty + 8 * at.stage);
-                if (k + 1 == k1) umma::commit<1>(smem_addr(&done));
+                if (k + n == k1) umma::commit<1>(smem_addr(&done));
             }
             __syncwarp();
         }
@@ -466,7 +473,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
     pdl_enter();
     const uint32_t ring = smem_addr(stages), bar_full = smem_addr(full), bar_empty = smem_addr(empty);
     const uint32_t bar_sum = smem_addr(sum_full), bar_free = smem_addr(sum_empty);
-    const uint32_t count = a.stages, bytes = a.stage_bytes, kb = a.kb;
+    const uint32_t count = a.stages, bytes = a.stage_bytes, unit = a.unit;
     if (warp == kCopyP || warp == kCopyQ) {
         // both CTAs' copies count on the first one's barrier; its phase cannot end
         // before that CTA's arrival, whichever copy lands first
@@ -478,17 +485,22 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             uint32_t pt, qt;
             tile_at(a, i, pt, qt);
             const int p0 = int(pt * 2 * kLanesP + rank * kLanesP), q0 = int(qt * a.width + rank * half);
-            for (uint32_t k = 0; k < kb; ++k, ++issued, at.next(count)) {
-                if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
-                if (umma::elect()) {
-                    if (warp == kCopyP) {
-                        if (rank == 0) umma::expect_tx(bar_full + 8 * at.stage, 2 * bytes);
-                        load_p<2, FP8, LAYOUT>(ring + at.stage * bytes, &mp, k, p0, bar_pair + 8 * at.stage);
-                    } else {
-                        load_q<2, FP8, LAYOUT>(ring + at.stage * bytes, &mq, k, q0, half, bar_pair + 8 * at.stage);
+            uint32_t k = 0;
+            for (uint32_t part = 0; part < a.splits && ok; ++part) {
+                for (const uint32_t k1 = split_begin(a, part + 1); k < k1; ++issued, at.next(count)) {
+                    if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
+                    const uint32_t n = min(unit, k1 - k);
+                    if (umma::elect()) {
+                        if (warp == kCopyP && rank == 0) umma::expect_tx(bar_full + 8 * at.stage, 2 * n * a.block_bytes);
+                        for (uint32_t u = 0; u < n; ++u) {
+                            const uint32_t to = ring + at.stage * bytes + u * a.block_bytes;
+                            if (warp == kCopyP) load_p<2, FP8, LAYOUT>(to, &mp, k + u, p0, bar_pair + 8 * at.stage);
+                            else load_q<2, FP8, LAYOUT>(to, &mq, k + u, q0, half, bar_pair + 8 * at.stage);
+                        }
                     }
+                    __syncwarp();
+                    k += n;
                 }
-                __syncwarp();
             }
         }
         drain(ok, min(issued, count), at, count, bar_empty, rank == 0 ? bar_full : bar_empty);
@@ -507,15 +519,18 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                     if (!(ok = umma::wait(bar_free + 8 * b, sums.parity(b) ^ 1))) break;
                     umma::fence_after_sync();
                     const uint32_t to = tmem + b * 256, k0 = k, k1 = split_begin(a, part + 1);
-                    for (; k < k1; ++k, at.next(count)) {
+                    for (; k < k1; at.next(count)) {
                         if (!(ok = umma::wait(bar_full + 8 * at.stage, at.parity))) break;
                         umma::fence_after_sync();
+                        const uint32_t n = min(unit, k1 - k);
                         if (umma::elect()) {
-                            multiply_block<2, FP8, LAYOUT>(d, at.stage * bytes, idesc, to, k == k0);
+                            for (uint32_t u = 0; u < n; ++u)
+                                multiply_block<2, FP8, LAYOUT>(d, at.stage * bytes + u * a.block_bytes, idesc, to, k + u == k0);
                             umma::commit<2>(bar_empty + 8 * at.stage);
-                            if (k + 1 == k1) umma::commit<2>(bar_sum + 8 * b);
+                            if (k + n == k1) umma::commit<2>(bar_sum + 8 * b);
                         }
                         __syncwarp();
+                        k += n;
                     }
                 }
             }
