@@ -9,8 +9,8 @@
 // 8 values; thread j of the row's nt threads owns chunks j, j + nt, ... (at
 // most K of them), sums each as the pairwise tree ((0+1)+(2+3))+((4+5)+(6+7))
 // and adds the chunks in increasing order; a warp folds by exchanging with
-// lanes at distance 16, 8, 4, 2, 1; the warps' results are added in
-// increasing order.  nt and K follow from H (shape_of).
+// lanes at distance 16, 8, 4, 2, 1; the warps' results are added pairwise
+// (0+1)+(2+3), ....  nt and K follow from H (shape_of).
 //
 // Three ways to move a row, with the same sums:
 //  * ring: rows of 16-byte aligned values (H % 8 == 0) longer than a warp
@@ -89,19 +89,38 @@ __device__ __forceinline__ float chunk_sum(const float* q) {
 }
 
 // Folds one value per thread over the row's threads (a warp, or the block):
-// every thread gets the result.  `shared` holds 32 floats and is free again
-// after the caller's next barrier.
+// every thread gets the result.  `shared` is free again after the caller's
+// next barrier; the warps' results meet in a pairwise tree, read four at a
+// time (one after the other they took 35 cycles each).
+constexpr int kMaxWarps = kMaxThreads / 32;
+
+struct Fold {
+    float4 v[kMaxWarps / 4];
+};
+
+// The places of warps that the row does not have hold zeros, which change no
+// sum and no maximum of magnitudes.  Before the first fold, with a barrier
+// between or the fold's own.
+__device__ __forceinline__ void clear_fold(Fold* f, int count) {
+    if (blockDim.x > 32)
+        for (int i = threadIdx.x; i < count * kMaxWarps; i += blockDim.x)
+            if (i % kMaxWarps >= int(blockDim.x >> 5)) reinterpret_cast<float*>(f)[i] = 0.0f;
+}
+
 template <class Op>
-__device__ __forceinline__ float fold(float v, float* shared, Op op) {
+__device__ __forceinline__ float fold(float v, Fold& shared, Op op) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) v = op(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
-    const uint32_t warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    if ((threadIdx.x & 31u) == 0) shared[threadIdx.x >> 5] = v;
+    if (blockDim.x == 32) return v;
+    if ((threadIdx.x & 31u) == 0) reinterpret_cast<float*>(&shared)[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = shared[0];
-    for (uint32_t i = 1; i < warps; ++i) v = op(v, shared[i]);
-    return v;
+    float t[kMaxWarps / 4];
+#pragma unroll
+    for (int i = 0; i < kMaxWarps / 4; ++i) {
+        const float4 x = shared.v[i];
+        t[i] = op(op(x.x, x.y), op(x.z, x.w));
+    }
+    return op(op(t[0], t[1]), op(t[2], t[3]));
 }
 
 struct Add {
@@ -111,7 +130,10 @@ struct Max {
     __device__ float operator()(float a, float b) const { return max_nan(a, b); }
 };
 
-// The bytes `shift` .. shift + 4 N - 1 of the 8 N bytes in w, to its first N words.
+// The bytes `shift` .. shift + 4 N - 1 (shift at most 4 N) of the 8 N bytes in
+// w, to its first N words: by words with selects (a branch on the words, the
+// same for the whole row, kept the loads of a row's chunks from going out
+// together: T = 20000, H = 1279 61 -> 82 us), then by the rest.
 template <int N>
 __device__ __forceinline__ void shift_bytes(uint32_t (&w)[2 * N], uint32_t shift) {
     const uint32_t words = shift / 4;
@@ -157,11 +179,12 @@ __device__ __forceinline__ void load_words(const Input& in, int64_t t, uint32_t 
         const uint32_t shift = uint32_t(reinterpret_cast<uintptr_t>(row) & 15u);
         const char* base = reinterpret_cast<const char*>(row) - shift;
         uint32_t v[K][8];
+        const bool inside = base >= in.lo && base + 2 * uint64_t(H) + 32 <= in.hi;   // with every vector of the row
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const uint32_t c = 8 * (j + k * nt);
             const char* q = base + 2 * c;
-            if (c < H && q >= in.lo && q + 32 <= in.hi) {
+            if (c < H && (inside || (q >= in.lo && q + 32 <= in.hi))) {
                 const uint4 x = __ldg(reinterpret_cast<const uint4*>(q)), y = __ldg(reinterpret_cast<const uint4*>(q) + 1);
                 v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
                 v[k][4] = y.x, v[k][5] = y.y, v[k][6] = y.z, v[k][7] = y.w;
@@ -188,9 +211,11 @@ __device__ __forceinline__ void load_words(const Input& in, int64_t t, uint32_t 
             shift_bytes<4>(v[k], shift);
             const uint32_t c = 8 * (j + k * nt);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (c + 2 * i + 1 >= H) v[k][i] &= c + 2 * i >= H ? 0u : 0xFFFFu;
-                w[k].w[i] = v[k][i];
+            for (int i = 0; i < 4; ++i) w[k].w[i] = v[k][i];
+            if (c < H && c + 8 > H) {   // the row's last chunk
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (c + 2 * i + 1 >= H) w[k].w[i] &= c + 2 * i >= H ? 0u : 0xFFFFu;
             }
         }
     }
@@ -344,7 +369,7 @@ __device__ __forceinline__ void load_weight(const float* __restrict__ w, uint32_
 
 // The row's sum of q in the order stated above.
 template <int K>
-__device__ __forceinline__ float row_sum(const float (&q)[8 * K], float* shared) {
+__device__ __forceinline__ float row_sum(const float (&q)[8 * K], Fold& shared) {
     float acc = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) acc = __fadd_rn(acc, chunk_sum(q + 8 * k));
@@ -353,7 +378,7 @@ __device__ __forceinline__ float row_sum(const float (&q)[8 * K], float* shared)
 
 // The row's output from v: 16-bit values, or E4M3 values and their scales.
 template <int DT, int K, bool VEC, int OUT>
-__device__ __forceinline__ void store_y(const FwdArgs& a, int64_t t, float (&s)[8 * K], float* shared, uint4* edge) {
+__device__ __forceinline__ void store_y(const FwdArgs& a, int64_t t, float (&s)[8 * K], Fold& shared, uint4* edge) {
     const uint32_t H = a.H, nt = blockDim.x, j = threadIdx.x;
     if constexpr (OUT == kOutSame) {
         store_row<DT, K, VEC>(static_cast<uint16_t*>(a.y) + t * int64_t(H), H, s, edge);
@@ -411,10 +436,11 @@ __device__ __forceinline__ void store_y(const FwdArgs& a, int64_t t, float (&s)[
 template <int DT, int K, bool VEC, int OUT>
 __global__ void __launch_bounds__(kMaxThreads, K <= 2 ? 2 : 1) fwd_kernel(const FwdArgs a) {
     pdl_enter();
-    __shared__ float shared[2][32];
+    __shared__ Fold shared[2];
     __shared__ uint4 edge[VEC ? 1 : 2][VEC ? 1 : kEdges];
     const int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
     if (t >= a.T) return;
+    clear_fold(shared, 2);
     const uint32_t H = a.H, j = threadIdx.x;
     float s[8 * K], q[8 * K];
     uint32_t total[K][4];
@@ -504,9 +530,10 @@ template <int DT, int K, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads, 1) bwd_kernel(const BwdArgs a) {
     pdl_enter();
     extern __shared__ __align__(16) float stage[];
-    __shared__ float shared[2][32];
+    __shared__ Fold shared[2];
     __shared__ uint4 edge[VEC ? 1 : 2][VEC ? 1 : kEdges];
     const uint32_t H = a.H, j = threadIdx.x, rows = blockDim.y;
+    clear_fold(shared, 2);
     const int64_t step = int64_t(gridDim.x) * rows;
     const Input in_s(a.s, a.s_stride, a.T, H), in_g(a.g, a.g_stride, a.T, H), in_t(a.grad_total, H, a.T, H);
     float acc[8 * K];
@@ -585,7 +612,7 @@ template <int DT, int K, int OUT, int MAXT>
 __global__ void __launch_bounds__(MAXT, K == 2 ? 2 : 1)
 fwd_ring_kernel(const FwdArgs a, const RingRows r, uint32_t stages) {
     extern __shared__ __align__(16) char ring[];
-    __shared__ float shared[2][2][32];
+    __shared__ Fold shared[2][2];
     __shared__ uint64_t full[kRingStages];
     __shared__ volatile int late;   // a wait ran out: no further copy, no further wait
     const uint32_t H = a.H, j = threadIdx.x, bytes = 2 * H;
@@ -594,6 +621,7 @@ fwd_ring_kernel(const FwdArgs a, const RingRows r, uint32_t stages) {
         mbar_init_fence();
         late = 0;
     }
+    clear_fold(shared[0], 4);
     __syncthreads();
     pdl_enter();
     const int64_t step = gridDim.x;
@@ -657,7 +685,7 @@ template <int DT, int K>
 __global__ void __launch_bounds__(kMaxThreads, 1)
 bwd_ring_kernel(const BwdArgs a, const RingRows r, uint32_t stages) {
     extern __shared__ __align__(16) char ring[];
-    __shared__ float shared[2][32];
+    __shared__ Fold shared[2];
     __shared__ uint64_t full[kRingStages];
     __shared__ volatile int late;   // a wait ran out: no further copy, no further wait
     const uint32_t H = a.H, j = threadIdx.x, bytes = 2 * H;
@@ -666,6 +694,7 @@ bwd_ring_kernel(const BwdArgs a, const RingRows r, uint32_t stages) {
         mbar_init_fence();
         late = 0;
     }
+    clear_fold(shared, 2);
     __syncthreads();
     pdl_enter();
     const int64_t step = gridDim.x;
