@@ -34,7 +34,7 @@ __device__ __forceinline__ float normal_cdf(float z) {
 // bits or fewer.
 template <int ACT>
 __device__ __forceinline__ float activation(float z) {
-    if constexpr (ACT == kActRelu) return z * (z > 0.0f ? 1.0f : 0.0f);
+    if constexpr (ACT == kActRelu) return z <= 0.0f ? 0.0f : z;   // (NaN stays)
     if constexpr (ACT == kActSilu) return __fdividef(z, 1.0f + __expf(-z));
     if constexpr (ACT == kActGelu) return z * normal_cdf(z);
     return z;

@@ -64,18 +64,8 @@ __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" : : "r"(addr), "r"(columns));
 }
 
-// 16 or 8 consecutive columns of the thread's lane (a warp reads and writes the
+// 8 consecutive columns of the thread's lane (a warp reads and writes the
 // lanes 32 * (warp % 4) ..); loaded values are valid after tmem_wait_ld.
-__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[16]) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
-}
-
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[8]) {
     uint32_t* r = reinterpret_cast<uint32_t*>(v);
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"

@@ -196,6 +196,18 @@ def _call(device, name: str, *args) -> None:
         raise LayerError(st, name)
 
 
+def _scratch(nbytes: int, device, stream):
+    """A workspace, kept from reuse until the work on a stream of the caller's is done."""
+    if not nbytes:
+        return None
+    t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        t.record_stream(stream)
+    return t
+
+
 def _ptr(t) -> int:
     return 0 if t is None else t.data_ptr()
 
@@ -270,7 +282,7 @@ def rms_norm_backward(grad_y: torch.Tensor, total: torch.Tensor, weight: torch.T
     grad_x = torch.empty((T, H), dtype=total.dtype, device=dev)
     grad_w = torch.empty(H, dtype=torch.float32, device=dev)
     need = lib.mhc_rms_norm_bwd_workspace(T, H)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    ws = _scratch(need, dev, stream)
     _call(dev, "mhc_rms_norm_bwd", grad_y.data_ptr(), total.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
           _ptr(grad_total), grad_x.data_ptr(), grad_w.data_ptr(), _ptr(ws), need, T, H, gs, ss, dt,
           _stream_handle(stream, dev))
@@ -312,7 +324,7 @@ def _linear(x, x_scale, w, w_scale, bias, activation, residual, out_dtype, keep,
     z = torch.empty((T, O), dtype=out_dtype, device=dev) if keep else None
     xp, wp = x.data_ptr(), w.data_ptr()
     need = lib.mhc_linear_workspace(T, I, O, xs, ws, 1 if fp8 else 2, 0 if (xp | wp) & 15 else 1)
-    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    work = _scratch(need, dev, stream)
     sh = _stream_handle(stream, dev)
     if fp8:
         _call(dev, "mhc_linear_fp8_fwd", xp, x_scale.data_ptr(), wp, w_scale.data_ptr(), _ptr(bias), _ptr(residual),
@@ -388,7 +400,7 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     gp, xp, wp = grad_y.data_ptr(), x.data_ptr(), weight.data_ptr()
     need = lib.mhc_linear_bwd_workspace(T, I, O, act, int(want[0]), int(want[1]), int(bias),
                                         0 if (gp | xp | wp) & 15 else 1)
-    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    work = _scratch(need, dev, stream)
     _call(dev, "mhc_linear_bwd", gp, xp, wp, _ptr(z if act else None), _ptr(grad_x), _ptr(grad_w), _ptr(grad_b),
           _ptr(work), need, T, I, O, act, dt, _stream_handle(stream, dev))
     return grad_x, grad_w, grad_b
