@@ -143,13 +143,12 @@ cudaError_t bwd_launch(BwdArgs a, Shape s, uint32_t blocks, cudaStream_t stream)
     if constexpr (VEC && (K == 2 || K == 4)) {
         const RingRows r = {{a.g, a.s, a.grad_total}, {a.g_stride, a.s_stride, int64_t(a.H)}, a.grad_total != nullptr ? 3u : 2u};
         const uint32_t row = a.H * 2 * r.arrays;
-        RingShape ring = ring_shape(row, (blocks + uint32_t(num_sms()) - 1) / uint32_t(num_sms()));
-        if (rows == 1 && ring.stages >= 2 && a.T > int64_t(blocks)) {
+        constexpr uint32_t kStages = 2;   // a third: 48.3 us against 46.0 at T = 4096, H = 7168
+        if (rows == 1 && kStages * row <= kRowSmem && a.T > int64_t(blocks)) {
             static std::atomic<uint64_t> ring_allowed{0};
             const cudaError_t e = timeouts_ptr(&a.timeouts);
             if (e != cudaSuccess) return e;
-            return launch_rows(bwd_ring_kernel<DT, K>, blocks, s.nt, 1, ring.stages * row, ring_allowed, stream, a, r,
-                               ring.stages);
+            return launch_rows(bwd_ring_kernel<DT, K>, blocks, s.nt, 1, kStages * row, ring_allowed, stream, a, r, kStages);
         }
     }
     return launch_rows(bwd_kernel<DT, K, VEC>, blocks, s.nt, rows, rows == 1 ? 0 : 8u * K * 32 * 4, allowed,
@@ -179,12 +178,15 @@ cudaError_t norm_fwd(const FwdArgs& a, int dtype, int out, cudaStream_t stream) 
 }
 
 // Blocks of the backward, each with a partial sum of grad_weight: for each of
-// 152 SMs as many as have 1024 threads (a constant, so that the sum's order
-// does not depend on the device), and no more than have rows.
+// 152 SMs as many as its registers run at once, 512 threads' worth and at most
+// four (a constant, so that the sum's order does not depend on the device), and
+// no more than have rows.  T = 4096, H = 7168: 46.0 us with one an SM, 48.2 with
+// two, 53.7 with four; T = 16384, H = 2048: 51.3 with four, 67.8 with two.
 uint32_t norm_bwd_partials(int64_t T, int64_t H) {
     const Shape s = shape_of(uint32_t(H));
-    const int64_t most = 152 * (1024 / s.nt < 8 ? 1024 / s.nt : 8);
-    const int64_t blocks = s.nt == 32 ? (T + kWarpRows - 1) / kWarpRows : T;
+    const uint32_t rows = s.nt == 32 ? kWarpRows : 1, fit = 512 / (s.nt * rows);
+    const int64_t most = 152 * (fit < 1 ? 1 : fit > 4 ? 4 : fit);
+    const int64_t blocks = (T + rows - 1) / rows;
     return uint32_t(blocks < most ? blocks : most);
 }
 
@@ -203,16 +205,11 @@ cudaError_t norm_bwd(BwdArgs a, float* grad_weight, float* workspace, int dtype,
 }
 
 cudaError_t column_sum(const float* partial, float* out, uint32_t P, int64_t H, int64_t pitch, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(uint32_t((H + 31) / 32));
-    cfg.blockDim = dim3(32, kColRows);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, column_sum_kernel, partial, out, P, uint32_t(H), uint32_t(pitch));
+    const uint32_t blocks = uint32_t((H + 31) / 32);
+    return pitch % 4 == 0 && aligned(partial, 16)
+               ? launch(column_sum_kernel<true>, blocks, 8 * kColGroups, stream, partial, out, P, uint32_t(H), uint32_t(pitch))
+               : launch(column_sum_kernel<false>, blocks, 8 * kColGroups, stream, partial, out, P, uint32_t(H),
+                        uint32_t(pitch));
 }
 
 }  // namespace layer

@@ -12,6 +12,11 @@
 // lanes at distance 16, 8, 4, 2, 1; the warps' results are added pairwise
 // (0+1)+(2+3), ....  nt and K follow from H (shape_of).
 //
+// Values are worked on in packed pairs (mhc_f32x2.cuh): half the instructions
+// of a row's chain.  No packed product is an operand of a packed sum that is
+// not written as one fused multiply-add here, so that every kernel rounds
+// alike.
+//
 // Three ways to move a row, with the same sums:
 //  * ring: rows of 16-byte aligned values (H % 8 == 0) longer than a warp
 //    holds, more of them than there are blocks: bulk copies bring a block's
@@ -28,6 +33,7 @@
 
 #include "mhc_bulk.cuh"
 #include "mhc_device.cuh"
+#include "mhc_f32x2.cuh"
 
 namespace mhc {
 namespace norm {
@@ -81,11 +87,6 @@ __device__ __forceinline__ uint16_t e4m3_pair(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
-}
-
-__device__ __forceinline__ float chunk_sum(const float* q) {
-    return __fadd_rn(__fadd_rn(__fadd_rn(q[0], q[1]), __fadd_rn(q[2], q[3])),
-                     __fadd_rn(__fadd_rn(q[4], q[5]), __fadd_rn(q[6], q[7])));
 }
 
 // Folds one value per thread over the row's threads (a warp, or the block):
@@ -221,23 +222,18 @@ __device__ __forceinline__ void load_words(const Input& in, int64_t t, uint32_t 
     }
 }
 
-template <int DT>
-__device__ __forceinline__ void chunk_values(const Words<4>& w, float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = Elem<DT>::lo(w.w[i]), v[2 * i + 1] = Elem<DT>::hi(w.w[i]);
+__device__ __forceinline__ F2 pfma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
 }
 
-template <int DT, int K, bool VEC>
-__device__ __forceinline__ void load_row(const Input& in, int64_t t, uint32_t H, float (&v)[8 * K]) {
-    Words<4> w[K];
-    load_words<K, VEC>(in, t, H, w);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        float x[8];
-        chunk_values<DT>(w[k], x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * k + i] = x[i];
-    }
+template <int DT>
+__device__ __forceinline__ F2 pair_of(uint32_t w) { return f2(Elem<DT>::lo(w), Elem<DT>::hi(w)); }
+
+// A chunk's sum of four packed products, in the chunk's tree.
+__device__ __forceinline__ float chunk_sum(const F2 (&q)[4]) {
+    return __fadd_rn(__fadd_rn(padd_halves(q[0]), padd_halves(q[1])), __fadd_rn(padd_halves(q[2]), padd_halves(q[3])));
 }
 
 // The values lo .. hi - 1 of the 8 that v would put at the aligned address `at`.
@@ -318,11 +314,11 @@ __device__ __forceinline__ void store_unaligned(char* row, uint32_t H, const uin
 }
 
 template <int DT, int K>
-__device__ __forceinline__ void pack_row(const float (&v)[8 * K], uint32_t (&w)[K][4]) {
+__device__ __forceinline__ void pack_row(const F2 (&v)[4 * K], uint32_t (&w)[K][4]) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[k][i] = Elem<DT>::pack(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
+        for (int i = 0; i < 4; ++i) w[k][i] = Elem<DT>::pack(f2_lo(v[4 * k + i]), f2_hi(v[4 * k + i]));
 }
 
 template <int K>
@@ -336,7 +332,7 @@ __device__ __forceinline__ void store_aligned(uint16_t* __restrict__ row, uint32
 
 // (without VEC with a barrier inside, for rows of more than one warp)
 template <int DT, int K, bool VEC>
-__device__ __forceinline__ void store_row(uint16_t* __restrict__ row, uint32_t H, const float (&v)[8 * K], uint4* edge) {
+__device__ __forceinline__ void store_row(uint16_t* __restrict__ row, uint32_t H, const F2 (&v)[4 * K], uint4* edge) {
     uint32_t w[K][4];
     pack_row<DT, K>(v, w);
     if constexpr (VEC) {
@@ -350,7 +346,7 @@ __device__ __forceinline__ void store_row(uint16_t* __restrict__ row, uint32_t H
 
 // The norm's weight at the thread's values (it stays in L1: 4 H bytes).
 template <int K, bool VEC>
-__device__ __forceinline__ void load_weight(const float* __restrict__ w, uint32_t H, float (&v)[8 * K]) {
+__device__ __forceinline__ void load_weight(const float* __restrict__ w, uint32_t H, F2 (&v)[4 * K]) {
     const uint32_t nt = blockDim.x, j = threadIdx.x;
     const bool vectors = VEC || (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
 #pragma unroll
@@ -358,32 +354,52 @@ __device__ __forceinline__ void load_weight(const float* __restrict__ w, uint32_
         const uint32_t c = 8 * (j + k * nt);
         if (vectors && c + (VEC ? 0 : 7) < H) {
             const float4 a = __ldg(reinterpret_cast<const float4*>(w + c)), b = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
-            v[8 * k] = a.x, v[8 * k + 1] = a.y, v[8 * k + 2] = a.z, v[8 * k + 3] = a.w;
-            v[8 * k + 4] = b.x, v[8 * k + 5] = b.y, v[8 * k + 6] = b.z, v[8 * k + 7] = b.w;
+            v[4 * k] = f2(a.x, a.y), v[4 * k + 1] = f2(a.z, a.w), v[4 * k + 2] = f2(b.x, b.y), v[4 * k + 3] = f2(b.z, b.w);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[8 * k + i] = !VEC && c + i < H ? __ldg(w + c + i) : 0.0f;
+            for (int i = 0; i < 4; ++i)
+                v[4 * k + i] = f2(!VEC && c + 2 * i < H ? __ldg(w + c + 2 * i) : 0.0f,
+                                  !VEC && c + 2 * i + 1 < H ? __ldg(w + c + 2 * i + 1) : 0.0f);
         }
     }
 }
 
-// The row's sum of q in the order stated above.
+// The thread's part of the row's sum of squares.
 template <int K>
-__device__ __forceinline__ float row_sum(const float (&q)[8 * K], Fold& shared) {
+__device__ __forceinline__ float squares(const F2 (&s)[4 * K]) {
     float acc = 0.0f;
 #pragma unroll
-    for (int k = 0; k < K; ++k) acc = __fadd_rn(acc, chunk_sum(q + 8 * k));
-    return fold(acc, shared, Add());
+    for (int k = 0; k < K; ++k) {
+        F2 q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = pmul(s[4 * k + i], s[4 * k + i]);
+        acc = __fadd_rn(acc, chunk_sum(q));
+    }
+    return acc;
+}
+
+__device__ __forceinline__ float rstd_of(float sum, uint32_t H, float eps) {
+    return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(H)), eps)));
+}
+
+template <int K>
+__device__ __forceinline__ void normalise(F2 (&s)[4 * K], float rstd, const F2 (&w)[4 * K]) {
+    const F2 r = f2(rstd, rstd);
+#pragma unroll
+    for (int i = 0; i < 4 * K; ++i) s[i] = pmul(pmul(s[i], r), w[i]);
 }
 
 // The row's output from v: 16-bit values, or E4M3 values and their scales.
 template <int DT, int K, bool VEC, int OUT>
-__device__ __forceinline__ void store_y(const FwdArgs& a, int64_t t, float (&s)[8 * K], Fold& shared, uint4* edge) {
+__device__ __forceinline__ void store_y(const FwdArgs& a, int64_t t, const F2 (&v)[4 * K], Fold& shared, uint4* edge) {
     const uint32_t H = a.H, nt = blockDim.x, j = threadIdx.x;
     if constexpr (OUT == kOutSame) {
-        store_row<DT, K, VEC>(static_cast<uint16_t*>(a.y) + t * int64_t(H), H, s, edge);
+        store_row<DT, K, VEC>(static_cast<uint16_t*>(a.y) + t * int64_t(H), H, v, edge);
     } else {
         uint8_t* y = static_cast<uint8_t*>(a.y) + t * int64_t(H);
+        float s[8 * K];
+#pragma unroll
+        for (int i = 0; i < 4 * K; ++i) s[2 * i] = f2_lo(v[i]), s[2 * i + 1] = f2_hi(v[i]);
         float inv[K];   // of the thread's chunks
         if constexpr (OUT == kOutFp8Row) {
             float m = kAmaxFloor;
@@ -442,42 +458,47 @@ __global__ void __launch_bounds__(kMaxThreads, K <= 2 ? 2 : 1) fwd_kernel(const 
     if (t >= a.T) return;
     clear_fold(shared, 2);
     const uint32_t H = a.H, j = threadIdx.x;
-    float s[8 * K], q[8 * K];
+    F2 s[4 * K];
     uint32_t total[K][4];
-    load_row<DT, K, VEC>(Input(a.x, a.x_stride, a.T, H), t, H, s);
-    if (a.residual != nullptr) {
-        load_row<DT, K, VEC>(Input(a.residual, a.residual_stride, a.T, H), t, H, q);
+    {
+        Words<4> x[K], r[K];
+        load_words<K, VEC>(Input(a.x, a.x_stride, a.T, H), t, H, x);
+        if (a.residual != nullptr) load_words<K, VEC>(Input(a.residual, a.residual_stride, a.T, H), t, H, r);
 #pragma unroll
-        for (int i = 0; i < 8 * K; ++i) s[i] = __fadd_rn(s[i], q[i]);
-        pack_row<DT, K>(s, total);
-        if constexpr (VEC) store_aligned<K>(a.total + t * int64_t(H), H, total);
-        else publish_edges<4, K>(edge[0], total);
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[4 * k + i] = pair_of<DT>(x[k].w[i]);
+        if (a.residual != nullptr) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[4 * k + i] = padd(s[4 * k + i], pair_of<DT>(r[k].w[i]));
+            pack_row<DT, K>(s, total);
+            if constexpr (VEC) store_aligned<K>(a.total + t * int64_t(H), H, total);
+            else publish_edges<4, K>(edge[0], total);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < 8 * K; ++i) q[i] = __fmul_rn(s[i], s[i]);
-    const float sum = row_sum<K>(q, shared[0]);   // (a barrier, where a row has more than one warp)
+    const float sum = fold(squares<K>(s), shared[0], Add());   // (a barrier, where a row has more than one warp)
     if constexpr (!VEC)
         if (a.residual != nullptr) store_unaligned<2, K>(reinterpret_cast<char*>(a.total + t * int64_t(H)), H, total, edge[0]);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(H)), a.eps)));
+    const float rstd = rstd_of(sum, H, a.eps);
     if (j == 0) a.rstd[t] = rstd;
-    load_weight<K, VEC>(a.weight, H, q);
-#pragma unroll
-    for (int i = 0; i < 8 * K; ++i) s[i] = __fmul_rn(__fmul_rn(s[i], rstd), q[i]);
+    F2 w[4 * K];
+    load_weight<K, VEC>(a.weight, H, w);
+    normalise<K>(s, rstd, w);
     store_y<DT, K, VEC, OUT>(a, t, s, shared[1], edge[VEC ? 0 : 1]);
 }
 
 // A chunk of the backward's first pass: adds g * n to acc and gives the
 // chunk's part of the sum of u * n.
 template <int DT>
-__device__ __forceinline__ float backward_terms(const Words<4>& g, const Words<4>& s, float rstd, const float* w, float* acc) {
-    float gv[8], nv[8], q[8];
-    chunk_values<DT>(g, gv);
-    chunk_values<DT>(s, nv);
+__device__ __forceinline__ float backward_terms(const Words<4>& g, const Words<4>& s, F2 rstd, const F2* w, F2* acc) {
+    F2 q[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        nv[i] = __fmul_rn(nv[i], rstd);
-        acc[i] = __fadd_rn(acc[i], __fmul_rn(gv[i], nv[i]));
-        q[i] = __fmul_rn(__fmul_rn(gv[i], w[i]), nv[i]);
+    for (int i = 0; i < 4; ++i) {
+        const F2 gv = pair_of<DT>(g.w[i]), n = pmul(pair_of<DT>(s.w[i]), rstd);
+        acc[i] = pfma(gv, n, acc[i]);
+        q[i] = pmul(pmul(gv, w[i]), n);
     }
     return chunk_sum(q);
 }
@@ -485,25 +506,19 @@ __device__ __forceinline__ float backward_terms(const Words<4>& g, const Words<4
 // And of the second: grad_x.
 template <int DT>
 __device__ __forceinline__ void backward_values(const Words<4>& g, const Words<4>& s, const Words<4>& more, bool with_more,
-                                                float rstd, float m, const float* w, float* v) {
-    float gv[8], nv[8];
-    chunk_values<DT>(g, gv);
-    chunk_values<DT>(s, nv);
+                                                F2 rstd, F2 minus_m, const F2* w, F2* v) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = __fmul_rn(rstd, __fsub_rn(__fmul_rn(gv[i], w[i]), __fmul_rn(__fmul_rn(nv[i], rstd), m)));
-    if (with_more) {
-        float tv[8];
-        chunk_values<DT>(more, tv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(v[i], tv[i]);
+    for (int i = 0; i < 4; ++i) {
+        const F2 n = pmul(pair_of<DT>(s.w[i]), rstd);
+        const F2 d = pfma(n, minus_m, pmul(pair_of<DT>(g.w[i]), w[i]));
+        v[i] = with_more ? pfma(rstd, d, pair_of<DT>(more.w[i])) : pmul(rstd, d);
     }
 }
 
 // A block's sums of grad_weight: to its row of the workspace, whose rows are
 // of whole chunks, or (`last`: the only block) to grad_weight itself.
 template <int K, bool VEC>
-__device__ __forceinline__ void store_partial(float* __restrict__ out, uint32_t H, bool last, const float (&acc)[8 * K]) {
+__device__ __forceinline__ void store_partial(float* __restrict__ out, uint32_t H, bool last, const F2 (&acc)[4 * K]) {
     const uint32_t nt = blockDim.x, j = threadIdx.x;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -511,13 +526,14 @@ __device__ __forceinline__ void store_partial(float* __restrict__ out, uint32_t 
         if (VEC || !last) {
             if (c < H) {
                 float4* p = reinterpret_cast<float4*>(out + c);
-                p[0] = make_float4(acc[8 * k], acc[8 * k + 1], acc[8 * k + 2], acc[8 * k + 3]);
-                p[1] = make_float4(acc[8 * k + 4], acc[8 * k + 5], acc[8 * k + 6], acc[8 * k + 7]);
+                const F2* v = acc + 4 * k;
+                p[0] = make_float4(f2_lo(v[0]), f2_hi(v[0]), f2_lo(v[1]), f2_hi(v[1]));
+                p[1] = make_float4(f2_lo(v[2]), f2_hi(v[2]), f2_lo(v[3]), f2_hi(v[3]));
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (c + i < H) out[c + i] = acc[8 * k + i];
+                if (c + i < H) out[c + i] = i & 1 ? f2_hi(acc[4 * k + i / 2]) : f2_lo(acc[4 * k + i / 2]);
         }
     }
 }
@@ -536,40 +552,43 @@ __global__ void __launch_bounds__(kMaxThreads, 1) bwd_kernel(const BwdArgs a) {
     clear_fold(shared, 2);
     const int64_t step = int64_t(gridDim.x) * rows;
     const Input in_s(a.s, a.s_stride, a.T, H), in_g(a.g, a.g_stride, a.T, H), in_t(a.grad_total, H, a.T, H);
-    float acc[8 * K];
+    F2 acc[4 * K];
 #pragma unroll
-    for (int i = 0; i < 8 * K; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < 4 * K; ++i) acc[i] = f2(0.0f, 0.0f);
     int turn = 0;
     for (int64_t t = int64_t(blockIdx.x) * rows + threadIdx.y; t < a.T; t += step, turn ^= 1) {
         Words<4> g[K], n[K], more[K];
         load_words<K, VEC>(in_s, t, H, n);
         load_words<K, VEC>(in_g, t, H, g);
         if (a.grad_total != nullptr) load_words<K, VEC>(in_t, t, H, more);
-        const float rstd = __ldg(a.rstd + t);
-        float w[8 * K], sum = 0.0f;
+        const float r1 = __ldg(a.rstd + t);
+        const F2 rstd = f2(r1, r1);
+        F2 w[4 * K];
         load_weight<K, VEC>(a.weight, H, w);
+        float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) sum = __fadd_rn(sum, backward_terms<DT>(g[k], n[k], rstd, w + 8 * k, acc + 8 * k));
-        const float m = __fdiv_rn(fold(sum, shared[turn], Add()), float(H));
-        float v[8 * K];
+        for (int k = 0; k < K; ++k) sum = __fadd_rn(sum, backward_terms<DT>(g[k], n[k], rstd, w + 4 * k, acc + 4 * k));
+        const float m = -__fdiv_rn(fold(sum, shared[turn], Add()), float(H));
+        F2 v[4 * K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) backward_values<DT>(g[k], n[k], more[k], a.grad_total != nullptr, rstd, m, w + 8 * k, v + 8 * k);
+        for (int k = 0; k < K; ++k)
+            backward_values<DT>(g[k], n[k], more[k], a.grad_total != nullptr, rstd, f2(m, m), w + 4 * k, v + 4 * k);
         store_row<DT, K, VEC>(a.grad_x + t * int64_t(H), H, v, edge[VEC ? 0 : turn]);
     }
     if (rows > 1) {   // the warps of a block one after the other, in shared memory
         for (uint32_t y = 0; y < rows; ++y) {
             if (threadIdx.y == y) {
 #pragma unroll
-                for (int i = 0; i < 8 * K; ++i) {
-                    const uint32_t at = j + i * 32;
-                    stage[at] = y == 0 ? acc[i] : __fadd_rn(stage[at], acc[i]);
+                for (int i = 0; i < 4 * K; ++i) {
+                    F2* at = reinterpret_cast<F2*>(stage) + j + i * 32;
+                    *at = y == 0 ? acc[i] : padd(*at, acc[i]);
                 }
             }
             __syncthreads();
         }
         if (threadIdx.y != 0) return;
 #pragma unroll
-        for (int i = 0; i < 8 * K; ++i) acc[i] = stage[j + i * 32];
+        for (int i = 0; i < 4 * K; ++i) acc[i] = reinterpret_cast<const F2*>(stage)[j + i * 32];
     }
     store_partial<K, VEC>(a.partial + int64_t(blockIdx.x) * a.pitch, H, gridDim.x == 1, acc);
 }
@@ -629,7 +648,7 @@ fwd_ring_kernel(const FwdArgs a, const RingRows r, uint32_t stages) {
     if (j == 0)
         for (; issued < stages && blockIdx.x + issued * step < a.T; ++issued)
             ring_copy(ring + issued * r.arrays * bytes, r, blockIdx.x + issued * step, bytes, full + issued);
-    float w[8 * K];
+    F2 w[4 * K];
     load_weight<K, true>(a.weight, H, w);
     uint32_t stage = 0, parity = 0;
     int turn = 0;
@@ -637,45 +656,30 @@ fwd_ring_kernel(const FwdArgs a, const RingRows r, uint32_t stages) {
         if (!late && !mbar_wait_fast(full + stage, parity)) late = 1;
         const char* row = ring + stage * r.arrays * bytes;
         Words<4> raw[K];
-        float s[8 * K];
+        F2 s[4 * K];
         stage_words<DT, K>(row, H, raw);
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float v[8];
-            chunk_values<DT>(raw[k], v);
+        for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[8 * k + i] = v[i];
-        }
+            for (int i = 0; i < 4; ++i) s[4 * k + i] = pair_of<DT>(raw[k].w[i]);
         if (r.arrays > 1) {
             stage_words<DT, K>(row + bytes, H, raw);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                float v[8];
-                chunk_values<DT>(raw[k], v);
+            for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[8 * k + i] = __fadd_rn(s[8 * k + i], v[i]);
-            }
+                for (int i = 0; i < 4; ++i) s[4 * k + i] = padd(s[4 * k + i], pair_of<DT>(raw[k].w[i]));
             store_row<DT, K, true>(a.total + t * int64_t(H), H, s, nullptr);
         }
-        float acc = 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float q[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(s[8 * k + i], s[8 * k + i]);
-            acc = __fadd_rn(acc, chunk_sum(q));
-        }
-        const float sum = fold(acc, shared[turn][0], Add());
+        const float sum = fold(squares<K>(s), shared[turn][0], Add());
         if (j == 0 && t + stages * step < a.T && !late) {
             fence_proxy_async_shared();
             ring_copy(ring + stage * r.arrays * bytes, r, t + stages * step, bytes, full + stage);
             ++issued;
         }
         if (++stage == stages) stage = 0, parity ^= 1;
-        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, float(H)), a.eps)));
+        const float rstd = rstd_of(sum, H, a.eps);
         if (j == 0) a.rstd[t] = rstd;
-#pragma unroll
-        for (int i = 0; i < 8 * K; ++i) s[i] = __fmul_rn(__fmul_rn(s[i], rstd), w[i]);
+        normalise<K>(s, rstd, w);
         store_y<DT, K, true, OUT>(a, t, s, shared[turn][1], nullptr);
     }
     if (j == 0 && late) ring_late(full, issued, stages, a.timeouts);
@@ -702,14 +706,15 @@ bwd_ring_kernel(const BwdArgs a, const RingRows r, uint32_t stages) {
     if (j == 0)
         for (; issued < stages && blockIdx.x + issued * step < a.T; ++issued)
             ring_copy(ring + issued * r.arrays * bytes, r, blockIdx.x + issued * step, bytes, full + issued);
-    float w[8 * K], acc[8 * K];
+    F2 w[4 * K], acc[4 * K];
     load_weight<K, true>(a.weight, H, w);
 #pragma unroll
-    for (int i = 0; i < 8 * K; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < 4 * K; ++i) acc[i] = f2(0.0f, 0.0f);
     uint32_t stage = 0, parity = 0;
     int turn = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += step, turn ^= 1) {
-        const float rstd = __ldg(a.rstd + t);
+        const float r1 = __ldg(a.rstd + t);
+        const F2 rstd = f2(r1, r1);
         if (!late && !mbar_wait_fast(full + stage, parity)) late = 1;
         const char* row = ring + stage * r.arrays * bytes;
         Words<4> g[K], n[K], more[K];
@@ -718,43 +723,62 @@ bwd_ring_kernel(const BwdArgs a, const RingRows r, uint32_t stages) {
         if (r.arrays > 2) stage_words<DT, K>(row + 2 * bytes, H, more);
         float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) sum = __fadd_rn(sum, backward_terms<DT>(g[k], n[k], rstd, w + 8 * k, acc + 8 * k));
-        const float m = __fdiv_rn(fold(sum, shared[turn], Add()), float(H));
+        for (int k = 0; k < K; ++k) sum = __fadd_rn(sum, backward_terms<DT>(g[k], n[k], rstd, w + 4 * k, acc + 4 * k));
+        const float m = -__fdiv_rn(fold(sum, shared[turn], Add()), float(H));
         if (j == 0 && t + stages * step < a.T && !late) {
             fence_proxy_async_shared();
             ring_copy(ring + stage * r.arrays * bytes, r, t + stages * step, bytes, full + stage);
             ++issued;
         }
         if (++stage == stages) stage = 0, parity ^= 1;
-        float v[8 * K];
+        F2 v[4 * K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) backward_values<DT>(g[k], n[k], more[k], r.arrays > 2, rstd, m, w + 8 * k, v + 8 * k);
+        for (int k = 0; k < K; ++k) backward_values<DT>(g[k], n[k], more[k], r.arrays > 2, rstd, f2(m, m), w + 4 * k, v + 4 * k);
         store_row<DT, K, true>(a.grad_x + t * int64_t(H), H, v, nullptr);
     }
     store_partial<K, true>(a.partial + int64_t(blockIdx.x) * a.pitch, H, false, acc);
     if (j == 0 && late) ring_late(full, issued, stages, a.timeouts);
 }
 
-// Column sums of partial [P,H] (row pitch `pitch`): block (32, 32); thread (x, y) adds the rows
-// y, y + 32, ... of column x in increasing order, then the 32 sums in
-// increasing order.  Also the bias gradient's last step.
-constexpr int kColRows = 32;
+// Column sums of partial [P,H] (row pitch `pitch`): a block takes 32 columns,
+// 8 threads with four each in 128 groups; group y adds the rows y, y + 128, ...
+// in increasing order, then a lane adds four groups and the lanes fold at
+// distance 16, 8, 4, 2, 1.  (The rows' latency is what it waits for: with 32
+// groups the norm's backward took 2.3 us more.)  VEC: pitch % 4 == 0 and a 16-byte aligned
+// partial.  Also the bias gradient's last step.
+constexpr int kColGroups = 128;
 
-static __global__ void __launch_bounds__(32 * kColRows)
+template <bool VEC>
+static __global__ void __launch_bounds__(8 * kColGroups)
 column_sum_kernel(const float* __restrict__ partial, float* __restrict__ out, uint32_t P, uint32_t H, uint32_t pitch) {
     pdl_enter();
-    __shared__ float part[kColRows][32];
-    const uint32_t c = blockIdx.x * 32 + threadIdx.x;
-    float acc = 0.0f;
+    __shared__ float part[32][kColGroups + 1];
+    const uint32_t x = threadIdx.x % 8, y = threadIdx.x / 8, c = blockIdx.x * 32 + 4 * x;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c < H)
-#pragma unroll 8
-        for (uint32_t p = threadIdx.y; p < P; p += kColRows) acc = __fadd_rn(acc, partial[uint64_t(p) * pitch + c]);
-    part[threadIdx.y][threadIdx.x] = acc;
-    __syncthreads();
-    if (threadIdx.y == 0 && c < H) {
+#pragma unroll 4
+        for (uint32_t p = y; p < P; p += kColGroups) {
+            const float* row = partial + uint64_t(p) * pitch + c;
+            if constexpr (VEC) {
+                const float4 v = *reinterpret_cast<const float4*>(row);
+                acc[0] = __fadd_rn(acc[0], v.x), acc[1] = __fadd_rn(acc[1], v.y);
+                acc[2] = __fadd_rn(acc[2], v.z), acc[3] = __fadd_rn(acc[3], v.w);
+            } else {
 #pragma unroll
-        for (int y = 1; y < kColRows; ++y) acc = __fadd_rn(acc, part[y][threadIdx.x]);
-        out[c] = acc;
+                for (int i = 0; i < 4; ++i)
+                    if (c + i < H) acc[i] = __fadd_rn(acc[i], row[i]);
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[4 * x + i][y] = acc[i];
+    __syncthreads();
+    {
+        const uint32_t lane = threadIdx.x & 31u, column = threadIdx.x / 32;   // a warp for each
+        const float* g = &part[column][4 * lane];
+        float v = __fadd_rn(__fadd_rn(g[0], g[1]), __fadd_rn(g[2], g[3]));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+        if (lane == 0 && blockIdx.x * 32 + column < H) out[blockIdx.x * 32 + column] = v;
     }
 }
 
