@@ -158,8 +158,13 @@ __device__ __forceinline__ void emit_rows(const Epilogue& e, int64_t N, bool n_o
     }
     uint16_t* p = e.y + int64_t(m0) * N + n;
 #pragma unroll
-    for (int c = 0; c < C; ++c, p += stride)
-        if (there(c)) *p = Elem<OUT>::cvt(v[c]);
+    for (int c = 0; c < C; c += 2) {
+        const uint32_t w = Elem<OUT>::pack(v[c], v[c + 1]);
+        if (there(c)) *p = uint16_t(w);
+        p += stride;
+        if (there(c + 1)) *p = uint16_t(w >> 16);
+        p += stride;
+    }
 }
 
 template <int OUT, int C>
@@ -346,7 +351,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
             umma::tmem_ld(tmem + (quarter * 32u << 16) + c, v);
             uint16_t r[kChunk];
             if (a.splits == 1) load_residual<kChunk>(a.e, n_ok, n, m0 + c, 1, m0 + valid, r);
-            umma::tmem_wait_ld();
+            umma::tmem_wait_ld(v);
             if (a.splits == 1) {
                 emit<OUT, kChunk>(a.e, a.N, n_ok, n, m0 + c, 1, m0 + valid, v, r, bias, cs);
             } else {
@@ -427,17 +432,17 @@ __device__ __forceinline__ void tile_at(const TileArgs& a, uint32_t i, uint32_t&
 }
 
 // The accumulator of each part of each tile in turn, and the parity of its
-// round: as many rounds as it was taken before.
+// round (one bit each): as many rounds as it was taken before.
 struct Sums {
-    uint32_t taken[2] = {0, 0}, last = 1;
+    uint32_t rounds = 3, last = 1;
     // (PARTS: the second part's is the second one, every other part's the first)
     template <bool PARTS>
     __device__ __forceinline__ uint32_t take(uint32_t part) {
         last = PARTS ? uint32_t(part == 1) : last ^ 1;
-        ++taken[last];
+        rounds ^= 1u << last;
         return last;
     }
-    __device__ __forceinline__ uint32_t parity(uint32_t b) const { return (taken[b] - 1) & 1; }
+    __device__ __forceinline__ uint32_t parity(uint32_t b) const { return rounds >> b & 1; }
 };
 
 template <bool FP8, int OUT, int LAYOUT, bool PARTS>
@@ -574,7 +579,8 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                     float v[kChunk], w[kChunk];
                     umma::tmem_ld(tw + c, v);
                     umma::tmem_ld(tw + 256 + c, w);
-                    umma::tmem_wait_ld();
+                    umma::tmem_wait_ld(v);
+                    umma::tmem_wait_ld(w);
                     // (the second part arrives where the sum goes)
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) v[i] = __fadd_rn(v[i], w[i]);
@@ -590,20 +596,25 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             const uint32_t from = tw + b * 256;
             uint16_t r[kChunk];   // a chunk's residual arrives while the chunk before it is worked on
             load_residual<kChunk>(a.e, n_ok, col, m0, 1, a.rows, r);
+            float next[kChunk];   // and its sums
+            umma::tmem_ld(from, next);
 #pragma unroll 1
             for (uint32_t c = 0; c < mine; c += kChunk) {
+                umma::tmem_wait_ld(next);
                 float v[kChunk];
-                umma::tmem_ld(from + c, v);
                 uint16_t now[kChunk];
 #pragma unroll
-                for (int k = 0; k < kChunk; ++k) now[k] = r[k];
-                if (c + kChunk < mine) load_residual<kChunk>(a.e, n_ok, col, m0 + c + kChunk, 1, a.rows, r);
-                umma::tmem_wait_ld();
+                for (int k = 0; k < kChunk; ++k) v[k] = next[k], now[k] = r[k];
+                if (c + kChunk < mine) {
+                    umma::tmem_ld(from + c + kChunk, next);
+                    load_residual<kChunk>(a.e, n_ok, col, m0 + c + kChunk, 1, a.rows, r);
+                } else {
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) umma::arrive_cluster(signal + 8 * b);
+                }
                 emit<OUT, kChunk>(a.e, a.N, n_ok, col, m0 + c, 1, a.rows, v, now, bias, cs);
             }
-            umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) umma::arrive_cluster(signal + 8 * b);
         }
         if (!ok) timed_out(a);
         umma::fence_before_sync();

@@ -83,7 +83,13 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const float (&v)[8]) {
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// After the wait for every load before it; the values pass through it, so that no use of them is moved before it.
+__device__ __forceinline__ void tmem_wait_ld(float (&v)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])
+                 :
+                 : "memory");
+}
 
 __device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -237,8 +243,11 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     return v;
 }
 
+// Signals without waiting for this thread's stores to global memory (a
+// release would: 10% of a product with 8 blocks of K): what it hands over, tensor
+// memory, fence_before_sync orders.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" : : "r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" : : "r"(bar) : "memory");
 }
 
 // Every thread of every CTA of the cluster.
