@@ -70,6 +70,9 @@ struct Product {
     bool a_mn, b_mn;              // rows run along m (n), one for each k; else along k.  b_mn where a_mn.
     bool by_row;                  // a row's sums must not depend on M (its tokens): the forward and grad_x
     int64_t M, N, K;
+    // the launch just before reads and writes other memory than this call's operands and output
+    // (the sum of a bias gradient, the other gradient's product): run beside it
+    bool beside;
     Epilogue e;
 };
 
@@ -93,6 +96,7 @@ struct TileArgs {
     uint32_t unit, block_bytes;   // blocks of K of a stage, and bytes of each
     uint32_t idesc;
     uint32_t p_tiles, q_tiles;
+    bool beside;                  // see Product
     unsigned int* timeouts;
 };
 
@@ -238,6 +242,11 @@ __device__ __forceinline__ void drain(bool& ok, uint32_t issued, umma::Ring at, 
     }
 }
 
+__device__ __forceinline__ void enter(const TileArgs& a) {
+    if (a.beside) pdl_start();
+    else pdl_enter();
+}
+
 __device__ __forceinline__ void timed_out(const TileArgs& a) { *a.timeouts = 1u; }
 
 // --------------------------------------------------------------------------
@@ -298,7 +307,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     // the thread's place in the parts, [column][lane], that take the stages' place
     // once every copy has landed and been read
     float* part = reinterpret_cast<float*>(stages) + quarter * 32 + lane;
-    pdl_enter();
+    enter(a);
     const float bias = a.e.bias != nullptr && n_ok ? __ldg(a.e.bias + n) : 0.0f;
     const float cs = a.e.col_scale != nullptr && n_ok ? __ldg(a.e.col_scale + n) : 1.0f;
     const uint32_t ring = smem_addr(stages), bar_full = smem_addr(full), bar_empty = smem_addr(empty);
@@ -392,6 +401,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     }
     umma::fence_after_sync();
     if (warp == kSplitCopy) umma::tmem_free<1>(tmem, columns);
+    if (a.beside) pdl_end();
 }
 
 // --------------------------------------------------------------------------
@@ -480,7 +490,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
     umma::cluster_sync();   // the other CTA's barriers are ready too
     umma::fence_after_sync();
     const uint32_t tmem = tmem_base;
-    pdl_enter();
+    enter(a);
     const uint32_t ring = smem_addr(stages), bar_full = smem_addr(full), bar_empty = smem_addr(empty);
     const uint32_t bar_sum = smem_addr(sum_full), bar_free = smem_addr(sum_empty);
     const uint32_t count = a.stages, bytes = a.stage_bytes, unit = a.unit;
@@ -623,6 +633,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
     umma::cluster_sync();   // neither CTA leaves while the other may still signal it
     umma::fence_after_sync();
     if (warp == kCopyP) umma::tmem_free<2>(tmem, kTmemColumns);
+    if (a.beside) pdl_end();
 }
 
 // Rows of values copied to a row pitch that starts every row on 16 bytes, for
@@ -685,6 +696,39 @@ static __global__ void __launch_bounds__(kRepackThreads) repack_kernel(const Rep
 // bandwidth; 50 us with the exact division and exponential).
 constexpr int kSlopeRows = 8;
 
+template <int W>
+struct Row;
+
+template <>
+struct Row<8> {
+    Words<4> w;
+    __device__ __forceinline__ void load(const uint16_t* p) { w = ld_stream<4>(p); }
+    template <int DT>
+    __device__ __forceinline__ float value(int i) const {
+        return i % 2 ? Elem<DT>::hi(w.w[i / 2]) : Elem<DT>::lo(w.w[i / 2]);
+    }
+};
+
+template <>
+struct Row<1> {
+    uint16_t w;
+    __device__ __forceinline__ void load(const uint16_t* p) { w = ld_stream2(p); }
+    template <int DT>
+    __device__ __forceinline__ float value(int) const { return Elem<DT>::one(w); }
+};
+
+template <int DT, int W>
+__device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[W]) {
+    if constexpr (W == 8) {
+        Words<4> o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o.w[i] = Elem<DT>::pack(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<Words<4>*>(p) = o;
+    } else {
+        *p = Elem<DT>::cvt(v[0]);
+    }
+}
+
 template <int DT, int W, int ACT>
 __global__ void __launch_bounds__(32 * kSlopeRows)
 slope_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ preact, uint16_t* __restrict__ u,
@@ -696,37 +740,30 @@ slope_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ preact
     float acc[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) acc[i] = 0.0f;
-    if (c < O) {
-#pragma unroll 2
-        for (int64_t t = t0 + threadIdx.y; t < t1; t += kSlopeRows) {
-            const int64_t at = t * O + c;
-            float v[W];
-            if constexpr (W == 8) {
-                const Words<4> gw = ld_stream<4>(g + at);
-                Words<4> zw;
-                if (ACT != kActNone) zw = ld_stream<4>(preact + at);
+    // four rows' loads are under way together: a row at a time waited out each
+    // one's latency (T = 1749, O = 552 11 us, now 7.8)
+    constexpr int kAhead = 4;
+    for (int64_t t = t0 + threadIdx.y; t < t1 && c < O; t += kAhead * kSlopeRows) {
+        Row<W> gr[kAhead], zr[kAhead];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[2 * i] = Elem<DT>::lo(gw.w[i]), v[2 * i + 1] = Elem<DT>::hi(gw.w[i]);
-                    if (ACT != kActNone) {
-                        v[2 * i] *= slope<ACT>(Elem<DT>::lo(zw.w[i]));
-                        v[2 * i + 1] *= slope<ACT>(Elem<DT>::hi(zw.w[i]));
-                    }
-                }
-                if (u != nullptr) {
-                    Words<4> o;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o.w[i] = Elem<DT>::pack(v[2 * i], v[2 * i + 1]);
-                    *reinterpret_cast<Words<4>*>(u + t * pitch + c) = o;
-                }
-            } else {
-                v[0] = Elem<DT>::one(g[at]);
-                if (ACT != kActNone) v[0] *= slope<ACT>(Elem<DT>::one(preact[at]));
-                if (u != nullptr) u[t * pitch + c] = Elem<DT>::cvt(v[0]);
+        for (int k = 0; k < kAhead; ++k)
+            if (t + k * kSlopeRows < t1) {
+                const int64_t at = (t + k * kSlopeRows) * O + c;
+                gr[k].load(g + at);
+                if (ACT != kActNone) zr[k].load(preact + at);
             }
 #pragma unroll
-            for (int i = 0; i < W; ++i) acc[i] = __fadd_rn(acc[i], v[i]);
-        }
+        for (int k = 0; k < kAhead; ++k)
+            if (t + k * kSlopeRows < t1) {
+                float v[W];
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    v[i] = gr[k].template value<DT>(i);
+                    if (ACT != kActNone) v[i] *= slope<ACT>(zr[k].template value<DT>(i));
+                    acc[i] = __fadd_rn(acc[i], v[i]);
+                }
+                if (u != nullptr) store_row<DT>(u + (t + k * kSlopeRows) * pitch + c, v);
+            }
     }
     if (partial == nullptr) return;
 #pragma unroll
