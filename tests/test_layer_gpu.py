@@ -374,6 +374,36 @@ def test_linear_backward(T, I, O, act, dtype):
     assert torch.equal(one[2], got[2])
 
 
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("T,D", [(40, 328), (700, 520), (2049, 1032), (700, 1023)])
+def test_linear_backward_calls_in_a_row(T, D, act):
+    """The kernels of a call overlap: grad_x read, and freed memory taken, by the call right after it."""
+    g = gen(T + D)
+    w = [normal(g, D, D, dtype=torch.bfloat16, spread=D ** -0.5) for _ in range(6)]
+    x, z, first = (normal(g, T, D, dtype=torch.bfloat16) for _ in range(3))
+
+    def chain(wait):
+        gy, out = first, []
+        for weight in w:
+            got = layer.linear_backward(gy, x, weight, z=None if act == "none" else z, activation=act)
+            wait()
+            out += got
+            gy = got[0]
+        return out
+
+    want = [t.clone() for t in chain(torch.cuda.synchronize)]
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(chain(lambda: None), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(lambda: None)
+    for _ in range(5):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_linear_masked_values():
     """NaN and infinities stay in the rows that hold them, also next to ragged edges."""
     x, _, w, _, _, _, _, y, bound, _ = linear_case(70, 100, 150, torch.bfloat16, "none", False, False)
