@@ -729,7 +729,7 @@ static __global__ void __launch_bounds__(kRepackThreads) repack_kernel(const Rep
 // u = g * act'(preact) over [T,O], rounded to u (row pitch `pitch`; null: not stored), and the
 // column sums of the unrounded u over each of gridDim.y runs of `rows` rows
 // in partial [gridDim.y, O] (null: not wanted).  Block (32, 8): 32 W columns,
-// 8 rows at a time.  HBM-bound: T = 4096, O = 7168 32 us (176 MB, 80% of the copy
+// 8 rows at a time.  HBM-bound: T = 4096, O = 7168 29 us (176 MB, 90% of the copy
 // bandwidth; 50 us with the exact division and exponential).
 constexpr int kSlopeRows = 8;
 
@@ -767,7 +767,7 @@ __device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[W]) {
 }
 
 template <int DT, int W, int ACT>
-__global__ void __launch_bounds__(32 * kSlopeRows)
+__global__ void __launch_bounds__(32 * kSlopeRows, 4)
 slope_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ preact, uint16_t* __restrict__ u,
              float* __restrict__ partial, int64_t T, int64_t O, int64_t pitch, int64_t rows) {
     pdl_enter();
@@ -777,9 +777,9 @@ slope_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ preact
     float acc[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) acc[i] = 0.0f;
-    // four rows' loads are under way together: a row at a time waited out each
-    // one's latency (T = 1749, O = 552 11 us, now 7.8)
-    constexpr int kAhead = 4;
+    // two rows' loads are under way together, in four blocks an SM: T = 16000, O = 2048
+    // 35 us, with four rows and three blocks 42
+    constexpr int kAhead = 2;
     for (int64_t t = t0 + threadIdx.y; t < t1 && c < O; t += kAhead * kSlopeRows) {
         Row<W> gr[kAhead], zr[kAhead];
 #pragma unroll
