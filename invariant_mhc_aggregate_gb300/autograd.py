@@ -15,13 +15,52 @@ Inputs may have any leading batch shape: ``residual [..., n, H]`` and
 ``pre [..., n]`` are flattened to tokens and the results reshaped back.  The
 pages' op has n = 4 streams and BF16 storage; n in {1, 2, 8} and FP16 storage
 run the library's general form (balanced pairwise tree, same roundings).
+
+The functions here are differentiable once (`rotary`, which is linear, any
+number of times): their backwards are kernels.  A gradient taken with
+``create_graph=True`` raises when it is differentiated again.
 """
 
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import binding, layer
+
+
+class _OnceMore(torch.autograd.Function):
+    """Passes gradients on; differentiating them raises."""
+
+    @staticmethod
+    def forward(ctx, name, *grads):
+        ctx.name = name
+        return tuple(g.view_as(g) for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name} is differentiable once: its gradients cannot be differentiated again")
+
+
+def _first_order(backward):
+    """For a backward made of kernels.  Under create_graph its results would
+    carry no graph and a second derivative would silently miss their terms;
+    they get one that raises instead.  (torch's once_differentiable does so
+    only where the incoming gradient requires one itself, not for the gradient
+    of a plain sum, which depends on the saved inputs all the same.)"""
+    @functools.wraps(backward)
+    def wrapper(ctx, *grads):
+        if not torch.is_grad_enabled():
+            return backward(ctx, *grads)
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        some = [g.detach().requires_grad_() for g in out if g is not None]
+        if not some:
+            return out
+        rest = iter(_OnceMore.apply(backward.__qualname__.split(".")[0], *some))
+        return tuple(None if g is None else next(rest) for g in out)
+    return wrapper
 
 
 class HAggregate(torch.autograd.Function):
@@ -41,6 +80,7 @@ class HAggregate(torch.autograd.Function):
         return out.reshape(*lead, H)
 
     @staticmethod
+    @_first_order
     def backward(ctx, grad_out: torch.Tensor):
         r, p = ctx.saved_tensors
         n, H = r.shape[-2], r.shape[-1]
@@ -85,6 +125,7 @@ class HAggregateSigmoid(torch.autograd.Function):
         return out.reshape(*lead, H)
 
     @staticmethod
+    @_first_order
     def backward(ctx, grad_out):
         r, m, a, bb = ctx.saved_tensors
         n, H = r.shape[-2], r.shape[-1]
@@ -138,6 +179,7 @@ class MhcPost(torch.autograd.Function):
         return out.reshape(*lead, n, H)
 
     @staticmethod
+    @_first_order
     def backward(ctx, grad_out):
         xx, yy, pp, rr = ctx.saved_tensors
         n, H = xx.shape[-2], xx.shape[-1]
@@ -191,6 +233,7 @@ class MhcPostSigmoid(torch.autograd.Function):
         return out.reshape(*lead, n, H)
 
     @staticmethod
+    @_first_order
     def backward(ctx, grad_out):
         xx, yy, mm, a, bb, rr = ctx.saved_tensors
         n, H = xx.shape[-2], xx.shape[-1]
@@ -239,6 +282,7 @@ class RmsNorm(torch.autograd.Function):
         return y.reshape(x.shape), total.reshape(x.shape) if ctx.with_residual else x.view_as(x)
 
     @staticmethod
+    @_first_order
     def backward(ctx, grad_y, grad_total):
         total, weight, rstd = ctx.saved_tensors
         H = total.shape[-1]
@@ -276,6 +320,7 @@ class Linear(torch.autograd.Function):
         return y.reshape(*x.shape[:-1], O)
 
     @staticmethod
+    @_first_order
     def backward(ctx, grad_y):
         x, w, *z = ctx.saved_tensors
         O = w.shape[0]
@@ -298,22 +343,23 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
 
 
 class Rotary(torch.autograd.Function):
-    """layer.rotary; the gradient is the rotation by the opposite angle."""
+    """layer.rotary; the gradient is the rotation by the opposite angle, which
+    is differentiable the same way."""
 
     @staticmethod
-    def forward(ctx, x, positions, frequencies, interleaved, scale):
+    def forward(ctx, x, positions, frequencies, interleaved, scale, inverse):
         ctx.save_for_backward(positions, frequencies)
-        ctx.interleaved, ctx.scale = interleaved, scale
-        return layer.rotary(x, positions, frequencies, interleaved=interleaved, scale=scale)
+        ctx.interleaved, ctx.scale, ctx.inverse = interleaved, scale, inverse
+        return layer.rotary(x, positions, frequencies, interleaved=interleaved, scale=scale, inverse=inverse)
 
     @staticmethod
     def backward(ctx, grad):
         positions, frequencies = ctx.saved_tensors
-        return (layer.rotary(grad.contiguous(), positions, frequencies, interleaved=ctx.interleaved, scale=ctx.scale,
-                             inverse=True), None, None, None, None)
+        return (Rotary.apply(grad.contiguous(), positions, frequencies, ctx.interleaved, ctx.scale, not ctx.inverse),
+                None, None, None, None, None)
 
 
 def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, interleaved: bool = False,
            scale: float = 1.0) -> torch.Tensor:
     """Differentiable layer.rotary of x [T,heads,D]."""
-    return Rotary.apply(x, positions, frequencies, interleaved, scale)
+    return Rotary.apply(x, positions, frequencies, interleaved, scale, False)
