@@ -278,7 +278,8 @@ class RmsNorm(torch.autograd.Function):
             raise ValueError(f"shape mismatch: x {tuple(x.shape)}, residual {tuple(residual.shape)}")
         y, total, rstd = layer.rms_norm(xx, weight.contiguous(), residual=rr, eps=eps)
         ctx.save_for_backward(total, weight, rstd)
-        ctx.with_residual = residual is not None
+        ctx.with_residual, ctx.shape = residual is not None, x.shape
+        ctx.set_materialize_grads(False)   # an unused output has no gradient, not one of zeros to be read
         return y.reshape(x.shape), total.reshape(x.shape) if ctx.with_residual else x.view_as(x)
 
     @staticmethod
@@ -286,10 +287,14 @@ class RmsNorm(torch.autograd.Function):
     def backward(ctx, grad_y, grad_total):
         total, weight, rstd = ctx.saved_tensors
         H = total.shape[-1]
-        gt = grad_total.reshape(-1, H).contiguous()
-        gx, gw = layer.rms_norm_backward(grad_y.reshape(-1, H).contiguous(), total, weight.contiguous(), rstd,
-                                         grad_total=gt)
-        gx = gx.reshape(grad_y.shape)
+        gt = None if grad_total is None else grad_total.reshape(-1, H).contiguous()
+        if grad_y is None:      # y is not used: total's gradient alone
+            gx, gw = None if gt is None else gt.clone(), torch.zeros_like(weight)
+        else:
+            gx, gw = layer.rms_norm_backward(grad_y.reshape(-1, H).contiguous(), total, weight.contiguous(), rstd,
+                                             grad_total=gt)
+        if gx is not None:
+            gx = gx.reshape(ctx.shape)
         return (gx if ctx.needs_input_grad[0] else None, gw if ctx.needs_input_grad[1] else None,
                 gx if ctx.with_residual and ctx.needs_input_grad[2] else None, None)
 

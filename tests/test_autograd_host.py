@@ -115,3 +115,33 @@ def test_rotary_second_derivative():
     want = 4 * 24 ** 2 * x.detach().double() ** 3
     # four roundings to 8 bits on the way
     assert ((got.double() - want).abs() <= 4 * 2.0 ** -8 * want.abs()).all()
+
+
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_norm_outputs_without_a_gradient(with_residual, monkeypatch):
+    """An unused output's gradient is not made up of zeros: the kernel then reads one input less."""
+    seen = []
+    monkeypatch.setattr(layer, "rms_norm_backward", lambda g, s, w, rstd, grad_total=None, stream=None: (
+        seen.append(grad_total), norm_backward(g, s, w, rstd, grad_total))[1])
+    x, w, r = bf(3, 5, 8), fp(8), bf(3, 5, 8) if with_residual else None
+    args = [x, w] + [r] * with_residual
+
+    def grads(loss):
+        return torch.autograd.grad(loss, args)
+
+    y, total = autograd.rms_norm(x, w, residual=r)
+    only_y = grads(y.float().square().sum())
+    assert seen == [None] and only_y[0].shape == x.shape
+    y, total = autograd.rms_norm(x, w, residual=r)
+    both = grads(y.float().square().sum() + total.float().square().sum())
+    assert len(seen) == 2 and torch.equal(seen[1], 2 * total.detach().reshape(-1, 8))
+    assert not torch.equal(both[0], only_y[0]) and torch.equal(both[1], only_y[1])
+    y, total = autograd.rms_norm(x, w, residual=r)
+    only_total = torch.autograd.grad(total.float().square().sum(), args, allow_unused=True)
+    assert torch.equal(only_total[0], 2 * total.detach()) and (only_total[1] is None or not only_total[1].any())
+    given = torch.ones_like(total)
+    torch.autograd.backward([autograd.rms_norm(x, w, residual=r)[1]], [given])
+    x.grad.zero_()                                     # the caller's tensor is not handed on
+    assert (given == 1).all()
+    if with_residual:
+        assert torch.equal(only_total[2], only_total[0]) and torch.equal(only_y[2], only_y[0])
