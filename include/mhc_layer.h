@@ -173,12 +173,15 @@ MHC_API int64_t mhc_linear_bwd_workspace(int64_t T, int64_t I, int64_t O, mhc_ac
  * out.  Frequencies scaled for long contexts are the caller's table; the
  * angle is reduced from the exact product, so positions of millions keep
  * their FP32 accuracy.
- *   x            in   dtype, T x heads x D with strides x_token, x_head
+ *   x            in   dtype, T x heads x D with strides x_token, x_head: a
+ *                     token's heads lie inside its stride (x_token at least
+ *                     (heads - 1) x_head + D) or a head's tokens inside the
+ *                     head's (x_head at least (T - 1) x_token + D)
  *   positions    in   int64 [T]
  *   frequencies  in   FP32 [R / 2]
- *   out          out  dtype, strides out_token, out_head; may be x itself
- *                     (same pointer and strides), and must otherwise not
- *                     overlap it
+ *   out          out  dtype, strides out_token, out_head, a token's heads
+ *                     inside its stride; may be x itself (same pointer and
+ *                     strides), and must otherwise not overlap it
  * 0 <= R <= D, R even, D <= 65536.
  */
 MHC_API mhc_status_t mhc_rotary(const void* x, const int64_t* positions, const float* frequencies,

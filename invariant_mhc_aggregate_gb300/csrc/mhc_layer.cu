@@ -396,13 +396,15 @@ mhc_status_t mhc_rotary(const void* x, const int64_t* positions, const float* fr
     if (!dtype_ok(dtype) || T < 0 || heads < 0 || D < 0 || R < 0 || R > D || R % 2 != 0) return MHC_ERR_INVALID_ARG;
     if (D > 65536 || heads > 65536) return MHC_ERR_UNSUPPORTED;
     if (T == 0 || heads == 0 || D == 0) return MHC_OK;
-    // a head's span, then a token's
+    // a head's span, then a token's; x may also hold a head's tokens inside the head's stride
     if (x_head < D || out_head < D || x_head > INT64_MAX / 2 / heads || out_head > INT64_MAX / 2 / heads)
         return MHC_ERR_INVALID_ARG;
     const int64_t x_row = (heads - 1) * x_head + D, out_row = (heads - 1) * out_head + D;
+    const bool by_head = x_token < x_row;
+    if (by_head && (x_token < D || x_token > INT64_MAX / 2 / T)) return MHC_ERR_INVALID_ARG;
     const Buffer outs[1] = {rows(out, T, out_row, out_token, 2)};
     const bool in_place = x == out && x_token == out_token && x_head == out_head;
-    const Buffer bx = rows(x, T, x_row, x_token, 2);
+    const Buffer bx = by_head ? rows(x, heads, (T - 1) * x_token + D, x_head, 2) : rows(x, T, x_row, x_token, 2);
     const Buffer ins[3] = {in_place ? Buffer() : bx, dense(positions, T, 1, 8, R == 0),
                            dense(frequencies, 1, R / 2, 4, R == 0)};
     if (!bx.ok || !valid(outs, ins)) return MHC_ERR_INVALID_ARG;

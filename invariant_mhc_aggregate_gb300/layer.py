@@ -436,11 +436,13 @@ def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", f
 
 def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, interleaved: bool = False,
            scale: float = 1.0, inverse: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """x [T,heads,D] (bf16 or f16, any token and head strides) with the first
-    R = 2 len(frequencies) values of each head rotated by positions[t] *
-    frequencies[j] and multiplied by `scale`; pairs are (j, j + R/2), or
-    (2j, 2j + 1) when interleaved.  positions int64 [T].  inverse rotates back
-    (the gradient).  `out` may be x itself."""
+    """x [T,heads,D] (bf16 or f16) with the first R = 2 len(frequencies) values
+    of each head rotated by positions[t] * frequencies[j] and multiplied by
+    `scale`; pairs are (j, j + R/2), or (2j, 2j + 1) when interleaved.  x's
+    heads are contiguous and lie in either order, tokens or heads outermost,
+    with any distances at which they do not overlap.  positions int64 [T].
+    inverse rotates back (the gradient).  `out`, tokens outermost, may be x
+    itself."""
     if stream is None and out is None:
         done = (_fast or _compiled()).rotary(x, positions, frequencies, interleaved, float(scale), inverse)
         if done is not None:
@@ -467,7 +469,11 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, 
         if one != 1 and D > 1:
             raise ValueError(f"{name}'s heads must be contiguous, got strides {t.stride()}")
         head = head if heads > 1 else D
-        strides += [token if T > 1 else max(heads - 1, 0) * head + D, head]
+        row = max(heads - 1, 0) * head + D
+        token = token if T > 1 else row
+        if name == "x" and T > 0 and heads > 0 and (head < D or token < D or (token < row and head < (T - 1) * token + D)):
+            raise ValueError(f"x's heads must not overlap, got strides {t.stride()}")
+        strides += [token, head]
     _call(dev, "mhc_rotary", x.data_ptr(), positions.data_ptr(), frequencies.data_ptr(), out.data_ptr(), T, heads, D,
           2 * frequencies.shape[0], *strides, scale, int(interleaved), int(inverse), dt, _stream_handle(stream, dev))
     return out
