@@ -264,6 +264,12 @@ def mhc_post_sigmoid(x: torch.Tensor, y: torch.Tensor, mix: torch.Tensor, alpha:
 # the layer between the aggregate and the post (the calls of .layer)
 # ---------------------------------------------------------------------------
 
+def _rows(t, n):
+    """t as rows of n values, copied where these are not contiguous (a transposed t) or share memory (a broadcast one)."""
+    t = t.reshape(-1, n)
+    return t if t.stride(1) == 1 and t.stride(0) != 0 else t.contiguous()
+
+
 class RmsNorm(torch.autograd.Function):
     """(y, total): total = x + residual, y its RMS norm times weight; one
     kernel forward, two backward (the weight's gradient is summed over tokens
@@ -272,10 +278,10 @@ class RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
         H = x.shape[-1]
-        xx = x.reshape(-1, H)
-        rr = None if residual is None else residual.reshape(-1, H)
         if residual is not None and residual.shape != x.shape:
             raise ValueError(f"shape mismatch: x {tuple(x.shape)}, residual {tuple(residual.shape)}")
+        xx = _rows(x, H)
+        rr = None if residual is None else _rows(residual, H)
         y, total, rstd = layer.rms_norm(xx, weight.contiguous(), residual=rr, eps=eps)
         ctx.save_for_backward(total, weight, rstd)
         ctx.with_residual, ctx.shape = residual is not None, x.shape
@@ -311,10 +317,11 @@ class Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, activation, residual):
         I, O = x.shape[-1], weight.shape[0]
-        xx, ww = x.reshape(-1, I).contiguous(), weight.contiguous()
-        rr = None if residual is None else residual.reshape(-1, O)
         if residual is not None and residual.shape != (*x.shape[:-1], O):
             raise ValueError(f"shape mismatch: x {tuple(x.shape)}, residual {tuple(residual.shape)}")
+        xx, ww = x.reshape(-1, I).contiguous(), weight.contiguous()   # (the backward takes dense ones)
+        rr = None if residual is None else _rows(residual, O)
+        bias = None if bias is None else bias.contiguous()
         z = None
         if activation == "none":
             y = layer.linear(xx, ww, bias=bias, activation=activation, residual=rr)
@@ -355,6 +362,8 @@ class Rotary(torch.autograd.Function):
     def forward(ctx, x, positions, frequencies, interleaved, scale, inverse):
         ctx.save_for_backward(positions, frequencies)
         ctx.interleaved, ctx.scale, ctx.inverse = interleaved, scale, inverse
+        if x.dim() == 3 and (x.stride(2) != 1 or 0 in x.stride()):
+            x = x.contiguous()
         return layer.rotary(x, positions, frequencies, interleaved=interleaved, scale=scale, inverse=inverse)
 
     @staticmethod

@@ -145,3 +145,58 @@ def test_norm_outputs_without_a_gradient(with_residual, monkeypatch):
     assert (given == 1).all()
     if with_residual:
         assert torch.equal(only_total[2], only_total[0]) and torch.equal(only_y[2], only_y[0])
+
+
+@pytest.fixture
+def strict(formulas, monkeypatch):
+    """The stand-ins refuse what the kernels' calls refuse: rows that are not contiguous or share memory."""
+    def rows(t):
+        assert t is None or t.dim() != 2 or ((t.stride(1) == 1 or t.shape[1] == 1) and (t.stride(0) >= t.shape[1] or t.shape[0] == 1))
+
+    def product_strict(f):
+        def call(x, w, bias=None, activation="none", residual=None, stream=None):
+            for t in (x, w, residual):
+                rows(t)
+            assert bias is None or bias.is_contiguous()
+            return f(x, w, bias, activation, residual)
+        return call
+
+    def norm_strict(x, w, residual=None, eps=1e-6, stream=None):
+        rows(x), rows(residual)
+        assert w.is_contiguous()
+        return norm(x, w, residual, eps)
+
+    def rotary_strict(x, p, f, interleaved=False, scale=1.0, inverse=False):
+        assert x.stride(2) == 1 and 0 not in x.stride()
+        return x * scale
+
+    monkeypatch.setattr(layer, "rms_norm", norm_strict)
+    monkeypatch.setattr(layer, "linear", product_strict(product))
+    monkeypatch.setattr(layer, "linear_preact", product_strict(product_preact))
+    monkeypatch.setattr(layer, "rotary", rotary_strict)
+
+
+def layouts(*shape):
+    """The same shape transposed in memory, and broadcast over the rows."""
+    return {"transposed": bf(*shape[:-2], shape[-1], shape[-2]).detach().transpose(-1, -2),
+            "broadcast": bf(shape[-1]).detach().expand(*shape)}
+
+
+@pytest.mark.parametrize("layout", ["transposed", "broadcast"])
+def test_layouts_of_inputs(layout, strict):
+    x, r, big = layouts(6, 8)[layout], layouts(6, 8)[layout], layouts(3, 6, 8)[layout]
+    w = torch.rand(16)[::2]
+    for a, b in ((autograd.rms_norm(x, w, residual=r), autograd.rms_norm(x.contiguous(), w.contiguous(), residual=r.contiguous())),
+                 (autograd.rms_norm(big, w, residual=big), autograd.rms_norm(big.contiguous(), w, residual=big.contiguous()))):
+        assert all(torch.equal(s, t) for s, t in zip(a, b))
+    wl, bias, out = bf(5, 8).detach(), torch.rand(10)[::2], layouts(6, 5)[layout]
+    for act in ("none", "relu"):
+        got = autograd.linear(x, wl, bias=bias, activation=act, residual=out)
+        assert torch.equal(got, autograd.linear(x.contiguous(), wl, bias=bias.contiguous(), activation=act, residual=out.contiguous()))
+    q = layouts(4, 2, 8)[layout]
+    assert torch.equal(autograd.rotary(q, torch.arange(4), torch.ones(4), scale=2.0), q * 2)
+    # gradients come in the inputs' shapes
+    x.requires_grad_(), r.requires_grad_()
+    y, total = autograd.rms_norm(x, w, residual=r)
+    (autograd.linear(y, wl, residual=out).float().sum() + total.float().sum()).backward()
+    assert x.grad.shape == x.shape and r.grad.shape == r.shape
