@@ -53,7 +53,7 @@ LAYER_LIB_PATH = os.path.join(LIB_DIR, LAYER_LIB_NAME)
 LAYER_SOURCES = [os.path.join(CSRC, f) for f in
                  ("mhc_layer.cu", "mhc_launch_norm.cu", "mhc_launch_linear.cu", "mhc_launch_rotary.cu")]
 LAYER_DEPS = LAYER_SOURCES + [os.path.join(CSRC, f) for f in
-                              ("mhc_layer_launch.cuh", "mhc_norm.cuh", "mhc_linear.cuh", "mhc_umma.cuh", "mhc_rotary.cuh",
+                              ("mhc_layer_launch.cuh", "mhc_norm.cuh", "mhc_linear.cuh", "mhc_linear_plan.h", "mhc_umma.cuh", "mhc_rotary.cuh",
                                "mhc_launch.cuh", "mhc_device.cuh", "mhc_coeffs.cuh", "mhc_shift.cuh",
                                "mhc_shift_bulk.cuh", "mhc_bulk.cuh", "mhc_f32x2.cuh", "fastdiv.cuh")] \
     + [os.path.join(INCLUDE, f) for f in ("mhc_layer.h", "mhc_h_aggregate.h")]

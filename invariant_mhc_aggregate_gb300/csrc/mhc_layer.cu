@@ -13,15 +13,13 @@ namespace mhc {
 namespace layer {
 
 int num_sms() {
-    static std::atomic<int> cached{0};
-    int n = cached.load(std::memory_order_relaxed);
+    static std::atomic<int> cached[kMaxDevices];
+    const int dev = current_device();
+    if (dev < 0) return 152;
+    int n = cached[dev].load(std::memory_order_relaxed);
     if (n == 0) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) {
-            n = 152;
-        }
-        cached.store(n, std::memory_order_relaxed);
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 152;
+        cached[dev].store(n, std::memory_order_relaxed);
     }
     return n;
 }
