@@ -146,14 +146,6 @@ __device__ __forceinline__ void pdl_enter() {
     asm volatile("griddepcontrol.launch_dependents;" :::);
 }
 
-// For a kernel that neither reads what the kernel before it writes nor writes
-// what that one reads, where that one itself lets its successor start only
-// after a wait for everything earlier: it starts at once (pdl_start), and waits
-// before it ends (pdl_end), so that its own end still means the end of every
-// kernel before it.
-__device__ __forceinline__ void pdl_start() { asm volatile("griddepcontrol.launch_dependents;" :::); }
-__device__ __forceinline__ void pdl_end() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // --------------------------------------------------------------------------
 // storage <-> FP32: BF16 widening is exact (the pattern is the upper half of
 // the binary32 one), binary16 widening is exact too (cvt.f32.f16); narrowing

@@ -163,7 +163,6 @@ cudaError_t product(const Product& p, int in, int out, cudaStream_t stream) {
     a.e = p.e;
     a.N = p.N;
     a.rows = uint32_t(p.M);
-    a.beside = p.beside;
     a.kb = uint32_t((p.K * size + 127) / 128);
     const bool p_mn = p.b_mn, q_mn = p.a_mn;
     cudaError_t e = timeouts_ptr(&a.timeouts);

@@ -224,7 +224,7 @@ mhc_status_t linear_fwd(const void* x, const float* x_scale, const void* w, cons
     mhc::linear::Product p;
     p.a = a.p, p.b = b.p;
     p.a_stride = a.stride, p.a_mn = false, p.b_stride = b.stride, p.b_mn = false;
-    p.by_row = true, p.beside = false;
+    p.by_row = true;
     p.M = T, p.N = O, p.K = I;
     p.e = {fp8 ? x_scale : nullptr, fp8 ? w_scale : nullptr, bias, static_cast<const uint16_t*>(residual),
            static_cast<uint16_t*>(y), static_cast<uint16_t*>(preact), residual_stride, int(act)};
@@ -358,13 +358,11 @@ mhc_status_t mhc_linear_bwd(const void* g, const void* x, const void* w, const v
         if (e != cudaSuccess) return finish(e);
     }
     mhc::linear::Product p;
-    p.beside = false;
     if (act != MHC_ACT_NONE || grad_bias != nullptr) {
         e = mhc::layer::slope(static_cast<const uint16_t*>(g),
                               act == MHC_ACT_NONE ? nullptr : static_cast<const uint16_t*>(preact), own, grad_bias,
                               partial, T, O, u.pitch(), int(act), dtype, cu(stream));
         if (e != cudaSuccess) return finish(e);
-        p.beside = grad_bias != nullptr && (runs > 1 || act == MHC_ACT_NONE);   // (what it needs is there before its sums are)
     }
     p.e = {nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, mhc::linear::kActNone};
     if (want_x) {   // [T,I] = u [T,O] . w [O,I]
@@ -374,7 +372,6 @@ mhc_status_t mhc_linear_bwd(const void* g, const void* x, const void* w, const v
         p.e.y = static_cast<uint16_t*>(grad_x);
         e = mhc::layer::product(p, dtype, dtype, cu(stream));
         if (e != cudaSuccess) return finish(e);
-        p.beside = true;
     }
     if (want_w) {   // [O,I] = u^T [O,T] . x [T,I]
         p.a = u.p, p.a_stride = u.stride, p.a_mn = true;

@@ -70,9 +70,6 @@ struct Product {
     bool a_mn, b_mn;              // rows run along m (n), one for each k; else along k.  b_mn where a_mn.
     bool by_row;                  // a row's sums must not depend on M (its tokens): the forward and grad_x
     int64_t M, N, K;
-    // the launch just before reads and writes other memory than this call's operands and output
-    // (the sum of a bias gradient, the other gradient's product): run beside it
-    bool beside;
     Epilogue e;
 };
 
@@ -96,7 +93,6 @@ struct TileArgs {
     uint32_t unit, block_bytes;   // blocks of K of a stage, and bytes of each
     uint32_t idesc;
     uint32_t p_tiles, q_tiles;
-    bool beside;                  // see Product
     unsigned int* timeouts;
 };
 
@@ -257,11 +253,6 @@ __device__ __forceinline__ void drain(bool& ok, uint32_t issued, umma::Ring at, 
     }
 }
 
-__device__ __forceinline__ void enter(const TileArgs& a) {
-    if (a.beside) pdl_start();
-    else pdl_enter();
-}
-
 __device__ __forceinline__ void timed_out(const TileArgs& a) { *a.timeouts = 1u; }
 
 // --------------------------------------------------------------------------
@@ -322,7 +313,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     // the thread's place in the parts, [column][lane], that take the stages' place
     // once every copy has landed and been read
     float* part = reinterpret_cast<float*>(stages) + quarter * 32 + lane;
-    enter(a);
+    pdl_enter();
     const float bias = a.e.bias != nullptr && n_ok ? __ldg(a.e.bias + n) : 0.0f;
     const float cs = a.e.col_scale != nullptr && n_ok ? __ldg(a.e.col_scale + n) : 1.0f;
     const uint32_t ring = smem_addr(stages), bar_full = smem_addr(full), bar_empty = smem_addr(empty);
@@ -416,7 +407,6 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     }
     umma::fence_after_sync();
     if (warp == kSplitCopy) umma::tmem_free<1>(tmem, columns);
-    if (a.beside) pdl_end();
 }
 
 // --------------------------------------------------------------------------
@@ -535,7 +525,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
     umma::cluster_sync();   // the other CTA's barriers are ready too
     umma::fence_after_sync();
     const uint32_t tmem = tmem_base;
-    enter(a);
+    pdl_enter();
     const uint32_t ring = smem_addr(stages), bar_full = smem_addr(full), bar_empty = smem_addr(empty);
     const uint32_t bar_sum = smem_addr(sum_full), bar_free = smem_addr(sum_empty);
     const uint32_t count = a.stages, bytes = a.stage_bytes, unit = a.unit;
@@ -670,7 +660,6 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
     umma::cluster_sync();   // neither CTA leaves while the other may still signal it
     umma::fence_after_sync();
     if (warp == kCopyP) umma::tmem_free<2>(tmem, kTmemColumns);
-    if (a.beside) pdl_end();
 }
 
 // Rows of values copied to a row pitch that starts every row on 16 bytes, for
