@@ -241,8 +241,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
 def rms_norm_fp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
                  group: int = 0, stream=None):
     """(y8, scale, total, rstd): as rms_norm, with y in E4M3 and FP32 scales,
-    one per row (group = 0: [T,1]) or per 128 channels (group = 128:
-    [T,ceil(H/128)]); y is about y8 * scale."""
+    one per row (group = 0: [T,1], as linear_fp8 takes them) or per 128
+    channels (group = 128: [T,ceil(H/128)], for a product of the caller's with
+    scales along K; linear_fp8 takes one a row); y is about y8 * scale."""
     if stream is None and (group == 0 or group == 128):
         out = (_fast or _compiled()).rms_norm(x, weight, residual, eps, group)
         if out is not None:
@@ -376,8 +377,10 @@ def linear_fp8(x8: torch.Tensor, x_scale: torch.Tensor, w8: torch.Tensor, w_scal
 def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, z: torch.Tensor | None = None,
                     activation: str = "none", bias: bool = True, want=(True, True), stream=None):
     """(grad_x, grad_weight, grad_bias) of linear, from the gradient of y and,
-    with an activation, the forward's z.  grad_bias is FP32, None when `bias`
-    is false; `want` says which of grad_x and grad_weight to compute."""
+    with an activation, the forward's z (all of them dense).  grad_bias is FP32,
+    None when `bias` is false; `want` says which of grad_x and grad_weight to
+    compute.  Both read grad_y * act'(z) rounded to the storage type, as the
+    tensor cores take it; grad_bias sums it unrounded."""
     if stream is None and activation in ACTIVATIONS:
         out = (_fast or _compiled()).linear_backward(grad_y, x, weight, z, ACTIVATIONS[activation], bias, want[0], want[1])
         if out is not None:
@@ -413,11 +416,16 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
 def rotary_frequencies(dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
                        trained: int = 4096, fast: float = 32.0, slow: float = 1.0, device="cuda") -> torch.Tensor:
     """The FP32 table [dim/2] of a head's rotated part of `dim` values:
-    base^(-2j/dim), with `scaling` for contexts `factor` times the trained
-    length: "linear" divides every frequency by the factor, "ntk" raises the
-    base so that the slowest one is divided by it, "yarn" divides those that
-    turn fewer than `slow` times over the trained length, keeps those that turn
-    more than `fast` times and blends in between."""
+    f_j = base^(-2j/dim), with `scaling` for contexts `factor` times the
+    trained length: "linear" divides every frequency by the factor; "ntk"
+    raises the base so that the slowest one is divided by it; "yarn" (Peng et
+    al., 2023, "NTK-by-parts") goes by the turns r_j = trained f_j / (2 pi) that
+    a pair makes over the trained length: f_j (k + (1 - k) / factor), where
+    k = (r_j - slow) / (fast - slow), held within 0 and 1.  That ramp is linear
+    in the turns.  Checkpoints whose table ramps linearly in the channel index
+    j between the two bounds differ in the channels between; their table goes
+    to `rotary` as it is, like any other.  The magnitude that goes with a
+    scaling (0.1 ln(factor) + 1 for "yarn") is `rotary`'s scale."""
     if dim <= 0 or dim % 2:
         raise ValueError(f"dim must be positive and even, got {dim}")
     if scaling == "ntk" and dim > 2:
