@@ -140,6 +140,7 @@ MHC_API mhc_status_t mhc_linear_fp8_fwd(const void* x8, const float* x_scale, co
  *   grad_w[o,i] = cvt( sum over t of cvt(u[t,o]) * x[t,i] )     [O,I]
  *   grad_bias[o] = sum over t of u[t,o]                          FP32 [O]
  *
+ * cvt(u) is what the products' 16-bit operands hold; grad_bias sums u itself.
  * Each of the three may be NULL and is then not computed.  (The residual's
  * gradient is g.)  x, w, g and preact are dense.  workspace:
  * mhc_linear_bwd_workspace(...) bytes, 16-byte aligned.

@@ -421,7 +421,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
 // the first one holds every other part.  (Sums in registers instead, 64 or
 // 128 columns a thread, spilled: T = 4096, 7168 x 7168 269 to 330 us.)  Bound by
 // the tensor cores and their power: T = 4096, 7168 x 7168 225 us (1870 TFLOP/s)
-// in short runs, with bias, gelu and residual 279 us in long ones.
+// in short runs, with bias, gelu and residual 278 us in long ones.
 //
 // Warps 0-15 read tensor memory (four warps for each quarter of the lanes, a
 // quarter of the columns each).  Warp 16 copies P, warp 18 copies Q (a block of K
@@ -717,7 +717,11 @@ static __global__ void __launch_bounds__(kRepackThreads) repack_kernel(const Rep
 
 // u = g * act'(preact) over [T,O], rounded to u (row pitch `pitch`; null: not stored), and the
 // column sums of the unrounded u over each of gridDim.y runs of `rows` rows
-// in partial [gridDim.y, O] (null: not wanted).  Block (32, 8): 32 W columns,
+// in partial [gridDim.y, O] (null: not wanted).  u is rounded to the storage type since both
+// products read it as an operand of the tensor cores, which take 16 bits: BF16 grad_x and
+// grad_w are then 2.35e-3 off in norm (1.66e-3 is their own last rounding; T = 4096, 4096 x
+// 7168, silu); a second operand for the rest of u would double the products' work.
+// Block (32, 8): 32 W columns,
 // 8 rows at a time.  HBM-bound: T = 4096, O = 7168 29 us (176 MB, 90% of the copy
 // bandwidth; 50 us with the exact division and exponential).
 constexpr int kSlopeRows = 8;

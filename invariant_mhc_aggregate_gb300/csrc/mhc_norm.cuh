@@ -4,10 +4,10 @@
 // HBM-bound: about 5 operations per value that is read or written once.  A
 // row is held in registers between the sum of squares and the output, so each
 // value crosses HBM once.  Measured at H = 7168 with the residual, of the
-// copy bandwidth: T = 65536 with 8-bit output 513 us (94%), T = 4096 38.9 us
-// (89%; its start and its last rows are the rest), backward T = 4096 47.0 us
-// (74%: one block an SM, whose rows follow one another through two passes and
-// a barrier).
+// copy bandwidth: T = 65536 with 8-bit output 513 us (96%), T = 4096 38.9 us
+// (90%; its start and its last rows are the rest), backward T = 4096 47.0 us
+// (75%: one block an SM, whose rows follow one another through two passes and
+// a barrier, and the column sums' launch after it).
 //
 // Order of a row's sum (it depends on H only): the row is cut into chunks of
 // 8 values; thread j of the row's nt threads owns chunks j, j + nt, ... (at
