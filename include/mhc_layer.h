@@ -2,8 +2,9 @@
  * mhc_layer.h -- C ABI of the layer operators that stand between the mHC
  * aggregate and the mHC post (mhc_h_aggregate.h) on GB300 (sm_103a): RMS norm
  * with the residual's addition and an 8-bit output, matrix product with bias,
- * activation and residual, and rotary positions, each with its gradient.
- * Library: libmhc_layer.so.
+ * activation and residual, the gated product of a feed-forward, and rotary
+ * positions, and of the model's end: the cross entropy of a product over a
+ * vocabulary; each with its gradient.  Library: libmhc_layer.so.
  *
  * Storage types are BF16 and IEEE binary16 (mhc_dtype_t) and, for the 8-bit
  * output and operands, E4M3 (4 exponent bits, 3 mantissa bits, largest value
@@ -28,8 +29,10 @@
  * Determinism.  Results do not depend on timing: repeated calls give
  * identical bytes, no operator uses floating-point atomics, and every sum has
  * a fixed order.  The norm's and rotary's outputs and the product's y, z and
- * grad_x of a token depend only on that token's inputs and on the row sizes,
- * not on T: any split of the batch along T gives the same bytes.
+ * grad_x (the gated product's among them) and a cross entropy's loss and lse
+ * of a token depend only on that token's inputs and on the row sizes, not on
+ * T: any split of the batch along T gives the same bytes.  (A cross entropy's
+ * gradients depend on T.)
  */
 #ifndef MHC_LAYER_H
 #define MHC_LAYER_H
@@ -40,7 +43,8 @@
 extern "C" {
 #endif
 
-/* Version of this ABI; changes when a declaration here changes. */
+/* Version of this ABI; changes when a declaration here changes in a way that a
+ * caller compiled against it would notice (not when one is added). */
 MHC_API int32_t mhc_layer_abi_version(void);
 
 /* ---- RMS norm -------------------------------------------------------------
@@ -160,6 +164,117 @@ MHC_API int64_t mhc_linear_workspace(int64_t T, int64_t I, int64_t O, int64_t x_
 MHC_API int64_t mhc_linear_bwd_workspace(int64_t T, int64_t I, int64_t O, mhc_activation_t act,
                                          int32_t want_x, int32_t want_w, int32_t want_bias,
                                          int32_t aligned);
+
+/* ---- Gated product -----------------------------------------------------------
+ *
+ * The first half of a gated feed-forward: both projections, the activation
+ * and their product in one kernel.  w [2 F, I] holds the gate's rows 0 .. F-1
+ * and the up projection's F .. 2 F-1:
+ *
+ *   z[t,j] = (sum over i of x[t,i] * w[j,i]) (* x_scale[t] * w_scale[j]) + bias[j]
+ *   y[t,f] = cvt( act(z[t,f]) * z[t,F + f] )
+ *
+ * x [T,I] and w of one type (row strides x_stride, w_stride), scales FP32 [T]
+ * and [2 F] with E4M3 operands; bias FP32 [2 F] or NULL; y [T,F]; preact
+ * [T,2 F] or NULL takes cvt(z).  The types, the activations and the sums are
+ * the product's; 2 F takes the place of O in its limits and in
+ * mhc_linear_workspace(T, I, 2 F, ...), whose bytes workspace has.
+ */
+MHC_API mhc_status_t mhc_gated_linear_fwd(const void* x, const void* w, const float* bias, void* y,
+                                          void* preact, void* workspace, int64_t workspace_bytes,
+                                          int64_t T, int64_t I, int64_t F, int64_t x_stride,
+                                          int64_t w_stride, mhc_activation_t act,
+                                          mhc_dtype_t dtype, mhc_stream_t stream);
+
+/* E4M3 operands; dtype is the type of y and preact. */
+MHC_API mhc_status_t mhc_gated_linear_fp8_fwd(const void* x8, const float* x_scale, const void* w8,
+                                              const float* w_scale, const float* bias, void* y,
+                                              void* preact, void* workspace,
+                                              int64_t workspace_bytes, int64_t T, int64_t I,
+                                              int64_t F, int64_t x_stride, int64_t w_stride,
+                                              mhc_activation_t act, mhc_dtype_t dtype,
+                                              mhc_stream_t stream);
+
+/* Gradients, from g (the gradient of y, dense [T,F]) and the forward's preact
+ * (dense [T,2 F]; for every activation):
+ *
+ *   u[t,f]     = (g[t,f] * preact[t,F + f]) * act'(preact[t,f])
+ *   u[t,F + f] = g[t,f] * act(preact[t,f])
+ *   grad_x[t,i] = cvt( sum over j of cvt(u[t,j]) * w[j,i] )      [T,I]
+ *   grad_w[j,i] = cvt( sum over t of cvt(u[t,j]) * x[t,i] )      [2 F,I]
+ *   grad_bias[j] = sum over t of u[t,j]                           FP32 [2 F]
+ *
+ * cvt(u) is what the products' 16-bit operands hold; grad_bias sums u itself.
+ * Each of the three may be NULL and is then not computed.  x and w have row
+ * strides.  workspace: mhc_gated_linear_bwd_workspace(...) bytes, 16-byte
+ * aligned; aligned as in mhc_linear_workspace.
+ */
+MHC_API mhc_status_t mhc_gated_linear_bwd(const void* g, const void* x, const void* w,
+                                          const void* preact, void* grad_x, void* grad_w,
+                                          float* grad_bias, void* workspace,
+                                          int64_t workspace_bytes, int64_t T, int64_t I, int64_t F,
+                                          int64_t x_stride, int64_t w_stride, mhc_activation_t act,
+                                          mhc_dtype_t dtype, mhc_stream_t stream);
+
+MHC_API int64_t mhc_gated_linear_bwd_workspace(int64_t T, int64_t I, int64_t F, int64_t x_stride,
+                                               int64_t w_stride, int32_t want_x, int32_t want_w,
+                                               int32_t want_bias, int32_t aligned);
+
+/* ---- Cross entropy over a vocabulary -------------------------------------------
+ *
+ * The cross entropy of the logits z = x w^T with a target each, which are
+ * never stored:
+ *
+ *   z[t,v]  = sum over i of x[t,i] * w[v,i]                       (FP32)
+ *   lse[t]  = log( sum over v of exp(z[t,v]) )
+ *   loss[t] = lse[t] - z[t,target[t]]
+ *
+ * x [T,I] and w [V,I] of one type (row strides x_stride, w_stride); target
+ * int64 [T]; loss and lse FP32 [T].  A token whose target is outside 0 .. V-1
+ * (negative, as -100, by custom) is ignored: its loss is 0; its lse is
+ * computed all the same.  workspace:
+ * mhc_linear_cross_entropy_workspace(...) bytes, 16-byte aligned.
+ */
+MHC_API mhc_status_t mhc_linear_cross_entropy_fwd(const void* x, const void* w,
+                                                  const int64_t* target, float* loss, float* lse,
+                                                  void* workspace, int64_t workspace_bytes,
+                                                  int64_t T, int64_t I, int64_t V,
+                                                  int64_t x_stride, int64_t w_stride,
+                                                  mhc_dtype_t dtype, mhc_stream_t stream);
+
+MHC_API int64_t mhc_linear_cross_entropy_workspace(int64_t T, int64_t I, int64_t V,
+                                                   int64_t x_stride, int64_t w_stride,
+                                                   int32_t aligned);
+
+/* Gradients, from the gradients of loss and of lse (FP32 [T]; either may be
+ * NULL, for zeros, not both) and the forward's lse.  With g[t] =
+ * grad_loss[t], 0 for an ignored token:
+ *
+ *   d[t,v] = (g[t] + grad_lse[t]) * exp(z[t,v] - lse[t]) - (v == target[t] ? g[t] : 0)
+ *   grad_x[t,i] = cvt( sum over v of cvt(d[t,v]) * w[v,i] )       [T,I]
+ *   grad_w[v,i] = cvt( sum over t of cvt(d[t,v]) * x[t,i] )       [V,I]
+ *
+ * The logits are computed again, by pieces of the vocabulary; cvt(d) is d
+ * rounded to the operands' type after a scaling by a power of two (one for
+ * the whole call, from the largest gradient, taken out again in FP32), so
+ * that binary16 holds small probabilities.  grad_x or grad_w may be NULL and
+ * is then not computed.  A token without a gradient (g + grad_lse and g both
+ * 0) has d = 0 whatever its logits; its x still enters grad_w as 0 * x, so
+ * x must be finite there too.  workspace:
+ * mhc_linear_cross_entropy_bwd_workspace(...) bytes, 16-byte aligned.
+ */
+MHC_API mhc_status_t mhc_linear_cross_entropy_bwd(const float* grad_loss, const float* grad_lse,
+                                                  const void* x, const void* w,
+                                                  const int64_t* target, const float* lse,
+                                                  void* grad_x, void* grad_w, void* workspace,
+                                                  int64_t workspace_bytes, int64_t T, int64_t I,
+                                                  int64_t V, int64_t x_stride, int64_t w_stride,
+                                                  mhc_dtype_t dtype, mhc_stream_t stream);
+
+MHC_API int64_t mhc_linear_cross_entropy_bwd_workspace(int64_t T, int64_t I, int64_t V,
+                                                       int64_t x_stride, int64_t w_stride,
+                                                       int32_t want_x, int32_t want_w,
+                                                       int32_t aligned);
 
 /* ---- Rotary positions --------------------------------------------------------
  *

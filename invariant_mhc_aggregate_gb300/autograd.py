@@ -354,6 +354,78 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     return Linear.apply(x, weight, bias, activation, residual)
 
 
+class GatedLinear(torch.autograd.Function):
+    """act(x w_gate^T + b_gate) * (x w_up^T + b_up); one product forward (with
+    the pre-activations the backward reads, where there is to be one), three
+    kernels backward."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, activation, keep):
+        I = x.shape[-1]
+        xx, ww = _rows(x, I), _rows(weight, weight.shape[-1])
+        bias = None if bias is None else bias.contiguous()
+        if not keep:
+            return layer.gated_linear(xx, ww, bias=bias, activation=activation).reshape(*x.shape[:-1], -1)
+        y, z = layer.gated_linear_preact(xx, ww, bias=bias, activation=activation)
+        ctx.save_for_backward(xx, ww, z)
+        ctx.activation, ctx.lead, ctx.with_bias = activation, x.shape[:-1], bias is not None
+        return y.reshape(*x.shape[:-1], y.shape[-1])
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, grad_y):
+        x, w, z = ctx.saved_tensors
+        if grad_y.dtype != x.dtype:
+            raise TypeError(f"the output gradient must be {x.dtype}, got {grad_y.dtype}")
+        need = ctx.needs_input_grad
+        gx = gw = gb = None
+        if need[0] or need[1] or (need[2] and ctx.with_bias):
+            gx, gw, gb = layer.gated_linear_backward(grad_y.reshape(-1, z.shape[1] // 2).contiguous(), x, w, z,
+                                                     activation=ctx.activation, bias=need[2] and ctx.with_bias,
+                                                     want=(need[0], need[1]))
+        return None if gx is None else gx.reshape(*ctx.lead, x.shape[-1]), gw, gb, None, None
+
+
+def gated_linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
+                 activation: str = "silu") -> torch.Tensor:
+    """Differentiable layer.gated_linear, for x [...,I] of any leading shape."""
+    keep = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias))
+    return GatedLinear.apply(x, weight, bias, activation, keep)
+
+
+class LinearCrossEntropy(torch.autograd.Function):
+    """(loss, lse) of the logits x weight^T and their targets; the logits are
+    stored in neither direction, the backward computes them again."""
+
+    @staticmethod
+    def forward(ctx, x, weight, target):
+        I = x.shape[-1]
+        if target.shape != x.shape[:-1]:
+            raise ValueError(f"shape mismatch: x {tuple(x.shape)}, target {tuple(target.shape)}")
+        xx, ww, tt = _rows(x, I), _rows(weight, weight.shape[-1]), target.reshape(-1).contiguous()
+        loss, lse = layer.linear_cross_entropy(xx, ww, tt)
+        ctx.save_for_backward(xx, ww, tt, lse)
+        ctx.shape = x.shape
+        ctx.set_materialize_grads(False)   # an unused output has no gradient, not one of zeros to be read
+        return loss.reshape(target.shape), lse.reshape(target.shape).clone()
+
+    @staticmethod
+    @_first_order
+    def backward(ctx, grad_loss, grad_lse):
+        x, w, target, lse = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if (grad_loss is None and grad_lse is None) or not (need[0] or need[1]):
+            return None, None, None
+        gl, gs = (None if g is None else g.reshape(-1).contiguous() for g in (grad_loss, grad_lse))
+        gx, gw = layer.linear_cross_entropy_backward(gl, x, w, target, lse, grad_lse=gs, want=(need[0], need[1]))
+        return None if gx is None else gx.reshape(ctx.shape), gw, None
+
+
+def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor):
+    """Differentiable (loss, lse) of layer.linear_cross_entropy, for x [...,I] and target [...] of any leading shape."""
+    return LinearCrossEntropy.apply(x, weight, target)
+
+
 class Rotary(torch.autograd.Function):
     """layer.rotary; the gradient is the rotation by the opposite angle, which
     is differentiable the same way."""

@@ -1,0 +1,88 @@
+// Launch shapes of the gated product.
+#include "mhc_gated.cuh"
+#include "mhc_linear_launch.cuh"
+
+namespace mhc {
+namespace layer {
+
+namespace {
+
+// w [2 F, I] as {I, F, 2}: a box has 128 bytes of K of 16 rows of the gate and
+// of the same 16 of the up projection, and rows at or past F read as zero in
+// each half.
+cudaError_t encode_gated(CUtensorMap* map, const void* w, int64_t F, int64_t I, int64_t stride, int64_t size) {
+    const PFN_cuTensorMapEncodeTiled_v12000 f = tensor_map_encoder();
+    if (f == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {cuuint64_t(I), cuuint64_t(F), 2};
+    const cuuint64_t strides[2] = {cuuint64_t(stride * size), cuuint64_t(F * stride * size)};
+    const cuuint32_t box[3] = {cuuint32_t(128 / size), 16, 2};
+    const cuuint32_t step[3] = {1, 1, 1};
+    const bool sectors = strides[0] % 32 == 0 && reinterpret_cast<uintptr_t>(w) % 32 == 0;   // (as in encode)
+    const CUresult r = f(map, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(w),
+                         dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         sectors ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <bool FP8, int OUT>
+cudaError_t launch_gated(bool pair, const TileArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed[3];
+    if (!pair) return launch_split_kernel(split_kernel<FP8, OUT, kBothK, kEndGated>, allowed[0], a, mp, mq, stream);
+    if (a.splits > 1)
+        return launch_pair_kernel(pair_kernel<FP8, OUT, kBothK, true, kEndGated>, allowed[1], a, pairs_of(a), mp, mq, stream);
+    return launch_pair_kernel(pair_kernel<FP8, OUT, kBothK, false, kEndGated>, allowed[2], a, pairs_of(a), mp, mq, stream);
+}
+
+template <int DT, int W>
+auto slope_kernel_of(int act) {
+    switch (act) {
+        case kActRelu: return gated::slope_kernel<DT, W, kActRelu>;
+        case kActSilu: return gated::slope_kernel<DT, W, kActSilu>;
+        case kActGelu: return gated::slope_kernel<DT, W, kActGelu>;
+        default: return gated::slope_kernel<DT, W, kActNone>;
+    }
+}
+
+}  // namespace
+
+cudaError_t gated_product(const Product& p, int in, int out, cudaStream_t stream) {
+    TileArgs a;
+    CUtensorMap mp, mq;
+    const Plan plan = plan_of(p.N, p.M, k_blocks(p, in), false, true);
+    cudaError_t e = lay_out(p, in, plan, a, mp, mq);
+    if (e != cudaSuccess) return e;
+    a.end = {};
+    a.end.half = p.N / 2;
+    e = encode_gated(&mp, p.b, p.N / 2, p.K, p.b_stride, in == kE4m3 ? 1 : 2);
+    if (e != cudaSuccess) return e;
+    if (in == kE4m3)
+        return out == kBF16 ? launch_gated<true, kBF16>(plan.pair, a, mp, mq, stream)
+                            : launch_gated<true, kF16>(plan.pair, a, mp, mq, stream);
+    return out == kBF16 ? launch_gated<false, kBF16>(plan.pair, a, mp, mq, stream)
+                        : launch_gated<false, kF16>(plan.pair, a, mp, mq, stream);
+}
+
+cudaError_t gated_slope(const uint16_t* g, const uint16_t* preact, uint16_t* u, float* grad_bias, float* partial, int64_t T,
+                        int64_t F, int64_t pitch, int act, int dtype, cudaStream_t stream) {
+    const int64_t runs = slope_partials(T), rows = (T + runs - 1) / runs;
+    float* sums = grad_bias == nullptr ? nullptr : runs > 1 ? partial : grad_bias;
+    const bool vec = F % 8 == 0 && pitch % 8 == 0 && aligned(g, 16) && aligned(preact, 16) && aligned(u, 16);   // null is aligned
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(uint32_t((F + (vec ? 255 : 31)) / (vec ? 256 : 32)), uint32_t(runs));
+    cfg.blockDim = dim3(32, kSlopeRows);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto* kernel = dtype == kBF16 ? (vec ? slope_kernel_of<kBF16, 8>(act) : slope_kernel_of<kBF16, 1>(act))
+                                  : (vec ? slope_kernel_of<kF16, 8>(act) : slope_kernel_of<kF16, 1>(act));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, g, preact, u, sums, T, F, pitch, rows);
+    if (e != cudaSuccess || grad_bias == nullptr || runs == 1) return e;
+    return column_sum(partial, grad_bias, uint32_t(runs), 2 * F, 2 * F, stream);
+}
+
+}  // namespace layer
+}  // namespace mhc

@@ -196,17 +196,27 @@ struct Operand {
 
 inline bool act_ok(int32_t a) { return a >= MHC_ACT_NONE && a <= MHC_ACT_GELU; }
 
+// Copies the operands that do not lie in place, two a launch.
+cudaError_t lay_out_again(const mhc::layer::RepackCall* calls, int count, mhc_stream_t stream) {
+    for (int i = 0; i < count; i += 2) {
+        const cudaError_t e = mhc::layer::repack(calls + i, count - i < 2 ? 1 : 2, cu(stream));
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// gated: w is [2 F, I] and O = 2 F, y [T, O / 2].
 mhc_status_t linear_fwd(const void* x, const float* x_scale, const void* w, const float* w_scale, const float* bias,
                         const void* residual, void* y, void* preact, void* workspace, int64_t workspace_bytes,
                         int64_t T, int64_t I, int64_t O, int64_t x_stride, int64_t w_stride, int64_t residual_stride,
-                        int32_t act, bool fp8, int32_t dtype, mhc_stream_t stream) {
+                        int32_t act, bool fp8, bool gated, int32_t dtype, mhc_stream_t stream) {
     if (!dtype_ok(dtype) || !act_ok(act) || T < 0 || I <= 0 || O <= 0) return MHC_ERR_INVALID_ARG;
     if (T > kMaxSide || I > kMaxSide || O > kMaxSide) return MHC_ERR_UNSUPPORTED;
     if (T == 0) return MHC_OK;
     const int64_t size = fp8 ? 1 : 2;
     Operand a(x, T, I, x_stride, size, aligned(x, 16)), b(w, O, I, w_stride, size, aligned(w, 16));
     const int64_t need = a.bytes() + b.bytes();
-    const Buffer outs[3] = {dense(y, T, O, 2), dense(preact, T, O, 2, true),
+    const Buffer outs[3] = {dense(y, T, gated ? O / 2 : O, 2), dense(preact, T, O, 2, true),
                             workspace_of(workspace, workspace_bytes, need)};
     const Buffer ins[6] = {rows(x, T, I, x_stride, size), rows(w, O, I, w_stride, size),
                            dense(x_scale, T, 1, 4, !fp8), dense(w_scale, O, 1, 4, !fp8), dense(bias, O, 1, 4, true),
@@ -217,10 +227,8 @@ mhc_status_t linear_fwd(const void* x, const float* x_scale, const void* w, cons
     int count = 0;
     a.place(at, calls, count);
     b.place(at, calls, count);
-    if (count > 0) {
-        const cudaError_t e = mhc::layer::repack(calls, count, cu(stream));
-        if (e != cudaSuccess) return finish(e);
-    }
+    const cudaError_t e = lay_out_again(calls, count, stream);
+    if (e != cudaSuccess) return finish(e);
     mhc::linear::Product p;
     p.a = a.p, p.b = b.p;
     p.a_stride = a.stride, p.a_mn = false, p.b_stride = b.stride, p.b_mn = false;
@@ -228,8 +236,29 @@ mhc_status_t linear_fwd(const void* x, const float* x_scale, const void* w, cons
     p.M = T, p.N = O, p.K = I;
     p.e = {fp8 ? x_scale : nullptr, fp8 ? w_scale : nullptr, bias, static_cast<const uint16_t*>(residual),
            static_cast<uint16_t*>(y), static_cast<uint16_t*>(preact), residual_stride, int(act)};
-    return finish(mhc::layer::product(p, fp8 ? mhc::linear::kE4m3 : int(dtype), dtype, cu(stream)));
+    const int in = fp8 ? mhc::linear::kE4m3 : int(dtype);
+    return finish(gated ? mhc::layer::gated_product(p, in, dtype, cu(stream)) : mhc::layer::product(p, in, dtype, cu(stream)));
 }
+
+// ---- cross entropy -------------------------------------------------------------
+
+// Entries of the vocabulary whose logits' gradients are in the workspace at a time.
+int64_t entropy_piece(int64_t T, int64_t V) {
+    const int64_t most = 16384;
+    return V < most ? (V + 63) / 64 * 64 : most;
+}
+
+struct EntropySizes {
+    int64_t piece, tokens, factor, d, sums;   // entries; bytes of each part of the workspace
+    EntropySizes(int64_t T, int64_t I, int64_t V, bool want_x) {
+        piece = entropy_piece(T, V);
+        tokens = T * int64_t(sizeof(mhc::linear::EntropyToken));
+        factor = 16;
+        d = round16(T * piece * 2);
+        sums = want_x && piece < V ? round16(T * I * 4) : 0;
+    }
+    int64_t bytes() const { return tokens + factor + d + sums; }
+};
 
 }  // namespace
 
@@ -282,7 +311,7 @@ mhc_status_t mhc_linear_fwd(const void* x, const void* w, const float* bias, con
                             int64_t x_stride, int64_t w_stride, int64_t residual_stride, mhc_activation_t act,
                             mhc_dtype_t dtype, mhc_stream_t stream) {
     return linear_fwd(x, nullptr, w, nullptr, bias, residual, y, preact, workspace, workspace_bytes, T, I, O, x_stride,
-                      w_stride, residual_stride, act, false, dtype, stream);
+                      w_stride, residual_stride, act, false, false, dtype, stream);
 }
 
 mhc_status_t mhc_linear_fp8_fwd(const void* x8, const float* x_scale, const void* w8, const float* w_scale,
@@ -291,7 +320,24 @@ mhc_status_t mhc_linear_fp8_fwd(const void* x8, const float* x_scale, const void
                                 int64_t w_stride, int64_t residual_stride, mhc_activation_t act, mhc_dtype_t dtype,
                                 mhc_stream_t stream) {
     return linear_fwd(x8, x_scale, w8, w_scale, bias, residual, y, preact, workspace, workspace_bytes, T, I, O,
-                      x_stride, w_stride, residual_stride, act, true, dtype, stream);
+                      x_stride, w_stride, residual_stride, act, true, false, dtype, stream);
+}
+
+mhc_status_t mhc_gated_linear_fwd(const void* x, const void* w, const float* bias, void* y, void* preact, void* workspace,
+                                  int64_t workspace_bytes, int64_t T, int64_t I, int64_t F, int64_t x_stride,
+                                  int64_t w_stride, mhc_activation_t act, mhc_dtype_t dtype, mhc_stream_t stream) {
+    if (F > kMaxSide / 2) return MHC_ERR_UNSUPPORTED;
+    return linear_fwd(x, nullptr, w, nullptr, bias, nullptr, y, preact, workspace, workspace_bytes, T, I, 2 * F, x_stride,
+                      w_stride, 2 * F, act, false, true, dtype, stream);
+}
+
+mhc_status_t mhc_gated_linear_fp8_fwd(const void* x8, const float* x_scale, const void* w8, const float* w_scale,
+                                      const float* bias, void* y, void* preact, void* workspace, int64_t workspace_bytes,
+                                      int64_t T, int64_t I, int64_t F, int64_t x_stride, int64_t w_stride,
+                                      mhc_activation_t act, mhc_dtype_t dtype, mhc_stream_t stream) {
+    if (F > kMaxSide / 2) return MHC_ERR_UNSUPPORTED;
+    return linear_fwd(x8, x_scale, w8, w_scale, bias, nullptr, y, preact, workspace, workspace_bytes, T, I, 2 * F,
+                      x_stride, w_stride, 2 * F, act, true, true, dtype, stream);
 }
 
 // The workspace of the backward: u with rows on 16-byte boundaries, where it
@@ -353,10 +399,8 @@ mhc_status_t mhc_linear_bwd(const void* g, const void* x, const void* w, const v
     if (want_x || want_w) u.place(at, calls, count);
     if (want_w) xo.place(at, calls, count);
     if (want_x) wo.place(at, calls, count);
-    for (int i = 0; i < count; i += 2) {
-        e = mhc::layer::repack(calls + i, count - i < 2 ? 1 : 2, cu(stream));
-        if (e != cudaSuccess) return finish(e);
-    }
+    e = lay_out_again(calls, count, stream);
+    if (e != cudaSuccess) return finish(e);
     mhc::linear::Product p;
     if (act != MHC_ACT_NONE || grad_bias != nullptr) {
         e = mhc::layer::slope(static_cast<const uint16_t*>(g),
@@ -382,6 +426,184 @@ mhc_status_t mhc_linear_bwd(const void* g, const void* x, const void* w, const v
         if (e != cudaSuccess) return finish(e);
     }
     return finish(cudaSuccess);
+}
+
+// The workspace of the gated backward: u with rows on 16-byte boundaries, the
+// operands laid out again, the column sums of the bias gradient.
+static int64_t gated_bwd_workspace(int64_t T, int64_t I, int64_t F, int64_t x_stride, int64_t w_stride, bool want_x,
+                                   bool want_w, bool want_bias, bool x_aligned, bool w_aligned) {
+    const int64_t runs = mhc::layer::slope_partials(T);
+    int64_t n = want_bias && runs > 1 ? round16(runs * 2 * F * 4) : 0;
+    if (want_x || want_w) n += T * round16(2 * F) * 2;
+    if (want_w) n += Operand(nullptr, T, I, x_stride, 2, x_aligned).bytes();
+    if (want_x) n += Operand(nullptr, 2 * F, I, w_stride, 2, w_aligned).bytes();
+    return n;
+}
+
+int64_t mhc_gated_linear_bwd_workspace(int64_t T, int64_t I, int64_t F, int64_t x_stride, int64_t w_stride,
+                                       int32_t want_x, int32_t want_w, int32_t want_bias, int32_t aligned) {
+    if (T <= 0 || I <= 0 || F <= 0 || T > kMaxSide || I > kMaxSide || F > kMaxSide / 2) return 0;
+    return gated_bwd_workspace(T, I, F, x_stride, w_stride, want_x != 0, want_w != 0, want_bias != 0, aligned != 0, aligned != 0);
+}
+
+mhc_status_t mhc_gated_linear_bwd(const void* g, const void* x, const void* w, const void* preact, void* grad_x,
+                                  void* grad_w, float* grad_bias, void* workspace, int64_t workspace_bytes, int64_t T,
+                                  int64_t I, int64_t F, int64_t x_stride, int64_t w_stride, mhc_activation_t act,
+                                  mhc_dtype_t dtype, mhc_stream_t stream) {
+    if (!dtype_ok(dtype) || !act_ok(act) || T < 0 || I <= 0 || F <= 0) return MHC_ERR_INVALID_ARG;
+    if (T > kMaxSide || I > kMaxSide || F > kMaxSide / 2) return MHC_ERR_UNSUPPORTED;
+    const int64_t O = 2 * F;
+    if (T == 0) {
+        const Buffer outs[2] = {dense(grad_w, O, I, 2, true), dense(grad_bias, O, 1, 4, true)};
+        if (!outs[0].ok || !outs[1].ok) return MHC_ERR_INVALID_ARG;
+        cudaError_t e = cudaSuccess;
+        if (grad_w != nullptr) e = cudaMemsetAsync(grad_w, 0, size_t(O) * I * 2, cu(stream));
+        if (e == cudaSuccess && grad_bias != nullptr) e = cudaMemsetAsync(grad_bias, 0, size_t(O) * 4, cu(stream));
+        return finish(e);
+    }
+    const bool want_x = grad_x != nullptr, want_w = grad_w != nullptr, want_u = want_x || want_w;
+    Operand xo(x, T, I, x_stride, 2, aligned(x, 16)), wo(w, O, I, w_stride, 2, aligned(w, 16));
+    const int64_t need = gated_bwd_workspace(T, I, F, x_stride, w_stride, want_x, want_w, grad_bias != nullptr,
+                                             aligned(x, 16), aligned(w, 16));
+    const Buffer outs[4] = {dense(grad_x, T, I, 2, true), dense(grad_w, O, I, 2, true), dense(grad_bias, O, 1, 4, true),
+                            workspace_of(workspace, workspace_bytes, need)};
+    const Buffer ins[4] = {dense(g, T, F, 2), rows(x, T, I, x_stride, 2, !want_w), rows(w, O, I, w_stride, 2, !want_x),
+                           dense(preact, T, O, 2)};
+    if (!valid(outs, ins)) return MHC_ERR_INVALID_ARG;
+    if (!want_u && grad_bias == nullptr) return MHC_OK;
+    char* at = static_cast<char*>(workspace);
+    const int64_t pitch = round16(O);
+    // what the tensor copies read first: on sectors in a workspace that starts on one
+    uint16_t* u = want_u ? reinterpret_cast<uint16_t*>(at) : nullptr;
+    if (want_u) at += T * pitch * 2;
+    mhc::layer::RepackCall calls[2];
+    int count = 0;
+    if (want_w) xo.place(at, calls, count);
+    if (want_x) wo.place(at, calls, count);
+    float* partial = reinterpret_cast<float*>(at);
+    cudaError_t e = lay_out_again(calls, count, stream);
+    if (e != cudaSuccess) return finish(e);
+    e = mhc::layer::gated_slope(static_cast<const uint16_t*>(g), static_cast<const uint16_t*>(preact), u, grad_bias, partial,
+                                T, F, pitch, int(act), dtype, cu(stream));
+    if (e != cudaSuccess) return finish(e);
+    mhc::linear::Product p;
+    p.e = {nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, mhc::linear::kActNone};
+    if (want_x) {   // [T,I] = u [T,2 F] . w [2 F,I]
+        p.a = u, p.a_stride = pitch, p.a_mn = false;
+        p.b = wo.p, p.b_stride = wo.stride, p.b_mn = true;
+        p.M = T, p.N = I, p.K = O, p.by_row = true;
+        p.e.y = static_cast<uint16_t*>(grad_x);
+        e = mhc::layer::product(p, dtype, dtype, cu(stream));
+        if (e != cudaSuccess) return finish(e);
+    }
+    if (want_w) {   // [2 F,I] = u^T [2 F,T] . x [T,I]
+        p.a = u, p.a_stride = pitch, p.a_mn = true;
+        p.b = xo.p, p.b_stride = xo.stride, p.b_mn = true;
+        p.M = O, p.N = I, p.K = T, p.by_row = false;
+        p.e.y = static_cast<uint16_t*>(grad_w);
+        e = mhc::layer::product(p, dtype, dtype, cu(stream));
+        if (e != cudaSuccess) return finish(e);
+    }
+    return finish(cudaSuccess);
+}
+
+static bool entropy_sizes_ok(int64_t T, int64_t I, int64_t V) { return T <= kMaxSide && I <= kMaxSide && V <= kMaxSide; }
+
+// The workspace of the forward: a pair for each group and token, the targets'
+// logits, the operands laid out again.
+static int64_t entropy_workspace(int64_t T, int64_t I, int64_t V, int64_t x_stride, int64_t w_stride, bool x_aligned,
+                                 bool w_aligned) {
+    return mhc::layer::entropy_groups(V) * T * 8 + T * 4 + 12 + Operand(nullptr, T, I, x_stride, 2, x_aligned).bytes() +
+           Operand(nullptr, V, I, w_stride, 2, w_aligned).bytes();
+}
+
+int64_t mhc_linear_cross_entropy_workspace(int64_t T, int64_t I, int64_t V, int64_t x_stride, int64_t w_stride,
+                                           int32_t aligned) {
+    if (T <= 0 || I <= 0 || V <= 0 || !entropy_sizes_ok(T, I, V)) return 0;
+    return entropy_workspace(T, I, V, x_stride, w_stride, aligned != 0, aligned != 0);
+}
+
+mhc_status_t mhc_linear_cross_entropy_fwd(const void* x, const void* w, const int64_t* target, float* loss, float* lse,
+                                          void* workspace, int64_t workspace_bytes, int64_t T, int64_t I, int64_t V,
+                                          int64_t x_stride, int64_t w_stride, mhc_dtype_t dtype, mhc_stream_t stream) {
+    if (!dtype_ok(dtype) || T < 0 || I <= 0 || V <= 0) return MHC_ERR_INVALID_ARG;
+    if (!entropy_sizes_ok(T, I, V)) return MHC_ERR_UNSUPPORTED;
+    if (T == 0) return MHC_OK;
+    Operand xo(x, T, I, x_stride, 2, aligned(x, 16)), wo(w, V, I, w_stride, 2, aligned(w, 16));
+    const int64_t need = entropy_workspace(T, I, V, x_stride, w_stride, aligned(x, 16), aligned(w, 16));
+    const Buffer outs[3] = {dense(loss, T, 1, 4), dense(lse, T, 1, 4), workspace_of(workspace, workspace_bytes, need)};
+    const Buffer ins[3] = {rows(x, T, I, x_stride, 2), rows(w, V, I, w_stride, 2), dense(target, T, 1, 8)};
+    if (!valid(outs, ins)) return MHC_ERR_INVALID_ARG;
+    char* at = static_cast<char*>(workspace);
+    mhc::layer::RepackCall calls[2];
+    int count = 0;
+    xo.place(at, calls, count);
+    wo.place(at, calls, count);
+    const cudaError_t e = lay_out_again(calls, count, stream);
+    if (e != cudaSuccess) return finish(e);
+    float2* partial = reinterpret_cast<float2*>(at);
+    at += mhc::layer::entropy_groups(V) * T * 8;
+    const mhc::layer::EntropyCall c = {xo.p, wo.p, target, T, I, V, xo.stride, wo.stride, int(dtype), cu(stream)};
+    return finish(mhc::layer::entropy_fwd(c, loss, lse, partial, reinterpret_cast<float*>(at)));
+}
+
+static int64_t entropy_bwd_workspace(int64_t T, int64_t I, int64_t V, int64_t x_stride, int64_t w_stride, bool want_x,
+                                     bool x_aligned, bool w_aligned) {
+    return EntropySizes(T, I, V, want_x).bytes() + Operand(nullptr, T, I, x_stride, 2, x_aligned).bytes() +
+           Operand(nullptr, V, I, w_stride, 2, w_aligned).bytes();
+}
+
+int64_t mhc_linear_cross_entropy_bwd_workspace(int64_t T, int64_t I, int64_t V, int64_t x_stride, int64_t w_stride,
+                                               int32_t want_x, int32_t want_w, int32_t aligned) {
+    if (T <= 0 || I <= 0 || V <= 0 || !entropy_sizes_ok(T, I, V) || (want_x == 0 && want_w == 0)) return 0;
+    return entropy_bwd_workspace(T, I, V, x_stride, w_stride, want_x != 0, aligned != 0, aligned != 0);
+}
+
+mhc_status_t mhc_linear_cross_entropy_bwd(const float* grad_loss, const float* grad_lse, const void* x, const void* w,
+                                          const int64_t* target, const float* lse, void* grad_x, void* grad_w,
+                                          void* workspace, int64_t workspace_bytes, int64_t T, int64_t I, int64_t V,
+                                          int64_t x_stride, int64_t w_stride, mhc_dtype_t dtype, mhc_stream_t stream) {
+    if (!dtype_ok(dtype) || T < 0 || I <= 0 || V <= 0) return MHC_ERR_INVALID_ARG;
+    if (!entropy_sizes_ok(T, I, V)) return MHC_ERR_UNSUPPORTED;
+    if (T == 0) {
+        const Buffer out = dense(grad_w, V, I, 2, true);
+        if (!out.ok) return MHC_ERR_INVALID_ARG;
+        return finish(grad_w == nullptr ? cudaSuccess : cudaMemsetAsync(grad_w, 0, size_t(V) * I * 2, cu(stream)));
+    }
+    const bool want_x = grad_x != nullptr, want_w = grad_w != nullptr;
+    Operand xo(x, T, I, x_stride, 2, aligned(x, 16)), wo(w, V, I, w_stride, 2, aligned(w, 16));
+    const EntropySizes sizes(T, I, V, want_x);
+    const int64_t need = !want_x && !want_w ? 0 : entropy_bwd_workspace(T, I, V, x_stride, w_stride, want_x, aligned(x, 16), aligned(w, 16));
+    const Buffer outs[3] = {dense(grad_x, T, I, 2, true), dense(grad_w, V, I, 2, true),
+                            workspace_of(workspace, workspace_bytes, need)};
+    const Buffer ins[6] = {dense(grad_loss, T, 1, 4, grad_lse != nullptr), dense(grad_lse, T, 1, 4, true), rows(x, T, I, x_stride, 2),
+                           rows(w, V, I, w_stride, 2), dense(target, T, 1, 8), dense(lse, T, 1, 4)};
+    if (!valid(outs, ins)) return MHC_ERR_INVALID_ARG;
+    if (!want_x && !want_w) return MHC_OK;
+    char* at = static_cast<char*>(workspace);
+    // what the tensor copies read first: on sectors in a workspace that starts on one
+    uint16_t* d = reinterpret_cast<uint16_t*>(at);
+    at += sizes.d;
+    mhc::layer::RepackCall calls[2];
+    int count = 0;
+    xo.place(at, calls, count);
+    wo.place(at, calls, count);
+    float* sums = reinterpret_cast<float*>(at);
+    at += sizes.sums;
+    auto* tokens = reinterpret_cast<mhc::linear::EntropyToken*>(at);
+    float* factor = reinterpret_cast<float*>(at + sizes.tokens);
+    cudaError_t e = lay_out_again(calls, count, stream);
+    const mhc::layer::EntropyCall c = {xo.p, wo.p, target, T, I, V, xo.stride, wo.stride, int(dtype), cu(stream)};
+    if (e == cudaSuccess) e = mhc::layer::entropy_tokens(c, grad_loss, grad_lse, lse, tokens, factor);
+    for (int64_t v = 0; v < V && e == cudaSuccess; v += sizes.piece) {
+        const int64_t n = V - v < sizes.piece ? V - v : sizes.piece;
+        e = mhc::layer::entropy_logit_grad(c, tokens, v, n, d, sizes.piece);
+        if (e == cudaSuccess && want_x)
+            e = mhc::layer::entropy_grad_x(c, d, sizes.piece, v, n, v == 0 ? nullptr : sums, v + n < V ? sums : nullptr, factor,
+                                           grad_x);
+        if (e == cudaSuccess && want_w) e = mhc::layer::entropy_grad_w(c, d, sizes.piece, v, n, factor, grad_w);
+    }
+    return finish(e);
 }
 
 mhc_status_t mhc_rotary(const void* x, const int64_t* positions, const float* frequencies, void* out, int64_t T,

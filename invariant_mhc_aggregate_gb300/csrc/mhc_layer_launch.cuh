@@ -54,6 +54,37 @@ cudaError_t repack(const RepackCall* calls, int count, cudaStream_t stream);   /
 cudaError_t slope(const uint16_t* g, const uint16_t* preact, uint16_t* u, float* grad_bias, float* partial, int64_t T,
                   int64_t O, int64_t pitch, int act, int dtype, cudaStream_t stream);
 int64_t slope_partials(int64_t T);
+// The gated product (mhc_launch_gated.cu): p.b is w [2 F, I], p.N = 2 F.
+cudaError_t gated_product(const linear::Product& p, int in, int out, cudaStream_t stream);
+// u = [g up act'(gate) | g act(gate)] of preact [T, 2 F]; the rest as in slope, with 2 F columns.
+cudaError_t gated_slope(const uint16_t* g, const uint16_t* preact, uint16_t* u, float* grad_bias, float* partial, int64_t T,
+                        int64_t F, int64_t pitch, int act, int dtype, cudaStream_t stream);
+
+// Cross entropy over a vocabulary (mhc_launch_entropy.cu).  The operands'
+// rows start on 16-byte boundaries.
+struct EntropyCall {
+    const void* x;
+    const void* w;
+    const int64_t* target;
+    int64_t T, I, V;
+    int64_t x_stride, w_stride;
+    int dtype;
+    cudaStream_t stream;
+};
+int64_t entropy_groups(int64_t V);
+// partial: entropy_groups(V) * T, at: T.
+cudaError_t entropy_fwd(const EntropyCall& c, float* loss, float* lse, float2* partial, float* at);
+cudaError_t entropy_tokens(const EntropyCall& c, const float* grad_loss, const float* grad_lse, const float* lse,
+                           linear::EntropyToken* tokens, float* factor);
+// The gradient of `count` logits from `first` on, [T,count] at row pitch `pitch`.
+cudaError_t entropy_logit_grad(const EntropyCall& c, const linear::EntropyToken* tokens, int64_t first, int64_t count, uint16_t* d,
+                               int64_t pitch);
+// grad_x += d w[first ..]: onto sum_in (null: onto nothing), into sum_out or, where that is null, rounded into grad_x.
+cudaError_t entropy_grad_x(const EntropyCall& c, const uint16_t* d, int64_t pitch, int64_t first, int64_t count, const float* sum_in,
+                           float* sum_out, const float* factor, void* grad_x);
+cudaError_t entropy_grad_w(const EntropyCall& c, const uint16_t* d, int64_t pitch, int64_t first, int64_t count, const float* factor,
+                           void* grad_w);
+
 // The device address of the flag that these kernels set when a bounded wait
 // runs out, for the current device.
 cudaError_t timeouts_ptr(unsigned int** p);

@@ -255,6 +255,153 @@ PyObject* linear_backward(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     });
 }
 
+// gated_linear(x, x_scale, w, w_scale, bias, act, out_type, keep) -> (y, z), as linear
+PyObject* gated_linear(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+    if (nargs != 8) return none();
+    return guarded([&]() -> PyObject* {
+        const at::Tensor *x = cuda_tensor(args[0]), *sx = nullptr, *w = cuda_tensor(args[2]), *sw = nullptr, *b = nullptr;
+        if (!x || !w || !optional(args[1], sx) || !optional(args[3], sw) || !optional(args[4], b) || x->dim() != 2 ||
+            w->dim() != 2 || (sx == nullptr) != (sw == nullptr))
+            return none();
+        const long act = PyLong_AsLong(args[5]);
+        long out = PyLong_AsLong(args[6]);
+        const bool keep = args[7] == Py_True, fp8 = sx != nullptr;
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            return none();
+        }
+        if (out < 0) out = storage(*x);
+        if (out < 0) return none();
+        const int64_t T = x->size(0), I = x->size(1), O = w->size(0), F = O / 2;
+        const at::Device dev = x->device();
+        const at::ScalarType type = out == 0 ? at::kBFloat16 : at::kHalf;
+        const at::ScalarType operand = fp8 ? at::kFloat8_e4m3fn : type;
+        int64_t xs, ws;
+        if (O % 2 != 0 || !rows_of(*x, operand, T, I, dev, xs) || !rows_of(*w, operand, O, I, dev, ws) ||
+            (fp8 && (!flat(*sx, at::kFloat, T, dev) || !flat(*sw, at::kFloat, O, dev))) ||
+            (b != nullptr && (b->dim() != 1 || !flat(*b, at::kFloat, O, dev))))
+            return none();
+        const c10::cuda::CUDAGuard guard(dev);
+        at::Tensor y = empty({T, F}, type, dev), z, work;
+        if (keep) z = empty({T, O}, type, dev);
+        void *xp = x->data_ptr(), *wp = w->data_ptr();
+        const bool aligned = ((reinterpret_cast<uintptr_t>(xp) | reinterpret_cast<uintptr_t>(wp)) & 15) == 0;
+        const int64_t need = mhc_linear_workspace(T, I, O, xs, ws, fp8 ? 1 : 2, aligned);
+        if (need > 0) work = empty({need}, at::kByte, dev);
+        void* workp = need > 0 ? work.data_ptr() : nullptr;
+        void* zp = keep ? z.data_ptr() : nullptr;
+        const float* bp = b == nullptr ? nullptr : b->data_ptr<float>();
+        const mhc_status_t st =
+            fp8 ? mhc_gated_linear_fp8_fwd(xp, sx->data_ptr<float>(), wp, sw->data_ptr<float>(), bp, y.data_ptr(), zp, workp,
+                                           need, T, I, F, xs, ws, mhc_activation_t(act), mhc_dtype_t(out), current(dev))
+                : mhc_gated_linear_fwd(xp, wp, bp, y.data_ptr(), zp, workp, need, T, I, F, xs, ws, mhc_activation_t(act),
+                                       mhc_dtype_t(out), current(dev));
+        return st == MHC_OK ? pack({&y, &z}) : none();
+    });
+}
+
+// gated_linear_backward(grad_y, x, w, z, act, bias, want_x, want_w) -> (grad_x, grad_w, grad_b)
+PyObject* gated_linear_backward(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+    if (nargs != 8) return none();
+    return guarded([&]() -> PyObject* {
+        const at::Tensor *g = cuda_tensor(args[0]), *x = cuda_tensor(args[1]), *w = cuda_tensor(args[2]), *z = cuda_tensor(args[3]);
+        if (!g || !x || !w || !z || x->dim() != 2 || w->dim() != 2) return none();
+        const long act = PyLong_AsLong(args[4]);
+        const int bias = PyObject_IsTrue(args[5]), want_x = PyObject_IsTrue(args[6]), want_w = PyObject_IsTrue(args[7]);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            return none();
+        }
+        const int dt = storage(*x);
+        const int64_t T = x->size(0), I = x->size(1), O = w->size(0), F = O / 2;
+        const at::Device dev = x->device();
+        const at::ScalarType type = x->scalar_type();
+        int64_t xs, ws, s;
+        if (dt < 0 || O % 2 != 0 || !rows_of(*x, type, T, I, dev, xs) || !rows_of(*w, type, O, I, dev, ws) ||
+            !rows_of(*g, type, T, F, dev, s) || s != F || !rows_of(*z, type, T, O, dev, s) || s != O)
+            return none();
+        const c10::cuda::CUDAGuard guard(dev);
+        at::Tensor gx, gw, gb, work;
+        if (want_x) gx = empty({T, I}, type, dev);
+        if (want_w) gw = empty({O, I}, type, dev);
+        if (bias) gb = empty({O}, at::kFloat, dev);
+        void *xp = x->data_ptr(), *wp = w->data_ptr();
+        const bool aligned = ((reinterpret_cast<uintptr_t>(xp) | reinterpret_cast<uintptr_t>(wp)) & 15) == 0;
+        const int64_t need = mhc_gated_linear_bwd_workspace(T, I, F, xs, ws, want_x, want_w, bias, aligned);
+        if (need > 0) work = empty({need}, at::kByte, dev);
+        const mhc_status_t st = mhc_gated_linear_bwd(g->data_ptr(), xp, wp, z->data_ptr(), want_x ? gx.data_ptr() : nullptr,
+                                                     want_w ? gw.data_ptr() : nullptr, bias ? gb.data_ptr<float>() : nullptr,
+                                                     need > 0 ? work.data_ptr() : nullptr, need, T, I, F, xs, ws,
+                                                     mhc_activation_t(act), mhc_dtype_t(dt), current(dev));
+        return st == MHC_OK ? pack({&gx, &gw, &gb}) : none();
+    });
+}
+
+// linear_cross_entropy(x, w, target) -> (loss, lse)
+PyObject* linear_cross_entropy(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+    if (nargs != 3) return none();
+    return guarded([&]() -> PyObject* {
+        const at::Tensor *x = cuda_tensor(args[0]), *w = cuda_tensor(args[1]), *target = cuda_tensor(args[2]);
+        if (!x || !w || !target || x->dim() != 2 || w->dim() != 2 || target->dim() != 1) return none();
+        const int dt = storage(*x);
+        const int64_t T = x->size(0), I = x->size(1), V = w->size(0);
+        const at::Device dev = x->device();
+        int64_t xs, ws;
+        if (dt < 0 || !rows_of(*x, x->scalar_type(), T, I, dev, xs) || !rows_of(*w, x->scalar_type(), V, I, dev, ws) ||
+            !flat(*target, at::kLong, T, dev))
+            return none();
+        const c10::cuda::CUDAGuard guard(dev);
+        at::Tensor loss = empty({T}, at::kFloat, dev), lse = empty({T}, at::kFloat, dev), work;
+        void *xp = x->data_ptr(), *wp = w->data_ptr();
+        const bool aligned = ((reinterpret_cast<uintptr_t>(xp) | reinterpret_cast<uintptr_t>(wp)) & 15) == 0;
+        const int64_t need = mhc_linear_cross_entropy_workspace(T, I, V, xs, ws, aligned);
+        if (need > 0) work = empty({need}, at::kByte, dev);
+        const mhc_status_t st = mhc_linear_cross_entropy_fwd(xp, wp, target->data_ptr<int64_t>(), loss.data_ptr<float>(),
+                                                             lse.data_ptr<float>(), need > 0 ? work.data_ptr() : nullptr, need,
+                                                             T, I, V, xs, ws, mhc_dtype_t(dt), current(dev));
+        return st == MHC_OK ? pack({&loss, &lse}) : none();
+    });
+}
+
+// linear_cross_entropy_backward(grad_loss, x, w, target, lse, grad_lse, want_x, want_w) -> (grad_x, grad_w)
+PyObject* linear_cross_entropy_backward(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+    if (nargs != 8) return none();
+    return guarded([&]() -> PyObject* {
+        const at::Tensor *gl = nullptr, *x = cuda_tensor(args[1]), *w = cuda_tensor(args[2]), *target = cuda_tensor(args[3]),
+                         *lse = cuda_tensor(args[4]), *gs = nullptr;
+        if (!x || !w || !target || !lse || !optional(args[0], gl) || !optional(args[5], gs) || x->dim() != 2 || w->dim() != 2 ||
+            target->dim() != 1 || lse->dim() != 1 || (gl == nullptr && gs == nullptr))
+            return none();
+        const int want_x = PyObject_IsTrue(args[6]), want_w = PyObject_IsTrue(args[7]);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            return none();
+        }
+        const int dt = storage(*x);
+        const int64_t T = x->size(0), I = x->size(1), V = w->size(0);
+        const at::Device dev = x->device();
+        int64_t xs, ws;
+        if (dt < 0 || !rows_of(*x, x->scalar_type(), T, I, dev, xs) || !rows_of(*w, x->scalar_type(), V, I, dev, ws) ||
+            !flat(*target, at::kLong, T, dev) || !flat(*lse, at::kFloat, T, dev) ||
+            (gl != nullptr && (gl->dim() != 1 || !flat(*gl, at::kFloat, T, dev))) ||
+            (gs != nullptr && (gs->dim() != 1 || !flat(*gs, at::kFloat, T, dev))))
+            return none();
+        const c10::cuda::CUDAGuard guard(dev);
+        at::Tensor gx, gw, work;
+        if (want_x) gx = empty({T, I}, x->scalar_type(), dev);
+        if (want_w) gw = empty({V, I}, x->scalar_type(), dev);
+        void *xp = x->data_ptr(), *wp = w->data_ptr();
+        const bool aligned = ((reinterpret_cast<uintptr_t>(xp) | reinterpret_cast<uintptr_t>(wp)) & 15) == 0;
+        const int64_t need = mhc_linear_cross_entropy_bwd_workspace(T, I, V, xs, ws, want_x, want_w, aligned);
+        if (need > 0) work = empty({need}, at::kByte, dev);
+        const mhc_status_t st = mhc_linear_cross_entropy_bwd(
+            static_cast<const float*>(ptr(gl)), static_cast<const float*>(ptr(gs)), xp, wp, target->data_ptr<int64_t>(),
+            lse->data_ptr<float>(), want_x ? gx.data_ptr() : nullptr, want_w ? gw.data_ptr() : nullptr,
+            need > 0 ? work.data_ptr() : nullptr, need, T, I, V, xs, ws, mhc_dtype_t(dt), current(dev));
+        return st == MHC_OK ? pack({&gx, &gw}) : none();
+    });
+}
+
 // rotary(x, positions, frequencies, interleaved, scale, inverse) -> (out,)
 PyObject* rotary(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     if (nargs != 6) return none();
@@ -289,6 +436,12 @@ PyMethodDef methods[] = {
     {"rms_norm_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rms_norm_backward)), METH_FASTCALL, nullptr},
     {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(linear)), METH_FASTCALL, nullptr},
     {"linear_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(linear_backward)), METH_FASTCALL, nullptr},
+    {"gated_linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(gated_linear)), METH_FASTCALL, nullptr},
+    {"gated_linear_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(gated_linear_backward)), METH_FASTCALL,
+     nullptr},
+    {"linear_cross_entropy", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(linear_cross_entropy)), METH_FASTCALL, nullptr},
+    {"linear_cross_entropy_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(linear_cross_entropy_backward)),
+     METH_FASTCALL, nullptr},
     {"rotary", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rotary)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

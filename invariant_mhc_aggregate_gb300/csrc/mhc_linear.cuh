@@ -77,6 +77,35 @@ struct Product {
 // rows along their lanes or columns ("MN-major").
 enum Layout { kBothK = 0, kPMnQK = 1, kBothMn = 2 };   // forward, grad_x, grad_w
 
+// What a product ends in: its own epilogue, or one of mhc_linear_ends.cuh.
+enum End {
+    kEndPlain = 0,
+    kEndGated = 1,     // act(gate) * up, of two projections side by side on the lanes
+    kEndSum = 2,       // added to FP32 sums, or their last addition, scaled and rounded
+    kEndProb = 3,      // the gradient of a cross entropy's logits
+    kEndEntropy = 4    // maxima and sums of exponentials over the output rows (pair_kernel alone)
+};
+
+// One token of a cross entropy's backward.
+struct __align__(16) EntropyToken {
+    float lse, spread, target_grad;   // d = spread * exp(z - lse), less target_grad at the target
+    int32_t target;                   // -1: ignored
+};
+
+// What the ends beside the plain one read and write; each uses its own part.
+struct EndArgs {
+    int64_t half;                     // kEndGated: F; the output's rows are F long, the lanes' 2 F
+    const float* sum_in;              // kEndSum: [M,N] added first, or null
+    float* sum_out;                   // where the sums go, or null: the last addition, into e.y
+    const float* factor;              // what that one is multiplied by
+    const EntropyToken* tokens;       // kEndProb: [M]
+    int32_t first;                    // the vocabulary's entry of output column 0
+    int64_t pitch;                    // of the output's rows
+    float2* partial;                  // kEndEntropy: [groups,N]: a group's maximum and its sum of exponentials
+    float* at;                        // [N] the target's logit
+    const int64_t* target;            // [N]
+};
+
 // How a tile lies: the output's contiguous index n on the lanes of tensor
 // memory (operand P = B, 128 lanes a CTA) and its rows m on the columns
 // (operand Q = A).  A warp then holds 32 consecutive n of one row, so every
@@ -84,6 +113,7 @@ enum Layout { kBothK = 0, kPMnQK = 1, kBothMn = 2 };   // forward, grad_x, grad_
 // the output, and bias and column scale are one register.
 struct TileArgs {
     Epilogue e;
+    EndArgs end;
     int64_t N;               // output columns
     uint32_t rows;           // output rows
     uint32_t kb;             // blocks of 128 bytes of K
@@ -196,10 +226,15 @@ __device__ __forceinline__ uint32_t split_begin(const TileArgs& a, uint32_t s) {
 }
 
 // One block of K of P (128 lanes from p0) and of Q (`columns` from q0) into a stage.
-template <int CG, bool FP8, int LAYOUT>
+template <int CG, bool FP8, int LAYOUT, int END>
 __device__ __forceinline__ void load_p(uint32_t stage, const CUtensorMap* mp, uint32_t k, int p0, uint32_t bar) {
     const int k0 = int(k * (FP8 ? 128u : 64u));
-    if constexpr (LAYOUT == kBothK) {
+    if constexpr (END == kEndGated) {
+        // 16 rows of the gate, then the same 16 of the up projection, in each 32 lanes
+#pragma unroll
+        for (int j = 0; j < int(kLanesP) / 32; ++j)
+            umma::tensor_copy_3d<CG>(stage + j * 32 * 128, mp, k0, p0 / 2 + 16 * j, 0, bar);
+    } else if constexpr (LAYOUT == kBothK) {
         umma::tensor_copy_2d<CG>(stage, mp, k0, p0, bar);
     } else {
         umma::tensor_copy_2d<CG>(stage, mp, p0, k0, bar);
@@ -255,6 +290,14 @@ __device__ __forceinline__ void drain(bool& ok, uint32_t issued, umma::Ring at, 
 
 __device__ __forceinline__ void timed_out(const TileArgs& a) { *a.timeouts = 1u; }
 
+}  // namespace linear
+}  // namespace mhc
+
+#include "mhc_linear_ends.cuh"
+
+namespace mhc {
+namespace linear {
+
 // --------------------------------------------------------------------------
 // Few tiles: one tile of 128 lanes x `width` columns a cluster of `splits`
 // CTAs, each of which sums its part of K; the parts meet in shared memory and
@@ -272,7 +315,7 @@ constexpr int kChunk = 8;   // columns that a warp takes out of tensor memory at
 constexpr uint32_t kSplitThreads = 32 * (kEpilogueWarps + 2);
 constexpr uint32_t kSplitCopy = kEpilogueWarps, kSplitMultiply = kSplitCopy + 1;   // warps
 
-template <bool FP8, int OUT, int LAYOUT>
+template <bool FP8, int OUT, int LAYOUT, int END = kEndPlain>
 __global__ void __launch_bounds__(kSplitThreads, 1)
 split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUtensorMap mq,
              const __grid_constant__ TileArgs a) {
@@ -308,8 +351,9 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     const uint32_t k0 = split_begin(a, rank), k1 = split_begin(a, rank + 1);
     const uint32_t quarter = warp % 4, group = warp / 4;
     const uint32_t valid = min(a.width, a.rows - m0);
-    const int64_t n = n0 + quarter * 32 + lane;
-    const bool n_ok = n < a.N;
+    int64_t n = n0 + quarter * 32 + lane;
+    bool n_ok = n < a.N;
+    if constexpr (END == kEndGated) n = gated_column(a.end.half, n, n_ok);
     // the thread's place in the parts, [column][lane], that take the stages' place
     // once every copy has landed and been read
     float* part = reinterpret_cast<float*>(stages) + quarter * 32 + lane;
@@ -330,7 +374,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
                 umma::expect_tx(bar_full + 8 * at.stage, n * a.block_bytes);
                 for (uint32_t u = 0; u < n; ++u) {
                     const uint32_t to = ring + at.stage * bytes + u * a.block_bytes;
-                    load_p<1, FP8, LAYOUT>(to, &mp, k + u, int(n0), bar_full + 8 * at.stage);
+                    load_p<1, FP8, LAYOUT, END>(to, &mp, k + u, int(n0), bar_full + 8 * at.stage);
                     load_q<1, FP8, LAYOUT>(to, &mq, k + u, int(m0), a.width, bar_full + 8 * at.stage);
                 }
             }
@@ -365,10 +409,11 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
             float v[kChunk];
             umma::tmem_ld(tmem + (quarter * 32u << 16) + c, v);
             uint16_t r[kChunk];
-            if (a.splits == 1) load_residual<kChunk>(a.e, n_ok, n, m0 + c, 1, m0 + valid, r);
+            if (END == kEndPlain && a.splits == 1) load_residual<kChunk>(a.e, n_ok, n, m0 + c, 1, m0 + valid, r);
             umma::tmem_wait_ld(v);
             if (a.splits == 1) {
-                emit_any<OUT, kChunk>(a.e, a.N, n_ok, n, m0 + c, 1, m0 + valid, v, r, bias, cs);
+                if constexpr (END == kEndPlain) emit_any<OUT, kChunk>(a.e, a.N, n_ok, n, m0 + c, 1, m0 + valid, v, r, bias, cs);
+                else emit_end<END, OUT, kChunk>(a, n_ok, n, m0 + c, 1, m0 + valid, v, bias, cs);
             } else {
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) part[(c + i) * kLanesP] = v[i];
@@ -385,7 +430,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
             const uint32_t at = smem_addr(part);
             for (uint32_t c = rank + group * kChunk * a.splits; c < valid; c += 4 * kChunk * a.splits) {
                 uint16_t res[kChunk];
-                load_residual<kChunk>(a.e, n_ok, n, m0 + c, a.splits, m0 + valid, res);
+                if constexpr (END == kEndPlain) load_residual<kChunk>(a.e, n_ok, n, m0 + c, a.splits, m0 + valid, res);
                 float v[kChunk];
                 for (uint32_t r = 0; r < a.splits; ++r) {
                     const uint32_t peer = umma::map_rank(at, r);
@@ -398,7 +443,10 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
 #pragma unroll
                     for (uint32_t i = 0; i < kChunk; ++i) v[i] = r == 0 ? w[i] : __fadd_rn(v[i], w[i]);
                 }
-                emit_any<OUT, kChunk>(a.e, a.N, n_ok, n, m0 + c, a.splits, m0 + valid, v, res, bias, cs);
+                if constexpr (END == kEndPlain)
+                    emit_any<OUT, kChunk>(a.e, a.N, n_ok, n, m0 + c, a.splits, m0 + valid, v, res, bias, cs);
+                else
+                    emit_end<END, OUT, kChunk>(a, n_ok, n, m0 + c, a.splits, m0 + valid, v, bias, cs);
             }
         }
         umma::cluster_sync();   // no CTA leaves while another reads its part
@@ -490,7 +538,7 @@ __device__ __forceinline__ void emit_tile(const TileArgs& a, uint32_t from, uint
     }
 }
 
-template <bool FP8, int OUT, int LAYOUT, bool PARTS>
+template <bool FP8, int OUT, int LAYOUT, bool PARTS, int END = kEndPlain>
 __global__ void __launch_bounds__(kPairThreads, 1)
 pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUtensorMap mq,
             const __grid_constant__ TileArgs a) {
@@ -549,7 +597,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                         if (warp == kCopyP && rank == 0) umma::expect_tx(bar_full + 8 * at.stage, 2 * n * a.block_bytes);
                         for (uint32_t u = 0; u < n; ++u) {
                             const uint32_t to = ring + at.stage * bytes + u * a.block_bytes;
-                            if (warp == kCopyP) load_p<2, FP8, LAYOUT>(to, &mp, k + u, p0, bar_pair + 8 * at.stage);
+                            if (warp == kCopyP) load_p<2, FP8, LAYOUT, END>(to, &mp, k + u, p0, bar_pair + 8 * at.stage);
                             else load_q<2, FP8, LAYOUT>(to, &mq, k + u, q0, half, bar_pair + 8 * at.stage);
                         }
                     }
@@ -600,14 +648,15 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
         for (uint32_t i = blockIdx.x / 2; i < tiles && ok; i += step) {
             uint32_t pt, qt;
             tile_at(a, i, pt, qt);
-            const int64_t col = int64_t(pt) * 2 * kLanesP + rank * kLanesP + quarter * 32 + lane;
+            int64_t col = int64_t(pt) * 2 * kLanesP + rank * kLanesP + quarter * 32 + lane;
             const uint32_t m0 = qt * a.width + c0;
-            const bool n_ok = col < a.N;
-            const float bias = a.e.bias != nullptr && col < a.N ? __ldg(a.e.bias + col) : 0.0f;
-            const float cs = a.e.col_scale != nullptr && col < a.N ? __ldg(a.e.col_scale + col) : 1.0f;
+            bool n_ok = col < a.N;
+            if constexpr (END == kEndGated) col = gated_column(a.end.half, col, n_ok);
+            const float bias = a.e.bias != nullptr && n_ok ? __ldg(a.e.bias + col) : 0.0f;
+            const float cs = a.e.col_scale != nullptr && n_ok ? __ldg(a.e.col_scale + col) : 1.0f;
             // the warp's residual (64 bytes of each row) to L2, under the multiplication:
             // a chunk at a time from memory took 2400 cycles each
-            if (a.e.residual != nullptr) {
+            if (END == kEndPlain && a.e.residual != nullptr) {
                 const int64_t col0 = col - lane;
                 for (uint32_t c = lane; c < mine; c += 32)
                     if (m0 + c < a.rows && col0 < a.N) umma::prefetch_l2(a.e.residual + int64_t(m0 + c) * a.e.residual_stride + col0);
@@ -645,7 +694,11 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             };
             // (the same for the whole warp)
             const bool all = __all_sync(0xFFFFFFFFu, n_ok) && m0 + mine <= a.rows;
-            if (a.e.residual != nullptr) {
+            if constexpr (END == kEndEntropy) {
+                entropy_tile(a, tw + b * 256, mine, m0, col, n_ok, give_back);
+            } else if constexpr (END != kEndPlain) {
+                end_tile<END, OUT>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, give_back);
+            } else if (a.e.residual != nullptr) {
                 if (all) emit_tile<OUT, true, true>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, give_back);
                 else emit_tile<OUT, false, true>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, give_back);
             } else {

@@ -1,5 +1,6 @@
 """Python binding of the layer operators in ``include/mhc_layer.h`` (ctypes):
-what stands between the mHC aggregate and the mHC post.
+what stands between the mHC aggregate and the mHC post, and the loss at the
+model's end.
 
     y, total, rstd = rms_norm(x, weight, residual=r)             # [T,H]
     y8, scale, total, rstd = rms_norm_fp8(x, weight, residual=r) # E4M3 and its scales
@@ -9,6 +10,14 @@ what stands between the mHC aggregate and the mHC post.
     y = linear_fp8(x8, x_scale, w8, w_scale, bias=b)
     y, z = linear_preact(x, w, bias=b, activation="silu")        # z for the backward
     grad_x, grad_w, grad_b = linear_backward(g, x, w, z=z, activation="silu")
+
+    h = gated_linear(x, w_gate_up)                               # silu(x w_gate^T) * (x w_up^T), one kernel
+    h = gated_linear_fp8(x8, x_scale, w8, w_scale)
+    h, z = gated_linear_preact(x, w_gate_up)
+    grad_x, grad_w, grad_b = gated_linear_backward(g, x, w_gate_up, z, bias=False)
+
+    loss, lse = linear_cross_entropy(x, w_vocab, target)         # the logits are not kept
+    grad_x, grad_w = linear_cross_entropy_backward(grad_loss, x, w_vocab, target, lse)
 
     q = rotary(q, positions, rotary_frequencies(128))            # [T,heads,D]
 
@@ -49,6 +58,14 @@ EXPORTS = (
     "mhc_linear_bwd",
     "mhc_linear_workspace",
     "mhc_linear_bwd_workspace",
+    "mhc_gated_linear_fwd",
+    "mhc_gated_linear_fp8_fwd",
+    "mhc_gated_linear_bwd",
+    "mhc_gated_linear_bwd_workspace",
+    "mhc_linear_cross_entropy_fwd",
+    "mhc_linear_cross_entropy_workspace",
+    "mhc_linear_cross_entropy_bwd",
+    "mhc_linear_cross_entropy_bwd_workspace",
     "mhc_rotary",
     "mhc_layer_last_cuda_error",
     "mhc_layer_wait_timeouts",
@@ -95,6 +112,14 @@ def load():
                 ("mhc_linear_bwd", i32, [p] * 8 + [i64] * 4 + [i32, i32, p]),
                 ("mhc_linear_workspace", i64, [i64] * 5 + [i32, i32]),
                 ("mhc_linear_bwd_workspace", i64, [i64] * 3 + [i32] * 5),
+                ("mhc_gated_linear_fwd", i32, [p] * 6 + [i64] * 6 + [i32, i32, p]),
+                ("mhc_gated_linear_fp8_fwd", i32, [p] * 8 + [i64] * 6 + [i32, i32, p]),
+                ("mhc_gated_linear_bwd", i32, [p] * 8 + [i64] * 6 + [i32, i32, p]),
+                ("mhc_gated_linear_bwd_workspace", i64, [i64] * 5 + [i32] * 4),
+                ("mhc_linear_cross_entropy_fwd", i32, [p] * 6 + [i64] * 6 + [i32, p]),
+                ("mhc_linear_cross_entropy_workspace", i64, [i64] * 5 + [i32]),
+                ("mhc_linear_cross_entropy_bwd", i32, [p] * 9 + [i64] * 6 + [i32, p]),
+                ("mhc_linear_cross_entropy_bwd_workspace", i64, [i64] * 5 + [i32] * 3),
                 ("mhc_rotary", i32, [p] * 4 + [i64] * 8 + [f32, i32, i32, i32, p]),
                 ("mhc_layer_last_cuda_error", i32, []),
                 ("mhc_layer_wait_timeouts", i64, [])):
@@ -407,6 +432,186 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     _call(dev, "mhc_linear_bwd", gp, xp, wp, _ptr(z if act else None), _ptr(grad_x), _ptr(grad_w), _ptr(grad_b),
           _ptr(work), need, T, I, O, act, dt, _stream_handle(stream, dev))
     return grad_x, grad_w, grad_b
+
+
+# ---------------------------------------------------------------------------
+# gated product
+# ---------------------------------------------------------------------------
+
+def _gated(x, x_scale, w, w_scale, bias, activation, out_dtype, keep, stream):
+    T, I = _two(x, "x")
+    O, _ = _two(w, "weight")
+    dev = x.device
+    fp8 = x_scale is not None
+    act = _activation(activation)
+    dt = _DTYPES.get(out_dtype)
+    if dt is None:
+        raise TypeError(f"{'dtype' if fp8 else 'x'} must be bfloat16 or float16, got {out_dtype}")
+    if O % 2:
+        raise ValueError(f"weight must have the gate's and as many of the up projection's rows, got {tuple(w.shape)}")
+    operand = _E4M3 if fp8 else out_dtype
+    xs = _rows(x, "x", operand, x.shape, dev)
+    ws = _rows(w, "weight", operand, (O, I), dev)
+    if fp8:
+        _flat(x_scale, "x_scale", torch.float32, (T, 1) if x_scale.dim() == 2 else (T,), dev)
+        _flat(w_scale, "w_scale", torch.float32, (O, 1) if w_scale.dim() == 2 else (O,), dev)
+    if bias is not None:
+        _flat(bias, "bias", torch.float32, (O,), dev)
+    lib = load()
+    y = torch.empty((T, O // 2), dtype=out_dtype, device=dev)
+    z = torch.empty((T, O), dtype=out_dtype, device=dev) if keep else None
+    xp, wp = x.data_ptr(), w.data_ptr()
+    need = lib.mhc_linear_workspace(T, I, O, xs, ws, 1 if fp8 else 2, 0 if (xp | wp) & 15 else 1)
+    work = _scratch(need, dev, stream)
+    sh = _stream_handle(stream, dev)
+    if fp8:
+        _call(dev, "mhc_gated_linear_fp8_fwd", xp, x_scale.data_ptr(), wp, w_scale.data_ptr(), _ptr(bias), y.data_ptr(),
+              _ptr(z), _ptr(work), need, T, I, O // 2, xs, ws, act, dt, sh)
+    else:
+        _call(dev, "mhc_gated_linear_fwd", xp, wp, _ptr(bias), y.data_ptr(), _ptr(z), _ptr(work), need, T, I, O // 2, xs, ws,
+              act, dt, sh)
+    return y, z
+
+
+def gated_linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, activation: str = "silu",
+                 stream=None) -> torch.Tensor:
+    """act(x w_gate^T + b_gate) * (x w_up^T + b_up), the first half of a gated
+    feed-forward, in one kernel: x [T,I], weight [2F,I] (the gate's F rows,
+    then the up projection's), the result [T,F], all bf16 or all f16 (x and
+    weight with any row stride); bias FP32 [2F]; activation as in `linear`."""
+    if stream is None and activation in ACTIVATIONS:
+        out = (_fast or _compiled()).gated_linear(x, None, weight, None, bias, ACTIVATIONS[activation], -1, False)
+        if out is not None:
+            return out[0]
+    return _gated(x, None, weight, None, bias, activation, x.dtype if isinstance(x, torch.Tensor) else None, False, stream)[0]
+
+
+def gated_linear_preact(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, activation: str = "silu",
+                        stream=None):
+    """(y, z): as gated_linear, and z = x weight^T + bias [T,2F] that gated_linear_backward reads."""
+    if stream is None and activation in ACTIVATIONS:
+        out = (_fast or _compiled()).gated_linear(x, None, weight, None, bias, ACTIVATIONS[activation], -1, True)
+        if out is not None:
+            return out
+    return _gated(x, None, weight, None, bias, activation, x.dtype if isinstance(x, torch.Tensor) else None, True, stream)
+
+
+def gated_linear_fp8(x8: torch.Tensor, x_scale: torch.Tensor, w8: torch.Tensor, w_scale: torch.Tensor,
+                     bias: torch.Tensor | None = None, activation: str = "silu", dtype: torch.dtype = torch.bfloat16,
+                     stream=None) -> torch.Tensor:
+    """gated_linear of E4M3 operands x8 [T,I] and w8 [2F,I] with one FP32 scale
+    per row of each (x_scale [T] or [T,1], w_scale [2F] or [2F,1]); the result
+    is of `dtype`."""
+    if stream is None and activation in ACTIVATIONS and dtype in _DTYPES and x_scale is not None:
+        out = (_fast or _compiled()).gated_linear(x8, x_scale, w8, w_scale, bias, ACTIVATIONS[activation], _DTYPES[dtype],
+                                                  False)
+        if out is not None:
+            return out[0]
+    if not isinstance(x_scale, torch.Tensor) or not isinstance(w_scale, torch.Tensor):
+        raise TypeError("x_scale and w_scale must be torch.Tensors")
+    return _gated(x8, x_scale, w8, w_scale, bias, activation, dtype, False, stream)[0]
+
+
+def gated_linear_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, z: torch.Tensor,
+                          activation: str = "silu", bias: bool = True, want=(True, True), stream=None):
+    """(grad_x, grad_weight, grad_bias) of gated_linear, from the gradient of y
+    and the forward's z (both dense; x and weight with any row stride).
+    grad_bias is FP32 [2F], None when `bias` is false; `want` says which of
+    grad_x and grad_weight to compute.  Both read the gradient of z rounded to
+    the storage type, as the tensor cores take it; grad_bias sums it unrounded."""
+    if stream is None and activation in ACTIVATIONS:
+        out = (_fast or _compiled()).gated_linear_backward(grad_y, x, weight, z, ACTIVATIONS[activation], bias, want[0],
+                                                           want[1])
+        if out is not None:
+            return out
+    T, I = _two(x, "x")
+    O, _ = _two(weight, "weight")
+    dt, dev = _storage(x, "x"), x.device
+    act = _activation(activation)
+    if O % 2:
+        raise ValueError(f"weight must have the gate's and as many of the up projection's rows, got {tuple(weight.shape)}")
+    xs = _rows(x, "x", x.dtype, x.shape, dev)
+    ws = _rows(weight, "weight", x.dtype, (O, I), dev)
+    _flat(grad_y, "grad_y", x.dtype, (T, O // 2), dev)
+    _flat(z, "z", x.dtype, (T, O), dev)
+    lib = load()
+    grad_x = torch.empty((T, I), dtype=x.dtype, device=dev) if want[0] else None
+    grad_w = torch.empty((O, I), dtype=x.dtype, device=dev) if want[1] else None
+    grad_b = torch.empty(O, dtype=torch.float32, device=dev) if bias else None
+    xp, wp = x.data_ptr(), weight.data_ptr()
+    need = lib.mhc_gated_linear_bwd_workspace(T, I, O // 2, xs, ws, int(want[0]), int(want[1]), int(bias),
+                                              0 if (xp | wp) & 15 else 1)
+    work = _scratch(need, dev, stream)
+    _call(dev, "mhc_gated_linear_bwd", grad_y.data_ptr(), xp, wp, z.data_ptr(), _ptr(grad_x), _ptr(grad_w), _ptr(grad_b),
+          _ptr(work), need, T, I, O // 2, xs, ws, act, dt, _stream_handle(stream, dev))
+    return grad_x, grad_w, grad_b
+
+
+# ---------------------------------------------------------------------------
+# cross entropy over a vocabulary
+# ---------------------------------------------------------------------------
+
+def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, stream=None):
+    """(loss, lse), FP32 [T], of the logits x weight^T, which are never stored:
+    lse their logsumexp, loss = lse - logit of the target.  x [T,I] and weight
+    [V,I], both bf16 or both f16, with any row stride; target int64 [T].  A
+    token whose target is outside 0 .. V-1 (-100, by custom) is ignored: loss
+    0.  The mean over the others is the caller's division by their number."""
+    if stream is None:
+        out = (_fast or _compiled()).linear_cross_entropy(x, weight, target)
+        if out is not None:
+            return out
+    T, I = _two(x, "x")
+    V, _ = _two(weight, "weight")
+    dt, dev = _storage(x, "x"), x.device
+    xs = _rows(x, "x", x.dtype, x.shape, dev)
+    ws = _rows(weight, "weight", x.dtype, (V, I), dev)
+    _flat(target, "target", torch.int64, (T,), dev)
+    lib = load()
+    loss, lse = (torch.empty(T, dtype=torch.float32, device=dev) for _ in range(2))
+    xp, wp = x.data_ptr(), weight.data_ptr()
+    need = lib.mhc_linear_cross_entropy_workspace(T, I, V, xs, ws, 0 if (xp | wp) & 15 else 1)
+    work = _scratch(need, dev, stream)
+    _call(dev, "mhc_linear_cross_entropy_fwd", xp, wp, target.data_ptr(), loss.data_ptr(), lse.data_ptr(), _ptr(work), need,
+          T, I, V, xs, ws, dt, _stream_handle(stream, dev))
+    return loss, lse
+
+
+def linear_cross_entropy_backward(grad_loss: torch.Tensor | None, x: torch.Tensor, weight: torch.Tensor,
+                                  target: torch.Tensor, lse: torch.Tensor, grad_lse: torch.Tensor | None = None,
+                                  want=(True, True), stream=None):
+    """(grad_x, grad_weight) of linear_cross_entropy, from the gradients of loss
+    and lse (FP32 [T]; either may be None) and the forward's lse; `want` says
+    which of the two to compute.  The logits are computed again by pieces of
+    the vocabulary; both products read their gradient rounded to the storage
+    type (after a scaling by a power of two, so that f16 holds small
+    probabilities)."""
+    if stream is None:
+        out = (_fast or _compiled()).linear_cross_entropy_backward(grad_loss, x, weight, target, lse, grad_lse, want[0],
+                                                                   want[1])
+        if out is not None:
+            return out
+    T, I = _two(x, "x")
+    V, _ = _two(weight, "weight")
+    dt, dev = _storage(x, "x"), x.device
+    xs = _rows(x, "x", x.dtype, x.shape, dev)
+    ws = _rows(weight, "weight", x.dtype, (V, I), dev)
+    _flat(target, "target", torch.int64, (T,), dev)
+    _flat(lse, "lse", torch.float32, (T,), dev)
+    if grad_loss is None and grad_lse is None:
+        raise ValueError("one of grad_loss and grad_lse must be given")
+    for t, name in ((grad_loss, "grad_loss"), (grad_lse, "grad_lse")):
+        if t is not None:
+            _flat(t, name, torch.float32, (T,), dev)
+    lib = load()
+    grad_x = torch.empty((T, I), dtype=x.dtype, device=dev) if want[0] else None
+    grad_w = torch.empty((V, I), dtype=x.dtype, device=dev) if want[1] else None
+    xp, wp = x.data_ptr(), weight.data_ptr()
+    need = lib.mhc_linear_cross_entropy_bwd_workspace(T, I, V, xs, ws, int(want[0]), int(want[1]), 0 if (xp | wp) & 15 else 1)
+    work = _scratch(need, dev, stream)
+    _call(dev, "mhc_linear_cross_entropy_bwd", _ptr(grad_loss), _ptr(grad_lse), xp, wp, target.data_ptr(), lse.data_ptr(),
+          _ptr(grad_x), _ptr(grad_w), _ptr(work), need, T, I, V, xs, ws, dt, _stream_handle(stream, dev))
+    return grad_x, grad_w
 
 
 # ---------------------------------------------------------------------------
