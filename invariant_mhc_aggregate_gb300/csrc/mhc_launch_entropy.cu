@@ -48,7 +48,8 @@ cudaError_t entropy_fwd(const EntropyCall& c, float* loss, float* lse, float2* p
     p.e = {};
     TileArgs a;
     CUtensorMap mp, mq;
-    cudaError_t e = lay_out(p, c.dtype, {true, entropy_width(c.V), 1}, a, mp, mq);
+    const uint32_t runs = uint32_t((k_blocks(p, c.dtype) + kEntropyRun - 1) / kEntropyRun);
+    cudaError_t e = lay_out(p, c.dtype, {true, entropy_width(c.V), runs}, a, mp, mq);
     if (e != cudaSuccess) return e;
     a.end = {};
     a.end.partial = partial, a.end.at = at, a.end.target = c.target;

@@ -662,6 +662,22 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                     if (m0 + c < a.rows && col0 < a.N) umma::prefetch_l2(a.e.residual + int64_t(m0 + c) * a.e.residual_stride + col0);
             }
             uint32_t b = 0;
+            if constexpr (END == kEndEntropy) {
+                float v[kEntropyMost / 8][8];
+                for (uint32_t part = 0; part < a.splits; ++part) {
+                    b = sums.take<false>(part);
+                    if (!(ok = umma::wait(bar_sum + 8 * b, sums.parity(b)))) break;
+                    umma::fence_after_sync();
+                    if (part == 0) entropy_add<true>(tw + b * 256, mine, v);
+                    else entropy_add<false>(tw + b * 256, mine, v);
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) umma::arrive_cluster(signal + 8 * b);
+                }
+                if (!ok) break;
+                entropy_tile(a, mine, m0, col, n_ok, v);
+                continue;
+            }
             for (uint32_t part = 0; part < a.splits; ++part) {
                 b = sums.take<PARTS>(part);
                 if (!(ok = umma::wait(bar_sum + 8 * b, sums.parity(b)))) break;
@@ -694,9 +710,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             };
             // (the same for the whole warp)
             const bool all = __all_sync(0xFFFFFFFFu, n_ok) && m0 + mine <= a.rows;
-            if constexpr (END == kEndEntropy) {
-                entropy_tile(a, tw + b * 256, mine, m0, col, n_ok, give_back);
-            } else if constexpr (END != kEndPlain) {
+            if constexpr (END != kEndPlain) {
                 end_tile<END, OUT>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, give_back);
             } else if (a.e.residual != nullptr) {
                 if (all) emit_tile<OUT, true, true>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, give_back);

@@ -201,35 +201,57 @@ __device__ __forceinline__ void join_groups(float& top, float& sum, float top2, 
     top = most;
 }
 
-template <typename GiveBack>
-__device__ __forceinline__ void entropy_tile(const TileArgs& a, uint32_t from, uint32_t mine, uint32_t m0, int64_t t, bool ok,
-                                             GiveBack give_back) {
+// The longest run of blocks of K that one accumulator sums: the tensor cores
+// cut off each addition's last bits, so a logit is short by about half a unit
+// of the last place for each 16 products.  Runs are added up in registers,
+// rounded to nearest: K = 7168 in one run, lse is 3.9e-6 off (in norm, against
+// 64 bits), in runs of 16 blocks 6e-7, FP32 sums of the plain form's 8e-7.
+constexpr uint32_t kEntropyRun = 16;
+constexpr int kEntropyMost = 64;   // entries of a thread
+
+// Adds a finished run of `mine` columns, in tensor memory at `from`, to v.
+template <bool FIRST>
+__device__ __forceinline__ void entropy_add(uint32_t from, uint32_t mine, float (&v)[kEntropyMost / 8][8]) {
+#pragma unroll
+    for (uint32_t i = 0; i < kEntropyMost / 8; i += 2) {
+        if (8 * i >= mine) break;
+        float w[2][8];
+        umma::tmem_ld(from + 8 * i, w[0]);
+        umma::tmem_ld(from + 8 * i + 8, w[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            umma::tmem_wait_ld(w[k]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i + k][j] = FIRST ? w[k][j] : __fadd_rn(v[i + k][j], w[k][j]);
+        }
+    }
+}
+
+// The group of the thread's logits v.
+__device__ __forceinline__ void entropy_tile(const TileArgs& a, uint32_t mine, uint32_t m0, int64_t t, bool ok,
+                                             float (&v)[kEntropyMost / 8][8]) {
     constexpr int kRun = 32;
     const int64_t target = ok ? __ldg(a.end.target + t) : -1;
     float top = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-    for (uint32_t c = 0; c < mine; c += kRun) {
-        float v[kRun / 8][8];
 #pragma unroll
-        for (int i = 0; i < kRun / 8; ++i) umma::tmem_ld(from + c + 8 * i, v[i]);
-#pragma unroll
-        for (int i = 0; i < kRun / 8; ++i) umma::tmem_wait_ld(v[i]);
-        if (c + kRun >= mine) give_back();
+    for (int c = 0; c < kEntropyMost; c += kRun) {
+        if (uint32_t(c) >= mine) break;
         const uint32_t first = m0 + c;
+        float(*q)[8] = v + c / 8;
         if (first + kRun > a.rows) {   // (the same for the whole warp)
 #pragma unroll
             for (int i = 0; i < kRun; ++i)
-                if (first + i >= a.rows) v[i / 8][i % 8] = -INFINITY;
+                if (first + i >= a.rows) q[i / 8][i % 8] = -INFINITY;
         }
         const int64_t rel = target - int64_t(first);
         if (__any_sync(0xFFFFFFFFu, rel >= 0 && rel < kRun)) {
 #pragma unroll
             for (int i = 0; i < kRun; ++i)
-                if (rel == i) a.end.at[t] = v[i / 8][i % 8];
+                if (rel == i) a.end.at[t] = q[i / 8][i % 8];
         }
         float most[8], part[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) most[j] = fmaxf(fmaxf(v[0][j], v[1][j]), fmaxf(v[2][j], v[3][j]));
+        for (int j = 0; j < 8; ++j) most[j] = fmaxf(fmaxf(q[0][j], q[1][j]), fmaxf(q[2][j], q[3][j]));
 #pragma unroll
         for (int s = 4; s > 0; s >>= 1)
 #pragma unroll
@@ -239,7 +261,7 @@ __device__ __forceinline__ void entropy_tile(const TileArgs& a, uint32_t from, u
         for (int j = 0; j < 8; ++j) {
             float w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = exp_fast(__fsub_rn(v[i][j], ref));
+            for (int i = 0; i < 4; ++i) w[i] = exp_fast(__fsub_rn(q[i][j], ref));
             part[j] = __fadd_rn(__fadd_rn(w[0], w[1]), __fadd_rn(w[2], w[3]));
         }
 #pragma unroll
