@@ -55,7 +55,7 @@ LAYER_SOURCES = [os.path.join(CSRC, f) for f in
                   "mhc_launch_entropy.cu")]
 LAYER_DEPS = LAYER_SOURCES + [os.path.join(CSRC, f) for f in
                               ("mhc_layer_launch.cuh", "mhc_norm.cuh", "mhc_linear.cuh", "mhc_linear_ends.cuh", "mhc_linear_launch.cuh",
-                               "mhc_linear_plan.h", "mhc_umma.cuh", "mhc_rotary.cuh", "mhc_gated.cuh", "mhc_entropy.cuh",
+                               "mhc_linear_plan.h", "mhc_umma.cuh", "mhc_rotary.cuh", "mhc_few.cuh", "mhc_gated.cuh", "mhc_entropy.cuh",
                                "mhc_launch.cuh", "mhc_device.cuh", "mhc_coeffs.cuh", "mhc_shift.cuh",
                                "mhc_shift_bulk.cuh", "mhc_bulk.cuh", "mhc_f32x2.cuh", "fastdiv.cuh")] \
     + [os.path.join(INCLUDE, f) for f in ("mhc_layer.h", "mhc_h_aggregate.h")]

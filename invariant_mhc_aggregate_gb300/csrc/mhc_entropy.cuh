@@ -8,51 +8,76 @@
 namespace mhc {
 namespace entropy {
 
-// lse and loss of 32 tokens a block: worker i takes the groups i, i + 32, ...
-// one after the other, then the workers' pairs meet in a tree; the order
-// depends on the number of groups alone.  HBM-bound where tokens are many
-// (8 bytes a group and token), by the loads' latency where they are few.
-constexpr int kWorkers = 32;
+// lse and loss from the units' pairs: THREADS threads a token (a warp, or a
+// block where a token has more groups than 256), thread i takes the groups i,
+// i + THREADS, ... one after the other, a group's units in increasing order,
+// then the threads' pairs meet in a tree; the order depends on V alone.
+// Bound by the loads' latency: T = 8, V = 32768 FIG_JOIN us.
+constexpr int kJoinThreads = 256;
 
-static __global__ void __launch_bounds__(32 * kWorkers)
+template <int THREADS>
+static __global__ void __launch_bounds__(kJoinThreads)
 join_kernel(const float2* __restrict__ partial, const float* __restrict__ at, const int64_t* __restrict__ target,
-            float* __restrict__ loss, float* __restrict__ lse, int64_t T, int64_t V, uint32_t groups) {
+            float* __restrict__ loss, float* __restrict__ lse, int64_t T, int64_t V, int64_t units, uint32_t of_a_group) {
     pdl_enter();
-    const uint32_t lane = threadIdx.x % 32, worker = threadIdx.x / 32;
-    __shared__ float2 part[kWorkers][32];
-    const int64_t t = int64_t(blockIdx.x) * 32 + lane;
+    const uint32_t i = threadIdx.x % THREADS;
+    const int64_t t = int64_t(blockIdx.x) * (kJoinThreads / THREADS) + threadIdx.x / THREADS;
     float top = -INFINITY, sum = 0.0f;
     if (t < T) {
-        const float2* p = partial + t;
-        uint32_t g = worker;
-        constexpr int kAhead = 4;
-        for (; g + (kAhead - 1) * kWorkers < groups; g += kAhead * kWorkers) {
-            float2 w[kAhead];
+        const float2* p = partial + t * units;
+        for (int64_t u = int64_t(i) * of_a_group; u < units; u += int64_t(THREADS) * of_a_group) {
+            float2 w[4];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) w[i] = __ldcs(p + int64_t(g + i * kWorkers) * T);
+            for (int k = 0; k < 4; ++k)
+                if (uint32_t(k) < of_a_group) w[k] = u + k < units ? __ldcs(p + u + k) : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) linear::join_groups(top, sum, w[i].x, w[i].y);
-        }
-        for (; g < groups; g += kWorkers) {
-            const float2 w = __ldcs(p + int64_t(g) * T);
-            linear::join_groups(top, sum, w.x, w.y);
+            for (int k = 1; k < 4; ++k)
+                if (uint32_t(k) < of_a_group) linear::join_groups(w[0].x, w[0].y, w[k].x, w[k].y);
+            linear::join_groups(top, sum, w[0].x, w[0].y);
         }
     }
-    part[worker][lane] = make_float2(top, sum);
-    for (int s = kWorkers / 2; s > 0; s >>= 1) {
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+        const float top2 = __shfl_xor_sync(0xFFFFFFFFu, top, s), sum2 = __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+        linear::join_groups(top, sum, top2, sum2);
+    }
+    if constexpr (THREADS > 32) {
+        __shared__ float2 part[THREADS / 32];
+        if (i % 32 == 0) part[i / 32] = make_float2(top, sum);
         __syncthreads();
-        if (int(worker) < s) {
-            const float2 w = part[worker + s][lane];
-            linear::join_groups(top, sum, w.x, w.y);
-            part[worker][lane] = make_float2(top, sum);
-        }
+        top = part[0].x, sum = part[0].y;
+#pragma unroll
+        for (int w = 1; w < THREADS / 32; ++w) linear::join_groups(top, sum, part[w].x, part[w].y);
     }
-    if (worker == 0 && t < T) {
+    if (i == 0 && t < T) {
         const float all = __fadd_rn(linear::reference(top), logf(sum));
         lse[t] = all;
-        const int64_t at_entry = target[t];
-        loss[t] = at_entry >= 0 && at_entry < V ? __fsub_rn(all, at[t]) : 0.0f;
+        const int64_t entry = target[t];
+        loss[t] = entry >= 0 && entry < V ? __fsub_rn(all, at[t]) : 0.0f;
     }
+}
+
+// grad_x from the parts' sums: their sum in increasing order, scaled and rounded.
+constexpr int kSumThreads = 256;
+
+template <int DT>
+static __global__ void __launch_bounds__(kSumThreads)
+sum_kernel(const float* __restrict__ sums, const float* __restrict__ factor, uint16_t* __restrict__ out, int64_t n, uint32_t parts) {
+    pdl_enter();
+    const float f = *factor;
+    const int64_t i = (int64_t(blockIdx.x) * kSumThreads + threadIdx.x) * 2;
+    if (i >= n) return;
+    const bool two = i + 1 < n;
+    float a = 0.0f, b = 0.0f;
+#pragma unroll 4
+    for (uint32_t p = 0; p < parts; ++p) {
+        const float* q = sums + int64_t(p) * n + i;
+        const float x = __ldcs(q), y = two ? __ldcs(q + 1) : 0.0f;
+        a = p == 0 ? x : __fadd_rn(a, x);
+        b = p == 0 ? y : __fadd_rn(b, y);
+    }
+    out[i] = Elem<DT>::cvt(__fmul_rn(a, f));
+    if (two) out[i + 1] = Elem<DT>::cvt(__fmul_rn(b, f));
 }
 
 // Each token's part of d, times a power of two that brings the largest

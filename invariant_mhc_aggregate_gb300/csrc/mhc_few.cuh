@@ -1,0 +1,201 @@
+// Products of few rows (sm_103a): the weight's bytes are the whole cost, so
+// its rows are dealt out evenly to all SMs and stream without a pause.
+#pragma once
+
+#include "mhc_linear.cuh"
+
+namespace mhc {
+namespace linear {
+
+// One persistent CTA an SM takes tiles of a.lanes output columns (weight rows,
+// a multiple of 16, at most 128: as many as make the CTAs' shares even) by all
+// of the call's rows, at most WIDTH.  Against split_kernel, whose tiles are
+// always 128 lanes and end in an epilogue of their own, no SM has a tile more
+// than the others and the copies of the next tile run under the end of this
+// one: T = 8, I = 2048, 32768 entries of a vocabulary FIG_CE_FEW us, T = 1,
+// 2048 -> 2 x 8192 FIG_GATED_ONE.
+//
+// The multiplications are 128 lanes high whatever a.lanes is: the rows of
+// shared memory past them are never written, and what they bring stays in
+// lanes that nobody reads.
+//
+// Parts of K are summed apart, in kSlots accumulators in turn, and added in
+// increasing order in registers: the bits of split_kernel and pair_kernel.
+//
+// Warps 0 .. 4 groups - 1 read tensor memory (a group is four warps, for the
+// quarters of the lanes, and has 8 or 16 columns), then one warp copies and one
+// multiplies.
+constexpr uint32_t kSlots = 4;
+
+template <int WIDTH>
+constexpr int kFewGroups = WIDTH < 32 ? WIDTH / 8 : 4;
+template <int WIDTH>
+constexpr uint32_t kFewThreads = 32 * (4 * kFewGroups<WIDTH> + 2);
+
+// The groups' maxima and sums of one tile: 16 lanes are 16 entries of the
+// vocabulary, and v one token's logit of each (entropy_tile has the same sums
+// in the same order).
+template <int C>
+__device__ __forceinline__ void entropy_lanes(const TileArgs& a, uint32_t m0, int64_t n, bool n_ok, float (&v)[C]) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const uint32_t m = m0 + c;
+        if (m >= a.rows) break;   // (the same for the whole warp)
+        if (n_ok && __ldg(a.end.target + m) == n) a.end.at[m] = v[c];
+        float top = n_ok ? v[c] : -INFINITY;
+        const float x = top;
+#pragma unroll
+        for (int s = 8; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+        float sum = exp_fast(__fsub_rn(x, reference(top)));
+#pragma unroll
+        for (int s = 8; s > 0; s >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, s));
+        if ((threadIdx.x & 15) == 0 && n_ok) a.end.partial[int64_t(m) * a.end.units + n / kEntropyUnit] = make_float2(top, sum);
+    }
+}
+
+template <bool FP8, int OUT, int WIDTH, int END>
+__global__ void __launch_bounds__(kFewThreads<WIDTH>, 1)
+few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUtensorMap mq, const __grid_constant__ TileArgs a) {
+    constexpr int kGroups = kFewGroups<WIDTH>, C = WIDTH / kGroups;   // columns of a thread
+    constexpr uint32_t kReaders = 4 * kGroups, kColumns = kSlots * WIDTH;
+    extern __shared__ char raw[];
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], sum_full[kSlots], sum_empty[kSlots];
+    __shared__ uint32_t tmem_base;
+    char* stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t tiles = a.p_tiles;
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < a.stages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (uint32_t s = 0; s < kSlots; ++s) {
+            mbar_init(sum_full + s, 1);
+            mbar_init(sum_empty + s, kReaders);
+        }
+        mbar_init_fence();
+    }
+    if (warp == kReaders) {
+        umma::tmem_alloc<1>(&tmem_base, kColumns);
+        if (lane == 0) {
+            umma::prefetch_map(&mp);
+            umma::prefetch_map(&mq);
+        }
+    }
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = tmem_base;
+    pdl_enter();
+    const uint32_t ring = smem_addr(stages), bar_full = smem_addr(full), bar_empty = smem_addr(empty);
+    const uint32_t bar_sum = smem_addr(sum_full), bar_free = smem_addr(sum_empty);
+    const uint32_t count = a.stages, bytes = a.stage_bytes, unit = a.unit;
+    if (warp == kReaders) {
+        umma::Ring at;
+        bool ok = true;
+        uint32_t issued = 0;
+        for (uint32_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+            const int p0 = int(i * a.lanes);
+            uint32_t k = 0;
+            for (uint32_t part = 0; part < a.splits && ok; ++part) {
+                for (const uint32_t k1 = split_begin(a, part + 1); k < k1; ++issued, at.next(count)) {
+                    if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
+                    const uint32_t n = min(unit, k1 - k);
+                    if (umma::elect()) {
+                        umma::expect_tx(bar_full + 8 * at.stage, n * (a.lanes + WIDTH) * 128);
+                        for (uint32_t u = 0; u < n; ++u) {
+                            const uint32_t to = ring + at.stage * bytes + u * a.block_bytes;
+                            load_p<1, FP8, kBothK, END, kFewRun>(to, &mp, k + u, p0, bar_full + 8 * at.stage, a.lanes);
+                            load_q<1, FP8, kBothK>(to, &mq, k + u, 0, WIDTH, bar_full + 8 * at.stage);
+                        }
+                    }
+                    __syncwarp();
+                    k += n;
+                }
+            }
+        }
+        drain(ok, min(issued, count), at, count, bar_empty, bar_full);
+        if (!ok) timed_out(a);
+    } else if (warp == kReaders + 1) {
+        const Descs d = descs<kBothK>(ring);
+        const uint32_t idesc = a.idesc;
+        umma::Ring at, sums;
+        bool ok = true;
+        for (uint32_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+            uint32_t k = 0;
+            for (uint32_t part = 0; part < a.splits && ok; ++part, sums.next(kSlots)) {
+                if (!(ok = umma::wait(bar_free + 8 * sums.stage, sums.parity ^ 1))) break;
+                umma::fence_after_sync();
+                const uint32_t to = tmem + sums.stage * WIDTH, k0 = k, k1 = split_begin(a, part + 1);
+                for (; k < k1; at.next(count)) {
+                    if (!(ok = umma::wait(bar_full + 8 * at.stage, at.parity))) break;
+                    umma::fence_after_sync();
+                    const uint32_t n = min(unit, k1 - k);
+                    if (umma::elect()) {
+                        for (uint32_t u = 0; u < n; ++u)
+                            multiply_block<1, FP8, kBothK>(d, at.stage * bytes + u * a.block_bytes, idesc, to, k + u == k0);
+                        umma::commit<1>(bar_empty + 8 * at.stage);
+                        if (k + n == k1) umma::commit<1>(bar_sum + 8 * sums.stage);
+                    }
+                    __syncwarp();
+                    k += n;
+                }
+            }
+        }
+        if (!ok) timed_out(a);
+    } else {
+        const uint32_t quarter = warp % 4, m0 = warp / 4 * C;   // the thread's lane, its columns m0 .. m0 + C
+        const uint32_t in_tile = quarter * 32 + lane;
+        const uint32_t tw = tmem + (quarter * 32u << 16) + m0;
+        umma::Ring sums;
+        bool ok = true;
+        for (uint32_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+            int64_t n = int64_t(i) * a.lanes + in_tile;
+            bool n_ok = n < a.N;
+            if constexpr (END == kEndGated) n = gated_column<kFewRun>(a.end.half, n, n_ok);
+            n_ok = n_ok && in_tile < a.lanes;
+            const float bias = a.e.bias != nullptr && n_ok ? __ldg(a.e.bias + n) : 0.0f;
+            const float cs = a.e.col_scale != nullptr && n_ok ? __ldg(a.e.col_scale + n) : 1.0f;
+            float v[C / 8][8];
+            for (uint32_t part = 0; part < a.splits; ++part, sums.next(kSlots)) {
+                if (!(ok = umma::wait(bar_sum + 8 * sums.stage, sums.parity))) break;
+                umma::fence_after_sync();
+                const uint32_t from = tw + sums.stage * WIDTH;
+                if (part == 0) {
+#pragma unroll
+                    for (int c = 0; c < C / 8; ++c) umma::tmem_ld(from + 8 * c, v[c]);
+#pragma unroll
+                    for (int c = 0; c < C / 8; ++c) umma::tmem_wait_ld(v[c]);
+                } else {
+                    float w[C / 8][8];
+#pragma unroll
+                    for (int c = 0; c < C / 8; ++c) umma::tmem_ld(from + 8 * c, w[c]);
+#pragma unroll
+                    for (int c = 0; c < C / 8; ++c) {
+                        umma::tmem_wait_ld(w[c]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[c][j] = __fadd_rn(v[c][j], w[c][j]);
+                    }
+                }
+                umma::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) umma::arrive_cluster(bar_free + 8 * sums.stage);
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < C / 8; ++c) {
+                if (m0 + 8 * c >= a.rows) break;
+                if constexpr (END == kEndEntropy) entropy_lanes<8>(a, m0 + 8 * c, n, n_ok, v[c]);
+                else emit_end<END, OUT, 8, kFewRun>(a, n_ok, n, m0 + 8 * c, 1, a.rows, v[c], bias, cs);
+            }
+        }
+        if (!ok) timed_out(a);
+        umma::fence_before_sync();
+    }
+    __syncthreads();
+    umma::fence_after_sync();
+    if (warp == kReaders) umma::tmem_free<1>(tmem, kColumns);
+}
+
+}  // namespace linear
+}  // namespace mhc

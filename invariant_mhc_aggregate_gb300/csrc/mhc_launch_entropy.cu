@@ -7,57 +7,64 @@ namespace layer {
 
 namespace {
 
-template <int END, int OUT, int LAYOUT>
-cudaError_t launch_end(bool pair, const TileArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t stream) {
-    static std::atomic<uint64_t> allowed[2];
-    if (!pair) return launch_split_kernel(split_kernel<false, OUT, LAYOUT, END>, allowed[0], a, mp, mq, stream);
-    return launch_pair_kernel(pair_kernel<false, OUT, LAYOUT, false, END>, allowed[1], a, pairs_of(a), mp, mq, stream);
-}
-
-// A product of 16-bit operands that ends in `end`.
 template <int END, int LAYOUT>
-cudaError_t product_into(const Product& p, const EndArgs& end, int dtype, cudaStream_t stream) {
-    TileArgs a;
-    CUtensorMap mp, mq;
-    const Plan plan = plan_of(p.N, p.M, k_blocks(p, dtype), p.a_mn, false);
-    const cudaError_t e = lay_out(p, dtype, plan, a, mp, mq);
-    if (e != cudaSuccess) return e;
-    a.end = end;
-    return dtype == kBF16 ? launch_end<END, kBF16, LAYOUT>(plan.pair, a, mp, mq, stream)
-                          : launch_end<END, kF16, LAYOUT>(plan.pair, a, mp, mq, stream);
+cudaError_t launch_end(const TileArgs& a, int dtype, uint32_t pairs, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed[2];
+    if (dtype == kBF16) return launch_pair_kernel(pair_kernel<false, kBF16, LAYOUT, false, END>, allowed[0], a, pairs, mp, mq, stream);
+    return launch_pair_kernel(pair_kernel<false, kF16, LAYOUT, false, END>, allowed[1], a, pairs, mp, mq, stream);
 }
 
-// Entries of the vocabulary of a tile.  The groups that are summed together
-// are a quarter of it, so it follows from V alone (a token's loss has the same
-// bits in every batch): 256 where that gives every pair of CTAs a tile
-// whatever the number of tokens, 128 below.
-uint32_t entropy_width(int64_t V) { return V >= 256 * kPairsAtOnce ? 256 : 128; }
+// The tile of rows (a multiple of 64: row_tile's 16 for each of four warps) that
+// pair_kernel takes, by plan_of's estimate of its rounds.
+uint32_t pair_width(int64_t N, int64_t M, int64_t kb, bool q_mn) {
+    uint32_t best = 256;
+    int64_t least = INT64_MAX;
+    for (int64_t w = 128; w <= 256; w += q_mn ? 128 : 64) {
+        const int64_t rounds = ((N + 255) / 256 * ((M + w - 1) / w) + kPairsAtOnce - 1) / kPairsAtOnce;
+        const int64_t cost = 21 * w + rounds * (kb * (41 * w / 20 > 300 ? 41 * w / 20 : 300) + 1500);
+        if (cost < least) least = cost, best = uint32_t(w);
+    }
+    return best;
+}
+
+// Entries of the vocabulary that are summed together before the join: they
+// follow from V alone, so that a token's loss has the same bits in every
+// batch.  With few tokens few_kernel writes their units of 16; else pair_kernel
+// takes 4 groups a tile: 64 entries where that gives every pair of CTAs a tile
+// whatever the number of tokens, 32 below.
+int64_t entropy_group(int64_t V) { return V >= 256 * kPairsAtOnce ? 64 : 32; }
 
 }  // namespace
 
-int64_t entropy_groups(int64_t V) {
-    const int64_t group = entropy_width(V) / 4;
-    return (V + group - 1) / group;
+int64_t entropy_pairs(int64_t T, int64_t V) {
+    const int64_t group = T <= kFewRows ? kEntropyUnit : entropy_group(V);
+    return T * ((V + group - 1) / group);
 }
 
 cudaError_t entropy_fwd(const EntropyCall& c, float* loss, float* lse, float2* partial, float* at) {
-    Product p;
-    p.a = c.w, p.a_stride = c.w_stride, p.a_mn = false;
-    p.b = c.x, p.b_stride = c.x_stride, p.b_mn = false;
-    p.M = c.V, p.N = c.T, p.K = c.I, p.by_row = true;
-    p.e = {};
+    const bool few = c.T <= kFewRows;
+    const int64_t group = entropy_group(c.V), units = entropy_pairs(c.T, c.V) / c.T, groups = (c.V + group - 1) / group;
+    Product p;   // the vocabulary on the lanes, or, with more tokens, the tokens
+    const Product by_entry = {c.x, c.w, c.x_stride, c.w_stride, false, false, true, c.T, c.V, c.I, {}};
+    const Product by_token = {c.w, c.x, c.w_stride, c.x_stride, false, false, true, c.V, c.T, c.I, {}};
+    p = few ? by_entry : by_token;
     TileArgs a;
     CUtensorMap mp, mq;
     const uint32_t runs = uint32_t((k_blocks(p, c.dtype) + kEntropyRun - 1) / kEntropyRun);
-    cudaError_t e = lay_out(p, c.dtype, {true, entropy_width(c.V), runs}, a, mp, mq);
+    cudaError_t e = few ? lay_out_few(p, c.dtype, few_lanes(c.V), runs, a, mp, mq)
+                        : lay_out(p, c.dtype, {true, uint32_t(4 * group), runs}, a, mp, mq);
     if (e != cudaSuccess) return e;
     a.end = {};
-    a.end.partial = partial, a.end.at = at, a.end.target = c.target;
+    a.end.partial = partial, a.end.units = units, a.end.at = at, a.end.target = c.target;
     static std::atomic<uint64_t> allowed{0};
-    e = launch_pair_kernel(pair_kernel<false, kBF16, kBothK, false, kEndEntropy>, allowed, a, pairs_of(a), mp, mq, c.stream);
+    e = few ? launch_few<false, kBF16, kEndEntropy>(a, mp, mq, c.stream)
+            : launch_pair_kernel(pair_kernel<false, kBF16, kBothK, false, kEndEntropy>, allowed, a, pairs_of(a), mp, mq, c.stream);
     if (e != cudaSuccess) return e;
-    return launch(entropy::join_kernel, uint32_t((c.T + 31) / 32), 32 * entropy::kWorkers, c.stream, partial, at, c.target,
-                  loss, lse, c.T, c.V, uint32_t(entropy_groups(c.V)));
+    const bool wide = groups > 256;
+    const int64_t per_block = wide ? 1 : entropy::kJoinThreads / 32;
+    return launch(wide ? entropy::join_kernel<entropy::kJoinThreads> : entropy::join_kernel<32>,
+                  uint32_t((c.T + per_block - 1) / per_block), entropy::kJoinThreads, c.stream, partial, at, c.target, loss, lse, c.T,
+                  c.V, units, few ? uint32_t(group / kEntropyUnit) : 1u);
 }
 
 cudaError_t entropy_tokens(const EntropyCall& c, const float* grad_loss, const float* grad_lse, const float* lse,
@@ -66,43 +73,65 @@ cudaError_t entropy_tokens(const EntropyCall& c, const float* grad_loss, const f
                   factor, c.T, c.V);
 }
 
+// d [T,count] with the tokens on the lanes: a thread has the entries of one token.
 cudaError_t entropy_logit_grad(const EntropyCall& c, const EntropyToken* tokens, int64_t first, int64_t count, uint16_t* d,
                                int64_t pitch) {
-    Product p;
-    p.a = c.x, p.a_stride = c.x_stride, p.a_mn = false;
-    p.b = static_cast<const uint16_t*>(c.w) + first * c.w_stride, p.b_stride = c.w_stride, p.b_mn = false;
-    p.M = c.T, p.N = count, p.K = c.I, p.by_row = false;
-    p.e = {};
+    const void* w = static_cast<const uint16_t*>(c.w) + first * c.w_stride;
+    Product p = {w, c.x, c.w_stride, c.x_stride, false, false, false, count, c.T, c.I, {}};
     p.e.y = d;
-    EndArgs end = {};
-    end.tokens = tokens, end.first = int32_t(first), end.pitch = pitch;
-    return product_into<kEndProb, kBothK>(p, end, c.dtype, c.stream);
+    TileArgs a;
+    CUtensorMap mp, mq;
+    const cudaError_t e = lay_out(p, c.dtype, {true, pair_width(c.T, count, k_blocks(p, c.dtype), false), 1}, a, mp, mq);
+    if (e != cudaSuccess) return e;
+    a.end = {};
+    a.end.tokens = tokens, a.end.first = int32_t(first), a.end.pitch = pitch;
+    return launch_end<kEndProb, kBothK>(a, c.dtype, pairs_of(a), mp, mq, c.stream);
 }
 
-cudaError_t entropy_grad_x(const EntropyCall& c, const uint16_t* d, int64_t pitch, int64_t first, int64_t count,
+uint32_t entropy_parts(int64_t T, int64_t I, int64_t count) { return sum_plan(I, T, (count + 63) / 64).splits; }
+
+cudaError_t entropy_grad_x(const EntropyCall& c, const uint16_t* d, int64_t pitch, int64_t first, int64_t count, uint32_t parts,
                            const float* sum_in, float* sum_out, const float* factor, void* grad_x) {
-    Product p;   // [T,I] += d [T,count] . w[first ..] [count,I]
-    p.a = d, p.a_stride = pitch, p.a_mn = false;
-    p.b = static_cast<const uint16_t*>(c.w) + first * c.w_stride, p.b_stride = c.w_stride, p.b_mn = true;
-    p.M = c.T, p.N = c.I, p.K = count, p.by_row = false;
-    p.e = {};
+    const void* w = static_cast<const uint16_t*>(c.w) + first * c.w_stride;
+    Product p = {d, w, pitch, c.w_stride, false, true, false, c.T, c.I, count, {}};   // [T,I] = d [T,count] . w[first ..] [count,I]
     p.e.y = static_cast<uint16_t*>(grad_x);
-    EndArgs end = {};
-    end.sum_in = sum_in, end.sum_out = sum_out, end.factor = factor;
-    return product_into<kEndSum, kPMnQK>(p, end, c.dtype, c.stream);
+    const int64_t kb = k_blocks(p, c.dtype);
+    Plan plan = sum_plan(c.I, c.T, kb);
+    plan.splits = kb < parts ? uint32_t(kb) : parts;   // (a last, shorter piece adds to the first of them)
+    TileArgs a;
+    CUtensorMap mp, mq;
+    const cudaError_t e = lay_out(p, c.dtype, plan, a, mp, mq);
+    if (e != cudaSuccess) return e;
+    a.end = {};
+    a.end.sum_in = sum_in, a.end.sum_out = sum_out, a.end.factor = factor;
+    return launch_end<kEndSum, kPMnQK>(a, c.dtype, pairs_of(a, a.splits), mp, mq, c.stream);
 }
 
+cudaError_t entropy_sum(const EntropyCall& c, const float* sums, uint32_t parts, const float* factor, void* grad_x) {
+    const int64_t n = c.T * c.I, blocks = (n + 2 * entropy::kSumThreads - 1) / (2 * entropy::kSumThreads);
+    if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    return launch(c.dtype == kBF16 ? entropy::sum_kernel<kBF16> : entropy::sum_kernel<kF16>, uint32_t(blocks), entropy::kSumThreads,
+                  c.stream, sums, factor, static_cast<uint16_t*>(grad_x), n, parts);
+}
+
+// [count,I] = d^T [count,T] . x [T,I].  Where grad_w's rows are whole 16-byte
+// vectors the vocabulary is on the lanes and a thread stores a row's values
+// in vectors; rows at any alignment have their values on the lanes.
 cudaError_t entropy_grad_w(const EntropyCall& c, const uint16_t* d, int64_t pitch, int64_t first, int64_t count,
                            const float* factor, void* grad_w) {
-    Product p;   // [count,I] = d^T [count,T] . x [T,I]
-    p.a = d, p.a_stride = pitch, p.a_mn = true;
-    p.b = c.x, p.b_stride = c.x_stride, p.b_mn = true;
-    p.M = count, p.N = c.I, p.K = c.T, p.by_row = false;
-    p.e = {};
-    p.e.y = static_cast<uint16_t*>(grad_w) + first * c.I;
-    EndArgs end = {};
-    end.factor = factor;
-    return product_into<kEndSum, kBothMn>(p, end, c.dtype, c.stream);
+    uint16_t* out = static_cast<uint16_t*>(grad_w) + first * c.I;
+    const bool rows = c.I % 8 == 0 && aligned(out, 16);
+    Product p = {c.x, d, c.x_stride, pitch, true, true, false, c.I, count, c.T, {}};
+    if (!rows) p = {d, c.x, pitch, c.x_stride, true, true, false, count, c.I, c.T, {}};
+    p.e.y = out;
+    TileArgs a;
+    CUtensorMap mp, mq;
+    const cudaError_t e = lay_out(p, c.dtype, {true, pair_width(p.N, p.M, k_blocks(p, c.dtype), true), 1}, a, mp, mq);
+    if (e != cudaSuccess) return e;
+    a.end = {};
+    a.end.factor = factor, a.end.pitch = c.I;
+    return rows ? launch_end<kEndRow, kBothMn>(a, c.dtype, pairs_of(a), mp, mq, c.stream)
+                : launch_end<kEndSum, kBothMn>(a, c.dtype, pairs_of(a), mp, mq, c.stream);
 }
 
 }  // namespace layer

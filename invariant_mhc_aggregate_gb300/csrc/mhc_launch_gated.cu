@@ -7,15 +7,15 @@ namespace layer {
 
 namespace {
 
-// w [2 F, I] as {I, F, 2}: a box has 128 bytes of K of 16 rows of the gate and
-// of the same 16 of the up projection, and rows at or past F read as zero in
-// each half.
-cudaError_t encode_gated(CUtensorMap* map, const void* w, int64_t F, int64_t I, int64_t stride, int64_t size) {
+// w [2 F, I] as {I, F, 2}: a box has 128 bytes of K of `run` rows of the gate
+// and of the same rows of the up projection, and rows at or past F read as
+// zero in each half.
+cudaError_t encode_gated(CUtensorMap* map, const void* w, int64_t F, int64_t I, int64_t stride, int64_t size, uint32_t run) {
     const PFN_cuTensorMapEncodeTiled_v12000 f = tensor_map_encoder();
     if (f == nullptr) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {cuuint64_t(I), cuuint64_t(F), 2};
     const cuuint64_t strides[2] = {cuuint64_t(stride * size), cuuint64_t(F * stride * size)};
-    const cuuint32_t box[3] = {cuuint32_t(128 / size), 16, 2};
+    const cuuint32_t box[3] = {cuuint32_t(128 / size), run, 2};
     const cuuint32_t step[3] = {1, 1, 1};
     const bool sectors = strides[0] % 32 == 0 && reinterpret_cast<uintptr_t>(w) % 32 == 0;   // (as in encode)
     const CUresult r = f(map, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(w),
@@ -50,12 +50,20 @@ cudaError_t gated_product(const Product& p, int in, int out, cudaStream_t stream
     TileArgs a;
     CUtensorMap mp, mq;
     const Plan plan = plan_of(p.N, p.M, k_blocks(p, in), false, true);
-    cudaError_t e = lay_out(p, in, plan, a, mp, mq);
+    const bool few = p.M <= kFewRows && plan.splits == 1;   // (parts of K are faster in a cluster's CTAs)
+    cudaError_t e = few ? lay_out_few(p, in, few_lanes(p.N), plan.splits, a, mp, mq) : lay_out(p, in, plan, a, mp, mq);
     if (e != cudaSuccess) return e;
     a.end = {};
     a.end.half = p.N / 2;
-    e = encode_gated(&mp, p.b, p.N / 2, p.K, p.b_stride, in == kE4m3 ? 1 : 2);
+    e = encode_gated(&mp, p.b, p.N / 2, p.K, p.b_stride, in == kE4m3 ? 1 : 2, few ? kFewRun : kGatedRun);
     if (e != cudaSuccess) return e;
+    if (few) {
+        if (in == kE4m3)
+            return out == kBF16 ? launch_few<true, kBF16, kEndGated>(a, mp, mq, stream)
+                                : launch_few<true, kF16, kEndGated>(a, mp, mq, stream);
+        return out == kBF16 ? launch_few<false, kBF16, kEndGated>(a, mp, mq, stream)
+                            : launch_few<false, kF16, kEndGated>(a, mp, mq, stream);
+    }
     if (in == kE4m3)
         return out == kBF16 ? launch_gated<true, kBF16>(plan.pair, a, mp, mq, stream)
                             : launch_gated<true, kF16>(plan.pair, a, mp, mq, stream);

@@ -8,6 +8,7 @@
 
 #include "mhc_layer.h"
 #include "mhc_layer_launch.cuh"
+#include "mhc_linear_plan.h"
 
 namespace mhc {
 namespace layer {
@@ -242,20 +243,28 @@ mhc_status_t linear_fwd(const void* x, const float* x_scale, const void* w, cons
 
 // ---- cross entropy -------------------------------------------------------------
 
-// Entries of the vocabulary whose logits' gradients are in the workspace at a time.
+// Entries of the vocabulary whose logits' gradients are in the workspace at a
+// time: 19456 (a tile of 256 for each pair of CTAs), more with fewer tokens
+// (2^24 gradients), fewer with very many (1 GB).
 int64_t entropy_piece(int64_t T, int64_t V) {
-    const int64_t most = 16384;
-    return V < most ? (V + 63) / 64 * 64 : most;
+    int64_t n = 256 * mhc::linear::kPairsAtOnce;
+    if (T * n < int64_t(1) << 24) n = (int64_t(1) << 24) / T;
+    if (T * n > int64_t(1) << 29) n = (int64_t(1) << 29) / T;
+    if (n < 4096) n = 4096;
+    const int64_t pieces = (V + n - 1) / n;
+    return ((V + pieces - 1) / pieces + 63) / 64 * 64;
 }
 
 struct EntropySizes {
     int64_t piece, tokens, factor, d, sums;   // entries; bytes of each part of the workspace
+    uint32_t parts;
     EntropySizes(int64_t T, int64_t I, int64_t V, bool want_x) {
         piece = entropy_piece(T, V);
         tokens = T * int64_t(sizeof(mhc::linear::EntropyToken));
         factor = 16;
         d = round16(T * piece * 2);
-        sums = want_x && piece < V ? round16(T * I * 4) : 0;
+        parts = want_x ? mhc::layer::entropy_parts(T, I, piece < V ? piece : V) : 1;
+        sums = want_x && (piece < V || parts > 1) ? round16(parts * T * I * 4) : 0;
     }
     int64_t bytes() const { return tokens + factor + d + sums; }
 };
@@ -513,7 +522,7 @@ static bool entropy_sizes_ok(int64_t T, int64_t I, int64_t V) { return T <= kMax
 // logits, the operands laid out again.
 static int64_t entropy_workspace(int64_t T, int64_t I, int64_t V, int64_t x_stride, int64_t w_stride, bool x_aligned,
                                  bool w_aligned) {
-    return mhc::layer::entropy_groups(V) * T * 8 + T * 4 + 12 + Operand(nullptr, T, I, x_stride, 2, x_aligned).bytes() +
+    return mhc::layer::entropy_pairs(T, V) * 8 + T * 4 + 12 + Operand(nullptr, T, I, x_stride, 2, x_aligned).bytes() +
            Operand(nullptr, V, I, w_stride, 2, w_aligned).bytes();
 }
 
@@ -542,7 +551,7 @@ mhc_status_t mhc_linear_cross_entropy_fwd(const void* x, const void* w, const in
     const cudaError_t e = lay_out_again(calls, count, stream);
     if (e != cudaSuccess) return finish(e);
     float2* partial = reinterpret_cast<float2*>(at);
-    at += mhc::layer::entropy_groups(V) * T * 8;
+    at += mhc::layer::entropy_pairs(T, V) * 8;
     const mhc::layer::EntropyCall c = {xo.p, wo.p, target, T, I, V, xo.stride, wo.stride, int(dtype), cu(stream)};
     return finish(mhc::layer::entropy_fwd(c, loss, lse, partial, reinterpret_cast<float*>(at)));
 }
@@ -599,10 +608,11 @@ mhc_status_t mhc_linear_cross_entropy_bwd(const float* grad_loss, const float* g
         const int64_t n = V - v < sizes.piece ? V - v : sizes.piece;
         e = mhc::layer::entropy_logit_grad(c, tokens, v, n, d, sizes.piece);
         if (e == cudaSuccess && want_x)
-            e = mhc::layer::entropy_grad_x(c, d, sizes.piece, v, n, v == 0 ? nullptr : sums, v + n < V ? sums : nullptr, factor,
-                                           grad_x);
+            e = mhc::layer::entropy_grad_x(c, d, sizes.piece, v, n, sizes.parts, v == 0 ? nullptr : sums,
+                                           v + n < V || sizes.parts > 1 ? sums : nullptr, factor, grad_x);
         if (e == cudaSuccess && want_w) e = mhc::layer::entropy_grad_w(c, d, sizes.piece, v, n, factor, grad_w);
     }
+    if (e == cudaSuccess && want_x && sizes.parts > 1) e = mhc::layer::entropy_sum(c, sums, sizes.parts, factor, grad_x);
     return finish(e);
 }
 

@@ -82,8 +82,11 @@ enum End {
     kEndPlain = 0,
     kEndGated = 1,     // act(gate) * up, of two projections side by side on the lanes
     kEndSum = 2,       // added to FP32 sums, or their last addition, scaled and rounded
-    kEndProb = 3,      // the gradient of a cross entropy's logits
-    kEndEntropy = 4    // maxima and sums of exponentials over the output rows (pair_kernel alone)
+    kEndEntropy = 3,   // maxima and sums of exponentials over a vocabulary
+    // transposed: the lanes are the output's rows and the columns its contiguous
+    // index (N and M of the product), so that a thread stores whole sectors
+    kEndProb = 4,      // the gradient of a cross entropy's logits
+    kEndRow = 5        // scaled and rounded
 };
 
 // One token of a cross entropy's backward.
@@ -97,14 +100,20 @@ struct EndArgs {
     int64_t half;                     // kEndGated: F; the output's rows are F long, the lanes' 2 F
     const float* sum_in;              // kEndSum: [M,N] added first, or null
     float* sum_out;                   // where the sums go, or null: the last addition, into e.y
-    const float* factor;              // what that one is multiplied by
-    const EntropyToken* tokens;       // kEndProb: [M]
+    const float* factor;              // what that one, or kEndRow's, is multiplied by
+    const EntropyToken* tokens;       // kEndProb: [N]
     int32_t first;                    // the vocabulary's entry of output column 0
-    int64_t pitch;                    // of the output's rows
-    float2* partial;                  // kEndEntropy: [groups,N]: a group's maximum and its sum of exponentials
-    float* at;                        // [N] the target's logit
-    const int64_t* target;            // [N]
+    int64_t pitch;                    // kEndProb, kEndRow: of the output's rows
+    float2* partial;                  // kEndEntropy: [tokens,units]: a unit's maximum and its sum of exponentials
+    int64_t units;
+    float* at;                        // [tokens] the target's logit
+    const int64_t* target;            // [tokens]
 };
+
+// Rows of the gate that lie together on the lanes of a gated tile, then the
+// same rows of the up projection: pairs of the two 16 (8 in few_kernel, whose
+// tiles are any multiple of 16 lanes) lanes apart.
+constexpr int kGatedRun = 16, kFewRun = 8;
 
 // How a tile lies: the output's contiguous index n on the lanes of tensor
 // memory (operand P = B, 128 lanes a CTA) and its rows m on the columns
@@ -119,8 +128,10 @@ struct TileArgs {
     uint32_t kb;             // blocks of 128 bytes of K
     uint32_t splits;         // of K; split s takes the blocks [s kb / splits, (s + 1) kb / splits)
     uint32_t width;          // output rows of a tile
+    uint32_t lanes;          // few_kernel: output columns of a tile
     uint32_t stages, stage_bytes;
     uint32_t unit, block_bytes;   // blocks of K of a stage, and bytes of each
+    uint32_t p_box;               // pair_kernel: rows of P that a K-major copy brings (lanes past them are nobody's)
     uint32_t idesc;
     uint32_t p_tiles, q_tiles;
     unsigned int* timeouts;
@@ -226,14 +237,15 @@ __device__ __forceinline__ uint32_t split_begin(const TileArgs& a, uint32_t s) {
 }
 
 // One block of K of P (128 lanes from p0) and of Q (`columns` from q0) into a stage.
-template <int CG, bool FP8, int LAYOUT, int END>
-__device__ __forceinline__ void load_p(uint32_t stage, const CUtensorMap* mp, uint32_t k, int p0, uint32_t bar) {
+template <int CG, bool FP8, int LAYOUT, int END, int RUN = kGatedRun>
+__device__ __forceinline__ void load_p(uint32_t stage, const CUtensorMap* mp, uint32_t k, int p0, uint32_t bar,
+                                       uint32_t lanes = kLanesP) {
     const int k0 = int(k * (FP8 ? 128u : 64u));
     if constexpr (END == kEndGated) {
-        // 16 rows of the gate, then the same 16 of the up projection, in each 32 lanes
 #pragma unroll
-        for (int j = 0; j < int(kLanesP) / 32; ++j)
-            umma::tensor_copy_3d<CG>(stage + j * 32 * 128, mp, k0, p0 / 2 + 16 * j, 0, bar);
+        for (int j = 0; j < int(kLanesP) / (2 * RUN); ++j)
+            if (uint32_t(j) * 2 * RUN < lanes)
+                umma::tensor_copy_3d<CG>(stage + j * 2 * RUN * 128, mp, k0, p0 / 2 + RUN * j, 0, bar);
     } else if constexpr (LAYOUT == kBothK) {
         umma::tensor_copy_2d<CG>(stage, mp, k0, p0, bar);
     } else {
@@ -353,7 +365,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     const uint32_t valid = min(a.width, a.rows - m0);
     int64_t n = n0 + quarter * 32 + lane;
     bool n_ok = n < a.N;
-    if constexpr (END == kEndGated) n = gated_column(a.end.half, n, n_ok);
+    if constexpr (END == kEndGated) n = gated_column<kGatedRun>(a.end.half, n, n_ok);
     // the thread's place in the parts, [column][lane], that take the stages' place
     // once every copy has landed and been read
     float* part = reinterpret_cast<float*>(stages) + quarter * 32 + lane;
@@ -549,7 +561,11 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = umma::cluster_rank();
     const uint32_t half = a.width / 2;
-    const uint32_t tiles = a.p_tiles * a.q_tiles, step = gridDim.x / 2;
+    // with kEndSum the parts of K are tiles of their own, whose sums stay apart
+    constexpr bool kApart = END == kEndSum;
+    const uint32_t of_a_part = a.p_tiles * a.q_tiles, tiles = kApart ? of_a_part * a.splits : of_a_part, step = gridDim.x / 2;
+    auto first_part = [&](uint32_t i) { return kApart ? i / of_a_part : 0u; };
+    auto last_part = [&](uint32_t i) { return kApart ? i / of_a_part + 1 : a.splits; };
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < a.stages; ++s) {
             mbar_init(full + s, 1);
@@ -586,15 +602,16 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
         uint32_t issued = 0;
         for (uint32_t i = blockIdx.x / 2; i < tiles && ok; i += step) {
             uint32_t pt, qt;
-            tile_at(a, i, pt, qt);
+            tile_at(a, kApart ? i % of_a_part : i, pt, qt);
             const int p0 = int(pt * 2 * kLanesP + rank * kLanesP), q0 = int(qt * a.width + rank * half);
-            uint32_t k = 0;
-            for (uint32_t part = 0; part < a.splits && ok; ++part) {
+            uint32_t k = kApart ? split_begin(a, first_part(i)) : 0;
+            for (uint32_t part = first_part(i); part < last_part(i) && ok; ++part) {
                 for (const uint32_t k1 = split_begin(a, part + 1); k < k1; ++issued, at.next(count)) {
                     if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
                     const uint32_t n = min(unit, k1 - k);
                     if (umma::elect()) {
-                        if (warp == kCopyP && rank == 0) umma::expect_tx(bar_full + 8 * at.stage, 2 * n * a.block_bytes);
+                        if (warp == kCopyP && rank == 0)
+                            umma::expect_tx(bar_full + 8 * at.stage, 2 * n * (a.block_bytes - (kLanesP - a.p_box) * 128));
                         for (uint32_t u = 0; u < n; ++u) {
                             const uint32_t to = ring + at.stage * bytes + u * a.block_bytes;
                             if (warp == kCopyP) load_p<2, FP8, LAYOUT, END>(to, &mp, k + u, p0, bar_pair + 8 * at.stage);
@@ -616,8 +633,8 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             Sums sums;
             bool ok = true;
             for (uint32_t i = blockIdx.x / 2; i < tiles && ok; i += step) {
-                uint32_t k = 0;
-                for (uint32_t part = 0; part < a.splits && ok; ++part) {
+                uint32_t k = kApart ? split_begin(a, first_part(i)) : 0;
+                for (uint32_t part = first_part(i); part < last_part(i) && ok; ++part) {
                     const uint32_t b = sums.take<PARTS>(part);
                     if (!(ok = umma::wait(bar_free + 8 * b, sums.parity(b) ^ 1))) break;
                     umma::fence_after_sync();
@@ -647,11 +664,11 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
         bool ok = true;
         for (uint32_t i = blockIdx.x / 2; i < tiles && ok; i += step) {
             uint32_t pt, qt;
-            tile_at(a, i, pt, qt);
+            tile_at(a, kApart ? i % of_a_part : i, pt, qt);
             int64_t col = int64_t(pt) * 2 * kLanesP + rank * kLanesP + quarter * 32 + lane;
             const uint32_t m0 = qt * a.width + c0;
             bool n_ok = col < a.N;
-            if constexpr (END == kEndGated) col = gated_column(a.end.half, col, n_ok);
+            if constexpr (END == kEndGated) col = gated_column<kGatedRun>(a.end.half, col, n_ok);
             const float bias = a.e.bias != nullptr && n_ok ? __ldg(a.e.bias + col) : 0.0f;
             const float cs = a.e.col_scale != nullptr && n_ok ? __ldg(a.e.col_scale + col) : 1.0f;
             // the warp's residual (64 bytes of each row) to L2, under the multiplication:
@@ -678,7 +695,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                 entropy_tile(a, mine, m0, col, n_ok, v);
                 continue;
             }
-            for (uint32_t part = 0; part < a.splits; ++part) {
+            for (uint32_t part = first_part(i); part < last_part(i); ++part) {
                 b = sums.take<PARTS>(part);
                 if (!(ok = umma::wait(bar_sum + 8 * b, sums.parity(b)))) break;
                 umma::fence_after_sync();
@@ -710,8 +727,10 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             };
             // (the same for the whole warp)
             const bool all = __all_sync(0xFFFFFFFFu, n_ok) && m0 + mine <= a.rows;
-            if constexpr (END != kEndPlain) {
-                end_tile<END, OUT>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, give_back);
+            if constexpr (END == kEndProb || END == kEndRow) {
+                row_tile<END, OUT>(a, tw + b * 256, mine, m0, col, n_ok, give_back);
+            } else if constexpr (END != kEndPlain) {
+                end_tile<END, OUT>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, first_part(i), give_back);
             } else if (a.e.residual != nullptr) {
                 if (all) emit_tile<OUT, true, true>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, give_back);
                 else emit_tile<OUT, false, true>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, give_back);

@@ -18,25 +18,26 @@ __device__ __forceinline__ float exp_fast(float x) {
 }
 
 // --------------------------------------------------------------------------
-// gated: of each 32 lanes, the first 16 are values f of the gate and the
-// others the same f of the up projection, so one exchange within the warp
-// brings a pair together and every value's activation is evaluated once.  A
-// row's stores are 32 contiguous bytes.
+// gated: RUN lanes hold values f of the gate and the next RUN lanes the same
+// f of the up projection, so one exchange within the warp brings a pair
+// together and every value's activation is evaluated once.  A row's stores
+// are 32 (16) contiguous bytes.
 // --------------------------------------------------------------------------
 
 // The row of w [2 F, I] (the column of z) that lane `index` of the tiles
 // holds; ok: there is one.
+template <int RUN>
 __device__ __forceinline__ int64_t gated_column(int64_t half, int64_t index, bool& ok) {
-    const int64_t f = (index >> 5) * 16 + (index & 15);
+    const int64_t f = index / (2 * RUN) * RUN + (index & (RUN - 1));
     ok = f < half;
-    return index & 16 ? half + f : f;
+    return index & RUN ? half + f : f;
 }
 
-template <int OUT, int C, bool ALL>
+template <int RUN, int OUT, int C, bool ALL>
 __device__ __forceinline__ void emit_gated(const TileArgs& a, bool n_ok, int64_t n, uint32_t m0, uint32_t step, uint32_t rows,
                                            float (&v)[C], float bias, float col_scale) {
     const Epilogue& e = a.e;
-    const bool up = (threadIdx.x & 16) != 0;
+    const bool up = (threadIdx.x & RUN) != 0;
     const int64_t half = a.end.half, f = up ? n - half : n;
     auto there = [&](uint32_t m) { return ALL || (n_ok && m < rows); };
     if (e.row_scale != nullptr) {
@@ -56,7 +57,7 @@ __device__ __forceinline__ void emit_gated(const TileArgs& a, bool n_ok, int64_t
     float gate[C / 2], other[C / 2];
 #pragma unroll
     for (int c = 0; c < C / 2; ++c) {
-        const float mine = up ? v[C / 2 + c] : v[c], theirs = __shfl_xor_sync(0xFFFFFFFFu, up ? v[c] : v[C / 2 + c], 16);
+        const float mine = up ? v[C / 2 + c] : v[c], theirs = __shfl_xor_sync(0xFFFFFFFFu, up ? v[c] : v[C / 2 + c], RUN);
         gate[c] = up ? theirs : mine;
         other[c] = up ? mine : theirs;
     }
@@ -83,16 +84,17 @@ __device__ __forceinline__ void emit_gated(const TileArgs& a, bool n_ok, int64_t
 }
 
 // --------------------------------------------------------------------------
-// sums: a product in pieces of K, added up in FP32; the last piece's sum is
-// scaled and rounded once
+// sums: a product in pieces of K (calls) and parts (tiles of one call), the
+// pieces added up in FP32, each part in a buffer of its own; without buffers,
+// the only sum is scaled and rounded here
 // --------------------------------------------------------------------------
 template <int OUT, int C, bool ALL>
 __device__ __forceinline__ void emit_sum(const TileArgs& a, bool n_ok, int64_t n, uint32_t m0, uint32_t step, uint32_t rows,
-                                         float (&v)[C]) {
-    const int64_t at = int64_t(m0) * a.N + n, stride = int64_t(step) * a.N;
+                                         float (&v)[C], uint32_t part) {
+    const int64_t at = int64_t(m0) * a.N + n, stride = int64_t(step) * a.N, apart = int64_t(part) * a.rows * a.N;
     auto there = [&](int c) { return ALL || (n_ok && m0 + c * step < rows); };
     if (a.end.sum_in != nullptr) {
-        const float* p = a.end.sum_in + at;
+        const float* p = a.end.sum_in + apart + at;
         float w[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) w[c] = there(c) ? __ldcs(p + c * stride) : 0.0f;
@@ -100,7 +102,7 @@ __device__ __forceinline__ void emit_sum(const TileArgs& a, bool n_ok, int64_t n
         for (int c = 0; c < C; ++c) v[c] = __fadd_rn(w[c], v[c]);
     }
     if (a.end.sum_out != nullptr) {
-        float* p = a.end.sum_out + at;
+        float* p = a.end.sum_out + apart + at;
 #pragma unroll
         for (int c = 0; c < C; ++c)
             if (there(c)) p[c * stride] = v[c];
@@ -113,53 +115,28 @@ __device__ __forceinline__ void emit_sum(const TileArgs& a, bool n_ok, int64_t n
     }
 }
 
-// --------------------------------------------------------------------------
-// the gradient of a cross entropy's logits, d = spread exp(z - lse) less the
-// target's gradient, from the logits' sums z.  It is rounded to the storage
-// type since both products that read it take 16-bit operands.
-// --------------------------------------------------------------------------
-template <int OUT, int C, bool ALL>
-__device__ __forceinline__ void emit_prob(const TileArgs& a, bool n_ok, int64_t n, uint32_t m0, uint32_t step, uint32_t rows,
-                                          float (&v)[C]) {
-    const int32_t entry = a.end.first + int32_t(n);
-    uint16_t* p = a.e.y + int64_t(m0) * a.end.pitch + n;
-    const int64_t stride = int64_t(step) * a.end.pitch;
-#pragma unroll
-    for (int c = 0; c < C; ++c, p += stride) {
-        const bool there = ALL || (n_ok && m0 + c * step < rows);
-        if (there) {
-            const float4 t = __ldg(reinterpret_cast<const float4*>(a.end.tokens) + m0 + c * step);
-            // (a token without a gradient has none whatever its logits are)
-            float d = t.y == 0.0f ? 0.0f : __fmul_rn(exp_fast(__fsub_rn(v[c], t.x)), t.y);
-            if (__float_as_int(t.w) == entry) d = __fsub_rn(d, t.z);
-            *p = Elem<OUT>::cvt(d);
-        }
-    }
-}
-
-template <int END, int OUT, int C, bool ALL>
+template <int END, int OUT, int C, bool ALL, int RUN>
 __device__ __forceinline__ void emit_of(const TileArgs& a, bool n_ok, int64_t n, uint32_t m0, uint32_t step, uint32_t rows,
-                                        float (&v)[C], float bias, float col_scale) {
-    if constexpr (END == kEndGated) emit_gated<OUT, C, ALL>(a, n_ok, n, m0, step, rows, v, bias, col_scale);
-    if constexpr (END == kEndSum) emit_sum<OUT, C, ALL>(a, n_ok, n, m0, step, rows, v);
-    if constexpr (END == kEndProb) emit_prob<OUT, C, ALL>(a, n_ok, n, m0, step, rows, v);
+                                        float (&v)[C], float bias, float col_scale, uint32_t part) {
+    if constexpr (END == kEndGated) emit_gated<RUN, OUT, C, ALL>(a, n_ok, n, m0, step, rows, v, bias, col_scale);
+    if constexpr (END == kEndSum) emit_sum<OUT, C, ALL>(a, n_ok, n, m0, step, rows, v, part);
 }
 
-// One chunk by itself (split_kernel).
-template <int END, int OUT, int C>
+// One chunk by itself (split_kernel, few_kernel).
+template <int END, int OUT, int C, int RUN = kGatedRun>
 __device__ __forceinline__ void emit_end(const TileArgs& a, bool n_ok, int64_t n, uint32_t m0, uint32_t step, uint32_t rows,
-                                         float (&v)[C], float bias, float col_scale) {
+                                         float (&v)[C], float bias, float col_scale, uint32_t part = 0) {
     if (__all_sync(0xFFFFFFFFu, n_ok) && m0 + (C - 1) * step < rows)
-        emit_of<END, OUT, C, true>(a, n_ok, n, m0, step, rows, v, bias, col_scale);
+        emit_of<END, OUT, C, true, RUN>(a, n_ok, n, m0, step, rows, v, bias, col_scale, part);
     else
-        emit_of<END, OUT, C, false>(a, n_ok, n, m0, step, rows, v, bias, col_scale);
+        emit_of<END, OUT, C, false, RUN>(a, n_ok, n, m0, step, rows, v, bias, col_scale, part);
 }
 
 // A warp's `mine` columns of a finished tile, from tensor memory at `from`
 // (pair_kernel); give_back after the last read of tensor memory.
 template <int END, int OUT, bool ALL, typename GiveBack>
 __device__ __forceinline__ void end_columns(const TileArgs& a, uint32_t from, uint32_t mine, uint32_t m0, int64_t col, bool n_ok,
-                                            float bias, float cs, GiveBack give_back) {
+                                            float bias, float cs, uint32_t part, GiveBack give_back) {
     constexpr int C = 8;
     float next[C];
     umma::tmem_ld(from, next);
@@ -171,25 +148,109 @@ __device__ __forceinline__ void end_columns(const TileArgs& a, uint32_t from, ui
         for (int k = 0; k < C; ++k) v[k] = next[k];
         if (c + C < mine) umma::tmem_ld(from + c + C, next);
         else give_back();
-        emit_of<END, OUT, C, ALL>(a, n_ok, col, m0 + c, 1, a.rows, v, bias, cs);
+        emit_of<END, OUT, C, ALL, kGatedRun>(a, n_ok, col, m0 + c, 1, a.rows, v, bias, cs, part);
     }
 }
 
 template <int END, int OUT, typename GiveBack>
 __device__ __forceinline__ void end_tile(const TileArgs& a, uint32_t from, uint32_t mine, uint32_t m0, int64_t col, bool n_ok,
-                                         float bias, float cs, GiveBack give_back) {
+                                         float bias, float cs, uint32_t part, GiveBack give_back) {
     if (__all_sync(0xFFFFFFFFu, n_ok) && m0 + mine <= a.rows)
-        end_columns<END, OUT, true>(a, from, mine, m0, col, n_ok, bias, cs, give_back);
+        end_columns<END, OUT, true>(a, from, mine, m0, col, n_ok, bias, cs, part, give_back);
     else
-        end_columns<END, OUT, false>(a, from, mine, m0, col, n_ok, bias, cs, give_back);
+        end_columns<END, OUT, false>(a, from, mine, m0, col, n_ok, bias, cs, part, give_back);
+}
+
+// --------------------------------------------------------------------------
+// rows: the lanes are the output's rows, so a thread has `mine` consecutive
+// values of one and stores 32 bytes at a time where the rows allow it.  (With
+// the contiguous index on the lanes a warp's store is 64 bytes: FIG_ROWS)
+//
+// kEndProb: d = spread exp(z - lse), less the target's gradient, from the
+// logits' sums z.  It is rounded to the storage type since both products that
+// read it take 16-bit operands.  A token without a gradient has d = 0 whatever
+// its logits are.
+// kEndRow: factor z.
+// --------------------------------------------------------------------------
+template <int END, int OUT, typename GiveBack>
+__device__ __forceinline__ void row_tile(const TileArgs& a, uint32_t from, uint32_t mine, uint32_t m0, int64_t row, bool ok,
+                                         GiveBack give_back) {
+    constexpr int C = 16;
+    uint16_t* p = a.e.y + row * a.end.pitch + m0;
+    float lse = 0.0f, factor = 0.0f, target_grad = 0.0f;
+    int32_t at = -1;   // the target's column
+    if constexpr (END == kEndProb) {
+        if (ok) {
+            const float4 t = __ldg(reinterpret_cast<const float4*>(a.end.tokens) + row);
+            lse = t.x, factor = t.y, target_grad = t.z;
+            at = __float_as_int(t.w) - a.end.first;
+        }
+    } else {
+        factor = __ldg(a.end.factor);
+    }
+    const uint32_t mask = ok ? uint32_t(reinterpret_cast<uintptr_t>(a.e.y) | uintptr_t(a.end.pitch * 2) | (m0 * 2)) & 31u : 31u;
+    const bool sectors = mask == 0, halves = (mask & 15u) == 0;   // (columns of a tile begin at multiples of 16)
+    float v[2][8];
+    umma::tmem_ld(from, v[0]);
+    umma::tmem_ld(from + 8, v[1]);
+#pragma unroll 1
+    for (uint32_t c = 0; c < mine; c += C) {
+        umma::tmem_wait_ld(v[0]);
+        umma::tmem_wait_ld(v[1]);
+        float x[C];
+#pragma unroll
+        for (int k = 0; k < C; ++k) x[k] = v[k / 8][k % 8];
+        if (c + C < mine) {
+            umma::tmem_ld(from + c + C, v[0]);
+            umma::tmem_ld(from + c + C + 8, v[1]);
+        } else {
+            give_back();
+        }
+        if constexpr (END == kEndProb) {
+            const bool some = factor != 0.0f;
+#pragma unroll
+            for (int k = 0; k < C; ++k) x[k] = some ? __fmul_rn(exp_fast(__fsub_rn(x[k], lse)), factor) : 0.0f;
+            const uint32_t rel = uint32_t(at) - (m0 + c);
+            if (__any_sync(0xFFFFFFFFu, rel < C)) {
+#pragma unroll
+                for (int k = 0; k < C; ++k)
+                    if (rel == uint32_t(k)) x[k] = __fsub_rn(x[k], target_grad);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < C; ++k) x[k] = __fmul_rn(x[k], factor);
+        }
+        uint32_t w[C / 2];
+#pragma unroll
+        for (int k = 0; k < C / 2; ++k) w[k] = Elem<OUT>::pack(x[2 * k], x[2 * k + 1]);
+        uint16_t* q = p + c;
+        const bool whole = m0 + c + C <= a.rows;
+        if (sectors && whole) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                         :
+                         : "l"(q), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
+        } else if (halves && whole) {
+            *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(q + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        } else if (ok) {
+#pragma unroll
+            for (int k = 0; k < C; ++k)
+                if (m0 + c + k < a.rows) q[k] = uint16_t(w[k / 2] >> (k % 2 * 16));
+        }
+    }
 }
 
 // --------------------------------------------------------------------------
 // cross entropy: the logits' lanes are tokens and their columns entries of
 // the vocabulary, so that a thread takes the maximum and the sum of
 // exponentials of its `mine` (32 or 64) entries in registers; one such pair a
-// group and token goes to memory, 1/16 or 1/32 of the logits' bytes in 16 bits.
+// group and token goes to memory, 1/8 or 1/16 of the logits' bytes in 16 bits.
+// A unit of 16 entries has a maximum and a sum of its own, units are joined in
+// increasing order, so that few_kernel, with the vocabulary on the lanes, has
+// the same sums in the same order.
 // --------------------------------------------------------------------------
+constexpr int kEntropyUnit = 16;
 
 // exp(x - ref(x)) needs a finite reference: an infinite maximum has 0.
 __device__ __forceinline__ float reference(float top) { return fabsf(top) < INFINITY ? top : 0.0f; }
@@ -230,40 +291,33 @@ __device__ __forceinline__ void entropy_add(uint32_t from, uint32_t mine, float 
 // The group of the thread's logits v.
 __device__ __forceinline__ void entropy_tile(const TileArgs& a, uint32_t mine, uint32_t m0, int64_t t, bool ok,
                                              float (&v)[kEntropyMost / 8][8]) {
-    constexpr int kRun = 32;
     const int64_t target = ok ? __ldg(a.end.target + t) : -1;
+    if (m0 + mine > a.rows) {   // (the same for the whole warp)
+#pragma unroll
+        for (int i = 0; i < kEntropyMost; ++i)
+            if (m0 + i >= a.rows) v[i / 8][i % 8] = -INFINITY;
+    }
+    const int64_t rel = target - int64_t(m0);
+    if (__any_sync(0xFFFFFFFFu, rel >= 0 && rel < mine)) {
+#pragma unroll
+        for (int i = 0; i < kEntropyMost; ++i)
+            if (rel == i && uint32_t(i) < mine) a.end.at[t] = v[i / 8][i % 8];
+    }
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < kEntropyMost; c += kRun) {
+    for (int c = 0; c < kEntropyMost; c += kEntropyUnit) {
         if (uint32_t(c) >= mine) break;
-        const uint32_t first = m0 + c;
         float(*q)[8] = v + c / 8;
-        if (first + kRun > a.rows) {   // (the same for the whole warp)
-#pragma unroll
-            for (int i = 0; i < kRun; ++i)
-                if (first + i >= a.rows) q[i / 8][i % 8] = -INFINITY;
-        }
-        const int64_t rel = target - int64_t(first);
-        if (__any_sync(0xFFFFFFFFu, rel >= 0 && rel < kRun)) {
-#pragma unroll
-            for (int i = 0; i < kRun; ++i)
-                if (rel == i) a.end.at[t] = q[i / 8][i % 8];
-        }
         float most[8], part[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) most[j] = fmaxf(fmaxf(q[0][j], q[1][j]), fmaxf(q[2][j], q[3][j]));
+        for (int j = 0; j < 8; ++j) most[j] = fmaxf(q[0][j], q[1][j]);
 #pragma unroll
         for (int s = 4; s > 0; s >>= 1)
 #pragma unroll
             for (int j = 0; j < s; ++j) most[j] = fmaxf(most[j], most[j + s]);
         const float ref = reference(most[0]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = exp_fast(__fsub_rn(q[i][j], ref));
-            part[j] = __fadd_rn(__fadd_rn(w[0], w[1]), __fadd_rn(w[2], w[3]));
-        }
+        for (int j = 0; j < 8; ++j) part[j] = __fadd_rn(exp_fast(__fsub_rn(q[0][j], ref)), exp_fast(__fsub_rn(q[1][j], ref)));
 #pragma unroll
         for (int s = 4; s > 0; s >>= 1)
 #pragma unroll
@@ -271,7 +325,7 @@ __device__ __forceinline__ void entropy_tile(const TileArgs& a, uint32_t mine, u
         if (c == 0) top = most[0], sum = part[0];
         else join_groups(top, sum, most[0], part[0]);
     }
-    if (ok && m0 < a.rows) a.end.partial[int64_t(m0 / mine) * a.N + t] = make_float2(top, sum);
+    if (ok && m0 < a.rows) a.end.partial[t * a.end.units + m0 / mine] = make_float2(top, sum);
 }
 
 }  // namespace linear

@@ -4,6 +4,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "mhc_few.cuh"
 #include "mhc_layer_launch.cuh"
 #include "mhc_linear_plan.h"
 
@@ -103,7 +104,8 @@ inline cudaError_t lay_out(const Product& p, int in, const Plan& plan, TileArgs&
     a.idesc = umma::instr_desc(in == kBF16 ? 1 : 0, p_mn, q_mn, lanes, a.width);
     cudaError_t e = timeouts_ptr(&a.timeouts);
     if (e != cudaSuccess) return e;
-    e = p_mn ? encode(&mp, p.b, p.K, p.N, p.b_stride, size, 64) : encode(&mp, p.b, p.N, p.K, p.b_stride, size, kLanesP);
+    a.p_box = plan.pair && !p_mn && p.N < int64_t(kLanesP) ? uint32_t((p.N + 7) / 8 * 8) : kLanesP;
+    e = p_mn ? encode(&mp, p.b, p.K, p.N, p.b_stride, size, 64) : encode(&mp, p.b, p.N, p.K, p.b_stride, size, a.p_box);
     if (e != cudaSuccess) return e;
     return q_mn ? encode(&mq, p.a, p.K, p.M, p.a_stride, size, 64) : encode(&mq, p.a, p.M, p.K, p.a_stride, size, box_q);
 }
@@ -129,9 +131,45 @@ cudaError_t launch_pair_kernel(Kernel kernel, std::atomic<uint64_t>& allowed, Ti
 }
 
 // Pairs of CTAs that tiles are given out to.
-inline uint32_t pairs_of(const TileArgs& a) {
-    const uint32_t tiles = a.p_tiles * a.q_tiles, pairs = uint32_t(num_sms()) / 2;
+inline uint32_t pairs_of(const TileArgs& a, uint32_t parts = 1) {
+    const uint32_t tiles = a.p_tiles * a.q_tiles * parts, pairs = uint32_t(num_sms()) / 2;
     return tiles < pairs ? tiles : pairs;
+}
+
+// few_kernel's tiles and operands: as lay_out, with p.M rows in one tile of
+// few_width of them and `lanes` output columns a tile.
+inline cudaError_t lay_out_few(const Product& p, int in, uint32_t lanes, uint32_t parts, TileArgs& a, CUtensorMap& mp, CUtensorMap& mq) {
+    const int64_t size = in == kE4m3 ? 1 : 2;
+    a.e = p.e;
+    a.N = p.N;
+    a.rows = uint32_t(p.M);
+    a.kb = uint32_t((p.K * size + 127) / 128);
+    a.width = few_width(p.M), a.lanes = lanes, a.splits = parts;
+    a.p_tiles = uint32_t((p.N + lanes - 1) / lanes), a.q_tiles = 1;
+    a.idesc = umma::instr_desc(in == kBF16 ? 1 : 0, false, false, kLanesP, a.width);
+    cudaError_t e = timeouts_ptr(&a.timeouts);
+    if (e != cudaSuccess) return e;
+    e = encode(&mp, p.b, p.N, p.K, p.b_stride, size, lanes);
+    if (e != cudaSuccess) return e;
+    return encode(&mq, p.a, p.M, p.K, p.a_stride, size, a.width);
+}
+
+template <bool FP8, int OUT, int WIDTH, int END>
+cudaError_t launch_few_width(TileArgs a, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed{0};
+    set_ring(a, kBytesP + WIDTH * 128);
+    const uint32_t sms = uint32_t(num_sms());
+    return launch_tiles(few_kernel<FP8, OUT, WIDTH, END>, allowed, dim3(a.p_tiles < sms ? a.p_tiles : sms), kFewThreads<WIDTH>,
+                        a.stages * a.stage_bytes + 1024, 1, stream, mp, mq, a);
+}
+
+template <bool FP8, int OUT, int END>
+cudaError_t launch_few(const TileArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t stream) {
+    switch (a.width) {
+        case 16: return launch_few_width<FP8, OUT, 16, END>(a, mp, mq, stream);
+        case 32: return launch_few_width<FP8, OUT, 32, END>(a, mp, mq, stream);
+        default: return launch_few_width<FP8, OUT, 64, END>(a, mp, mq, stream);
+    }
 }
 
 }  // namespace layer

@@ -70,5 +70,38 @@ inline Plan plan_of(int64_t N, int64_t M, int64_t kb, bool q_mn, bool by_row) {
     return best;
 }
 
+// few_kernel: rows it takes, its tiles' columns of them, and the lanes (weight
+// rows) that make the SMs' shares even: as few rounds of tiles as 128 lanes
+// allow, each of them full.
+constexpr int64_t kFewRows = 64;
+
+inline uint32_t few_width(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : 64; }
+
+inline uint32_t few_lanes(int64_t N) {
+    const int64_t sms = kClustersAtOnce[0], rounds = (N + 128 * sms - 1) / (128 * sms);
+    const int64_t lanes = ((N + sms * rounds - 1) / (sms * rounds) + 15) / 16 * 16;
+    return uint32_t(lanes < 128 ? lanes : 128);
+}
+
+// A gradient summed over `kb` blocks of K (a piece of a vocabulary), [M,N]:
+// pairs of CTAs, tiles of `width` rows, and parts of K that are tiles of their
+// own, so that few tiles fill the GPU; none longer than 256 blocks (16384
+// terms), since the tensor cores' sums cut off bits.  The cheapest by plan_of's
+// estimate of a round; joining parts costs their sums' way through memory.
+inline Plan sum_plan(int64_t N, int64_t M, int64_t kb) {
+    Plan best = {true, 128, 1};
+    int64_t least = INT64_MAX;
+    for (int64_t parts = (kb + 255) / 256; parts == (kb + 255) / 256 || (parts <= 32 && kb >= 4 * parts); ++parts) {
+        const int64_t join = parts > 1 ? 4000 + parts * M * N * 8 / 3000 : 0, blocks = (kb + parts - 1) / parts;
+        for (int64_t w = 128; w <= 256; w += 32) {
+            const int64_t rounds = ((N + 255) / 256 * ((M + w - 1) / w) * parts + kPairsAtOnce - 1) / kPairsAtOnce;
+            const int64_t block = 41 * w / 20 > 300 ? 41 * w / 20 : 300;
+            const int64_t cost = 6000 + 21 * w + rounds * (blocks * block + 1500) + join;
+            if (cost < least) least = cost, best = {true, uint32_t(w), uint32_t(parts)};
+        }
+    }
+    return best;
+}
+
 }  // namespace linear
 }  // namespace mhc
