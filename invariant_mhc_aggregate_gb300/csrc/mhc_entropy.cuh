@@ -1,6 +1,6 @@
 // The kernels around the products of a cross entropy over a vocabulary
-// (definitions in mhc_layer.h): the join of the groups' maxima and sums, and
-// what each token brings to the gradient of its logits.
+// (definitions in mhc_layer.h): the join of the groups' maxima and sums,
+// the sum of grad_x's parts, and the scale of binary16 gradients.
 #pragma once
 
 #include "mhc_linear.cuh"
@@ -62,9 +62,9 @@ constexpr int kSumThreads = 256;
 
 template <int DT>
 static __global__ void __launch_bounds__(kSumThreads)
-sum_kernel(const float* __restrict__ sums, const float* __restrict__ factor, uint16_t* __restrict__ out, int64_t n, uint32_t parts) {
+sum_kernel(const float* __restrict__ sums, const float* __restrict__ scale, uint16_t* __restrict__ out, int64_t n, uint32_t parts) {
     pdl_enter();
-    const float f = *factor;
+    const float f = scale == nullptr ? 1.0f : scale[1];
     const int64_t i = (int64_t(blockIdx.x) * kSumThreads + threadIdx.x) * 2;
     if (i >= n) return;
     const bool two = i + 1 < n;
@@ -80,52 +80,37 @@ sum_kernel(const float* __restrict__ sums, const float* __restrict__ factor, uin
     if (two) out[i + 1] = Elem<DT>::cvt(__fmul_rn(b, f));
 }
 
-// Each token's part of d, times a power of two that brings the largest
-// gradient to 2^13 .. 2^14: binary16 operands then hold probabilities down to
-// 2^-38 of it (BF16 ones need it not and lose nothing).  factor: its inverse.
-// One block, since the power is of all tokens.
-constexpr int kTokenThreads = 1024;
+// Binary16 alone: scale[0] is a power of two that brings the largest gradient
+// of a token to 2^13 .. 2^14, so that the logits' gradients hold probabilities
+// down to 2^-38 of it, and scale[1] its inverse.  One block, since it is of all
+// tokens.
+constexpr int kScaleThreads = 1024;
 
-static __global__ void __launch_bounds__(kTokenThreads)
-token_kernel(const float* __restrict__ grad_loss, const float* __restrict__ grad_lse, const int64_t* __restrict__ target,
-             const float* __restrict__ lse, linear::EntropyToken* __restrict__ tokens, float* __restrict__ factor, int64_t T,
-             int64_t V) {
+static __global__ void __launch_bounds__(kScaleThreads)
+scale_kernel(const float* __restrict__ grad_loss, const float* __restrict__ grad_lse, const int64_t* __restrict__ target,
+             float* __restrict__ scale, int64_t T, int64_t V) {
     pdl_enter();
-    __shared__ float most[kTokenThreads / 32];
-    auto gradients = [&](int64_t t, float& spread, float& at_target, int64_t& entry) {
-        entry = target[t];
-        at_target = grad_loss != nullptr && entry >= 0 && entry < V ? grad_loss[t] : 0.0f;
-        spread = grad_lse == nullptr ? at_target : __fadd_rn(at_target, grad_lse[t]);
-    };
+    __shared__ float most[kScaleThreads / 32];
     float m = 0.0f;
-    for (int64_t t = threadIdx.x; t < T; t += kTokenThreads) {
-        float spread, at_target;
-        int64_t entry;
-        gradients(t, spread, at_target, entry);
-        m = fmaxf(m, fmaxf(fabsf(spread), fabsf(at_target)));
+    for (int64_t t = threadIdx.x; t < T; t += kScaleThreads) {
+        const int64_t entry = target[t];
+        const float g = grad_loss != nullptr && entry >= 0 && entry < V ? grad_loss[t] : 0.0f;
+        const float spread = grad_lse == nullptr ? g : __fadd_rn(g, grad_lse[t]);
+        m = fmaxf(m, fmaxf(fabsf(spread), fabsf(g)));
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
     if (threadIdx.x % 32 == 0) most[threadIdx.x / 32] = m;
     __syncthreads();
-    m = most[threadIdx.x % 32];
+    if (threadIdx.x >= 32) return;
+    m = most[threadIdx.x];
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+    if (threadIdx.x != 0) return;
     int power = 0;
     if (m > 0.0f && m < INFINITY) power = min(13 - ilogbf(m), 126);
-    const float scale = ldexpf(1.0f, power);
-    if (threadIdx.x == 0) *factor = ldexpf(1.0f, -power);
-    for (int64_t t = threadIdx.x; t < T; t += kTokenThreads) {
-        float spread, at_target;
-        int64_t entry;
-        gradients(t, spread, at_target, entry);
-        linear::EntropyToken k;
-        k.lse = lse[t];
-        k.spread = __fmul_rn(spread, scale);
-        k.target_grad = __fmul_rn(at_target, scale);
-        k.target = entry >= 0 && entry < V ? int32_t(entry) : -1;
-        tokens[t] = k;
-    }
+    scale[0] = ldexpf(1.0f, power);
+    scale[1] = ldexpf(1.0f, -power);
 }
 
 }  // namespace entropy

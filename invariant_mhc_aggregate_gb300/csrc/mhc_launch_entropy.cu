@@ -14,12 +14,12 @@ cudaError_t launch_end(const TileArgs& a, int dtype, uint32_t pairs, const CUten
     return launch_pair_kernel(pair_kernel<false, kF16, LAYOUT, false, END>, allowed[1], a, pairs, mp, mq, stream);
 }
 
-// The tile of rows (a multiple of 64: row_tile's 16 for each of four warps) that
-// pair_kernel takes, by plan_of's estimate of its rounds.
-uint32_t pair_width(int64_t N, int64_t M, int64_t kb, bool q_mn) {
+// The tile of rows (a multiple of `step`) that pair_kernel takes, by plan_of's
+// estimate of its rounds.
+uint32_t pair_width(int64_t N, int64_t M, int64_t kb, int64_t step) {
     uint32_t best = 256;
     int64_t least = INT64_MAX;
-    for (int64_t w = 128; w <= 256; w += q_mn ? 128 : 64) {
+    for (int64_t w = 128; w <= 256; w += step) {
         const int64_t rounds = ((N + 255) / 256 * ((M + w - 1) / w) + kPairsAtOnce - 1) / kPairsAtOnce;
         const int64_t cost = 21 * w + rounds * (kb * (41 * w / 20 > 300 ? 41 * w / 20 : 300) + 1500);
         if (cost < least) least = cost, best = uint32_t(w);
@@ -29,9 +29,8 @@ uint32_t pair_width(int64_t N, int64_t M, int64_t kb, bool q_mn) {
 
 // Entries of the vocabulary that are summed together before the join: they
 // follow from V alone, so that a token's loss has the same bits in every
-// batch.  With few tokens few_kernel writes their units of 16; else pair_kernel
-// takes 4 groups a tile: 64 entries where that gives every pair of CTAs a tile
-// whatever the number of tokens, 32 below.
+// batch: 64, and 32 where tiles of 64 a thread would leave SMs without one.
+// With few tokens few_kernel writes their units of 16.
 int64_t entropy_group(int64_t V) { return V >= 256 * kPairsAtOnce ? 64 : 32; }
 
 }  // namespace
@@ -51,11 +50,12 @@ cudaError_t entropy_fwd(const EntropyCall& c, float* loss, float* lse, float2* p
     TileArgs a;
     CUtensorMap mp, mq;
     const uint32_t runs = uint32_t((k_blocks(p, c.dtype) + kEntropyRun - 1) / kEntropyRun);
+    const uint32_t width = group == 64 ? 256 : pair_width(c.T, c.V, k_blocks(p, c.dtype), 128);
     cudaError_t e = few ? lay_out_few(p, c.dtype, few_lanes(c.V), runs, a, mp, mq)
-                        : lay_out(p, c.dtype, {true, uint32_t(4 * group), runs}, a, mp, mq);
+                        : lay_out(p, c.dtype, {true, width, runs}, a, mp, mq);
     if (e != cudaSuccess) return e;
     a.end = {};
-    a.end.partial = partial, a.end.units = units, a.end.at = at, a.end.target = c.target;
+    a.end.partial = partial, a.end.units = units, a.end.group = uint32_t(group), a.end.at = at, a.end.target = c.target;
     static std::atomic<uint64_t> allowed{0};
     e = few ? launch_few<false, kBF16, kEndEntropy>(a, mp, mq, c.stream)
             : launch_pair_kernel(pair_kernel<false, kBF16, kBothK, false, kEndEntropy>, allowed, a, pairs_of(a), mp, mq, c.stream);
@@ -67,31 +67,30 @@ cudaError_t entropy_fwd(const EntropyCall& c, float* loss, float* lse, float2* p
                   c.V, units, few ? uint32_t(group / kEntropyUnit) : 1u);
 }
 
-cudaError_t entropy_tokens(const EntropyCall& c, const float* grad_loss, const float* grad_lse, const float* lse,
-                           EntropyToken* tokens, float* factor) {
-    return launch(entropy::token_kernel, 1, entropy::kTokenThreads, c.stream, grad_loss, grad_lse, c.target, lse, tokens,
-                  factor, c.T, c.V);
+cudaError_t entropy_scale(const EntropyCall& c, const EntropyGrads& g) {
+    return launch(entropy::scale_kernel, 1, entropy::kScaleThreads, c.stream, g.loss, g.lse, c.target, g.scale, c.T, c.V);
 }
 
 // d [T,count] with the tokens on the lanes: a thread has the entries of one token.
-cudaError_t entropy_logit_grad(const EntropyCall& c, const EntropyToken* tokens, int64_t first, int64_t count, uint16_t* d,
-                               int64_t pitch) {
+cudaError_t entropy_logit_grad(const EntropyCall& c, const EntropyGrads& g, const float* lse, int64_t first, int64_t count,
+                               uint16_t* d, int64_t pitch) {
     const void* w = static_cast<const uint16_t*>(c.w) + first * c.w_stride;
     Product p = {w, c.x, c.w_stride, c.x_stride, false, false, false, count, c.T, c.I, {}};
     p.e.y = d;
     TileArgs a;
     CUtensorMap mp, mq;
-    const cudaError_t e = lay_out(p, c.dtype, {true, pair_width(c.T, count, k_blocks(p, c.dtype), false), 1}, a, mp, mq);
+    const cudaError_t e = lay_out(p, c.dtype, {true, pair_width(c.T, count, k_blocks(p, c.dtype), 32), 1}, a, mp, mq);
     if (e != cudaSuccess) return e;
     a.end = {};
-    a.end.tokens = tokens, a.end.first = int32_t(first), a.end.pitch = pitch;
+    a.end.scale = g.scale, a.end.target = c.target, a.end.lse = lse, a.end.grad_loss = g.loss, a.end.grad_lse = g.lse;
+    a.end.first = first, a.end.entries = c.V, a.end.pitch = pitch;
     return launch_end<kEndProb, kBothK>(a, c.dtype, pairs_of(a), mp, mq, c.stream);
 }
 
 uint32_t entropy_parts(int64_t T, int64_t I, int64_t count) { return sum_plan(I, T, (count + 63) / 64).splits; }
 
 cudaError_t entropy_grad_x(const EntropyCall& c, const uint16_t* d, int64_t pitch, int64_t first, int64_t count, uint32_t parts,
-                           const float* sum_in, float* sum_out, const float* factor, void* grad_x) {
+                           const float* sum_in, float* sum_out, const float* scale, void* grad_x) {
     const void* w = static_cast<const uint16_t*>(c.w) + first * c.w_stride;
     Product p = {d, w, pitch, c.w_stride, false, true, false, c.T, c.I, count, {}};   // [T,I] = d [T,count] . w[first ..] [count,I]
     p.e.y = static_cast<uint16_t*>(grad_x);
@@ -103,22 +102,22 @@ cudaError_t entropy_grad_x(const EntropyCall& c, const uint16_t* d, int64_t pitc
     const cudaError_t e = lay_out(p, c.dtype, plan, a, mp, mq);
     if (e != cudaSuccess) return e;
     a.end = {};
-    a.end.sum_in = sum_in, a.end.sum_out = sum_out, a.end.factor = factor;
+    a.end.sum_in = sum_in, a.end.sum_out = sum_out, a.end.scale = scale;
     return launch_end<kEndSum, kPMnQK>(a, c.dtype, pairs_of(a, a.splits), mp, mq, c.stream);
 }
 
-cudaError_t entropy_sum(const EntropyCall& c, const float* sums, uint32_t parts, const float* factor, void* grad_x) {
+cudaError_t entropy_sum(const EntropyCall& c, const float* sums, uint32_t parts, const float* scale, void* grad_x) {
     const int64_t n = c.T * c.I, blocks = (n + 2 * entropy::kSumThreads - 1) / (2 * entropy::kSumThreads);
     if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     return launch(c.dtype == kBF16 ? entropy::sum_kernel<kBF16> : entropy::sum_kernel<kF16>, uint32_t(blocks), entropy::kSumThreads,
-                  c.stream, sums, factor, static_cast<uint16_t*>(grad_x), n, parts);
+                  c.stream, sums, scale, static_cast<uint16_t*>(grad_x), n, parts);
 }
 
 // [count,I] = d^T [count,T] . x [T,I].  Where grad_w's rows are whole 16-byte
 // vectors the vocabulary is on the lanes and a thread stores a row's values
 // in vectors; rows at any alignment have their values on the lanes.
 cudaError_t entropy_grad_w(const EntropyCall& c, const uint16_t* d, int64_t pitch, int64_t first, int64_t count,
-                           const float* factor, void* grad_w) {
+                           const float* scale, void* grad_w) {
     uint16_t* out = static_cast<uint16_t*>(grad_w) + first * c.I;
     const bool rows = c.I % 8 == 0 && aligned(out, 16);
     Product p = {c.x, d, c.x_stride, pitch, true, true, false, c.I, count, c.T, {}};
@@ -126,10 +125,10 @@ cudaError_t entropy_grad_w(const EntropyCall& c, const uint16_t* d, int64_t pitc
     p.e.y = out;
     TileArgs a;
     CUtensorMap mp, mq;
-    const cudaError_t e = lay_out(p, c.dtype, {true, pair_width(p.N, p.M, k_blocks(p, c.dtype), true), 1}, a, mp, mq);
+    const cudaError_t e = lay_out(p, c.dtype, {true, pair_width(p.N, p.M, k_blocks(p, c.dtype), 128), 1}, a, mp, mq);
     if (e != cudaSuccess) return e;
     a.end = {};
-    a.end.factor = factor, a.end.pitch = c.I;
+    a.end.scale = scale, a.end.pitch = c.I;
     return rows ? launch_end<kEndRow, kBothMn>(a, c.dtype, pairs_of(a), mp, mq, c.stream)
                 : launch_end<kEndSum, kBothMn>(a, c.dtype, pairs_of(a), mp, mq, c.stream);
 }

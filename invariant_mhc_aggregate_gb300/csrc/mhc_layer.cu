@@ -256,17 +256,15 @@ int64_t entropy_piece(int64_t T, int64_t V) {
 }
 
 struct EntropySizes {
-    int64_t piece, tokens, factor, d, sums;   // entries; bytes of each part of the workspace
+    int64_t piece, d, sums;   // entries; bytes of each part of the workspace, with 16 for the scale
     uint32_t parts;
     EntropySizes(int64_t T, int64_t I, int64_t V, bool want_x) {
         piece = entropy_piece(T, V);
-        tokens = T * int64_t(sizeof(mhc::linear::EntropyToken));
-        factor = 16;
         d = round16(T * piece * 2);
         parts = want_x ? mhc::layer::entropy_parts(T, I, piece < V ? piece : V) : 1;
         sums = want_x && (piece < V || parts > 1) ? round16(parts * T * I * 4) : 0;
     }
-    int64_t bytes() const { return tokens + factor + d + sums; }
+    int64_t bytes() const { return d + sums + 16; }
 };
 
 }  // namespace
@@ -599,20 +597,21 @@ mhc_status_t mhc_linear_cross_entropy_bwd(const float* grad_loss, const float* g
     wo.place(at, calls, count);
     float* sums = reinterpret_cast<float*>(at);
     at += sizes.sums;
-    auto* tokens = reinterpret_cast<mhc::linear::EntropyToken*>(at);
-    float* factor = reinterpret_cast<float*>(at + sizes.tokens);
+    // BF16 has the exponents of FP32 and needs no scale
+    float* scale = dtype == MHC_DTYPE_F16 ? reinterpret_cast<float*>(at) : nullptr;
     cudaError_t e = lay_out_again(calls, count, stream);
     const mhc::layer::EntropyCall c = {xo.p, wo.p, target, T, I, V, xo.stride, wo.stride, int(dtype), cu(stream)};
-    if (e == cudaSuccess) e = mhc::layer::entropy_tokens(c, grad_loss, grad_lse, lse, tokens, factor);
+    const mhc::layer::EntropyGrads grads = {grad_loss, grad_lse, scale};
+    if (e == cudaSuccess && scale != nullptr) e = mhc::layer::entropy_scale(c, grads);
     for (int64_t v = 0; v < V && e == cudaSuccess; v += sizes.piece) {
         const int64_t n = V - v < sizes.piece ? V - v : sizes.piece;
-        e = mhc::layer::entropy_logit_grad(c, tokens, v, n, d, sizes.piece);
+        e = mhc::layer::entropy_logit_grad(c, grads, lse, v, n, d, sizes.piece);
         if (e == cudaSuccess && want_x)
             e = mhc::layer::entropy_grad_x(c, d, sizes.piece, v, n, sizes.parts, v == 0 ? nullptr : sums,
-                                           v + n < V || sizes.parts > 1 ? sums : nullptr, factor, grad_x);
-        if (e == cudaSuccess && want_w) e = mhc::layer::entropy_grad_w(c, d, sizes.piece, v, n, factor, grad_w);
+                                           v + n < V || sizes.parts > 1 ? sums : nullptr, scale, grad_x);
+        if (e == cudaSuccess && want_w) e = mhc::layer::entropy_grad_w(c, d, sizes.piece, v, n, scale, grad_w);
     }
-    if (e == cudaSuccess && want_x && sizes.parts > 1) e = mhc::layer::entropy_sum(c, sums, sizes.parts, factor, grad_x);
+    if (e == cudaSuccess && want_x && sizes.parts > 1) e = mhc::layer::entropy_sum(c, sums, sizes.parts, scale, grad_x);
     return finish(e);
 }
 

@@ -74,19 +74,25 @@ struct EntropyCall {
 // partial: entropy_pairs(T, V), at: T.
 int64_t entropy_pairs(int64_t T, int64_t V);
 cudaError_t entropy_fwd(const EntropyCall& c, float* loss, float* lse, float2* partial, float* at);
-cudaError_t entropy_tokens(const EntropyCall& c, const float* grad_loss, const float* grad_lse, const float* lse,
-                           linear::EntropyToken* tokens, float* factor);
+// The gradients of loss and lse (either may be null) and, binary16 alone (else
+// null), the power of two and its inverse that entropy_scale writes.
+struct EntropyGrads {
+    const float* loss;
+    const float* lse;
+    float* scale;
+};
+cudaError_t entropy_scale(const EntropyCall& c, const EntropyGrads& g);
 // The gradient of `count` logits from `first` on, [T,count] at row pitch `pitch`.
-cudaError_t entropy_logit_grad(const EntropyCall& c, const linear::EntropyToken* tokens, int64_t first, int64_t count, uint16_t* d,
-                               int64_t pitch);
+cudaError_t entropy_logit_grad(const EntropyCall& c, const EntropyGrads& g, const float* lse, int64_t first, int64_t count,
+                               uint16_t* d, int64_t pitch);
 // grad_x += d w[first ..], in `parts` parts of the vocabulary (entropy_parts of a whole piece): onto sum_in [parts,T,I]
 // (null: onto nothing), into sum_out or, where that is null (one part), scaled and rounded into grad_x.
 uint32_t entropy_parts(int64_t T, int64_t I, int64_t count);
 cudaError_t entropy_grad_x(const EntropyCall& c, const uint16_t* d, int64_t pitch, int64_t first, int64_t count, uint32_t parts,
-                           const float* sum_in, float* sum_out, const float* factor, void* grad_x);
+                           const float* sum_in, float* sum_out, const float* scale, void* grad_x);
 // grad_x from the parts' sums.
-cudaError_t entropy_sum(const EntropyCall& c, const float* sums, uint32_t parts, const float* factor, void* grad_x);
-cudaError_t entropy_grad_w(const EntropyCall& c, const uint16_t* d, int64_t pitch, int64_t first, int64_t count, const float* factor,
+cudaError_t entropy_sum(const EntropyCall& c, const float* sums, uint32_t parts, const float* scale, void* grad_x);
+cudaError_t entropy_grad_w(const EntropyCall& c, const uint16_t* d, int64_t pitch, int64_t first, int64_t count, const float* scale,
                            void* grad_w);
 
 // The device address of the flag that these kernels set when a bounded wait

@@ -89,25 +89,22 @@ enum End {
     kEndRow = 5        // scaled and rounded
 };
 
-// One token of a cross entropy's backward.
-struct __align__(16) EntropyToken {
-    float lse, spread, target_grad;   // d = spread * exp(z - lse), less target_grad at the target
-    int32_t target;                   // -1: ignored
-};
-
 // What the ends beside the plain one read and write; each uses its own part.
 struct EndArgs {
     int64_t half;                     // kEndGated: F; the output's rows are F long, the lanes' 2 F
     const float* sum_in;              // kEndSum: [M,N] added first, or null
     float* sum_out;                   // where the sums go, or null: the last addition, into e.y
-    const float* factor;              // what that one, or kEndRow's, is multiplied by
-    const EntropyToken* tokens;       // kEndProb: [N]
-    int32_t first;                    // the vocabulary's entry of output column 0
+    const float* scale;               // binary16 gradients of logits: what they are multiplied by, then its inverse; or null
+    const int64_t* target;            // kEndEntropy, kEndProb: [tokens]
+    const float* lse;                 // kEndProb: [tokens], with the gradients of the loss and of lse (or null)
+    const float* grad_loss;
+    const float* grad_lse;
+    int64_t first, entries;           // the vocabulary's entry of output column 0; the whole vocabulary's
     int64_t pitch;                    // kEndProb, kEndRow: of the output's rows
     float2* partial;                  // kEndEntropy: [tokens,units]: a unit's maximum and its sum of exponentials
     int64_t units;
+    uint32_t group;                   // entries of a unit, where pair_kernel writes it
     float* at;                        // [tokens] the target's logit
-    const int64_t* target;            // [tokens]
 };
 
 // Rows of the gate that lie together on the lanes of a gated tile, then the
@@ -679,6 +676,8 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                     if (m0 + c < a.rows && col0 < a.N) umma::prefetch_l2(a.e.residual + int64_t(m0 + c) * a.e.residual_stride + col0);
             }
             uint32_t b = 0;
+            RowHead head;
+            if constexpr (END == kEndProb || END == kEndRow) head = row_head<END>(a, col, n_ok);
             if constexpr (END == kEndEntropy) {
                 float v[kEntropyMost / 8][8];
                 for (uint32_t part = 0; part < a.splits; ++part) {
@@ -728,7 +727,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             // (the same for the whole warp)
             const bool all = __all_sync(0xFFFFFFFFu, n_ok) && m0 + mine <= a.rows;
             if constexpr (END == kEndProb || END == kEndRow) {
-                row_tile<END, OUT>(a, tw + b * 256, mine, m0, col, n_ok, give_back);
+                row_tile<END, OUT>(a, head, tw - c0 + b * 256, warp / 4, qt * a.width, col, n_ok, give_back);
             } else if constexpr (END != kEndPlain) {
                 end_tile<END, OUT>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, first_part(i), give_back);
             } else if (a.e.residual != nullptr) {

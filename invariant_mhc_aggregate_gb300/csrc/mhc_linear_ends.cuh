@@ -107,7 +107,7 @@ __device__ __forceinline__ void emit_sum(const TileArgs& a, bool n_ok, int64_t n
         for (int c = 0; c < C; ++c)
             if (there(c)) p[c * stride] = v[c];
     } else {
-        const float factor = __ldg(a.end.factor);
+        const float factor = a.end.scale == nullptr ? 1.0f : __ldg(a.end.scale + 1);
         uint16_t* p = a.e.y + at;
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -162,67 +162,87 @@ __device__ __forceinline__ void end_tile(const TileArgs& a, uint32_t from, uint3
 }
 
 // --------------------------------------------------------------------------
-// rows: the lanes are the output's rows, so a thread has `mine` consecutive
-// values of one and stores 32 bytes at a time where the rows allow it.  (With
-// the contiguous index on the lanes a warp's store is 64 bytes: FIG_ROWS)
+// rows: the lanes are the output's rows, so a thread has runs of 16 values of
+// one (each fourth run of the tile, its group's) and stores 32 bytes at a time
+// where the rows allow it.  (With the contiguous index on the lanes a warp's
+// store is 64 bytes: FIG_ROWS)
 //
-// kEndProb: d = spread exp(z - lse), less the target's gradient, from the
-// logits' sums z.  It is rounded to the storage type since both products that
-// read it take 16-bit operands.  A token without a gradient has d = 0 whatever
-// its logits are.
-// kEndRow: factor z.
+// kEndProb: d = scale ((g + grad_lse) exp(z - lse) - (at the target) g), from
+// the logits' sums z; g is the gradient of the loss, 0 for an ignored token.
+// It is rounded to the storage type since both products that read it take
+// 16-bit operands.  A token without a gradient has d = 0 whatever its logits
+// are.
+// kEndRow: z / scale.
 // --------------------------------------------------------------------------
-template <int END, int OUT, typename GiveBack>
-__device__ __forceinline__ void row_tile(const TileArgs& a, uint32_t from, uint32_t mine, uint32_t m0, int64_t row, bool ok,
-                                         GiveBack give_back) {
-    constexpr int C = 16;
-    uint16_t* p = a.e.y + row * a.end.pitch + m0;
-    float lse = 0.0f, factor = 0.0f, target_grad = 0.0f;
-    int32_t at = -1;   // the target's column
+struct RowHead {
+    float lse = 0.0f, factor = 1.0f, target_grad = 0.0f;
+    int64_t at = -1;   // the target's column
+};
+
+// (read while the row's sums are still under way)
+template <int END>
+__device__ __forceinline__ RowHead row_head(const TileArgs& a, int64_t row, bool ok) {
+    RowHead h;
     if constexpr (END == kEndProb) {
         if (ok) {
-            const float4 t = __ldg(reinterpret_cast<const float4*>(a.end.tokens) + row);
-            lse = t.x, factor = t.y, target_grad = t.z;
-            at = __float_as_int(t.w) - a.end.first;
+            const int64_t target = __ldg(a.end.target + row);
+            const float g = a.end.grad_loss == nullptr ? 0.0f : __ldg(a.end.grad_loss + row);
+            const float scale = a.end.scale == nullptr ? 1.0f : __ldg(a.end.scale);
+            h.lse = __ldg(a.end.lse + row);
+            if (target >= 0 && target < a.end.entries) {
+                h.at = target - a.end.first;
+                h.target_grad = g;
+            }
+            h.factor = a.end.grad_lse == nullptr ? h.target_grad : __fadd_rn(h.target_grad, __ldg(a.end.grad_lse + row));
+            h.target_grad = __fmul_rn(h.target_grad, scale);
+            h.factor = __fmul_rn(h.factor, scale);
         }
-    } else {
-        factor = __ldg(a.end.factor);
+    } else if (a.end.scale != nullptr) {
+        h.factor = __ldg(a.end.scale + 1);
     }
+    return h;
+}
+
+template <int END, int OUT, typename GiveBack>
+__device__ __forceinline__ void row_tile(const TileArgs& a, const RowHead& h, uint32_t from, uint32_t group, uint32_t m0, int64_t row,
+                                         bool ok, GiveBack give_back) {
+    constexpr uint32_t C = 16, kStep = 4 * C;
+    uint16_t* p = a.e.y + row * a.end.pitch + m0;
     const uint32_t mask = ok ? uint32_t(reinterpret_cast<uintptr_t>(a.e.y) | uintptr_t(a.end.pitch * 2) | (m0 * 2)) & 31u : 31u;
     const bool sectors = mask == 0, halves = (mask & 15u) == 0;   // (columns of a tile begin at multiples of 16)
     float v[2][8];
-    umma::tmem_ld(from, v[0]);
-    umma::tmem_ld(from + 8, v[1]);
+    umma::tmem_ld(from + group * C, v[0]);
+    umma::tmem_ld(from + group * C + 8, v[1]);
 #pragma unroll 1
-    for (uint32_t c = 0; c < mine; c += C) {
+    for (uint32_t c = group * C; c < a.width; c += kStep) {
         umma::tmem_wait_ld(v[0]);
         umma::tmem_wait_ld(v[1]);
         float x[C];
 #pragma unroll
-        for (int k = 0; k < C; ++k) x[k] = v[k / 8][k % 8];
-        if (c + C < mine) {
-            umma::tmem_ld(from + c + C, v[0]);
-            umma::tmem_ld(from + c + C + 8, v[1]);
+        for (int k = 0; k < int(C); ++k) x[k] = v[k / 8][k % 8];
+        if (c + kStep < a.width) {
+            umma::tmem_ld(from + c + kStep, v[0]);
+            umma::tmem_ld(from + c + kStep + 8, v[1]);
         } else {
             give_back();
         }
         if constexpr (END == kEndProb) {
-            const bool some = factor != 0.0f;
+            const bool some = h.factor != 0.0f;
 #pragma unroll
-            for (int k = 0; k < C; ++k) x[k] = some ? __fmul_rn(exp_fast(__fsub_rn(x[k], lse)), factor) : 0.0f;
-            const uint32_t rel = uint32_t(at) - (m0 + c);
-            if (__any_sync(0xFFFFFFFFu, rel < C)) {
+            for (int k = 0; k < int(C); ++k) x[k] = some ? __fmul_rn(exp_fast(__fsub_rn(x[k], h.lse)), h.factor) : 0.0f;
+            const int64_t rel = h.at - int64_t(m0 + c);
+            if (__any_sync(0xFFFFFFFFu, rel >= 0 && rel < int64_t(C))) {
 #pragma unroll
-                for (int k = 0; k < C; ++k)
-                    if (rel == uint32_t(k)) x[k] = __fsub_rn(x[k], target_grad);
+                for (int k = 0; k < int(C); ++k)
+                    if (rel == k) x[k] = __fsub_rn(x[k], h.target_grad);
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < C; ++k) x[k] = __fmul_rn(x[k], factor);
+            for (int k = 0; k < int(C); ++k) x[k] = __fmul_rn(x[k], h.factor);
         }
         uint32_t w[C / 2];
 #pragma unroll
-        for (int k = 0; k < C / 2; ++k) w[k] = Elem<OUT>::pack(x[2 * k], x[2 * k + 1]);
+        for (int k = 0; k < int(C) / 2; ++k) w[k] = Elem<OUT>::pack(x[2 * k], x[2 * k + 1]);
         uint16_t* q = p + c;
         const bool whole = m0 + c + C <= a.rows;
         if (sectors && whole) {
@@ -235,7 +255,7 @@ __device__ __forceinline__ void row_tile(const TileArgs& a, uint32_t from, uint3
             *reinterpret_cast<uint4*>(q + 8) = make_uint4(w[4], w[5], w[6], w[7]);
         } else if (ok) {
 #pragma unroll
-            for (int k = 0; k < C; ++k)
+            for (int k = 0; k < int(C); ++k)
                 if (m0 + c + k < a.rows) q[k] = uint16_t(w[k / 2] >> (k % 2 * 16));
         }
     }
@@ -245,7 +265,7 @@ __device__ __forceinline__ void row_tile(const TileArgs& a, uint32_t from, uint3
 // cross entropy: the logits' lanes are tokens and their columns entries of
 // the vocabulary, so that a thread takes the maximum and the sum of
 // exponentials of its `mine` (32 or 64) entries in registers; one such pair a
-// group and token goes to memory, 1/8 or 1/16 of the logits' bytes in 16 bits.
+// group (32 or 64 entries) and token goes to memory, 1/8 or 1/16 of the logits' bytes in 16 bits.
 // A unit of 16 entries has a maximum and a sum of its own, units are joined in
 // increasing order, so that few_kernel, with the vocabulary on the lanes, has
 // the same sums in the same order.
@@ -322,10 +342,14 @@ __device__ __forceinline__ void entropy_tile(const TileArgs& a, uint32_t mine, u
         for (int s = 4; s > 0; s >>= 1)
 #pragma unroll
             for (int j = 0; j < s; ++j) part[j] = __fadd_rn(part[j], part[j + s]);
-        if (c == 0) top = most[0], sum = part[0];
+        if (c % 32 == 0 && (c == 0 || a.end.group == 32)) top = most[0], sum = part[0];
         else join_groups(top, sum, most[0], part[0]);
+        // a group's end
+        if (c % 32 == 16 && (c % 64 == 48 || a.end.group == 32)) {
+            const uint32_t first = m0 + c + kEntropyUnit - a.end.group;
+            if (ok && first < a.rows) a.end.partial[t * a.end.units + first / a.end.group] = make_float2(top, sum);
+        }
     }
-    if (ok && m0 < a.rows) a.end.partial[t * a.end.units + m0 / mine] = make_float2(top, sum);
 }
 
 }  // namespace linear
