@@ -404,10 +404,11 @@ class LinearCrossEntropy(torch.autograd.Function):
             raise ValueError(f"shape mismatch: x {tuple(x.shape)}, target {tuple(target.shape)}")
         xx, ww, tt = _rows(x, I), _rows(weight, weight.shape[-1]), target.reshape(-1).contiguous()
         loss, lse = layer.linear_cross_entropy(xx, ww, tt)
+        lse = lse.reshape(target.shape)
         ctx.save_for_backward(xx, ww, tt, lse)
         ctx.shape = x.shape
         ctx.set_materialize_grads(False)   # an unused output has no gradient, not one of zeros to be read
-        return loss.reshape(target.shape), lse.reshape(target.shape).clone()
+        return loss.reshape(target.shape), lse
 
     @staticmethod
     @_first_order
@@ -417,7 +418,7 @@ class LinearCrossEntropy(torch.autograd.Function):
         if (grad_loss is None and grad_lse is None) or not (need[0] or need[1]):
             return None, None, None
         gl, gs = (None if g is None else g.reshape(-1).contiguous() for g in (grad_loss, grad_lse))
-        gx, gw = layer.linear_cross_entropy_backward(gl, x, w, target, lse, grad_lse=gs, want=(need[0], need[1]))
+        gx, gw = layer.linear_cross_entropy_backward(gl, x, w, target, lse.reshape(-1), grad_lse=gs, want=(need[0], need[1]))
         return None if gx is None else gx.reshape(ctx.shape), gw, None
 
 

@@ -105,7 +105,7 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
                         umma::expect_tx(bar_full + 8 * at.stage, n * (a.lanes + WIDTH) * 128);
                         for (uint32_t u = 0; u < n; ++u) {
                             const uint32_t to = ring + at.stage * bytes + u * a.block_bytes;
-                            load_p<1, FP8, kBothK, END, kFewRun>(to, &mp, k + u, p0, bar_full + 8 * at.stage, a.lanes);
+                            load_p<1, FP8, kBothK, END>(to, &mp, k + u, p0, bar_full + 8 * at.stage, int(a.end.half), a.lanes);
                             load_q<1, FP8, kBothK>(to, &mq, k + u, 0, WIDTH, bar_full + 8 * at.stage);
                         }
                     }
@@ -151,9 +151,9 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
         bool ok = true;
         for (uint32_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
             int64_t n = int64_t(i) * a.lanes + in_tile;
-            bool n_ok = n < a.N;
-            if constexpr (END == kEndGated) n = gated_column<kFewRun>(a.end.half, n, n_ok);
-            n_ok = n_ok && in_tile < a.lanes;
+            bool n_ok = n < a.N && in_tile < a.lanes;
+            Gated gated;
+            if constexpr (END == kEndGated) gated = gated_place(a, stages, warp / 4, in_tile, int64_t(i) * (a.lanes / 2), n, n_ok);
             const float bias = a.e.bias != nullptr && n_ok ? __ldg(a.e.bias + n) : 0.0f;
             const float cs = a.e.col_scale != nullptr && n_ok ? __ldg(a.e.col_scale + n) : 1.0f;
             float v[C / 8][8];
@@ -181,12 +181,13 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
                 __syncwarp();
                 if (lane == 0) umma::arrive_cluster(bar_free + 8 * sums.stage);
             }
+            if constexpr (END == kEndGated) ok = group_all(gated, ok);   // (the group's warps meet in every chunk)
             if (!ok) break;
 #pragma unroll
             for (int c = 0; c < C / 8; ++c) {
                 if (m0 + 8 * c >= a.rows) break;
                 if constexpr (END == kEndEntropy) entropy_lanes<8>(a, m0 + 8 * c, n, n_ok, v[c]);
-                else emit_end<END, OUT, 8, kFewRun>(a, n_ok, n, m0 + 8 * c, 1, a.rows, v[c], bias, cs);
+                else gated_chunk<OUT>(a, gated, n_ok, n, m0 + 8 * c, 1, a.rows, v[c], bias, cs);
             }
         }
         if (!ok) timed_out(a);

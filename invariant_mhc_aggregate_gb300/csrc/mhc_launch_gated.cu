@@ -7,31 +7,15 @@ namespace layer {
 
 namespace {
 
-// w [2 F, I] as {I, F, 2}: a box has 128 bytes of K of `run` rows of the gate
-// and of the same rows of the up projection, and rows at or past F read as
-// zero in each half.
-cudaError_t encode_gated(CUtensorMap* map, const void* w, int64_t F, int64_t I, int64_t stride, int64_t size, uint32_t run) {
-    const PFN_cuTensorMapEncodeTiled_v12000 f = tensor_map_encoder();
-    if (f == nullptr) return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {cuuint64_t(I), cuuint64_t(F), 2};
-    const cuuint64_t strides[2] = {cuuint64_t(stride * size), cuuint64_t(F * stride * size)};
-    const cuuint32_t box[3] = {cuuint32_t(128 / size), run, 2};
-    const cuuint32_t step[3] = {1, 1, 1};
-    const bool sectors = strides[0] % 32 == 0 && reinterpret_cast<uintptr_t>(w) % 32 == 0;   // (as in encode)
-    const CUresult r = f(map, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(w),
-                         dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                         sectors ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <bool FP8, int OUT>
 cudaError_t launch_gated(bool pair, const TileArgs& a, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed[3];
-    if (!pair) return launch_split_kernel(split_kernel<FP8, OUT, kBothK, kEndGated>, allowed[0], a, mp, mq, stream);
+    if (!pair) return launch_split_kernel(split_kernel<FP8, OUT, kBothK, kEndGated>, allowed[0], a, mp, mq, stream, kGatedBytes);
     if (a.splits > 1)
-        return launch_pair_kernel(pair_kernel<FP8, OUT, kBothK, true, kEndGated>, allowed[1], a, pairs_of(a), mp, mq, stream);
-    return launch_pair_kernel(pair_kernel<FP8, OUT, kBothK, false, kEndGated>, allowed[2], a, pairs_of(a), mp, mq, stream);
+        return launch_pair_kernel(pair_kernel<FP8, OUT, kBothK, true, kEndGated>, allowed[1], a, pairs_of(a), mp, mq, stream,
+                                  kGatedBytes);
+    return launch_pair_kernel(pair_kernel<FP8, OUT, kBothK, false, kEndGated>, allowed[2], a, pairs_of(a), mp, mq, stream,
+                              kGatedBytes);
 }
 
 template <int DT, int W>
@@ -53,10 +37,13 @@ cudaError_t gated_product(const Product& p, int in, int out, cudaStream_t stream
     const bool few = p.M <= kFewRows && plan.splits == 1;   // (parts of K are faster in a cluster's CTAs)
     cudaError_t e = few ? lay_out_few(p, in, few_lanes(p.N), plan.splits, a, mp, mq) : lay_out(p, in, plan, a, mp, mq);
     if (e != cudaSuccess) return e;
+    // half a tile's lanes a copy: rows of the gate (past its end, of the up projection: nobody's lanes), then of the up
+    // projection (past its end, zeros)
+    e = encode(&mp, p.b, p.N, p.K, p.b_stride, in == kE4m3 ? 1 : 2, a.lanes / 2);
+    if (e != cudaSuccess) return e;
+    a.p_box = kLanesP;   // (two boxes)
     a.end = {};
     a.end.half = p.N / 2;
-    e = encode_gated(&mp, p.b, p.N / 2, p.K, p.b_stride, in == kE4m3 ? 1 : 2, few ? kFewRun : kGatedRun);
-    if (e != cudaSuccess) return e;
     if (few) {
         if (in == kE4m3)
             return out == kBF16 ? launch_few<true, kBF16, kEndGated>(a, mp, mq, stream)

@@ -80,7 +80,7 @@ enum Layout { kBothK = 0, kPMnQK = 1, kBothMn = 2 };   // forward, grad_x, grad_
 // What a product ends in: its own epilogue, or one of mhc_linear_ends.cuh.
 enum End {
     kEndPlain = 0,
-    kEndGated = 1,     // act(gate) * up, of two projections side by side on the lanes
+    kEndGated = 1,     // act(gate) * up, of two projections on the two halves of a tile's lanes
     kEndSum = 2,       // added to FP32 sums, or their last addition, scaled and rounded
     kEndEntropy = 3,   // maxima and sums of exponentials over a vocabulary
     // transposed: the lanes are the output's rows and the columns its contiguous
@@ -91,7 +91,8 @@ enum End {
 
 // What the ends beside the plain one read and write; each uses its own part.
 struct EndArgs {
-    int64_t half;                     // kEndGated: F; the output's rows are F long, the lanes' 2 F
+    int64_t half;                     // kEndGated: F; the output's rows are F long, w has 2 F
+    uint32_t exchange;                // where in shared memory the two halves meet (bytes from the stages on)
     const float* sum_in;              // kEndSum: [M,N] added first, or null
     float* sum_out;                   // where the sums go, or null: the last addition, into e.y
     const float* scale;               // binary16 gradients of logits: what they are multiplied by, then its inverse; or null
@@ -107,10 +108,6 @@ struct EndArgs {
     float* at;                        // [tokens] the target's logit
 };
 
-// Rows of the gate that lie together on the lanes of a gated tile, then the
-// same rows of the up projection: pairs of the two 16 (8 in few_kernel, whose
-// tiles are any multiple of 16 lanes) lanes apart.
-constexpr int kGatedRun = 16, kFewRun = 8;
 
 // How a tile lies: the output's contiguous index n on the lanes of tensor
 // memory (operand P = B, 128 lanes a CTA) and its rows m on the columns
@@ -125,7 +122,7 @@ struct TileArgs {
     uint32_t kb;             // blocks of 128 bytes of K
     uint32_t splits;         // of K; split s takes the blocks [s kb / splits, (s + 1) kb / splits)
     uint32_t width;          // output rows of a tile
-    uint32_t lanes;          // few_kernel: output columns of a tile
+    uint32_t lanes;          // few_kernel: output columns of a tile; kLanesP in the others
     uint32_t stages, stage_bytes;
     uint32_t unit, block_bytes;   // blocks of K of a stage, and bytes of each
     uint32_t p_box;               // pair_kernel: rows of P that a K-major copy brings (lanes past them are nobody's)
@@ -234,15 +231,14 @@ __device__ __forceinline__ uint32_t split_begin(const TileArgs& a, uint32_t s) {
 }
 
 // One block of K of P (128 lanes from p0) and of Q (`columns` from q0) into a stage.
-template <int CG, bool FP8, int LAYOUT, int END, int RUN = kGatedRun>
-__device__ __forceinline__ void load_p(uint32_t stage, const CUtensorMap* mp, uint32_t k, int p0, uint32_t bar,
-                                       uint32_t lanes = kLanesP) {
+// (gated: of the gate's rows, then of as many of the up projection's, `half` rows on.)
+template <int CG, bool FP8, int LAYOUT, int END>
+__device__ __forceinline__ void load_p(uint32_t stage, const CUtensorMap* mp, uint32_t k, int p0, uint32_t bar, int half,
+                                       uint32_t lanes) {
     const int k0 = int(k * (FP8 ? 128u : 64u));
     if constexpr (END == kEndGated) {
-#pragma unroll
-        for (int j = 0; j < int(kLanesP) / (2 * RUN); ++j)
-            if (uint32_t(j) * 2 * RUN < lanes)
-                umma::tensor_copy_3d<CG>(stage + j * 2 * RUN * 128, mp, k0, p0 / 2 + RUN * j, 0, bar);
+        umma::tensor_copy_2d<CG>(stage, mp, k0, p0 / 2, bar);
+        umma::tensor_copy_2d<CG>(stage + lanes * 64, mp, k0, half + p0 / 2, bar);
     } else if constexpr (LAYOUT == kBothK) {
         umma::tensor_copy_2d<CG>(stage, mp, k0, p0, bar);
     } else {
@@ -362,7 +358,8 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     const uint32_t valid = min(a.width, a.rows - m0);
     int64_t n = n0 + quarter * 32 + lane;
     bool n_ok = n < a.N;
-    if constexpr (END == kEndGated) n = gated_column<kGatedRun>(a.end.half, n, n_ok);
+    Gated gated;
+    if constexpr (END == kEndGated) gated = gated_place(a, stages, group, quarter * 32 + lane, n0 / 2, n, n_ok);
     // the thread's place in the parts, [column][lane], that take the stages' place
     // once every copy has landed and been read
     float* part = reinterpret_cast<float*>(stages) + quarter * 32 + lane;
@@ -383,7 +380,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
                 umma::expect_tx(bar_full + 8 * at.stage, n * a.block_bytes);
                 for (uint32_t u = 0; u < n; ++u) {
                     const uint32_t to = ring + at.stage * bytes + u * a.block_bytes;
-                    load_p<1, FP8, LAYOUT, END>(to, &mp, k + u, int(n0), bar_full + 8 * at.stage);
+                    load_p<1, FP8, LAYOUT, END>(to, &mp, k + u, int(n0), bar_full + 8 * at.stage, int(a.end.half), kLanesP);
                     load_q<1, FP8, LAYOUT>(to, &mq, k + u, int(m0), a.width, bar_full + 8 * at.stage);
                 }
             }
@@ -415,6 +412,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
         umma::fence_after_sync();
         // group g of four warps takes the chunks g, g + 4, ... of the columns
         for (uint32_t c = group * kChunk; c < valid; c += 4 * kChunk) {
+            __syncwarp();   // (after stores that some lanes make)
             float v[kChunk];
             umma::tmem_ld(tmem + (quarter * 32u << 16) + c, v);
             uint16_t r[kChunk];
@@ -422,7 +420,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
             umma::tmem_wait_ld(v);
             if (a.splits == 1) {
                 if constexpr (END == kEndPlain) emit_any<OUT, kChunk>(a.e, a.N, n_ok, n, m0 + c, 1, m0 + valid, v, r, bias, cs);
-                else emit_end<END, OUT, kChunk>(a, n_ok, n, m0 + c, 1, m0 + valid, v, bias, cs);
+                else gated_chunk<OUT>(a, gated, n_ok, n, m0 + c, 1, m0 + valid, v, bias, cs);
             } else {
 #pragma unroll
                 for (int i = 0; i < kChunk; ++i) part[(c + i) * kLanesP] = v[i];
@@ -455,7 +453,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
                 if constexpr (END == kEndPlain)
                     emit_any<OUT, kChunk>(a.e, a.N, n_ok, n, m0 + c, a.splits, m0 + valid, v, res, bias, cs);
                 else
-                    emit_end<END, OUT, kChunk>(a, n_ok, n, m0 + c, a.splits, m0 + valid, v, bias, cs);
+                    gated_chunk<OUT>(a, gated, n_ok, n, m0 + c, a.splits, m0 + valid, v, bias, cs);
             }
         }
         umma::cluster_sync();   // no CTA leaves while another reads its part
@@ -532,6 +530,7 @@ __device__ __forceinline__ void emit_tile(const TileArgs& a, uint32_t from, uint
     int64_t at = int64_t(m0) * a.N + col;
 #pragma unroll 1
     for (uint32_t c = 0; c < mine; c += kChunk, at += kChunk * a.N) {
+        __syncwarp();   // (after stores that some lanes make)
         umma::tmem_wait_ld(next);
         float v[kChunk];
         uint16_t now[kChunk];
@@ -611,7 +610,8 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                             umma::expect_tx(bar_full + 8 * at.stage, 2 * n * (a.block_bytes - (kLanesP - a.p_box) * 128));
                         for (uint32_t u = 0; u < n; ++u) {
                             const uint32_t to = ring + at.stage * bytes + u * a.block_bytes;
-                            if (warp == kCopyP) load_p<2, FP8, LAYOUT, END>(to, &mp, k + u, p0, bar_pair + 8 * at.stage);
+                            if (warp == kCopyP)
+                                load_p<2, FP8, LAYOUT, END>(to, &mp, k + u, p0, bar_pair + 8 * at.stage, int(a.end.half), kLanesP);
                             else load_q<2, FP8, LAYOUT>(to, &mq, k + u, q0, half, bar_pair + 8 * at.stage);
                         }
                     }
@@ -665,7 +665,9 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             int64_t col = int64_t(pt) * 2 * kLanesP + rank * kLanesP + quarter * 32 + lane;
             const uint32_t m0 = qt * a.width + c0;
             bool n_ok = col < a.N;
-            if constexpr (END == kEndGated) col = gated_column<kGatedRun>(a.end.half, col, n_ok);
+            Gated gated;
+            if constexpr (END == kEndGated)
+                gated = gated_place(a, stages, warp / 4, quarter * 32 + lane, (int64_t(pt) * 2 + rank) * (kLanesP / 2), col, n_ok);
             const float bias = a.e.bias != nullptr && n_ok ? __ldg(a.e.bias + col) : 0.0f;
             const float cs = a.e.col_scale != nullptr && n_ok ? __ldg(a.e.col_scale + col) : 1.0f;
             // the warp's residual (64 bytes of each row) to L2, under the multiplication:
@@ -718,6 +720,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                 if (lane == 0) umma::arrive_cluster(signal);
                 b = 1;
             }
+            if constexpr (END == kEndGated) ok = group_all(gated, ok);   // (the group's warps meet in every chunk)
             if (!ok) break;
             auto give_back = [&] {
                 umma::fence_before_sync();
@@ -728,8 +731,10 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             const bool all = __all_sync(0xFFFFFFFFu, n_ok) && m0 + mine <= a.rows;
             if constexpr (END == kEndProb || END == kEndRow) {
                 row_tile<END, OUT>(a, head, tw - c0 + b * 256, warp / 4, qt * a.width, col, n_ok, give_back);
-            } else if constexpr (END != kEndPlain) {
-                end_tile<END, OUT>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, first_part(i), give_back);
+            } else if constexpr (END == kEndGated) {
+                gated_tile<OUT>(a, gated, tw + b * 256, mine, m0, col, n_ok, bias, cs, give_back);
+            } else if constexpr (END == kEndSum) {
+                sum_tile<OUT>(a, tw + b * 256, mine, m0, col, n_ok, first_part(i), give_back);
             } else if (a.e.residual != nullptr) {
                 if (all) emit_tile<OUT, true, true>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, give_back);
                 else emit_tile<OUT, false, true>(a, tw + b * 256, mine, m0, col, n_ok, bias, cs, give_back);

@@ -18,69 +18,116 @@ __device__ __forceinline__ float exp_fast(float x) {
 }
 
 // --------------------------------------------------------------------------
-// gated: RUN lanes hold values f of the gate and the next RUN lanes the same
-// f of the up projection, so one exchange within the warp brings a pair
-// together and every value's activation is evaluated once.  A row's stores
-// are 32 (16) contiguous bytes.
+// gated: the first half of a tile's lanes is values f of the gate, the second
+// half the same f of the up projection (two copies of weight rows as they
+// are).  The four warps of a group, which hold the lanes of the same columns,
+// put 8 columns of z in shared memory at a time and take it out by pairs: every
+// value's activation is evaluated once, and a warp stores 64 contiguous bytes.
 // --------------------------------------------------------------------------
+constexpr uint32_t kExchange = 8 * kLanesP * 4;   // bytes of a group
 
-// The row of w [2 F, I] (the column of z) that lane `index` of the tiles
-// holds; ok: there is one.
-template <int RUN>
-__device__ __forceinline__ int64_t gated_column(int64_t half, int64_t index, bool& ok) {
-    const int64_t f = index / (2 * RUN) * RUN + (index & (RUN - 1));
-    ok = f < half;
-    return index & RUN ? half + f : f;
+struct Gated {
+    float* z;             // the group's [8][kLanesP]
+    uint32_t barrier;     // the group's
+    uint32_t lane;        // of the tile
+    int64_t f0;           // the tile's first f
+};
+
+// The thread's place; n becomes the row of w (the column of z) that its lane
+// holds, n_ok whether there is one.
+__device__ __forceinline__ Gated gated_place(const TileArgs& a, char* stages, uint32_t group, uint32_t lane, int64_t f0, int64_t& n,
+                                             bool& n_ok) {
+    const uint32_t half = a.lanes / 2;
+    const int64_t f = f0 + (lane < half ? lane : lane - half);
+    n = lane < half ? f : a.end.half + f;
+    n_ok = lane < a.lanes && f < a.end.half;
+    return {reinterpret_cast<float*>(stages + a.end.exchange + group * kExchange), 1 + group, lane, f0};
 }
 
-template <int RUN, int OUT, int C, bool ALL>
-__device__ __forceinline__ void emit_gated(const TileArgs& a, bool n_ok, int64_t n, uint32_t m0, uint32_t step, uint32_t rows,
-                                           float (&v)[C], float bias, float col_scale) {
+// Whether `ok` holds in all four warps of the group.
+__device__ __forceinline__ bool group_all(const Gated& g, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t"
+        "}"
+        : "=r"(all)
+        : "r"(uint32_t(ok)), "r"(g.barrier)
+        : "memory");
+    return all != 0;
+}
+
+template <int ACT>
+__device__ __forceinline__ void gate_all(float (&v)[4]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = activation<ACT>(v[c]);
+}
+
+// 8 columns of z (output rows m0, m0 + step, ...), by the whole group.
+template <int OUT>
+__device__ __forceinline__ void gated_chunk(const TileArgs& a, const Gated& g, bool n_ok, int64_t n, uint32_t m0, uint32_t step,
+                                            uint32_t rows, float (&v)[8], float bias, float col_scale) {
     const Epilogue& e = a.e;
-    const bool up = (threadIdx.x & RUN) != 0;
-    const int64_t half = a.end.half, f = up ? n - half : n;
-    auto there = [&](uint32_t m) { return ALL || (n_ok && m < rows); };
+    const int64_t half = a.end.half;
     if (e.row_scale != nullptr) {
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (there(m0 + c * step)) v[c] = __fmul_rn(__fmul_rn(v[c], __ldg(e.row_scale + m0 + c * step)), col_scale);
+        for (int c = 0; c < 8; ++c)
+            if (m0 + c * step < rows) v[c] = __fmul_rn(__fmul_rn(v[c], __ldg(e.row_scale + m0 + c * step)), col_scale);
     }
 #pragma unroll
-    for (int c = 0; c < C; ++c) v[c] = __fadd_rn(v[c], bias);
+    for (int c = 0; c < 8; ++c) v[c] = __fadd_rn(v[c], bias);
     if (e.preact != nullptr) {
         uint16_t* p = e.preact + int64_t(m0) * (2 * half) + n;
 #pragma unroll
-        for (int c = 0; c < C; ++c, p += step * (2 * half))
-            if (there(m0 + c * step)) *p = Elem<OUT>::cvt(v[c]);
+        for (int c = 0; c < 8; ++c, p += step * (2 * half))
+            if (n_ok && m0 + c * step < rows) *p = Elem<OUT>::cvt(v[c]);
     }
-    // the gate's lane takes the first half of the rows, the other lane the second
-    float gate[C / 2], other[C / 2];
+    named_sync(g.barrier, 128);   // the chunk before has been taken out
 #pragma unroll
-    for (int c = 0; c < C / 2; ++c) {
-        const float mine = up ? v[C / 2 + c] : v[c], theirs = __shfl_xor_sync(0xFFFFFFFFu, up ? v[c] : v[C / 2 + c], RUN);
-        gate[c] = up ? theirs : mine;
-        other[c] = up ? mine : theirs;
-    }
+    for (int c = 0; c < 8; ++c) g.z[c * kLanesP + g.lane] = v[c];
+    named_sync(g.barrier, 128);
+    // the first two warps take columns 0 .. 3 of 64 values f, the other two 4 .. 7
+    const uint32_t i = g.lane & 63, c0 = g.lane >> 6 << 2;
+    const float* z = g.z + c0 * kLanesP + i;
+    float gate[4], up[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) gate[c] = z[c * kLanesP], up[c] = z[c * kLanesP + a.lanes / 2];
     switch (e.act) {
-        case kActRelu:
-#pragma unroll
-            for (int c = 0; c < C / 2; ++c) gate[c] = activation<kActRelu>(gate[c]);
-            break;
-        case kActSilu:
-#pragma unroll
-            for (int c = 0; c < C / 2; ++c) gate[c] = activation<kActSilu>(gate[c]);
-            break;
-        case kActGelu:
-#pragma unroll
-            for (int c = 0; c < C / 2; ++c) gate[c] = activation<kActGelu>(gate[c]);
-            break;
+        case kActRelu: gate_all<kActRelu>(gate); break;
+        case kActSilu: gate_all<kActSilu>(gate); break;
+        case kActGelu: gate_all<kActGelu>(gate); break;
         default: break;
     }
-    const uint32_t first = m0 + (up ? C / 2 * step : 0);
-    uint16_t* p = e.y + int64_t(first) * half + f;
+    if (i < a.lanes / 2 && g.f0 + i < half) {
+        uint32_t m = m0 + c0 * step;
+        uint16_t* p = e.y + int64_t(m) * half + g.f0 + i;
 #pragma unroll
-    for (int c = 0; c < C / 2; ++c, p += step * half)
-        if (there(first + c * step)) *p = Elem<OUT>::cvt(__fmul_rn(gate[c], other[c]));
+        for (int c = 0; c < 4; ++c, m += step, p += step * half)
+            if (m < rows) *p = Elem<OUT>::cvt(__fmul_rn(gate[c], up[c]));
+    }
+    __syncwarp();
+}
+
+// A warp's `mine` columns of a finished tile, from tensor memory at `from`
+// (pair_kernel); give_back after the last read of tensor memory.
+template <int OUT, typename GiveBack>
+__device__ __forceinline__ void gated_tile(const TileArgs& a, const Gated& g, uint32_t from, uint32_t mine, uint32_t m0, int64_t col,
+                                           bool n_ok, float bias, float cs, GiveBack give_back) {
+    float next[8];
+    umma::tmem_ld(from, next);
+#pragma unroll 1
+    for (uint32_t c = 0; c < mine; c += 8) {
+        umma::tmem_wait_ld(next);
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = next[k];
+        if (c + 8 < mine) umma::tmem_ld(from + c + 8, next);
+        else give_back();
+        gated_chunk<OUT>(a, g, n_ok, col, m0 + c, 1, a.rows, v, bias, cs);
+    }
 }
 
 // --------------------------------------------------------------------------
@@ -115,50 +162,34 @@ __device__ __forceinline__ void emit_sum(const TileArgs& a, bool n_ok, int64_t n
     }
 }
 
-template <int END, int OUT, int C, bool ALL, int RUN>
-__device__ __forceinline__ void emit_of(const TileArgs& a, bool n_ok, int64_t n, uint32_t m0, uint32_t step, uint32_t rows,
-                                        float (&v)[C], float bias, float col_scale, uint32_t part) {
-    if constexpr (END == kEndGated) emit_gated<RUN, OUT, C, ALL>(a, n_ok, n, m0, step, rows, v, bias, col_scale);
-    if constexpr (END == kEndSum) emit_sum<OUT, C, ALL>(a, n_ok, n, m0, step, rows, v, part);
-}
-
-// One chunk by itself (split_kernel, few_kernel).
-template <int END, int OUT, int C, int RUN = kGatedRun>
-__device__ __forceinline__ void emit_end(const TileArgs& a, bool n_ok, int64_t n, uint32_t m0, uint32_t step, uint32_t rows,
-                                         float (&v)[C], float bias, float col_scale, uint32_t part = 0) {
-    if (__all_sync(0xFFFFFFFFu, n_ok) && m0 + (C - 1) * step < rows)
-        emit_of<END, OUT, C, true, RUN>(a, n_ok, n, m0, step, rows, v, bias, col_scale, part);
-    else
-        emit_of<END, OUT, C, false, RUN>(a, n_ok, n, m0, step, rows, v, bias, col_scale, part);
-}
-
-// A warp's `mine` columns of a finished tile, from tensor memory at `from`
-// (pair_kernel); give_back after the last read of tensor memory.
-template <int END, int OUT, bool ALL, typename GiveBack>
-__device__ __forceinline__ void end_columns(const TileArgs& a, uint32_t from, uint32_t mine, uint32_t m0, int64_t col, bool n_ok,
-                                            float bias, float cs, uint32_t part, GiveBack give_back) {
+template <int OUT, bool ALL, typename GiveBack>
+__device__ __forceinline__ void sum_columns(const TileArgs& a, uint32_t from, uint32_t mine, uint32_t m0, int64_t col, bool n_ok,
+                                            uint32_t part, GiveBack give_back) {
     constexpr int C = 8;
     float next[C];
     umma::tmem_ld(from, next);
 #pragma unroll 1
     for (uint32_t c = 0; c < mine; c += C) {
+        __syncwarp();   // (after stores that some lanes make)
         umma::tmem_wait_ld(next);
         float v[C];
 #pragma unroll
         for (int k = 0; k < C; ++k) v[k] = next[k];
         if (c + C < mine) umma::tmem_ld(from + c + C, next);
         else give_back();
-        emit_of<END, OUT, C, ALL, kGatedRun>(a, n_ok, col, m0 + c, 1, a.rows, v, bias, cs, part);
+        emit_sum<OUT, C, ALL>(a, n_ok, col, m0 + c, 1, a.rows, v, part);
     }
 }
 
-template <int END, int OUT, typename GiveBack>
-__device__ __forceinline__ void end_tile(const TileArgs& a, uint32_t from, uint32_t mine, uint32_t m0, int64_t col, bool n_ok,
-                                         float bias, float cs, uint32_t part, GiveBack give_back) {
+// A warp's `mine` columns of a finished tile, from tensor memory at `from`
+// (pair_kernel); give_back after the last read of tensor memory.
+template <int OUT, typename GiveBack>
+__device__ __forceinline__ void sum_tile(const TileArgs& a, uint32_t from, uint32_t mine, uint32_t m0, int64_t col, bool n_ok,
+                                         uint32_t part, GiveBack give_back) {
     if (__all_sync(0xFFFFFFFFu, n_ok) && m0 + mine <= a.rows)
-        end_columns<END, OUT, true>(a, from, mine, m0, col, n_ok, bias, cs, part, give_back);
+        sum_columns<OUT, true>(a, from, mine, m0, col, n_ok, part, give_back);
     else
-        end_columns<END, OUT, false>(a, from, mine, m0, col, n_ok, bias, cs, part, give_back);
+        sum_columns<OUT, false>(a, from, mine, m0, col, n_ok, part, give_back);
 }
 
 // --------------------------------------------------------------------------
@@ -215,6 +246,7 @@ __device__ __forceinline__ void row_tile(const TileArgs& a, const RowHead& h, ui
     umma::tmem_ld(from + group * C + 8, v[1]);
 #pragma unroll 1
     for (uint32_t c = group * C; c < a.width; c += kStep) {
+        __syncwarp();   // (after stores that some lanes make)
         umma::tmem_wait_ld(v[0]);
         umma::tmem_wait_ld(v[1]);
         float x[C];

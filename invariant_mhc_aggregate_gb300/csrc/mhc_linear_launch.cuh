@@ -82,12 +82,17 @@ cudaError_t launch_tiles(Kernel kernel, std::atomic<uint64_t>& allowed, dim3 gri
 // a block, which take longer than the multiplications of narrow tiles (M = 512
 // at 4096 x 4096 32.4 -> 20.8 us, one row at 7168 x 7168 21.7 -> 19.6), where
 // three such stages fit: all but split_kernel's widest tiles.
-inline void set_ring(TileArgs& a, uint32_t block_bytes) {
+// `beside`: bytes that a kernel wants beside the ring.
+inline void set_ring(TileArgs& a, uint32_t block_bytes, uint32_t beside) {
+    const uint32_t ring = kRingBytes - beside;
     a.block_bytes = block_bytes;
-    a.unit = kRingBytes / (2 * block_bytes) >= 3 ? 2 : 1;
+    a.unit = ring / (2 * block_bytes) >= 3 ? 2 : 1;
     a.stage_bytes = a.unit * block_bytes;
-    a.stages = kRingBytes / a.stage_bytes < kMaxStages ? kRingBytes / a.stage_bytes : kMaxStages;
+    a.stages = ring / a.stage_bytes < kMaxStages ? ring / a.stage_bytes : kMaxStages;
 }
+
+// Shared memory in which the warps of a gated tile exchange its halves.
+constexpr uint32_t kGatedBytes = kEpilogueWarps / 4 * kExchange;
 
 // A product's tiles and operands as `plan` lays them out: the arguments and the two tensor maps.
 inline cudaError_t lay_out(const Product& p, int in, const Plan& plan, TileArgs& a, CUtensorMap& mp, CUtensorMap& mq) {
@@ -98,7 +103,7 @@ inline cudaError_t lay_out(const Product& p, int in, const Plan& plan, TileArgs&
     a.N = p.N;
     a.rows = uint32_t(p.M);
     a.kb = uint32_t((p.K * size + 127) / 128);
-    a.width = plan.width, a.splits = plan.splits;
+    a.width = plan.width, a.splits = plan.splits, a.lanes = kLanesP;
     a.p_tiles = uint32_t((p.N + lanes - 1) / lanes);
     a.q_tiles = uint32_t((p.M + a.width - 1) / a.width);
     a.idesc = umma::instr_desc(in == kBF16 ? 1 : 0, p_mn, q_mn, lanes, a.width);
@@ -115,19 +120,21 @@ inline int64_t k_blocks(const Product& p, int in) { return (p.K * (in == kE4m3 ?
 // split_kernel and pair_kernel by name: one cluster a tile, or a pair of CTAs for each of `pairs` tiles at a time.
 template <typename Kernel>
 cudaError_t launch_split_kernel(Kernel kernel, std::atomic<uint64_t>& allowed, TileArgs a, const CUtensorMap& mp, const CUtensorMap& mq,
-                                cudaStream_t stream) {
-    set_ring(a, kBytesP + a.width * 128);
+                                cudaStream_t stream, uint32_t beside = 0) {
+    set_ring(a, kBytesP + a.width * 128, beside);
     const uint32_t parts = a.splits > 1 ? a.width * kLanesP * 4 : 0;
     const uint32_t ring = a.stages * a.stage_bytes;
-    return launch_tiles(kernel, allowed, dim3(a.p_tiles * a.splits, a.q_tiles), kSplitThreads, (ring > parts ? ring : parts) + 1024,
+    a.end.exchange = ring > parts ? ring : parts;
+    return launch_tiles(kernel, allowed, dim3(a.p_tiles * a.splits, a.q_tiles), kSplitThreads, a.end.exchange + beside + 1024,
                         a.splits, stream, mp, mq, a);
 }
 
 template <typename Kernel>
 cudaError_t launch_pair_kernel(Kernel kernel, std::atomic<uint64_t>& allowed, TileArgs a, uint32_t pairs, const CUtensorMap& mp,
-                               const CUtensorMap& mq, cudaStream_t stream) {
-    set_ring(a, kBytesP + a.width / 2 * 128);
-    return launch_tiles(kernel, allowed, dim3(2 * pairs), kPairThreads, a.stages * a.stage_bytes + 1024, 2, stream, mp, mq, a);
+                               const CUtensorMap& mq, cudaStream_t stream, uint32_t beside = 0) {
+    set_ring(a, kBytesP + a.width / 2 * 128, beside);
+    a.end.exchange = a.stages * a.stage_bytes;
+    return launch_tiles(kernel, allowed, dim3(2 * pairs), kPairThreads, a.end.exchange + beside + 1024, 2, stream, mp, mq, a);
 }
 
 // Pairs of CTAs that tiles are given out to.
@@ -157,10 +164,11 @@ inline cudaError_t lay_out_few(const Product& p, int in, uint32_t lanes, uint32_
 template <bool FP8, int OUT, int WIDTH, int END>
 cudaError_t launch_few_width(TileArgs a, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    set_ring(a, kBytesP + WIDTH * 128);
-    const uint32_t sms = uint32_t(num_sms());
+    const uint32_t sms = uint32_t(num_sms()), beside = END == kEndGated ? kGatedBytes : 0;
+    set_ring(a, kBytesP + WIDTH * 128, beside);
+    a.end.exchange = a.stages * a.stage_bytes;
     return launch_tiles(few_kernel<FP8, OUT, WIDTH, END>, allowed, dim3(a.p_tiles < sms ? a.p_tiles : sms), kFewThreads<WIDTH>,
-                        a.stages * a.stage_bytes + 1024, 1, stream, mp, mq, a);
+                        a.end.exchange + beside + 1024, 1, stream, mp, mq, a);
 }
 
 template <bool FP8, int OUT, int END>

@@ -137,7 +137,10 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 
 // mbar_wait of mhc_bulk.cuh without a call (a kernel whose sums stay in
 // registers across a wait would spill them around one), and without a look at
-// the timer, which takes longer than most waits, in the first polls.
+// the timer, which takes longer than most waits, in the first polls.  By whole
+// warps: the lanes poll one by one and may find a phase complete in different
+// polls, but leave together, since the tensor-memory instructions after a
+// wait must be executed by the warp as a whole.
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
@@ -153,14 +156,14 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
 }
 
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
-    if (try_wait(bar, parity)) return true;
+    if (__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) return true;
 #pragma unroll 1
     for (int i = 0; i < 1024; ++i)
-        if (try_wait(bar, parity)) return true;
+        if (__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) return true;
     const uint64_t t0 = global_ns();
     do {
-        if (try_wait(bar, parity)) return true;
-    } while (global_ns() - t0 < kWaitLimitNs);
+        if (__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) return true;
+    } while (__all_sync(0xFFFFFFFFu, global_ns() - t0 < kWaitLimitNs));
     return false;
 }
 
@@ -219,25 +222,6 @@ __device__ __forceinline__ void tensor_copy_2d(uint32_t dst, const CUtensorMap* 
             "{%2, %3}], [%4];"
             :
             : "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar)
-            : "memory");
-}
-
-// The same of a 3-D tensor map.
-template <int CG>
-__device__ __forceinline__ void tensor_copy_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
-    if constexpr (CG == 1)
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-            "[%5];"
-            :
-            : "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
-            "{%2, %3, %4}], [%5];"
-            :
-            : "r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
             : "memory");
 }
 
