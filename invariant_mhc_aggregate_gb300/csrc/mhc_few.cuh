@@ -147,9 +147,10 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
         const uint32_t quarter = warp % 4, m0 = warp / 4 * C;   // the thread's lane, its columns m0 .. m0 + C
         const uint32_t in_tile = quarter * 32 + lane;
         const uint32_t tw = tmem + (quarter * 32u << 16) + m0;
+        constexpr bool kTogether = END == kEndGated;   // (as in pair_kernel)
         umma::Ring sums;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+        for (uint32_t i = blockIdx.x; i < tiles && (ok || kTogether); i += gridDim.x) {
             int64_t n = int64_t(i) * a.lanes + in_tile;
             bool n_ok = n < a.N && in_tile < a.lanes;
             Gated gated;
@@ -158,7 +159,8 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
             const float cs = a.e.col_scale != nullptr && n_ok ? __ldg(a.e.col_scale + n) : 1.0f;
             float v[C / 8][8];
             for (uint32_t part = 0; part < a.splits; ++part, sums.next(kSlots)) {
-                if (!(ok = umma::wait(bar_sum + 8 * sums.stage, sums.parity))) break;
+                ok = ok && umma::wait(bar_sum + 8 * sums.stage, sums.parity);
+                if (!ok && !kTogether) break;
                 umma::fence_after_sync();
                 const uint32_t from = tw + sums.stage * WIDTH;
                 if (part == 0) {
@@ -181,8 +183,7 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
                 __syncwarp();
                 if (lane == 0) umma::arrive_cluster(bar_free + 8 * sums.stage);
             }
-            if constexpr (END == kEndGated) ok = group_all(gated, ok);   // (the group's warps meet in every chunk)
-            if (!ok) break;
+            if (!ok && !kTogether) break;
 #pragma unroll
             for (int c = 0; c < C / 8; ++c) {
                 if (m0 + 8 * c >= a.rows) break;

@@ -657,9 +657,11 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
         const uint32_t quarter = warp % 4, mine = a.width / 4, c0 = warp / 4 * mine;   // its columns: c0 .. c0 + mine
         const uint32_t tw = tmem + (quarter * 32u << 16) + c0;
         const uint32_t signal = umma::map_rank(bar_free, 0);
+        // a gated group's warps meet in every chunk of every tile: after a wait that ran out they go on without waits
+        constexpr bool kTogether = END == kEndGated;
         Sums sums;
         bool ok = true;
-        for (uint32_t i = blockIdx.x / 2; i < tiles && ok; i += step) {
+        for (uint32_t i = blockIdx.x / 2; i < tiles && (ok || kTogether); i += step) {
             uint32_t pt, qt;
             tile_at(a, kApart ? i % of_a_part : i, pt, qt);
             int64_t col = int64_t(pt) * 2 * kLanesP + rank * kLanesP + quarter * 32 + lane;
@@ -698,7 +700,8 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             }
             for (uint32_t part = first_part(i); part < last_part(i); ++part) {
                 b = sums.take<PARTS>(part);
-                if (!(ok = umma::wait(bar_sum + 8 * b, sums.parity(b)))) break;
+                ok = ok && umma::wait(bar_sum + 8 * b, sums.parity(b));
+                if (!ok && !kTogether) break;
                 umma::fence_after_sync();
                 if (!PARTS || part == 0) continue;
                 // the second accumulator becomes the sum of the parts so far
@@ -720,8 +723,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                 if (lane == 0) umma::arrive_cluster(signal);
                 b = 1;
             }
-            if constexpr (END == kEndGated) ok = group_all(gated, ok);   // (the group's warps meet in every chunk)
-            if (!ok) break;
+            if (!ok && !kTogether) break;
             auto give_back = [&] {
                 umma::fence_before_sync();
                 __syncwarp();

@@ -44,22 +44,6 @@ __device__ __forceinline__ Gated gated_place(const TileArgs& a, char* stages, ui
     return {reinterpret_cast<float*>(stages + a.end.exchange + group * kExchange), 1 + group, lane, f0};
 }
 
-// Whether `ok` holds in all four warps of the group.
-__device__ __forceinline__ bool group_all(const Gated& g, bool ok) {
-    uint32_t all;
-    asm volatile(
-        "{\n\t"
-        ".reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t"
-        "}"
-        : "=r"(all)
-        : "r"(uint32_t(ok)), "r"(g.barrier)
-        : "memory");
-    return all != 0;
-}
-
 template <int ACT>
 __device__ __forceinline__ void gate_all(float (&v)[4]) {
 #pragma unroll

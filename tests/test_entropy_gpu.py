@@ -129,7 +129,8 @@ def test_tokens_do_not_depend_on_the_batch(I, V):
     x, w, target, *_ = case(T, I, V, BF)
     whole = layer.linear_cross_entropy(x, w, target)
     assert all(torch.equal(a, b) for a, b in zip(layer.linear_cross_entropy(x, w, target), whole))
-    for lo, hi in ((0, 1), (333, 334), (699, 700), (3, 40), (100, 229), (0, 512)):
+    for lo, hi in ((0, 1), (333, 334), (699, 700), (3, 40), (100, 229), (0, 512), (5, 21), (5, 22), (5, 37), (5, 38), (5, 69),
+                   (5, 70), (5, 133), (5, 134)):
         part = layer.linear_cross_entropy(x[lo:hi], w, target[lo:hi])
         assert all(torch.equal(a, b[lo:hi]) for a, b in zip(part, whole)), (lo, hi)
 
@@ -374,6 +375,26 @@ def test_past_32_bits():
     ref = (flat @ x64)[None].expand(len(others), -1)
     bound = (1.1 * U[BF] * flat) @ x64.abs() + sums(T, flat @ x64.abs())
     within(gw[others], ref, bound[None] + U[BF] * ref.abs() + 2.0 ** -20 * 20 * (flat @ x64.abs())[None], "grad_w elsewhere")
+
+
+def test_many_tokens_past_32_bits():
+    """More than 2^31 gradients of logits in the workspace; few tokens have one."""
+    T, I, V = 600000, 16, 4096
+    g = gen(10)
+    x, w = normal(g, T, I, dtype=BF), normal(g, V, I, dtype=BF)
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    at = torch.tensor([0, 255, T // 2, T - 2, T - 1], device="cuda")
+    loss, lse = layer.linear_cross_entropy(x, w, target)
+    z = x[at].double() @ w.double().t()
+    off = sums(I, x[at].double().abs() @ w.double().abs().t())
+    check_forward(loss[at], lse[at], z, off, target[at])
+    gl = torch.zeros(T, device="cuda")
+    gl[at] = normal(g, 5)
+    gx, gw = layer.linear_cross_entropy_backward(gl, x, w, target, lse)
+    assert int((gx != 0).any(-1).sum()) == 5
+    check_backward((gx[at], None), x[at], w, target[at], z, off, lse[at], gl[at], None, BF)
+    # grad_w: the other tokens add zeros; a sum over T in the tensor cores loses nothing to them
+    check_backward((None, gw), x[at], w, target[at], z, off, lse[at], gl[at], None, BF)
 
 
 def differences(f, args, h=1e-5):

@@ -156,7 +156,7 @@ def test_strides(lead, extra):
     assert all(torch.equal(p, q) for p, q in zip(got, want))
 
 
-@pytest.mark.parametrize("I,F", [(7168, 1024), (4096, 3600), (1024, 512), (1279, 150), (512, 12)])
+@pytest.mark.parametrize("I,F", [(7168, 1024), (4096, 3600), (1024, 512), (1279, 150), (512, 12), (520, 8200), (256, 5001)])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_rows_do_not_depend_on_the_batch(I, F, fp8):
     if fp8:
@@ -171,7 +171,8 @@ def test_rows_do_not_depend_on_the_batch(I, F, fp8):
 
     whole = run(0, T)
     assert torch.equal(run(0, T), whole)
-    for lo, hi in ((0, 1), (777, 778), (1499, 1500), (3, 40), (100, 229), (640, 940), (0, 700)):
+    for lo, hi in ((0, 1), (777, 778), (1499, 1500), (3, 40), (100, 229), (640, 940), (0, 700), (5, 21), (5, 22), (5, 37), (5, 38),
+                   (5, 69), (5, 70)):
         assert torch.equal(run(lo, hi), whole[lo:hi]), (lo, hi)
 
 
@@ -261,6 +262,19 @@ def test_calls_in_a_row_and_in_a_graph(T, D):
             t.zero_()
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T,I,F", [(7550, 383, 136), (5000, 1024, 24), (40, 520, 9000)])
+def test_many_calls_in_a_row(T, I, F):
+    """Thousands of calls whose kernels overlap all give the same bytes, and each of them ends."""
+    x, _, w, _, b, z, off = case(T, I, F, BF, False)
+    want = layer.gated_linear(x, w, activation="relu")
+    check(want, z, off, "relu", BF)
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for _ in range(100):
+            got = layer.gated_linear(x, w, activation="relu")
+        assert torch.equal(got, want)
 
 
 def test_other_stream():

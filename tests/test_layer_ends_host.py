@@ -2,6 +2,8 @@
 they reject without touching a GPU, their workspaces, and the autograd
 functions' own part with the kernels' calls replaced by torch formulas."""
 
+import subprocess
+
 import pytest
 import torch
 
@@ -162,6 +164,40 @@ def test_cross_entropy_backward_refusals(lib):
     ws = lib.mhc_linear_cross_entropy_bwd_workspace
     assert ws(4096, 4096, 1 << 20, 4096, 4096, 1, 1, 1) < 4096 * (1 << 20) // 2
     assert ws(0, 64, V, 64, 64, 1, 1, 1) == 0
+
+
+# --- plans, which no device is asked for
+
+PROGRAM = """
+#include <cstdio>
+#include "mhc_linear_plan.h"
+int main() {
+    long long N, M, kb;
+    while (std::scanf("%lld %lld %lld", &N, &M, &kb) == 3) {
+        const mhc::linear::Plan p = mhc::linear::sum_plan(N, M, kb);
+        std::printf("%u %u %u %u\\n", p.width, p.splits, mhc::linear::few_lanes(N), mhc::linear::few_width(M));
+    }
+}
+"""
+
+
+def test_plans(tmp_path):
+    (tmp_path / "plan.cpp").write_text(PROGRAM)
+    exe = str(tmp_path / "plan")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", _build.CSRC, "-o", exe, str(tmp_path / "plan.cpp")], check=True)
+    cases = [(N, M, kb) for N in (1, 16, 255, 1000, 4096, 9728, 9729, 16384, 19456, 19457, 28672, 65536, 151936, 1 << 24)
+             for M in (1, 16, 17, 33, 64, 200, 4096, 70000) for kb in (1, 3, 64, 255, 256, 257, 516, 1500, 131072)]
+    text = "".join("%d %d %d\n" % c for c in cases)
+    out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.split("\n")
+    for (N, M, kb), line in zip(cases, out):
+        width, parts, lanes, few = (int(v) for v in line.split())
+        assert width % 32 == 0 and 128 <= width <= 256
+        assert 1 <= parts <= kb and -(-kb // parts) <= 256             # every part has a block, none more than 256
+        assert lanes % 16 == 0 and 16 <= lanes <= 128
+        # an SM's share of the weight is within one granule of 16 rows a round of the even one
+        rounds = -(-N // (128 * 152))
+        assert -(-(-(-N // lanes)) // 152) <= rounds and lanes * rounds <= -(-N // 152) + 16 * rounds + rounds
+        assert few in (16, 32, 64) and (M > 64 or few >= M)
 
 
 # --- autograd
