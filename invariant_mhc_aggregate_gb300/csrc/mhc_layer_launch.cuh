@@ -54,6 +54,10 @@ cudaError_t repack(const RepackCall* calls, int count, cudaStream_t stream);   /
 cudaError_t slope(const uint16_t* g, const uint16_t* preact, uint16_t* u, float* grad_bias, float* partial, int64_t T,
                   int64_t O, int64_t pitch, int act, int dtype, cudaStream_t stream);
 int64_t slope_partials(int64_t T);
+// p.e.y [M,N] = cvt(a^T b) (scaled by scale[1] where scale is not null) with rows of both operands along m and n: a weight's
+// gradient, stored a row a thread (mhc_launch_entropy.cu).
+cudaError_t row_product(const linear::Product& p, const float* scale, int dtype, cudaStream_t stream);
+
 // The gated product (mhc_launch_gated.cu): p.b is w [2 F, I], p.N = 2 F.
 cudaError_t gated_product(const linear::Product& p, int in, int out, cudaStream_t stream);
 // u = [g up act'(gate) | g act(gate)] of preact [T, 2 F]; the rest as in slope, with 2 F columns.
