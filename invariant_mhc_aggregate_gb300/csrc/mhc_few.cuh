@@ -159,7 +159,7 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
             const float cs = a.e.col_scale != nullptr && n_ok ? __ldg(a.e.col_scale + n) : 1.0f;
             float v[C / 8][8];
             for (uint32_t part = 0; part < a.splits; ++part, sums.next(kSlots)) {
-                ok = ok && umma::wait(bar_sum + 8 * sums.stage, sums.parity);
+                ok = ok && umma::wait_warp(bar_sum + 8 * sums.stage, sums.parity);
                 if (!ok && !kTogether) break;
                 umma::fence_after_sync();
                 const uint32_t from = tw + sums.stage * WIDTH;

@@ -408,7 +408,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
             __syncwarp();
         }
     } else {
-        if (!umma::wait(smem_addr(&done), 0)) timed_out(a);
+        if (!umma::wait_warp(smem_addr(&done), 0)) timed_out(a);
         umma::fence_after_sync();
         // group g of four warps takes the chunks g, g + 4, ... of the columns
         for (uint32_t c = group * kChunk; c < valid; c += 4 * kChunk) {
@@ -686,7 +686,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                 float v[kEntropyMost / 8][8];
                 for (uint32_t part = 0; part < a.splits; ++part) {
                     b = sums.take<false>(part);
-                    if (!(ok = umma::wait(bar_sum + 8 * b, sums.parity(b)))) break;
+                    if (!(ok = umma::wait_warp(bar_sum + 8 * b, sums.parity(b)))) break;
                     umma::fence_after_sync();
                     if (part == 0) entropy_add<true>(tw + b * 256, mine, v);
                     else entropy_add<false>(tw + b * 256, mine, v);
@@ -700,7 +700,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             }
             for (uint32_t part = first_part(i); part < last_part(i); ++part) {
                 b = sums.take<PARTS>(part);
-                ok = ok && umma::wait(bar_sum + 8 * b, sums.parity(b));
+                ok = ok && umma::wait_warp(bar_sum + 8 * b, sums.parity(b));
                 if (!ok && !kTogether) break;
                 umma::fence_after_sync();
                 if (!PARTS || part == 0) continue;

@@ -137,10 +137,7 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 
 // mbar_wait of mhc_bulk.cuh without a call (a kernel whose sums stay in
 // registers across a wait would spill them around one), and without a look at
-// the timer, which takes longer than most waits, in the first polls.  By whole
-// warps: the lanes poll one by one and may find a phase complete in different
-// polls, but leave together, since the tensor-memory instructions after a
-// wait must be executed by the warp as a whole.
+// the timer, which takes longer than most waits, in the first polls.
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
@@ -156,15 +153,23 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
 }
 
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
-    if (__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) return true;
+    if (try_wait(bar, parity)) return true;
 #pragma unroll 1
     for (int i = 0; i < 1024; ++i)
-        if (__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) return true;
+        if (try_wait(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     do {
-        if (__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) return true;
-    } while (__all_sync(0xFFFFFFFFu, global_ns() - t0 < kWaitLimitNs));
+        if (try_wait(bar, parity)) return true;
+    } while (global_ns() - t0 < kWaitLimitNs);
     return false;
+}
+
+// The same by a whole warp, whose lanes poll one by one but leave together:
+// the tensor-memory instructions after it must be executed by all of them.
+// (Copies and multiplications choose their lane by an instruction that does
+// the same.)
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, wait(bar, parity));
 }
 
 __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
