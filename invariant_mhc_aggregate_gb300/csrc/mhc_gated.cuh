@@ -11,7 +11,8 @@ namespace gated {
 // `pitch`; null: not stored), and the column sums of the unrounded u over each
 // of gridDim.y runs of `rows` rows in partial [gridDim.y, 2 F] (null: not
 // wanted).  Block (32, 8): 32 W columns of each half, 8 rows at a time.
-// HBM-bound: 10 bytes a value of g.
+// HBM-bound: 10 bytes a value of g, T = 4096, F = 7168 44 us (6.7 TB/s; 48 with the
+// column sums).
 template <int DT, int W, int ACT>
 __global__ void __launch_bounds__(32 * linear::kSlopeRows, 3)
 slope_kernel(const uint16_t* __restrict__ g, const uint16_t* __restrict__ preact, uint16_t* __restrict__ u,

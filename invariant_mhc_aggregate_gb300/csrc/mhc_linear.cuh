@@ -108,7 +108,6 @@ struct EndArgs {
     float* at;                        // [tokens] the target's logit
 };
 
-
 // How a tile lies: the output's contiguous index n on the lanes of tensor
 // memory (operand P = B, 128 lanes a CTA) and its rows m on the columns
 // (operand Q = A).  A warp then holds 32 consecutive n of one row, so every
@@ -684,6 +683,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             if constexpr (END == kEndProb || END == kEndRow) head = row_head<END>(a, col, n_ok);
             if constexpr (END == kEndEntropy) {
                 float v[kEntropyMost / 8][8];
+                const int64_t target = n_ok ? __ldg(a.end.target + col) : -1;
                 for (uint32_t part = 0; part < a.splits; ++part) {
                     b = sums.take<false>(part);
                     if (!(ok = umma::wait_warp(bar_sum + 8 * b, sums.parity(b)))) break;
@@ -695,7 +695,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                     if (lane == 0) umma::arrive_cluster(signal + 8 * b);
                 }
                 if (!ok) break;
-                entropy_tile(a, mine, m0, col, n_ok, v);
+                entropy_tile(a, mine, m0, col, n_ok, target, v);
                 continue;
             }
             for (uint32_t part = first_part(i); part < last_part(i); ++part) {

@@ -23,6 +23,11 @@ __device__ __forceinline__ float exp_fast(float x) {
 // are).  The four warps of a group, which hold the lanes of the same columns,
 // put 8 columns of z in shared memory at a time and take it out by pairs: every
 // value's activation is evaluated once, and a warp stores 64 contiguous bytes.
+// T = 4096, 7168 -> 2 x 14336 880 us in short runs (1910 TFLOP/s; the tensor
+// cores), with z 4096 -> 2 x 7168 271 us.  (Gate and up rows in turn on the
+// lanes by small boxes of a 3-D map, paired by shuffles, were as fast, but one
+// call in some 30000 of T = 7550, 3823 -> 2 x 136 never ended, for a reason that
+// was not found; 300000 of these do.)
 // --------------------------------------------------------------------------
 constexpr uint32_t kExchange = 8 * kLanesP * 4;   // bytes of a group
 
@@ -179,8 +184,9 @@ __device__ __forceinline__ void sum_tile(const TileArgs& a, uint32_t from, uint3
 // --------------------------------------------------------------------------
 // rows: the lanes are the output's rows, so a thread has runs of 16 values of
 // one (each fourth run of the tile, its group's) and stores 32 bytes at a time
-// where the rows allow it.  (With the contiguous index on the lanes a warp's
-// store is 64 bytes: FIG_ROWS)
+// where the rows allow it, 1 KB a warp (with the contiguous index on the lanes
+// 64 bytes; short K is bound by the stores: the gradients of T = 8 tokens, I =
+// 1024, 128000 entries 195 -> 158 us, T = 1024 668 -> 591).
 //
 // kEndProb: d = scale ((g + grad_lse) exp(z - lse) - (at the target) g), from
 // the logits' sums z; g is the gradient of the loss, 0 for an ignored token.
@@ -281,10 +287,12 @@ __device__ __forceinline__ void row_tile(const TileArgs& a, const RowHead& h, ui
 // cross entropy: the logits' lanes are tokens and their columns entries of
 // the vocabulary, so that a thread takes the maximum and the sum of
 // exponentials of its `mine` (32 or 64) entries in registers; one such pair a
-// group (32 or 64 entries) and token goes to memory, 1/8 or 1/16 of the logits' bytes in 16 bits.
-// A unit of 16 entries has a maximum and a sum of its own, units are joined in
-// increasing order, so that few_kernel, with the vocabulary on the lanes, has
-// the same sums in the same order.
+// group (32 or 64 entries) and token goes to memory, 1/8 or 1/16 of the
+// logits' bytes in 16 bits.  A unit of 16 entries has a maximum and a sum of its
+// own, units are joined in increasing order, so that few_kernel, with the
+// vocabulary on the lanes, has the same sums in the same order.  Under the
+// multiplications of the next tile: T = 4096, I = 7168, 65536 entries 1.95 ms in
+// short runs (1970 TFLOP/s), bound by the tensor cores and their power.
 // --------------------------------------------------------------------------
 constexpr int kEntropyUnit = 16;
 
@@ -302,7 +310,8 @@ __device__ __forceinline__ void join_groups(float& top, float& sum, float top2, 
 // cut off each addition's last bits, so a logit is short by about half a unit
 // of the last place for each 16 products.  Runs are added up in registers,
 // rounded to nearest: K = 7168 in one run, lse is 3.9e-6 off (in norm, against
-// 64 bits), in runs of 16 blocks 6e-7, FP32 sums of the plain form's 8e-7.
+// 64 bits), in runs of 16 blocks 5e-7, with 32-bit products and sums 8e-7; the
+// time is the same.
 constexpr uint32_t kEntropyRun = 16;
 constexpr int kEntropyMost = 64;   // entries of a thread
 
@@ -324,10 +333,9 @@ __device__ __forceinline__ void entropy_add(uint32_t from, uint32_t mine, float 
     }
 }
 
-// The group of the thread's logits v.
-__device__ __forceinline__ void entropy_tile(const TileArgs& a, uint32_t mine, uint32_t m0, int64_t t, bool ok,
+// The groups of the thread's logits v, of token t (ok: there is one).
+__device__ __forceinline__ void entropy_tile(const TileArgs& a, uint32_t mine, uint32_t m0, int64_t t, bool ok, int64_t target,
                                              float (&v)[kEntropyMost / 8][8]) {
-    const int64_t target = ok ? __ldg(a.end.target + t) : -1;
     if (m0 + mine > a.rows) {   // (the same for the whole warp)
 #pragma unroll
         for (int i = 0; i < kEntropyMost; ++i)

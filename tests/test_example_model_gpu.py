@@ -54,3 +54,37 @@ def test_example_model():
     want = torch.logsumexp(logits, -1) - logits.gather(1, target[1:8].clamp(min=0)[:, None])[:, 0]
     assert off(scores, want) < 0.06
     assert layer.wait_timeouts() == 0
+
+
+def test_two_streams():
+    """A gated product and a cross entropy with their gradients on two streams at once: the bytes of each alone."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+
+    def normal(*shape):
+        return (torch.randn(*shape, generator=gen, device="cuda") * shape[-1] ** -0.25).to(torch.bfloat16)
+
+    x, w, v = normal(700, 1024), normal(2 * 1400, 1024), normal(9001, 1024)
+    target = torch.randint(0, 9001, (700,), generator=gen, device="cuda")
+
+    def first():
+        y, z = layer.gated_linear_preact(x, w)
+        return (y, z, layer.gated_linear(x[:9], w), *layer.gated_linear_backward(y, x, w, z))
+
+    def second():
+        loss, lse = layer.linear_cross_entropy(x, v, target)
+        return (loss, lse, *layer.linear_cross_entropy(x[:9], v, target[:9]),
+                *layer.linear_cross_entropy_backward(loss, x, v, target, lse))
+
+    want = [[t.clone() for t in f()] for f in (first, second)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [[], []]
+        for _ in range(10):
+            for k, f in enumerate((first, second)):
+                with torch.cuda.stream(streams[k]):
+                    got[k] = f()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(s, t) for s, t in zip(a, b))
+    assert layer.wait_timeouts() == 0
