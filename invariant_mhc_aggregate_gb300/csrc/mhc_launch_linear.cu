@@ -95,7 +95,7 @@ cudaError_t repack(const RepackCall* calls, int count, cudaStream_t stream) {
         r[i].by_row = make_fastdiv_u32(r[i].per_row);
         r[i].length = uint64_t(c.length), r[i].stride = uint64_t(c.stride);
         r[i].bytes = uint64_t(c.rows - 1) * r[i].stride + r[i].length;
-        blocks[i] = (r[i].vectors + kRepackThreads - 1) / kRepackThreads;
+        blocks[i] = (r[i].vectors + kRepackThreads * kRepackVectors - 1) / (kRepackThreads * kRepackVectors);
     }
     if (blocks[0] + blocks[1] > 0x7FFFFFFFull) return cudaErrorInvalidValue;
     return launch(repack_kernel, uint32_t(blocks[0] + blocks[1]), kRepackThreads, stream, r[0], r[1], uint32_t(blocks[0]));

@@ -756,8 +756,11 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
 
 // Rows of values copied to a row pitch that starts every row on 16 bytes, for
 // operands that the tensor copies cannot read in place: up to two of them in
-// one launch.  A thread writes one 16-byte vector from the two aligned ones
-// that hold its bytes (one by one where those reach outside the source).
+// one launch.  A thread writes two 16-byte vectors, each from the two aligned
+// ones that hold its bytes (one by one where those reach outside the source):
+// all four loads are under way together, 50259 rows of 1279 values 45 -> 35 us
+// (7.3 TB/s read and written) of a cross entropy of 1023 tokens, 5462 such rows
+// 1.6 us less; four vectors a thread have too few threads (1 us more again).
 struct Repack {
     const char* src;
     char* dst;
@@ -769,42 +772,56 @@ struct Repack {
 };
 
 constexpr uint32_t kRepackThreads = 256;
+constexpr int kRepackVectors = 2;
 
 static __global__ void __launch_bounds__(kRepackThreads) repack_kernel(const Repack first, const Repack second, uint32_t blocks) {
     pdl_enter();
     const bool one = blockIdx.x < blocks;
     const Repack& r = one ? first : second;
-    const uint64_t i = uint64_t(one ? blockIdx.x : blockIdx.x - blocks) * kRepackThreads + threadIdx.x;
-    if (i >= r.vectors) return;
-    const uint64_t row = r.vectors <= 0xFFFFFFFFull ? fastdiv_u32(uint32_t(i), r.by_row) : i / r.per_row;
-    const uint64_t c = (i - row * r.per_row) * 16;         // byte within the row
-    const char* p = r.src + row * r.stride + c;
-    const uint32_t shift = uint32_t(reinterpret_cast<uintptr_t>(p) & 15u);
-    const char* base = p - shift;
-    uint32_t w[8];
-    if (base >= r.src && base + 32 <= r.src + r.bytes) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(base)), b = __ldg(reinterpret_cast<const uint4*>(base) + 1);
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-        // whole words first, then the rest of the shift
+    const uint64_t begin = uint64_t(one ? blockIdx.x : blockIdx.x - blocks) * (kRepackThreads * kRepackVectors) + threadIdx.x;
+    const char* from[kRepackVectors];
+    uint64_t column[kRepackVectors];
+    uint4 a[kRepackVectors], b[kRepackVectors];
+    bool fast[kRepackVectors];
 #pragma unroll
-        for (int s = 2; s > 0; s >>= 1)
-            if ((shift / 4) & s) {
-#pragma unroll
-                for (int k = 0; k + s < 8; ++k) w[k] = w[k + s];
-            }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 8 * (shift & 3u));
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            w[k] = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c + 4 * k + j < r.length) w[k] |= uint32_t(static_cast<uint8_t>(__ldg(p + 4 * k + j))) << (8 * j);
-        }
+    for (int v = 0; v < kRepackVectors; ++v) {
+        const uint64_t i = begin + v * kRepackThreads;
+        const uint64_t row = r.vectors <= 0xFFFFFFFFull ? fastdiv_u32(uint32_t(i), r.by_row) : i / r.per_row;
+        column[v] = (i - row * r.per_row) * 16;         // byte within the row
+        from[v] = r.src + row * r.stride + column[v];
+        const char* base = from[v] - (reinterpret_cast<uintptr_t>(from[v]) & 15u);
+        fast[v] = i < r.vectors && base >= r.src && base + 32 <= r.src + r.bytes;
+        if (fast[v]) a[v] = __ldg(reinterpret_cast<const uint4*>(base)), b[v] = __ldg(reinterpret_cast<const uint4*>(base) + 1);
     }
-    // (bytes past the row's end are read by nobody: the tensor map ends with the row)
-    *reinterpret_cast<uint4*>(r.dst + i * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int v = 0; v < kRepackVectors; ++v) {
+        const uint64_t i = begin + v * kRepackThreads;
+        if (i >= r.vectors) return;
+        uint32_t w[8];
+        if (fast[v]) {
+            const uint32_t shift = uint32_t(reinterpret_cast<uintptr_t>(from[v]) & 15u);
+            w[0] = a[v].x, w[1] = a[v].y, w[2] = a[v].z, w[3] = a[v].w, w[4] = b[v].x, w[5] = b[v].y, w[6] = b[v].z, w[7] = b[v].w;
+            // whole words first, then the rest of the shift
+#pragma unroll
+            for (int s = 2; s > 0; s >>= 1)
+                if ((shift / 4) & s) {
+#pragma unroll
+                    for (int k = 0; k + s < 8; ++k) w[k] = w[k + s];
+                }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 8 * (shift & 3u));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                w[k] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (column[v] + 4 * k + j < r.length) w[k] |= uint32_t(static_cast<uint8_t>(__ldg(from[v] + 4 * k + j))) << (8 * j);
+            }
+        }
+        // (bytes past the row's end are read by nobody: the tensor map ends with the row)
+        *reinterpret_cast<uint4*>(r.dst + i * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 
 // u = g * act'(preact) over [T,O], rounded to u (row pitch `pitch`; null: not stored), and the
