@@ -45,14 +45,8 @@ __device__ __forceinline__ void entropy_lanes(const TileArgs& a, uint32_t m0, in
         const uint32_t m = m0 + c;
         if (m >= a.rows) break;   // (the same for the whole warp)
         if (n_ok && __ldg(a.end.target + m) == n) a.end.at[m] = v[c];
-        float top = n_ok ? v[c] : -INFINITY;
-        const float x = top;
-#pragma unroll
-        for (int s = 8; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
-        float sum = exp_fast(__fsub_rn(x, reference(top)));
-#pragma unroll
-        for (int s = 8; s > 0; s >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, s));
-        if ((threadIdx.x & 15) == 0 && n_ok) a.end.partial[int64_t(m) * a.end.units + n / kEntropyUnit] = make_float2(top, sum);
+        const float2 of = entropy_unit(n_ok ? v[c] : -INFINITY);
+        if ((threadIdx.x & 15) == 0 && n_ok) a.end.partial[int64_t(m) * a.end.units + n / kEntropyUnit] = of;
     }
 }
 
@@ -66,7 +60,12 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
     __shared__ uint32_t tmem_base;
     char* stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const uint32_t tiles = a.p_tiles;
+    // (with kEndSum the parts of K are tiles of their own, as in pair_kernel)
+    constexpr bool kApart = END == kEndSum;
+    const uint32_t tiles = kApart ? a.p_tiles * a.splits : a.p_tiles;
+    auto tile_of = [&](uint32_t i) { return kApart ? i % a.p_tiles : i; };
+    auto first_part = [&](uint32_t i) { return kApart ? i / a.p_tiles : 0u; };
+    auto last_part = [&](uint32_t i) { return kApart ? i / a.p_tiles + 1 : a.splits; };
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < a.stages; ++s) {
             mbar_init(full + s, 1);
@@ -98,9 +97,9 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
         bool ok = true;
         uint32_t issued = 0;
         for (uint32_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
-            const int p0 = int(i * a.lanes);
-            uint32_t k = 0;
-            for (uint32_t part = 0; part < a.splits && ok; ++part) {
+            const int p0 = int(tile_of(i) * a.lanes);
+            uint32_t k = kApart ? split_begin(a, first_part(i)) : 0;
+            for (uint32_t part = first_part(i); part < last_part(i) && ok; ++part) {
                 for (const uint32_t k1 = split_begin(a, part + 1); k < k1; ++issued, at.next(count)) {
                     if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
                     const uint32_t n = min(unit, k1 - k);
@@ -125,8 +124,8 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
         umma::Ring at, sums;
         bool ok = true;
         for (uint32_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
-            uint32_t k = 0;
-            for (uint32_t part = 0; part < a.splits && ok; ++part, sums.next(kSlots)) {
+            uint32_t k = kApart ? split_begin(a, first_part(i)) : 0;
+            for (uint32_t part = first_part(i); part < last_part(i) && ok; ++part, sums.next(kSlots)) {
                 if (!(ok = umma::wait(bar_free + 8 * sums.stage, sums.parity ^ 1))) break;
                 umma::fence_after_sync();
                 const uint32_t to = tmem + sums.stage * WIDTH, k0 = k, k1 = split_begin(a, part + 1);
@@ -154,19 +153,19 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
         umma::Ring sums;
         bool ok = true;
         for (uint32_t i = blockIdx.x; i < tiles && (ok || kTogether); i += gridDim.x) {
-            int64_t n = int64_t(i) * a.lanes + in_tile;
+            int64_t n = int64_t(tile_of(i)) * a.lanes + in_tile;
             bool n_ok = n < a.N && in_tile < a.lanes;
             Gated gated;
             if constexpr (END == kEndGated) gated = gated_place(a, stages, warp / 4, in_tile, int64_t(i) * (a.lanes / 2), n, n_ok);
             const float bias = a.e.bias != nullptr && n_ok ? __ldg(a.e.bias + n) : 0.0f;
             const float cs = a.e.col_scale != nullptr && n_ok ? __ldg(a.e.col_scale + n) : 1.0f;
             float v[C / 8][8];
-            for (uint32_t part = 0; part < a.splits; ++part, sums.next(kSlots)) {
+            for (uint32_t part = first_part(i); part < last_part(i); ++part, sums.next(kSlots)) {
                 ok = ok && umma::wait_warp(bar_sum + 8 * sums.stage, sums.parity);
                 if (!ok && !kTogether) break;
                 umma::fence_after_sync();
                 const uint32_t from = tw + sums.stage * WIDTH;
-                if (part == 0) {
+                if (kApart || part == 0) {
 #pragma unroll
                     for (int c = 0; c < C / 8; ++c) umma::tmem_ld(from + 8 * c, v[c]);
 #pragma unroll
@@ -191,6 +190,7 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
             for (int c = 0; c < C / 8; ++c) {
                 if (m0 + 8 * c >= a.rows) break;
                 if constexpr (END == kEndEntropy) entropy_lanes<8>(a, m0 + 8 * c, n, n_ok, v[c]);
+                else if constexpr (END == kEndSum) emit_sum<OUT, 8, false>(a, n_ok, n, m0 + 8 * c, 1, a.rows, v[c], first_part(i));
                 else gated_chunk<OUT>(a, gated, n_ok, n, m0 + 8 * c, 1, a.rows, v[c], bias, cs);
             }
         }

@@ -78,6 +78,8 @@ struct EntropyCall {
 // partial: entropy_pairs(T, V), at: T.
 int64_t entropy_pairs(int64_t T, int64_t V);
 cudaError_t entropy_fwd(const EntropyCall& c, float* loss, float* lse, float2* partial, float* at);
+// The same through the logits' FP32 sums over the runs of K in memory (entropy_apart): sums [entropy_runs,T,V].
+cudaError_t entropy_fwd_apart(const EntropyCall& c, float* loss, float* lse, float* sums);
 // The gradients of loss and lse (either may be null) and, binary16 alone (else
 // null), the power of two and its inverse that entropy_scale writes.
 struct EntropyGrads {
@@ -89,6 +91,9 @@ cudaError_t entropy_scale(const EntropyCall& c, const EntropyGrads& g);
 // The gradient of `count` logits from `first` on, [T,count] at row pitch `pitch`.
 cudaError_t entropy_logit_grad(const EntropyCall& c, const EntropyGrads& g, const float* lse, int64_t first, int64_t count,
                                uint16_t* d, int64_t pitch);
+// That of all of them through such sums.
+cudaError_t entropy_logit_grad_apart(const EntropyCall& c, const EntropyGrads& g, const float* lse, float* sums, uint16_t* d,
+                                     int64_t pitch);
 // grad_x += d w[first ..], in `parts` parts of the vocabulary (entropy_parts of a whole piece): onto sum_in [parts,T,I]
 // (null: onto nothing), into sum_out or, where that is null (one part), scaled and rounded into grad_x.
 uint32_t entropy_parts(int64_t T, int64_t I, int64_t count);

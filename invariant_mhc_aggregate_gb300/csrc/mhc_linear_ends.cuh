@@ -306,13 +306,23 @@ __device__ __forceinline__ void join_groups(float& top, float& sum, float top2, 
     top = most;
 }
 
+// A unit's maximum and sum of exponentials, of 16 lanes' entries x (-inf past the vocabulary).
+__device__ __forceinline__ float2 entropy_unit(float x) {
+    float top = x;
+#pragma unroll
+    for (int s = 8; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, s));
+    float sum = exp_fast(__fsub_rn(x, reference(top)));
+#pragma unroll
+    for (int s = 8; s > 0; s >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xFFFFFFFFu, sum, s));
+    return make_float2(top, sum);
+}
+
 // The longest run of blocks of K that one accumulator sums: the tensor cores
 // cut off each addition's last bits, so a logit is short by about half a unit
 // of the last place for each 16 products.  Runs are added up in registers,
 // rounded to nearest: K = 7168 in one run, lse is 3.9e-6 off (in norm, against
-// 64 bits), in runs of 16 blocks 5e-7, with 32-bit products and sums 8e-7; the
-// time is the same.
-constexpr uint32_t kEntropyRun = 16;
+// 64 bits), in runs of 16 blocks (kEntropyRun) 5e-7, with 32-bit products and
+// sums 8e-7; the time is the same.
 constexpr int kEntropyMost = 64;   // entries of a thread
 
 // Adds a finished run of `mine` columns, in tensor memory at `from`, to v.

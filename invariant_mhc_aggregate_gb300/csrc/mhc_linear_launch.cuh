@@ -165,9 +165,10 @@ template <bool FP8, int OUT, int WIDTH, int END>
 cudaError_t launch_few_width(TileArgs a, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
     const uint32_t sms = uint32_t(num_sms()), beside = END == kEndGated ? kGatedBytes : 0;
+    const uint32_t tiles = END == kEndSum ? a.p_tiles * a.splits : a.p_tiles;
     set_ring(a, kBytesP + WIDTH * 128, beside);
     a.end.exchange = a.stages * a.stage_bytes;
-    return launch_tiles(few_kernel<FP8, OUT, WIDTH, END>, allowed, dim3(a.p_tiles < sms ? a.p_tiles : sms), kFewThreads<WIDTH>,
+    return launch_tiles(few_kernel<FP8, OUT, WIDTH, END>, allowed, dim3(tiles < sms ? tiles : sms), kFewThreads<WIDTH>,
                         a.end.exchange + beside + 1024, 1, stream, mp, mq, a);
 }
 

@@ -83,6 +83,47 @@ inline uint32_t few_lanes(int64_t N) {
     return uint32_t(lanes < 128 ? lanes : 128);
 }
 
+// A cross entropy's logits are summed in runs of at most 16 blocks of K
+// (mhc_linear_ends.cuh says why).  A small vocabulary has few tiles, each of
+// which goes through all of K by itself: there the runs are tiles of their
+// own, whose sums meet in memory, in FP32, in the same order (I = 7168 and V = 1024:
+// T = 1 26.3 -> 9.6 us, T = 128 27.5 -> 11.7, T = 512 27.6 -> 18.0; I = 2048, V = 4096: T = 16
+// 13.2 -> 9.9).  Past these limits the sums' way costs more than the empty SMs
+// (V = 12288: T = 1, I = 7168 32.4 us, so 45.8; T = 256, 4096 x 4096 19.5, so 28.5); at
+// them the two are even (V = 8192: T = 1, I = 4096 20.1, 20.3; T = 64 25.0, 20.9).
+constexpr uint32_t kEntropyRun = 16;
+
+inline uint32_t entropy_runs(int64_t kb) { return uint32_t((kb + kEntropyRun - 1) / kEntropyRun); }
+
+inline bool entropy_apart(int64_t T, int64_t V, int64_t kb) {
+    return kb > kEntropyRun && V <= 8192 && T <= 512 && T * V <= int64_t(1) << 19;
+}
+
+// few_kernel's lanes for such tiles, and pair_kernel's width (of tokens): the cheapest
+// rounds of `runs` tiles for each of theirs.  A block of K costs few_kernel its
+// multiplications or its copies (24 bytes a cycle and SM).
+inline uint32_t apart_lanes(int64_t N, int64_t runs) {
+    uint32_t best = 128;
+    int64_t least = INT64_MAX;
+    for (int64_t lanes = 128; lanes >= 16; lanes -= 16) {
+        const int64_t rounds = ((N + lanes - 1) / lanes * runs + kClustersAtOnce[0] - 1) / kClustersAtOnce[0];
+        const int64_t cost = rounds * (280 > 16 * lanes / 3 ? 280 : 16 * lanes / 3);
+        if (cost < least) least = cost, best = uint32_t(lanes);
+    }
+    return best;
+}
+
+inline uint32_t apart_width(int64_t N, int64_t M, int64_t runs) {
+    uint32_t best = 128;
+    int64_t least = INT64_MAX;
+    for (int64_t w = 128; w <= 256; w += 32) {
+        const int64_t rounds = ((N + 255) / 256 * ((M + w - 1) / w) * runs + kPairsAtOnce - 1) / kPairsAtOnce;
+        const int64_t cost = 21 * w + rounds * (kEntropyRun * (41 * w / 20 > 300 ? 41 * w / 20 : 300) + 1500);
+        if (cost < least) least = cost, best = uint32_t(w);
+    }
+    return best;
+}
+
 // A gradient summed over `kb` blocks of K (a piece of a vocabulary), [M,N]:
 // pairs of CTAs, tiles of `width` rows, and parts of K that are tiles of their
 // own, so that few tiles fill the GPU; none longer than 256 blocks (16384

@@ -108,6 +108,55 @@ def test_forward(T, I, V, whole, dtype):
     check_forward(*layer.linear_cross_entropy(x, w, target), z, off, target)
 
 
+# small vocabularies whose runs of K are tiles of their own (T V at most 2^19, V at most 8192, T at most 512,
+# I above 1024, above 1984 in the gradients too), and the first sizes that are not so
+RUNS = [(1, 1025, 8192), (64, 2048, 8192), (64, 1032, 8193), (65, 2000, 8065), (65, 2000, 8066), (512, 1985, 1024), (513, 1984, 1000),
+        (16, 7168, 257), (3, 6296, 4584), (200, 2664, 1363), (2, 1090, 17), (31, 2048, 1), (128, 2047, 4096), (160, 4096, 3000),
+        (300, 2056, 40)]
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("T,I,V", RUNS)
+def test_runs_of_their_own(T, I, V, whole, dtype):
+    x, w, target, z, off = case(T, I, V, dtype, whole)
+    loss, lse = layer.linear_cross_entropy(x, w, target)
+    check_forward(loss, lse, z, off, target)
+    g = gen(V)
+    gl, gs = normal(g, T), normal(g, T)
+    got = layer.linear_cross_entropy_backward(gl, x, w, target, lse, grad_lse=gs)
+    check_backward(got, x, w, target, z, off, lse, gl, gs, dtype)
+    one = layer.linear_cross_entropy_backward(gl, x, w, target, lse, grad_lse=gs, want=(False, True))
+    assert one[0] is None and torch.equal(one[1], got[1])
+    check_backward(layer.linear_cross_entropy_backward(None, x, w, target, lse, grad_lse=gs), x, w, target, z, off, lse, None,
+                   gs, dtype)
+
+
+@pytest.mark.parametrize("I,V", [(1100, 8192), (2048, 1000), (7168, 300)])
+def test_runs_of_their_own_have_the_same_bits(I, V):
+    T = 700
+    x, w, target, *_ = case(T, I, V, BF)
+    whole = layer.linear_cross_entropy(x, w, target)
+    for lo, hi in ((0, 1), (333, 334), (3, 40), (5, 69), (5, 70), (100, 229), (0, 512), (0, 513)):
+        part = layer.linear_cross_entropy(x[lo:hi], w, target[lo:hi])
+        assert all(torch.equal(a, b[lo:hi]) for a, b in zip(part, whole)), (lo, hi)
+
+
+def test_runs_of_their_own_with_nan_and_infinities():
+    x, w, target, z, off = case(70, 2100, 1500, BF)
+    x[13, 7] = float("nan")
+    x[69, 2099] = float("inf")
+    x[1] = float("nan")                    # an ignored token: its loss is still 0
+    loss, lse = layer.linear_cross_entropy(x, w, target)
+    keep = [i for i in range(70) if i not in (1, 13, 69)]
+    check_forward(loss[keep], lse[keep], z[keep], off[keep], target[keep])
+    assert loss[1] == 0 and torch.isnan(lse[1]) and torch.isnan(loss[13]) and not torch.isfinite(loss[69])
+    # tokens without a gradient have none, whatever their logits
+    target[:] = -100
+    gx, gw = layer.linear_cross_entropy_backward(torch.ones(70, device="cuda"), x.nan_to_num(0.0, 0.0), w, target, lse)
+    assert (gx == 0).all() and (gw == 0).all()
+
+
 @pytest.mark.parametrize("V", [100, 20001])
 def test_spread_logits(V):
     """Logits hundreds apart, equal ones, and one far above the rest at each end."""

@@ -200,6 +200,35 @@ def test_plans(tmp_path):
         assert few in (16, 32, 64) and (M > 64 or few >= M)
 
 
+RUNS = """
+#include <cstdio>
+#include "mhc_linear_plan.h"
+int main() {
+    long long T, V, kb;
+    while (std::scanf("%lld %lld %lld", &T, &V, &kb) == 3) {
+        const long long runs = mhc::linear::entropy_runs(kb);
+        std::printf("%d %lld %u %u\\n", int(mhc::linear::entropy_apart(T, V, kb)), runs, mhc::linear::apart_lanes(V, runs),
+                    mhc::linear::apart_width(V, T, runs));
+    }
+}
+"""
+
+
+def test_runs_of_a_small_vocabulary(tmp_path):
+    (tmp_path / "runs.cpp").write_text(RUNS)
+    exe = str(tmp_path / "runs")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", _build.CSRC, "-o", exe, str(tmp_path / "runs.cpp")], check=True)
+    cases = [(T, V, kb) for T in (1, 64, 65, 128, 512, 513, 1 << 20) for V in (1, 17, 1000, 4096, 8065, 8066, 8192, 8193, 1 << 24)
+             for kb in (1, 16, 17, 32, 33, 112, 1 << 24)]
+    text = "".join("%d %d %d\n" % c for c in cases)
+    out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.split("\n")
+    for (T, V, kb), line in zip(cases, out):
+        apart, runs, lanes, width = (int(v) for v in line.split())
+        assert runs == -(-kb // 16)
+        assert apart == (kb > 16 and V <= 8192 and T <= 512 and T * V <= 1 << 19)
+        assert lanes % 16 == 0 and 16 <= lanes <= 128 and width % 32 == 0 and 128 <= width <= 256
+
+
 # --- autograd
 
 B = torch.bfloat16
