@@ -409,3 +409,25 @@ def test_autograd():
     grad, = torch.autograd.grad(loss, x, create_graph=True)
     with pytest.raises(RuntimeError, match="once"):
         (loss + grad.float().pow(2).sum()).backward()
+
+
+def test_weights_made_by_the_launch_before():
+    """A few rows' product reads its weight ahead of the launch before it, which here writes that weight, over and over."""
+    T, I, F = 8, 1024, 4096
+    g = gen(91)
+    x, a = normal(g, T, I, dtype=BF), normal(g, 2 * F, 256, dtype=BF)
+    b = [normal(g, I, 256, dtype=BF, spread=2.0 ** -8) for _ in range(4)]
+    want = []
+    for k in range(4):
+        w = layer.linear(a, b[k])
+        torch.cuda.synchronize()
+        want.append(layer.gated_linear(x, w).clone())
+    assert not torch.equal(want[0], want[1])
+    lib = layer.load()
+    w, y = torch.empty(2 * F, I, dtype=BF, device="cuda"), [torch.empty(T, F, dtype=BF, device="cuda") for _ in range(40)]
+    s = torch.cuda.current_stream().cuda_stream
+    for i in range(40):
+        assert lib.mhc_linear_fwd(a.data_ptr(), b[i % 4].data_ptr(), 0, 0, w.data_ptr(), 0, 0, 0, 2 * F, 256, I, 256, 256, I, 0, 0, s) == 0
+        assert lib.mhc_gated_linear_fwd(x.data_ptr(), w.data_ptr(), 0, y[i].data_ptr(), 0, 0, 0, T, I, F, I, I, 2, 0, s) == 0
+    torch.cuda.synchronize()
+    assert all(torch.equal(y[i], want[i % 4]) for i in range(40))
