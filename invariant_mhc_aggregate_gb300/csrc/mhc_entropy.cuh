@@ -13,24 +13,35 @@ namespace entropy {
 // i + THREADS, ... one after the other, a group's units in increasing order,
 // then the threads' pairs meet in a tree; the order depends on V alone.
 // Bound by the loads' latency where tokens are few (T = 8, V = 32768 6.1 us by
-// itself, about 3 behind the product), by HBM where they are many (T = 4096, V =
+// itself, cold, about 3 behind the product), so four groups' are under way at a
+// time (one: T = 200, 512 x 8000 9.7 us of the whole, four 7.7; T = 1, 2048 x 151936 104.7,
+// 102.7), by HBM where they are many (T = 4096, V =
 // 32768 13.3 us, cold).
 constexpr int kJoinThreads = 256;
+constexpr int kJoinBatch = 4;   // groups of a thread whose loads are under way together
 
-// Thread i's groups, and the threads' together (THREADS of them; part: shared
-// memory for a pair a warp).
-template <int THREADS, typename Load>
+// Thread i's groups, of at most MOST units, and the threads' together (THREADS
+// of them; part: shared memory for a pair a warp).
+template <int THREADS, int MOST, typename Load>
 __device__ __forceinline__ float2 join_units(Load load, int64_t units, uint32_t of_a_group, uint32_t i, float2* part) {
     float top = -INFINITY, sum = 0.0f;
-    for (int64_t u = int64_t(i) * of_a_group; u < units; u += int64_t(THREADS) * of_a_group) {
-        float2 w[4];
+    const int64_t step = int64_t(THREADS) * of_a_group;
+    for (int64_t u0 = int64_t(i) * of_a_group; u0 < units; u0 += kJoinBatch * step) {
+        float2 w[kJoinBatch][MOST];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (uint32_t(k) < of_a_group) w[k] = u + k < units ? load(u + k) : make_float2(-INFINITY, 0.0f);
+        for (int j = 0; j < kJoinBatch; ++j)
 #pragma unroll
-        for (int k = 1; k < 4; ++k)
-            if (uint32_t(k) < of_a_group) linear::join_groups(w[0].x, w[0].y, w[k].x, w[k].y);
-        linear::join_groups(top, sum, w[0].x, w[0].y);
+            for (int k = 0; k < MOST; ++k)
+                if (uint32_t(k) < of_a_group)
+                    w[j][k] = u0 + j * step + k < units ? load(u0 + j * step + k) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j) {
+            if (u0 + j * step >= units) break;
+#pragma unroll
+            for (int k = 1; k < MOST; ++k)
+                if (uint32_t(k) < of_a_group) linear::join_groups(w[j][0].x, w[j][0].y, w[j][k].x, w[j][k].y);
+            linear::join_groups(top, sum, w[j][0].x, w[j][0].y);
+        }
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) {
@@ -47,7 +58,7 @@ __device__ __forceinline__ float2 join_units(Load load, int64_t units, uint32_t 
     return make_float2(top, sum);
 }
 
-template <int THREADS>
+template <int THREADS, int MOST>
 static __global__ void __launch_bounds__(kJoinThreads)
 join_kernel(const float2* __restrict__ partial, const float* __restrict__ at, const int64_t* __restrict__ target,
             float* __restrict__ loss, float* __restrict__ lse, int64_t T, int64_t V, int64_t units, uint32_t of_a_group) {
@@ -56,7 +67,7 @@ join_kernel(const float2* __restrict__ partial, const float* __restrict__ at, co
     const uint32_t i = threadIdx.x % THREADS;
     const int64_t t = int64_t(blockIdx.x) * (kJoinThreads / THREADS) + threadIdx.x / THREADS;
     const float2* p = partial + t * units;
-    const float2 of = join_units<THREADS>([&](int64_t u) { return __ldcs(p + u); }, t < T ? units : 0, of_a_group, i, part);
+    const float2 of = join_units<THREADS, MOST>([&](int64_t u) { return __ldcs(p + u); }, t < T ? units : 0, of_a_group, i, part);
     if (i == 0 && t < T) {
         const float all = __fadd_rn(linear::reference(of.x), logf(of.y));
         lse[t] = all;
@@ -108,8 +119,8 @@ apart_join_kernel(const float* __restrict__ sums, const int64_t* __restrict__ ta
     const bool wide = (units + of_a_group - 1) / of_a_group > kJoinThreads;
     if (threadIdx.x >= (wide ? kJoinThreads : 32)) return;
     auto load = [&](int64_t u) { return pairs[u]; };
-    const float2 of = wide ? join_units<kJoinThreads>(load, units, of_a_group, threadIdx.x, part)
-                           : join_units<32>(load, units, of_a_group, threadIdx.x, part);
+    const float2 of = wide ? join_units<kJoinThreads, 4>(load, units, of_a_group, threadIdx.x, part)
+                           : join_units<32, 4>(load, units, of_a_group, threadIdx.x, part);
     if (threadIdx.x == 0) {
         const float all = __fadd_rn(linear::reference(of.x), logf(of.y));
         lse[t] = all;

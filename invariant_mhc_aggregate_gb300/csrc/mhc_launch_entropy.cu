@@ -102,7 +102,10 @@ cudaError_t entropy_fwd(const EntropyCall& c, float* loss, float* lse, float2* p
     if (e != cudaSuccess) return e;
     const bool wide = groups > 256;
     const int64_t per_block = wide ? 1 : entropy::kJoinThreads / 32;
-    return launch(wide ? entropy::join_kernel<entropy::kJoinThreads> : entropy::join_kernel<32>,
+    constexpr int kWide = entropy::kJoinThreads;
+    auto* join = few ? (wide ? entropy::join_kernel<kWide, 4> : entropy::join_kernel<32, 4>)
+                     : (wide ? entropy::join_kernel<kWide, 1> : entropy::join_kernel<32, 1>);
+    return launch(join,
                   uint32_t((c.T + per_block - 1) / per_block), entropy::kJoinThreads, c.stream, partial, at, c.target, loss, lse, c.T,
                   c.V, units, few ? uint32_t(group / kEntropyUnit) : 1u);
 }
