@@ -255,9 +255,10 @@ MHC_API int64_t mhc_linear_cross_entropy_workspace(int64_t T, int64_t I, int64_t
  *   grad_w[v,i] = cvt( sum over t of cvt(d[t,v]) * x[t,i] )       [V,I]
  *
  * The logits are computed again, by pieces of the vocabulary; cvt(d) is d
- * rounded to the operands' type, with binary16 after a scaling by a power of
- * two (one for the whole call, from the largest gradient, taken out again in
- * FP32), so that it holds small probabilities.  grad_x or grad_w may be NULL and
+ * rounded to the operands' type after a scaling (one for the whole call, a
+ * power of two over the largest |g|, taken out again in FP32), so that
+ * binary16 holds small probabilities and a g that all tokens share, as that of
+ * a mean, is not rounded.  grad_x or grad_w may be NULL and
  * is then not computed.  A token without a gradient (g + grad_lse and g both
  * 0) has d = 0 whatever its logits; its x still enters grad_w as 0 * x, so
  * x must be finite there too.  workspace:

@@ -1,6 +1,7 @@
 // The kernels around the products of a cross entropy over a vocabulary
 // (definitions in mhc_layer.h): the join of the groups' maxima and sums,
-// the sum of grad_x's parts, and the scale of binary16 gradients.
+// the same and the logits' gradients from sums over runs of K, and the sum of
+// grad_x's parts.
 #pragma once
 
 #include "mhc_linear.cuh"
@@ -136,9 +137,11 @@ template <int DT>
 static __global__ void __launch_bounds__(kApartGradThreads)
 apart_grad_kernel(const float* __restrict__ sums, const linear::TileArgs a, int64_t V, uint32_t runs, uint32_t by_token) {
     pdl_enter();
+    const linear::Scale scale = linear::scale_of<kApartGradThreads>(a.end, a.rows);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.end.inverse = scale.inverse;
     const int64_t t = blockIdx.x / by_token, n = (int64_t(blockIdx.x % by_token) * kApartGradThreads + threadIdx.x) * 2;
     if (n >= V) return;
-    const linear::RowHead h = linear::row_head<linear::kEndProb>(a, t, true);
+    const linear::RowHead h = linear::row_head<linear::kEndProb>(a, t, true, scale.by);
     const bool two = n + 1 < V;
     const float* p = sums + t * V + n;
     float x = __ldcs(p), y = two ? __ldcs(p + 1) : 0.0f;
@@ -163,7 +166,7 @@ template <int DT>
 static __global__ void __launch_bounds__(kSumThreads)
 sum_kernel(const float* __restrict__ sums, const float* __restrict__ scale, uint16_t* __restrict__ out, int64_t n, uint32_t parts) {
     pdl_enter();
-    const float f = scale == nullptr ? 1.0f : scale[1];
+    const float f = *scale;
     const int64_t i = (int64_t(blockIdx.x) * kSumThreads + threadIdx.x) * 2;
     if (i >= n) return;
     const bool two = i + 1 < n;
@@ -177,39 +180,6 @@ sum_kernel(const float* __restrict__ sums, const float* __restrict__ scale, uint
     }
     out[i] = Elem<DT>::cvt(__fmul_rn(a, f));
     if (two) out[i + 1] = Elem<DT>::cvt(__fmul_rn(b, f));
-}
-
-// Binary16 alone: scale[0] is a power of two that brings the largest gradient
-// of a token to 2^13 .. 2^14, so that the logits' gradients hold probabilities
-// down to 2^-38 of it, and scale[1] its inverse.  One block, since it is of all
-// tokens.
-constexpr int kScaleThreads = 1024;
-
-static __global__ void __launch_bounds__(kScaleThreads)
-scale_kernel(const float* __restrict__ grad_loss, const float* __restrict__ grad_lse, const int64_t* __restrict__ target,
-             float* __restrict__ scale, int64_t T, int64_t V) {
-    pdl_enter();
-    __shared__ float most[kScaleThreads / 32];
-    float m = 0.0f;
-    for (int64_t t = threadIdx.x; t < T; t += kScaleThreads) {
-        const int64_t entry = target[t];
-        const float g = grad_loss != nullptr && entry >= 0 && entry < V ? grad_loss[t] : 0.0f;
-        const float spread = grad_lse == nullptr ? g : __fadd_rn(g, grad_lse[t]);
-        m = fmaxf(m, fmaxf(fabsf(spread), fabsf(g)));
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-    if (threadIdx.x % 32 == 0) most[threadIdx.x / 32] = m;
-    __syncthreads();
-    if (threadIdx.x >= 32) return;
-    m = most[threadIdx.x];
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-    if (threadIdx.x != 0) return;
-    int power = 0;
-    if (m > 0.0f && m < INFINITY) power = min(13 - ilogbf(m), 126);
-    scale[0] = ldexpf(1.0f, power);
-    scale[1] = ldexpf(1.0f, -power);
 }
 
 }  // namespace entropy

@@ -110,10 +110,6 @@ cudaError_t entropy_fwd(const EntropyCall& c, float* loss, float* lse, float2* p
                   c.V, units, few ? uint32_t(group / kEntropyUnit) : 1u);
 }
 
-cudaError_t entropy_scale(const EntropyCall& c, const EntropyGrads& g) {
-    return launch(entropy::scale_kernel, 1, entropy::kScaleThreads, c.stream, g.loss, g.lse, c.target, g.scale, c.T, c.V);
-}
-
 // d [T,count] with the tokens on the lanes: a thread has the entries of one token.
 cudaError_t entropy_logit_grad(const EntropyCall& c, const EntropyGrads& g, const float* lse, int64_t first, int64_t count,
                                uint16_t* d, int64_t pitch) {
@@ -125,7 +121,7 @@ cudaError_t entropy_logit_grad(const EntropyCall& c, const EntropyGrads& g, cons
     const cudaError_t e = lay_out(p, c.dtype, {true, pair_width(c.T, count, k_blocks(p, c.dtype), 32), 1}, a, mp, mq);
     if (e != cudaSuccess) return e;
     a.end = {};
-    a.end.scale = g.scale, a.end.target = c.target, a.end.lse = lse, a.end.grad_loss = g.loss, a.end.grad_lse = g.lse;
+    a.end.inverse = g.inverse, a.end.target = c.target, a.end.lse = lse, a.end.grad_loss = g.loss, a.end.grad_lse = g.lse;
     a.end.first = first, a.end.entries = c.V, a.end.pitch = pitch;
     return launch_end<kEndProb, kBothK>(a, c.dtype, pairs_of(a), mp, mq, c.stream);
 }
@@ -138,7 +134,7 @@ cudaError_t entropy_logit_grad_apart(const EntropyCall& c, const EntropyGrads& g
     TileArgs a = {};
     a.e.y = d;
     a.rows = uint32_t(c.T);
-    a.end.scale = g.scale, a.end.target = c.target, a.end.lse = lse, a.end.grad_loss = g.loss, a.end.grad_lse = g.lse;
+    a.end.inverse = g.inverse, a.end.target = c.target, a.end.lse = lse, a.end.grad_loss = g.loss, a.end.grad_lse = g.lse;
     a.end.entries = c.V, a.end.pitch = pitch;
     const uint32_t by_token = uint32_t((c.V + 2 * entropy::kApartGradThreads - 1) / (2 * entropy::kApartGradThreads));
     return launch(c.dtype == kBF16 ? entropy::apart_grad_kernel<kBF16> : entropy::apart_grad_kernel<kF16>, uint32_t(c.T) * by_token,

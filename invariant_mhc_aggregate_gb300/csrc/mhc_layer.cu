@@ -615,12 +615,10 @@ mhc_status_t mhc_linear_cross_entropy_bwd(const float* grad_loss, const float* g
     wo.place(at, calls, count);
     float* sums = reinterpret_cast<float*>(at);
     at += sizes.sums;
-    // BF16 has the exponents of FP32 and needs no scale
-    float* scale = dtype == MHC_DTYPE_F16 ? reinterpret_cast<float*>(at) : nullptr;
+    float* scale = reinterpret_cast<float*>(at);
     cudaError_t e = lay_out_again(calls, count, stream);
     const mhc::layer::EntropyCall c = {xo.p, wo.p, target, T, I, V, xo.stride, wo.stride, int(dtype), cu(stream)};
     const mhc::layer::EntropyGrads grads = {grad_loss, grad_lse, scale};
-    if (e == cudaSuccess && scale != nullptr) e = mhc::layer::entropy_scale(c, grads);
     for (int64_t v = 0; v < V && e == cudaSuccess; v += sizes.piece) {
         const int64_t n = V - v < sizes.piece ? V - v : sizes.piece;
         e = sizes.apart ? mhc::layer::entropy_logit_grad_apart(c, grads, lse, sums, d, sizes.piece)

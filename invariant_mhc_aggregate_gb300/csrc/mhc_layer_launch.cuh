@@ -54,7 +54,7 @@ cudaError_t repack(const RepackCall* calls, int count, cudaStream_t stream);   /
 cudaError_t slope(const uint16_t* g, const uint16_t* preact, uint16_t* u, float* grad_bias, float* partial, int64_t T,
                   int64_t O, int64_t pitch, int act, int dtype, cudaStream_t stream);
 int64_t slope_partials(int64_t T);
-// p.e.y [M,N] = cvt(a^T b) (scaled by scale[1] where scale is not null) with rows of both operands along m and n: a weight's
+// p.e.y [M,N] = cvt(a^T b) (by *scale where scale is not null) with rows of both operands along m and n: a weight's
 // gradient, stored a row a thread (mhc_launch_entropy.cu).
 cudaError_t row_product(const linear::Product& p, const float* scale, int dtype, cudaStream_t stream);
 
@@ -80,14 +80,13 @@ int64_t entropy_pairs(int64_t T, int64_t V);
 cudaError_t entropy_fwd(const EntropyCall& c, float* loss, float* lse, float2* partial, float* at);
 // The same through the logits' FP32 sums over the runs of K in memory (entropy_apart): sums [entropy_runs,T,V].
 cudaError_t entropy_fwd_apart(const EntropyCall& c, float* loss, float* lse, float* sums);
-// The gradients of loss and lse (either may be null) and, binary16 alone (else
-// null), the power of two and its inverse that entropy_scale writes.
+// The gradients of loss and lse (either may be null), and where the logits' gradients leave what takes their scale out
+// again: the factor `scale` of the products and sums below.
 struct EntropyGrads {
     const float* loss;
     const float* lse;
-    float* scale;
+    float* inverse;
 };
-cudaError_t entropy_scale(const EntropyCall& c, const EntropyGrads& g);
 // The gradient of `count` logits from `first` on, [T,count] at row pitch `pitch`.
 cudaError_t entropy_logit_grad(const EntropyCall& c, const EntropyGrads& g, const float* lse, int64_t first, int64_t count,
                                uint16_t* d, int64_t pitch);

@@ -95,7 +95,8 @@ struct EndArgs {
     uint32_t exchange;                // where in shared memory the two halves meet (bytes from the stages on)
     const float* sum_in;              // kEndSum: [M,N] added first, or null
     float* sum_out;                   // where the sums go, or null: the last addition, into e.y
-    const float* scale;               // binary16 gradients of logits: what they are multiplied by, then its inverse; or null
+    const float* scale;               // kEndSum, kEndRow: what the sums are multiplied by, or null
+    float* inverse;                   // kEndProb: where that goes, of the scale of this call's values (scale_of)
     const int64_t* target;            // kEndEntropy, kEndProb: [tokens]
     const float* lse;                 // kEndProb: [tokens], with the gradients of the loss and of lse (or null)
     const float* grad_loss;
@@ -658,6 +659,11 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
         const uint32_t signal = umma::map_rank(bar_free, 0);
         // a gated group's warps meet in every chunk of every tile: after a wait that ran out they go on without waits
         constexpr bool kTogether = END == kEndGated;
+        Scale scale = {1.0f, 1.0f};
+        if constexpr (END == kEndProb) {   // under the first tile's multiplications
+            scale = scale_of<32 * kEpilogueWarps>(a.end, a.N);
+            if (blockIdx.x == 0 && threadIdx.x == 0) *a.end.inverse = scale.inverse;
+        }
         Sums sums;
         bool ok = true;
         for (uint32_t i = blockIdx.x / 2; i < tiles && (ok || kTogether); i += step) {
@@ -680,7 +686,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             }
             uint32_t b = 0;
             RowHead head;
-            if constexpr (END == kEndProb || END == kEndRow) head = row_head<END>(a, col, n_ok);
+            if constexpr (END == kEndProb || END == kEndRow) head = row_head<END>(a, col, n_ok, scale.by);
             if constexpr (END == kEndEntropy) {
                 float v[kEntropyMost / 8][8];
                 const int64_t target = n_ok ? __ldg(a.end.target + col) : -1;

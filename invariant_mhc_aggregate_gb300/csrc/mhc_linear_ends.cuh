@@ -143,7 +143,7 @@ __device__ __forceinline__ void emit_sum(const TileArgs& a, bool n_ok, int64_t n
         for (int c = 0; c < C; ++c)
             if (there(c)) p[c * stride] = v[c];
     } else {
-        const float factor = a.end.scale == nullptr ? 1.0f : __ldg(a.end.scale + 1);
+        const float factor = a.end.scale == nullptr ? 1.0f : __ldg(a.end.scale);
         uint16_t* p = a.e.y + at;
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -188,27 +188,64 @@ __device__ __forceinline__ void sum_tile(const TileArgs& a, uint32_t from, uint3
 // 64 bytes; short K is bound by the stores: the gradients of T = 8 tokens, I =
 // 1024, 128000 entries 195 -> 158 us, T = 1024 668 -> 591).
 //
-// kEndProb: d = scale ((g + grad_lse) exp(z - lse) - (at the target) g), from
-// the logits' sums z; g is the gradient of the loss, 0 for an ignored token.
-// It is rounded to the storage type since both products that read it take
-// 16-bit operands.  A token without a gradient has d = 0 whatever its logits
-// are.
-// kEndRow: z / scale.
+// kEndProb: d = s ((g + grad_lse) exp(z - lse) - (at the target) g), from the
+// logits' sums z; g is the gradient of the loss, 0 for an ignored token.  It is
+// rounded to the storage type since both products that read it take 16-bit
+// operands.  A token without a gradient has d = 0 whatever its logits are.
+// kEndRow: z by the scale.
 // --------------------------------------------------------------------------
 struct RowHead {
     float lse = 0.0f, factor = 1.0f, target_grad = 0.0f;
     int64_t at = -1;   // the target's column
 };
 
+// The scale s of a call's d.  A mean over tokens gives all of them one g, whose
+// rounding to 16 bits would put every target's gradient off by the same part, up
+// to 2^-9 (the mean of 3686 tokens: BF16 gradients 3.0e-3 off in norm, so 2.2e-3);
+// s is a power of two over the largest |g|, which leaves such a g none.  The power of two brings the
+// largest gradient to 2^13 .. 2^14, so that binary16 holds probabilities down to
+// 2^-38 of it.  Without a usable g, s is the power of two alone.
+struct Scale {
+    float by, inverse;
+};
+
+// By THREADS threads (from 0 on) over all of the call's tokens.
+template <int THREADS>
+__device__ __forceinline__ Scale scale_of(const EndArgs& e, int64_t tokens) {
+    __shared__ float2 part[THREADS / 32];
+    float one = 0.0f, most = 0.0f;   // the largest |g|, |g + grad_lse|
+#pragma unroll 4
+    for (int64_t t = threadIdx.x; t < tokens; t += THREADS) {
+        const int64_t target = __ldg(e.target + t);
+        const float g = e.grad_loss != nullptr && target >= 0 && target < e.entries ? __ldg(e.grad_loss + t) : 0.0f;
+        const float spread = e.grad_lse == nullptr ? g : __fadd_rn(g, __ldg(e.grad_lse + t));
+        one = fmaxf(one, fabsf(g)), most = fmaxf(most, fmaxf(fabsf(g), fabsf(spread)));
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+        one = fmaxf(one, __shfl_xor_sync(0xFFFFFFFFu, one, s));
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, s));
+    }
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = make_float2(one, most);
+    named_sync(1, THREADS);
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) one = fmaxf(one, part[w].x), most = fmaxf(most, part[w].y);
+    const float tiny = 7.8886091e-31f, huge = 1.2676506e30f;   // 2^-100, 2^100
+    if (!(one >= tiny && one <= huge && most <= huge)) one = 1.0f;
+    const float r = __frcp_rn(one), top = __fmul_rn(most, r);
+    int power = 0;
+    if (top > 0.0f && top < INFINITY) power = min(13 - ilogbf(top), 126);
+    return {ldexpf(r, power), ldexpf(one, -power)};
+}
+
 // (read while the row's sums are still under way)
 template <int END>
-__device__ __forceinline__ RowHead row_head(const TileArgs& a, int64_t row, bool ok) {
+__device__ __forceinline__ RowHead row_head(const TileArgs& a, int64_t row, bool ok, float scale) {
     RowHead h;
     if constexpr (END == kEndProb) {
         if (ok) {
             const int64_t target = __ldg(a.end.target + row);
             const float g = a.end.grad_loss == nullptr ? 0.0f : __ldg(a.end.grad_loss + row);
-            const float scale = a.end.scale == nullptr ? 1.0f : __ldg(a.end.scale);
             h.lse = __ldg(a.end.lse + row);
             if (target >= 0 && target < a.end.entries) {
                 h.at = target - a.end.first;
@@ -219,7 +256,7 @@ __device__ __forceinline__ RowHead row_head(const TileArgs& a, int64_t row, bool
             h.factor = __fmul_rn(h.factor, scale);
         }
     } else if (a.end.scale != nullptr) {
-        h.factor = __ldg(a.end.scale + 1);
+        h.factor = __ldg(a.end.scale);
     }
     return h;
 }

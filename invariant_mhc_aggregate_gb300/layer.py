@@ -584,8 +584,8 @@ def linear_cross_entropy_backward(grad_loss: torch.Tensor | None, x: torch.Tenso
     and lse (FP32 [T]; either may be None) and the forward's lse; `want` says
     which of the two to compute.  The logits are computed again by pieces of
     the vocabulary; both products read their gradient rounded to the storage
-    type (after a scaling by a power of two, so that f16 holds small
-    probabilities)."""
+    type (after a scaling, so that f16 holds small probabilities and a gradient
+    that all tokens share, as that of a mean, is not rounded)."""
     if stream is None:
         out = (_fast or _compiled()).linear_cross_entropy_backward(grad_loss, x, weight, target, lse, grad_lse, want[0],
                                                                    want[1])

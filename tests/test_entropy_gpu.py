@@ -280,6 +280,31 @@ def test_small_probabilities_in_binary16():
     check_backward(got, x, w, target, z, off, lse, gl, None, HF)
 
 
+@pytest.mark.parametrize("I", [128, 2048])
+@pytest.mark.parametrize("dtype", BOTH)
+def test_a_gradient_that_all_tokens_share_is_not_rounded(dtype, I):
+    """A mean's: with g halfway between two values of the type, every target's gradient would be off by half a step."""
+    T, V = 256, 4096
+    g = gen(17)
+    x, w = normal(g, T, I, dtype=dtype), normal(g, V, I, dtype=dtype, spread=0.125 * I ** -0.5)
+    target = torch.randperm(V, generator=g, device="cuda")[:T]
+    share = 2.0 ** -12 * (1 + U[dtype])
+    gl = torch.full((T,), share, device="cuda")
+    loss, lse = layer.linear_cross_entropy(x, w, target)
+    gx, gw = layer.linear_cross_entropy_backward(gl, x, w, target, lse)
+    p = torch.exp(x.double() @ w.double().t() - lse.double()[:, None])
+    d = p.clone()
+    d[torch.arange(T, device="cuda"), target] -= 1
+    # p at a target is lost at most (under half a step of 1), the others have their own rounding, then the last one
+    # (and 2^-16 for the logits, the exponentials, the scale and the sums)
+    lost = float(p[torch.arange(T, device="cuda"), target].max())
+    assert lost <= 2.0 ** -10
+    for got, want, size, one in ((gx, d @ w.double(), p @ w.double().abs(), w[target].double().abs()),
+                                 (gw[target], (d.t() @ x.double())[target], (p.t() @ x.double().abs())[target], x.double().abs())):
+        bound = share * (U[dtype] * want.abs() + (1 + U[dtype]) * ((lost + 2.0 ** -16) * one + (U[dtype] + 2.0 ** -16) * size)) + TINY[dtype]
+        within(got, share * want, bound, "gradient")
+
+
 def test_ignored_tokens_have_no_gradient():
     T, I, V = 200, 256, 3000
     x, w, target, z, off = case(T, I, V, BF)
