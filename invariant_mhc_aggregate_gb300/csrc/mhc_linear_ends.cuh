@@ -200,11 +200,12 @@ struct RowHead {
 };
 
 // The scale s of a call's d.  A mean over tokens gives all of them one g, whose
-// rounding to 16 bits would put every target's gradient off by the same part, up
-// to 2^-9 (the mean of 3686 tokens: BF16 gradients 3.0e-3 off in norm, so 2.2e-3);
-// s is a power of two over the largest |g|, which leaves such a g none.  The power of two brings the
-// largest gradient to 2^13 .. 2^14, so that binary16 holds probabilities down to
-// 2^-38 of it.  Without a usable g, s is the power of two alone.
+// rounding to 16 bits would put every target's gradient off by the same part,
+// up to half a step (a mean of some 3690 tokens: BF16 gradients 3.0e-3 off in
+// norm, so 1.9e-3); s is a power of two over the largest |g|, which leaves such a
+// g none.  The power of two brings the largest gradient to 2^13 .. 2^14, so that
+// binary16 holds probabilities down to 2^-38 of it.  Without a usable g, s is
+// the power of two alone.
 struct Scale {
     float by, inverse;
 };
