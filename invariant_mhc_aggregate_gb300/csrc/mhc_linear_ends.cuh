@@ -231,7 +231,7 @@ __device__ __forceinline__ Scale scale_of(const EndArgs& e, int64_t tokens) {
     named_sync(1, THREADS);
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) one = fmaxf(one, part[w].x), most = fmaxf(most, part[w].y);
-    const float tiny = 7.8886091e-31f, huge = 1.2676506e30f;   // 2^-100, 2^100
+    const float tiny = 8.6736174e-19f, huge = 1.1529215e18f;   // 2^-60, 2^60: their quotient is finite
     if (!(one >= tiny && one <= huge && most <= huge)) one = 1.0f;
     const float r = __frcp_rn(one), top = __fmul_rn(most, r);
     int power = 0;

@@ -305,6 +305,18 @@ def test_a_gradient_that_all_tokens_share_is_not_rounded(dtype, I):
         within(got, share * want, bound, "gradient")
 
 
+@pytest.mark.parametrize("I", [64, 2048])
+@pytest.mark.parametrize("loss_power,lse_power", [(-90, 90), (-50, 50), (50, -50), (90, -90), (-100, -100), (-30, 0)])
+def test_gradients_far_apart(loss_power, lse_power, I):
+    T, V = 70, 300
+    x, w, target, z, off = case(T, I, V, BF)
+    loss, lse = layer.linear_cross_entropy(x, w, target)
+    g = gen(29)
+    gl, gs = (normal(g, T).abs().clamp(min=0.01) * 2.0 ** k for k in (loss_power, lse_power))
+    check_backward(layer.linear_cross_entropy_backward(gl, x, w, target, lse, grad_lse=gs), x, w, target, z, off, lse, gl, gs, BF)
+    check_backward(layer.linear_cross_entropy_backward(gl, x, w, target, lse), x, w, target, z, off, lse, gl, None, BF)
+
+
 def test_ignored_tokens_have_no_gradient():
     T, I, V = 200, 256, 3000
     x, w, target, z, off = case(T, I, V, BF)
