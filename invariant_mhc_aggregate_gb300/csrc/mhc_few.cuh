@@ -122,7 +122,7 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
             uint32_t k = kApart ? split_begin(a, first_part(i)) : 0;
             for (uint32_t part = first_part(i); part < last_part(i) && ok; ++part) {
                 for (const uint32_t k1 = split_begin(a, part + 1); k < k1; ++issued, at.next(count)) {
-                    if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
+                    if (!(ok = umma::wait_warp(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
                     const uint32_t n = min(unit, k1 - k);
                     if (umma::elect()) {
                         umma::expect_tx(bar_full + 8 * at.stage, n * (a.lanes + WIDTH) * 128);
@@ -147,11 +147,11 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
         for (uint32_t i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
             uint32_t k = kApart ? split_begin(a, first_part(i)) : 0;
             for (uint32_t part = first_part(i); part < last_part(i) && ok; ++part, sums.next(kSlots)) {
-                if (!(ok = umma::wait(bar_free + 8 * sums.stage, sums.parity ^ 1))) break;
+                if (!(ok = umma::wait_warp(bar_free + 8 * sums.stage, sums.parity ^ 1))) break;
                 umma::fence_after_sync();
                 const uint32_t to = tmem + sums.stage * WIDTH, k0 = k, k1 = split_begin(a, part + 1);
                 for (; k < k1; at.next(count)) {
-                    if (!(ok = umma::wait(bar_full + 8 * at.stage, at.parity))) break;
+                    if (!(ok = umma::wait_warp(bar_full + 8 * at.stage, at.parity))) break;
                     umma::fence_after_sync();
                     const uint32_t n = min(unit, k1 - k);
                     if (umma::elect()) {

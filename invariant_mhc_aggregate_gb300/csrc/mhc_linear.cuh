@@ -289,7 +289,7 @@ __device__ __forceinline__ void drain(bool& ok, uint32_t issued, umma::Ring at, 
     for (uint32_t i = 0; i < issued; ++i) {
         if (at.stage == 0) at.stage = count, at.parity ^= 1;
         --at.stage;
-        ok = umma::wait((ok ? bar_empty : bar_full) + 8 * at.stage, at.parity) && ok;
+        ok = umma::wait_warp((ok ? bar_empty : bar_full) + 8 * at.stage, at.parity) && ok;
     }
 }
 
@@ -374,7 +374,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
         uint32_t k = k0, issued = 0;
         for (; k < k1; k += unit, ++issued, at.next(count)) {
             // (the first round finds every stage free: the phase before a new barrier's first one)
-            if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
+            if (!(ok = umma::wait_warp(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
             const uint32_t n = min(unit, k1 - k);
             if (umma::elect()) {
                 umma::expect_tx(bar_full + 8 * at.stage, n * a.block_bytes);
@@ -393,7 +393,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
         const uint32_t idesc = a.idesc;
         umma::Ring at;
         for (uint32_t k = k0; k < k1; k += unit, at.next(count)) {
-            if (!umma::wait(bar_full + 8 * at.stage, at.parity)) {
+            if (!umma::wait_warp(bar_full + 8 * at.stage, at.parity)) {
                 timed_out(a);
                 break;
             }
@@ -603,7 +603,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
             uint32_t k = kApart ? split_begin(a, first_part(i)) : 0;
             for (uint32_t part = first_part(i); part < last_part(i) && ok; ++part) {
                 for (const uint32_t k1 = split_begin(a, part + 1); k < k1; ++issued, at.next(count)) {
-                    if (!(ok = umma::wait(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
+                    if (!(ok = umma::wait_warp(bar_empty + 8 * at.stage, at.parity ^ 1))) break;
                     const uint32_t n = min(unit, k1 - k);
                     if (umma::elect()) {
                         if (warp == kCopyP && rank == 0)
@@ -633,11 +633,11 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
                 uint32_t k = kApart ? split_begin(a, first_part(i)) : 0;
                 for (uint32_t part = first_part(i); part < last_part(i) && ok; ++part) {
                     const uint32_t b = sums.take<PARTS>(part);
-                    if (!(ok = umma::wait(bar_free + 8 * b, sums.parity(b) ^ 1))) break;
+                    if (!(ok = umma::wait_warp(bar_free + 8 * b, sums.parity(b) ^ 1))) break;
                     umma::fence_after_sync();
                     const uint32_t to = tmem + b * 256, k0 = k, k1 = split_begin(a, part + 1);
                     for (; k < k1; at.next(count)) {
-                        if (!(ok = umma::wait(bar_full + 8 * at.stage, at.parity))) break;
+                        if (!(ok = umma::wait_warp(bar_full + 8 * at.stage, at.parity))) break;
                         umma::fence_after_sync();
                         const uint32_t n = min(unit, k1 - k);
                         if (umma::elect()) {

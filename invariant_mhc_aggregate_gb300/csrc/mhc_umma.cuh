@@ -164,10 +164,11 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
     return false;
 }
 
-// The same by a whole warp, whose lanes poll one by one but leave together:
-// the tensor-memory instructions after it must be executed by all of them.
-// (Copies and multiplications choose their lane by an instruction that does
-// the same.)
+// The same by a whole warp: its lanes poll one by one, each with a limit of its
+// own, but one vote ends the wait for all of them, with one answer.  Every wait
+// of the kernels is this one.  What follows, tensor-memory instructions or the
+// choice of a lane (elect), wants the whole warp: lanes that got through just
+// before the limit would wait there without end for others that ran out of it.
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
     return __all_sync(0xFFFFFFFFu, wait(bar, parity));
 }
