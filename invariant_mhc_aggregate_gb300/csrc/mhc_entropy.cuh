@@ -51,7 +51,7 @@ __device__ __forceinline__ float2 join_units(Load load, int64_t units, uint32_t 
     }
     if constexpr (THREADS > 32) {
         if (i % 32 == 0) part[i / 32] = make_float2(top, sum);
-        named_sync(1, THREADS);
+        umma::group_sync(1, THREADS);
         top = part[0].x, sum = part[0].y;
 #pragma unroll
         for (int w = 1; w < THREADS / 32; ++w) linear::join_groups(top, sum, part[w].x, part[w].y);

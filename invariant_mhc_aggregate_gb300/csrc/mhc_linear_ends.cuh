@@ -74,10 +74,10 @@ __device__ __forceinline__ void gated_chunk(const TileArgs& a, const Gated& g, b
         for (int c = 0; c < 8; ++c, p += step * (2 * half))
             if (n_ok && m0 + c * step < rows) *p = Elem<OUT>::cvt(v[c]);
     }
-    named_sync(g.barrier, 128);   // the chunk before has been taken out
+    umma::group_sync(g.barrier, 128);   // the chunk before has been taken out
 #pragma unroll
     for (int c = 0; c < 8; ++c) g.z[c * kLanesP + g.lane] = v[c];
-    named_sync(g.barrier, 128);
+    umma::group_sync(g.barrier, 128);
     // the first two warps take columns 0 .. 3 of 64 values f, the other two 4 .. 7
     const uint32_t i = g.lane & 63, c0 = g.lane >> 6 << 2;
     const float* z = g.z + c0 * kLanesP + i;
@@ -228,7 +228,7 @@ __device__ __forceinline__ Scale scale_of(const EndArgs& e, int64_t tokens) {
         most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, s));
     }
     if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = make_float2(one, most);
-    named_sync(1, THREADS);
+    umma::group_sync(1, THREADS);
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) one = fmaxf(one, part[w].x), most = fmaxf(most, part[w].y);
     const float tiny = 8.6736174e-19f, huge = 1.1529215e18f;   // 2^-60, 2^60: their quotient is finite

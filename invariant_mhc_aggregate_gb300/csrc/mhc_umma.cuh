@@ -173,6 +173,14 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
     return __all_sync(0xFFFFFFFFu, wait(bar, parity));
 }
 
+// named_sync by warps whose lanes may have come apart, after loads or stores
+// that some of them make: the barrier (bar.sync, whose warps are whole by its
+// definition) finds them together.
+__device__ __forceinline__ void group_sync(uint32_t id, uint32_t threads) {
+    __syncwarp();
+    named_sync(id, threads);
+}
+
 __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" : : "r"(bar), "r"(bytes) : "memory");
 }

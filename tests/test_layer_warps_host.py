@@ -20,3 +20,14 @@ def test_a_warp_ends_a_wait_with_one_answer():
         assert not re.search(r"umma::(try_)?wait\(", SOURCES[name]), name
         waits += SOURCES[name].count("umma::wait_warp(")
     assert waits == 13
+
+
+def test_groups_of_warps_meet_as_whole_warps():
+    """The named barrier counts whole warps (bar.sync): after a store of some lanes they come together first."""
+    assert re.search(r"void group_sync\(uint32_t id, uint32_t threads\) \{\s*__syncwarp\(\);\s*named_sync\(id, threads\);\s*\}",
+                     SOURCES["mhc_umma.cuh"])
+    meetings = 0
+    for name in TENSOR:
+        assert "named_sync(" not in SOURCES[name], name
+        meetings += SOURCES[name].count("umma::group_sync(")
+    assert meetings == 4
