@@ -412,11 +412,11 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
         umma::fence_after_sync();
         // group g of four warps takes the chunks g, g + 4, ... of the columns
         for (uint32_t c = group * kChunk; c < valid; c += 4 * kChunk) {
-            __syncwarp();   // (after stores that some lanes make)
-            float v[kChunk];
-            umma::tmem_ld(tmem + (quarter * 32u << 16) + c, v);
             uint16_t r[kChunk];
             if (END == kEndPlain && a.splits == 1) load_residual<kChunk>(a.e, n_ok, n, m0 + c, 1, m0 + valid, r);
+            __syncwarp();   // (after loads and stores that some lanes make)
+            float v[kChunk];
+            umma::tmem_ld(tmem + (quarter * 32u << 16) + c, v);
             umma::tmem_wait_ld(v);
             if (a.splits == 1) {
                 if constexpr (END == kEndPlain) emit_any<OUT, kChunk>(a.e, a.N, n_ok, n, m0 + c, 1, m0 + valid, v, r, bias, cs);
@@ -524,7 +524,10 @@ template <int OUT, bool ALL, bool RES, typename GiveBack>
 __device__ __forceinline__ void emit_tile(const TileArgs& a, uint32_t from, uint32_t mine, uint32_t m0, int64_t col, bool n_ok,
                                           float bias, float cs, GiveBack give_back) {
     uint16_t r[kChunk];
-    if constexpr (RES) load_residual<kChunk>(a.e, n_ok, col, m0, 1, a.rows, r);
+    if constexpr (RES) {
+        load_residual<kChunk>(a.e, n_ok, col, m0, 1, a.rows, r);
+        __syncwarp();   // (after loads that some lanes make)
+    }
     float next[kChunk];
     umma::tmem_ld(from, next);
     int64_t at = int64_t(m0) * a.N + col;

@@ -31,3 +31,64 @@ def test_groups_of_warps_meet_as_whole_warps():
         assert "named_sync(" not in SOURCES[name], name
         meetings += SOURCES[name].count("umma::group_sync(")
     assert meetings == 4
+
+
+TOGETHER = r"__syncwarp\(\)|wait_warp\(|__all_sync\(|__any_sync\(|group_sync\(|gated_chunk<"
+APART = (r"load_residual<|\bemit<|emit_any<|emit_sum<|give_back\(\)|if \(lane == 0\)|n_ok \?|if \(ok\)|if \(n_ok|if \(there|if \(sectors"
+         r"|if \(halves|prefetch_l2\(|row_head<|elect\(\)|entropy_tile\(|entropy_lanes<")
+WHOLE = (r"tmem_ld\(|tmem_st\(|tmem_wait_ld\(|tmem_wait_st\(|entropy_add<|emit_tile<|sum_tile<|sum_columns<|row_tile<|gated_tile<")
+
+
+def body(code, at):
+    """The block that opens at or after `at`, and where it ends."""
+    start = code.index("{", at)
+    depth = 0
+    for i in range(start, len(code)):
+        depth += {"{": 1, "}": -1}.get(code[i], 0)
+        if depth == 0:
+            return code[start + 1:i], i + 1
+    raise AssertionError("no end")
+
+
+def unrolled(code):
+    """Every loop's body twice, so that what ends one round stands before the next."""
+    out, at = "", 0
+    for m in re.finditer(r"\bfor \(", code):
+        if m.start() < at:
+            continue
+        depth, i = 0, m.end() - 1
+        while True:
+            depth += {"(": 1, ")": -1}.get(code[i], 0)
+            i += 1
+            if depth == 0:
+                break
+        out += code[at:i]
+        if code[i:].lstrip().startswith("{"):
+            inside, at = body(code, i)
+            out += 2 * unrolled(inside)
+        else:
+            at = code.index(";", i) + 1
+            out += 2 * code[i:at]
+    return out + code[at:]
+
+
+def test_tensor_memory_is_read_and_written_by_whole_warps():
+    """tcgen05's loads, stores and waits are .aligned: undefined where a warp's lanes have come apart.  Between what only some
+    lanes do (loads and stores at ragged edges, signals of one lane) and such an instruction stands something that brings
+    them together."""
+    functions = places = 0
+    for name in ("mhc_linear.cuh", "mhc_linear_ends.cuh", "mhc_few.cuh"):
+        code = SOURCES[name]
+        for m in re.finditer(r"__device__ __forceinline__ void (\w+)\(|__global__ void __launch_bounds__\([^{;]*?\)\s+(\w+)\(", code):
+            text, _ = body(code, m.end())
+            if not re.search(WHOLE, text):
+                continue
+            functions += 1
+            together = True            # (a caller is held to it where it calls; a tile's end is the last of its round)
+            for t in re.finditer(f"({WHOLE})|({TOGETHER})|({APART})", unrolled(text)):
+                if t.group(1):
+                    places += 1
+                    assert together, (name, m.group(1) or m.group(2), t.group(0))
+                else:
+                    together = t.group(2) is not None
+    assert functions == 9 and places > 40
