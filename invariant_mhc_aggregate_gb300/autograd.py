@@ -365,7 +365,8 @@ class GatedLinear(torch.autograd.Function):
         xx, ww = _rows(x, I), _rows(weight, weight.shape[-1])
         bias = None if bias is None else bias.contiguous()
         if not keep:
-            return layer.gated_linear(xx, ww, bias=bias, activation=activation).reshape(*x.shape[:-1], -1)
+            y = layer.gated_linear(xx, ww, bias=bias, activation=activation)
+            return y.reshape(*x.shape[:-1], y.shape[-1])
         y, z = layer.gated_linear_preact(xx, ww, bias=bias, activation=activation)
         ctx.save_for_backward(xx, ww, z)
         ctx.activation, ctx.lead, ctx.with_bias = activation, x.shape[:-1], bias is not None
