@@ -362,7 +362,7 @@ class GatedLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, activation, keep):
         I = x.shape[-1]
-        xx, ww = _rows(x, I), _rows(weight, weight.shape[-1])
+        xx, ww = _rows(x, I), _rows(weight, layer._two(weight, "weight")[1])
         bias = None if bias is None else bias.contiguous()
         if not keep:
             y = layer.gated_linear(xx, ww, bias=bias, activation=activation)
@@ -403,7 +403,7 @@ class LinearCrossEntropy(torch.autograd.Function):
         I = x.shape[-1]
         if target.shape != x.shape[:-1]:
             raise ValueError(f"shape mismatch: x {tuple(x.shape)}, target {tuple(target.shape)}")
-        xx, ww, tt = _rows(x, I), _rows(weight, weight.shape[-1]), target.reshape(-1).contiguous()
+        xx, ww, tt = _rows(x, I), _rows(weight, layer._two(weight, "weight")[1]), target.reshape(-1).contiguous()
         loss, lse = layer.linear_cross_entropy(xx, ww, tt)
         lse = lse.reshape(target.shape)
         ctx.save_for_backward(xx, ww, tt, lse)

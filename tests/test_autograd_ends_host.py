@@ -52,3 +52,15 @@ def test_no_tokens(formulas, lead):
     assert loss.shape == lse.shape == lead
     (loss.sum() + lse.sum()).backward()
     assert x.grad.shape == x.shape
+
+
+@pytest.mark.parametrize("shape", [(8,), (2, 5, 8), (1, 10, 8)])
+def test_a_weight_has_two_dimensions(formulas, shape):
+    """Refused where it is given, not by the gradient's shape in the backward."""
+    x, w = torch.ones(3, 8, dtype=B).requires_grad_(), torch.ones(*shape, dtype=B).requires_grad_()
+    with pytest.raises(ValueError, match="weight must be 2-d"):
+        autograd.gated_linear(x, w)
+    with pytest.raises(ValueError, match="weight must be 2-d"):
+        autograd.linear_cross_entropy(x, w, torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(ValueError, match="weight must be 2-d"), torch.no_grad():
+        autograd.gated_linear(x, w)
