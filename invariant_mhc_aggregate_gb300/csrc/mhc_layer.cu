@@ -243,19 +243,6 @@ mhc_status_t linear_fwd(const void* x, const float* x_scale, const void* w, cons
 
 // ---- cross entropy -------------------------------------------------------------
 
-// Entries of the vocabulary whose logits' gradients are in the workspace at a
-// time: 19456 (a tile of 256 for each pair of CTAs), more with fewer tokens
-// (256 MB: T = 1024, 1024 x 128000 591 us in pieces of 32 MB, 497; T = 4096, 7168 x
-// 131072 13.8 ms in pieces of 160 MB, 13.3), fewer with very many (1 GB).
-int64_t entropy_piece(int64_t T, int64_t V) {
-    int64_t n = 256 * mhc::linear::kPairsAtOnce;
-    if (T * n < int64_t(1) << 27) n = (int64_t(1) << 27) / T;
-    if (T * n > int64_t(1) << 29) n = (int64_t(1) << 29) / T;
-    if (n < 4096) n = 4096;
-    const int64_t pieces = (V + n - 1) / n;
-    return ((V + pieces - 1) / pieces + 63) / 64 * 64;
-}
-
 int64_t apart_bytes(int64_t T, int64_t V, int64_t kb) { return round16(mhc::linear::entropy_runs(kb) * T * V * 4); }
 
 struct EntropySizes {
@@ -264,7 +251,7 @@ struct EntropySizes {
     bool apart;
     EntropySizes(int64_t T, int64_t I, int64_t V, bool want_x) {
         const int64_t kb = (I + 63) / 64;
-        piece = entropy_piece(T, V);
+        piece = mhc::linear::entropy_piece(T, V);
         d = round16(T * piece * 2);
         parts = want_x ? mhc::layer::entropy_parts(T, I, piece < V ? piece : V) : 1;
         sums = want_x && (piece < V || parts > 1) ? round16(parts * T * I * 4) : 0;

@@ -124,6 +124,19 @@ inline uint32_t apart_width(int64_t N, int64_t M, int64_t runs) {
     return best;
 }
 
+// Entries of the vocabulary whose logits' gradients are in the workspace at a
+// time: 19456 (a tile of 256 for each pair of CTAs), more with fewer tokens
+// (256 MB: T = 1024, 1024 x 128000 591 us in pieces of 32 MB, 497; T = 4096, 7168 x
+// 131072 13.8 ms in pieces of 160 MB, 13.3), fewer with very many (1 GB).
+inline int64_t entropy_piece(int64_t T, int64_t V) {
+    int64_t n = 256 * kPairsAtOnce;
+    if (T * n < int64_t(1) << 27) n = (int64_t(1) << 27) / T;
+    if (T * n > int64_t(1) << 29) n = (int64_t(1) << 29) / T;
+    if (n < 4096) n = 4096;
+    const int64_t pieces = (V + n - 1) / n;
+    return ((V + pieces - 1) / pieces + 63) / 64 * 64;
+}
+
 // A gradient summed over `kb` blocks of K (a piece of a vocabulary), [M,N]:
 // pairs of CTAs, tiles of `width` rows, and parts of K that are tiles of their
 // own, so that few tiles fill the GPU; none longer than 256 blocks (16384

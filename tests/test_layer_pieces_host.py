@@ -1,0 +1,50 @@
+"""The pieces of a vocabulary and the parts of its sums: which sizes of _ends.py take which, from the plan alone."""
+
+import subprocess
+
+import _ends
+from invariant_mhc_aggregate_gb300 import _build
+
+PROGRAM = """
+#include <cstdio>
+#include "mhc_linear_plan.h"
+int main() {
+    long long T, I, V;
+    while (std::scanf("%lld %lld %lld", &T, &I, &V) == 3) {
+        const long long piece = mhc::linear::entropy_piece(T, V), pieces = (V + piece - 1) / piece;
+        const mhc::linear::Plan p = mhc::linear::sum_plan(I, T, ((piece < V ? piece : V) + 63) / 64);
+        std::printf("%lld %lld %u %lld\\n", piece, pieces, p.splits, (V - (pieces - 1) * piece + 63) / 64);
+    }
+}
+"""
+
+
+def ask(tmp_path, cases):
+    (tmp_path / "pieces.cpp").write_text(PROGRAM)
+    exe = str(tmp_path / "pieces")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", _build.CSRC, "-o", exe, str(tmp_path / "pieces.cpp")], check=True)
+    text = "".join("%d %d %d\n" % c for c in cases)
+    out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.split("\n")
+    return [tuple(int(v) for v in line.split()) for line in out if line]
+
+
+def test_sizes_take_their_ways(tmp_path):
+    cases = [*(c + (None,) for c in _ends.PIECES), _ends.SHORT]
+    for (T, I, V, pieces, parts, last), got in zip(cases, ask(tmp_path, [c[:3] for c in cases])):
+        assert got[1:3] == (pieces, parts), (T, I, V, got)
+        assert last is None or (got[3] == last and last < parts)
+    assert {c[4] == 1 for c in _ends.PIECES} == {True, False} and all(c[3] > 1 for c in _ends.PIECES)
+
+
+def test_pieces_are_legal(tmp_path):
+    cases = [(T, 64, V) for T in (1, 7, 64, 1000, 4096, 6899, 6900, 27594, 27595, 131072, 131073, 1 << 24)
+             for V in (1, 63, 64, 4096, 4097, 19456, 19457, 131072, 1 << 22)]
+    for (T, _, V), (piece, pieces, parts, last) in zip(cases, ask(tmp_path, cases)):
+        assert piece % 64 == 0 and 1 <= last <= -(-piece // 64) and (pieces - 1) * piece < V <= pieces * piece
+        # 256 MB of d with few tokens, a tile of 256 entries for each pair of CTAs or 1 GB with more, 4096 entries at least
+        assert piece <= max(1 << 27, T * 256 * 76) // T + 64 and (T * piece <= (1 << 29) + 64 * T or piece <= 4096)
+
+
+def test_grad_w_by_rows_has_its_tiles():
+    for T, I, F in _ends.BY_ROWS:
+        assert I % 16 == 0 and -(-2 * F // 256) * -(-I // 256) >= 76
