@@ -205,6 +205,7 @@ MHC_API mhc_status_t mhc_gated_linear_fp8_fwd(const void* x8, const float* x_sca
  *   grad_bias[j] = sum over t of u[t,j]                           FP32 [2 F]
  *
  * cvt(u) is what the products' 16-bit operands hold; grad_bias sums u itself.
+ * grad_w is summed in runs of at most 16384 tokens, which are added in FP32.
  * Each of the three may be NULL and is then not computed.  x and w have row
  * strides.  workspace: mhc_gated_linear_bwd_workspace(...) bytes, 16-byte
  * aligned; aligned as in mhc_linear_workspace.
@@ -258,7 +259,8 @@ MHC_API int64_t mhc_linear_cross_entropy_workspace(int64_t T, int64_t I, int64_t
  * rounded to the operands' type after a scaling (one for the whole call, a
  * power of two over the largest |g|, taken out again in FP32), so that
  * binary16 holds small probabilities and a g that all tokens share, as that of
- * a mean, is not rounded.  grad_x or grad_w may be NULL and
+ * a mean, is not rounded.  Sums over entries and over tokens are taken in runs
+ * of at most 16384, which are added in FP32.  grad_x or grad_w may be NULL and
  * is then not computed.  A token without a gradient (g + grad_lse and g both
  * 0) has d = 0 whatever its logits; its x still enters grad_w as 0 * x, so
  * x must be finite there too.  workspace:

@@ -159,14 +159,14 @@ apart_grad_kernel(const float* __restrict__ sums, const linear::TileArgs a, int6
     *reinterpret_cast<uint32_t*>(a.e.y + t * a.end.pitch + n) = Elem<DT>::pack(x, y);   // (the pitch is even and holds the pair)
 }
 
-// grad_x from the parts' sums: their sum in increasing order, scaled and rounded.
+// A gradient from its parts' sums: their sum in increasing order, scaled (where scale is not null) and rounded.
 constexpr int kSumThreads = 256;
 
 template <int DT>
 static __global__ void __launch_bounds__(kSumThreads)
 sum_kernel(const float* __restrict__ sums, const float* __restrict__ scale, uint16_t* __restrict__ out, int64_t n, uint32_t parts) {
     pdl_enter();
-    const float f = *scale;
+    const float f = scale == nullptr ? 1.0f : *scale;
     const int64_t i = (int64_t(blockIdx.x) * kSumThreads + threadIdx.x) * 2;
     if (i >= n) return;
     const bool two = i + 1 < n;

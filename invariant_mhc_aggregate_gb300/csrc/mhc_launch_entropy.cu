@@ -7,11 +7,26 @@ namespace layer {
 
 namespace {
 
-template <int END, int LAYOUT>
+template <int END, int LAYOUT, bool PARTS = false>
 cudaError_t launch_end(const TileArgs& a, int dtype, uint32_t pairs, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed[2];
-    if (dtype == kBF16) return launch_pair_kernel(pair_kernel<false, kBF16, LAYOUT, false, END>, allowed[0], a, pairs, mp, mq, stream);
-    return launch_pair_kernel(pair_kernel<false, kF16, LAYOUT, false, END>, allowed[1], a, pairs, mp, mq, stream);
+    if (dtype == kBF16) return launch_pair_kernel(pair_kernel<false, kBF16, LAYOUT, PARTS, END>, allowed[0], a, pairs, mp, mq, stream);
+    return launch_pair_kernel(pair_kernel<false, kF16, LAYOUT, PARTS, END>, allowed[1], a, pairs, mp, mq, stream);
+}
+
+// A sum over tokens by itself, in parts one after the other where there are many (kSumBlocks).
+template <int END>
+cudaError_t launch_tokens(const TileArgs& a, int dtype, const CUtensorMap& mp, const CUtensorMap& mq, cudaStream_t stream) {
+    return a.splits > 1 ? launch_end<END, kBothMn, true>(a, dtype, pairs_of(a), mp, mq, stream)
+                        : launch_end<END, kBothMn>(a, dtype, pairs_of(a), mp, mq, stream);
+}
+
+// out [n] from the parts' sums.
+cudaError_t sum_up(const float* sums, uint32_t parts, const float* scale, void* out, int64_t n, int dtype, cudaStream_t stream) {
+    const int64_t blocks = (n + 2 * entropy::kSumThreads - 1) / (2 * entropy::kSumThreads);
+    if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    return launch(dtype == kBF16 ? entropy::sum_kernel<kBF16> : entropy::sum_kernel<kF16>, uint32_t(blocks), entropy::kSumThreads,
+                  stream, sums, scale, static_cast<uint16_t*>(out), n, parts);
 }
 
 // The tile of rows (a multiple of `step`) that pair_kernel takes, by plan_of's
@@ -161,10 +176,7 @@ cudaError_t entropy_grad_x(const EntropyCall& c, const uint16_t* d, int64_t pitc
 }
 
 cudaError_t entropy_sum(const EntropyCall& c, const float* sums, uint32_t parts, const float* scale, void* grad_x) {
-    const int64_t n = c.T * c.I, blocks = (n + 2 * entropy::kSumThreads - 1) / (2 * entropy::kSumThreads);
-    if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    return launch(c.dtype == kBF16 ? entropy::sum_kernel<kBF16> : entropy::sum_kernel<kF16>, uint32_t(blocks), entropy::kSumThreads,
-                  c.stream, sums, scale, static_cast<uint16_t*>(grad_x), n, parts);
+    return sum_up(sums, parts, scale, grad_x, c.T * c.I, c.dtype, c.stream);
 }
 
 // [count,I] = d^T [count,T] . x [T,I].  Where grad_w's rows are whole sectors
@@ -179,11 +191,12 @@ cudaError_t entropy_grad_w(const EntropyCall& c, const uint16_t* d, int64_t pitc
     if (c.I % 16 == 0 && aligned(out, 32)) return row_product(p, scale, c.dtype, c.stream);
     TileArgs a;
     CUtensorMap mp, mq;
-    const cudaError_t e = lay_out(p, c.dtype, {true, pair_width(p.N, p.M, k_blocks(p, c.dtype), 128), 1}, a, mp, mq);
+    const int64_t kb = k_blocks(p, c.dtype);
+    const cudaError_t e = lay_out(p, c.dtype, {true, pair_width(p.N, p.M, kb, 128), sum_parts(kb)}, a, mp, mq);
     if (e != cudaSuccess) return e;
     a.end = {};
     a.end.scale = scale;
-    return launch_end<kEndSum, kBothMn>(a, c.dtype, pairs_of(a), mp, mq, c.stream);
+    return launch_tokens<kEndSum>(a, c.dtype, mp, mq, c.stream);
 }
 
 cudaError_t row_product(const Product& p, const float* scale, int dtype, cudaStream_t stream) {
@@ -192,11 +205,23 @@ cudaError_t row_product(const Product& p, const float* scale, int dtype, cudaStr
     t.e.y = p.e.y;
     TileArgs a;
     CUtensorMap mp, mq;
-    const cudaError_t e = lay_out(t, dtype, {true, pair_width(t.N, t.M, k_blocks(t, dtype), 128), 1}, a, mp, mq);
+    const int64_t kb = k_blocks(t, dtype);
+    const cudaError_t e = lay_out(t, dtype, {true, pair_width(t.N, t.M, kb, 128), sum_parts(kb)}, a, mp, mq);
     if (e != cudaSuccess) return e;
     a.end = {};
     a.end.scale = scale, a.end.pitch = p.N;
-    return launch_end<kEndRow, kBothMn>(a, dtype, pairs_of(a), mp, mq, stream);
+    return launch_tokens<kEndRow>(a, dtype, mp, mq, stream);
+}
+
+cudaError_t apart_product(const Product& p, float* sums, int dtype, cudaStream_t stream) {
+    TileArgs a;
+    CUtensorMap mp, mq;
+    cudaError_t e = lay_out(p, dtype, sum_plan(p.N, p.M, k_blocks(p, dtype), 128), a, mp, mq);
+    if (e != cudaSuccess) return e;
+    a.end = {};
+    a.end.sum_out = sums;
+    e = launch_end<kEndSum, kBothMn>(a, dtype, pairs_of(a, a.splits), mp, mq, stream);
+    return e == cudaSuccess ? sum_up(sums, a.splits, nullptr, p.e.y, p.M * p.N, dtype, stream) : e;
 }
 
 }  // namespace layer

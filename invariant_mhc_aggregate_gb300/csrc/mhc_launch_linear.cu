@@ -70,9 +70,12 @@ int64_t take_wait_timeouts() {
 }
 
 cudaError_t product(const Product& p, int in, int out, cudaStream_t stream) {
+    return product(p, plan_of(p.N, p.M, k_blocks(p, in), p.a_mn, p.by_row), in, out, stream);
+}
+
+cudaError_t product(const Product& p, const Plan& plan, int in, int out, cudaStream_t stream) {
     TileArgs a;
     CUtensorMap mp, mq;
-    const Plan plan = plan_of(p.N, p.M, k_blocks(p, in), p.a_mn, p.by_row);
     const cudaError_t e = lay_out(p, in, plan, a, mp, mq);
     if (e != cudaSuccess) return e;
     a.end = {};

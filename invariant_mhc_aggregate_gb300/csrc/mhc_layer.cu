@@ -432,14 +432,21 @@ mhc_status_t mhc_linear_bwd(const void* g, const void* x, const void* w, const v
     return finish(cudaSuccess);
 }
 
+// Bytes of the sums of a gated grad_w of few tiles and very many tokens.
+static int64_t token_sums_bytes(int64_t T, int64_t I, int64_t F) {
+    const int64_t kb = (T + 63) / 64;
+    if (!mhc::linear::token_apart(mhc::linear::token_plan(I, 2 * F, kb), kb)) return 0;
+    return round16(mhc::linear::sum_plan(I, 2 * F, kb, 128).splits * 2 * F * I * 4);
+}
+
 // The workspace of the gated backward: u with rows on 16-byte boundaries, the
-// operands laid out again, the column sums of the bias gradient.
+// operands laid out again, the sums of grad_w, the column sums of the bias gradient.
 static int64_t gated_bwd_workspace(int64_t T, int64_t I, int64_t F, int64_t x_stride, int64_t w_stride, bool want_x,
                                    bool want_w, bool want_bias, bool x_aligned, bool w_aligned) {
     const int64_t runs = mhc::layer::slope_partials(T);
     int64_t n = want_bias && runs > 1 ? round16(runs * 2 * F * 4) : 0;
     if (want_x || want_w) n += T * round16(2 * F) * 2;
-    if (want_w) n += Operand(nullptr, T, I, x_stride, 2, x_aligned).bytes();
+    if (want_w) n += Operand(nullptr, T, I, x_stride, 2, x_aligned).bytes() + token_sums_bytes(T, I, F);
     if (want_x) n += Operand(nullptr, 2 * F, I, w_stride, 2, w_aligned).bytes();
     return n;
 }
@@ -484,6 +491,9 @@ mhc_status_t mhc_gated_linear_bwd(const void* g, const void* x, const void* w, c
     int count = 0;
     if (want_w) xo.place(at, calls, count);
     if (want_x) wo.place(at, calls, count);
+    const int64_t sum_bytes = want_w ? token_sums_bytes(T, I, F) : 0;
+    float* sums = reinterpret_cast<float*>(at);
+    at += sum_bytes;
     float* partial = reinterpret_cast<float*>(at);
     cudaError_t e = lay_out_again(calls, count, stream);
     if (e != cudaSuccess) return finish(e);
@@ -510,7 +520,9 @@ mhc_status_t mhc_gated_linear_bwd(const void* g, const void* x, const void* w, c
         // 10.3 us, by rows 11.2), rows off 32 bytes with their values on the lanes (T = 193, 7352 -> 2 x 3307 70, by rows 94)
         const bool by_rows = I % 16 == 0 && aligned(grad_w, 32) &&
                              ((O + 255) / 256) * ((I + 255) / 256) >= mhc::linear::kPairsAtOnce;
-        e = by_rows ? mhc::layer::row_product(p, nullptr, dtype, cu(stream)) : mhc::layer::product(p, dtype, dtype, cu(stream));
+        if (by_rows) e = mhc::layer::row_product(p, nullptr, dtype, cu(stream));
+        else if (sum_bytes > 0) e = mhc::layer::apart_product(p, sums, dtype, cu(stream));
+        else e = mhc::layer::product(p, mhc::linear::token_plan(I, O, (T + 63) / 64), dtype, dtype, cu(stream));
         if (e != cudaSuccess) return finish(e);
     }
     return finish(cudaSuccess);

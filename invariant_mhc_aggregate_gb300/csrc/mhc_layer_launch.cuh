@@ -7,6 +7,7 @@
 
 #include "mhc_launch.cuh"
 #include "mhc_linear.cuh"
+#include "mhc_linear_plan.h"
 #include "mhc_norm.cuh"
 
 namespace mhc {
@@ -39,8 +40,9 @@ cudaError_t rotary(const RotaryCall& c);
 cudaError_t column_sum(const float* partial, float* out, uint32_t P, int64_t H, int64_t pitch, cudaStream_t stream);
 
 // Matrix product (mhc_launch_linear.cu).  in, out: kBF16, kF16; in also
-// kE4m3.  Every operand's rows start on 16-byte boundaries.
+// kE4m3.  Every operand's rows start on 16-byte boundaries.  plan: plan_of's, or another.
 cudaError_t product(const linear::Product& p, int in, int out, cudaStream_t stream);
+cudaError_t product(const linear::Product& p, const linear::Plan& plan, int in, int out, cudaStream_t stream);
 // An operand whose rows (`length` bytes, `stride` bytes apart) are copied to
 // rows of `pitch` bytes (a multiple of 16).
 struct RepackCall {
@@ -57,6 +59,8 @@ int64_t slope_partials(int64_t T);
 // p.e.y [M,N] = cvt(a^T b) (by *scale where scale is not null) with rows of both operands along m and n: a weight's
 // gradient, stored a row a thread (mhc_launch_entropy.cu).
 cudaError_t row_product(const linear::Product& p, const float* scale, int dtype, cudaStream_t stream);
+// The same from sums [parts,M,N] over sum_plan's parts of K, tiles of their own.
+cudaError_t apart_product(const linear::Product& p, float* sums, int dtype, cudaStream_t stream);
 
 // The gated product (mhc_launch_gated.cu): p.b is w [2 F, I], p.N = 2 F.
 cudaError_t gated_product(const linear::Product& p, int in, int out, cudaStream_t stream);

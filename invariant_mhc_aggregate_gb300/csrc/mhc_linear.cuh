@@ -560,8 +560,8 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = umma::cluster_rank();
     const uint32_t half = a.width / 2;
-    // with kEndSum the parts of K are tiles of their own, whose sums stay apart
-    constexpr bool kApart = END == kEndSum;
+    // with kEndSum the parts of K are tiles of their own, whose sums stay apart (but with PARTS)
+    constexpr bool kApart = END == kEndSum && !PARTS;
     const uint32_t of_a_part = a.p_tiles * a.q_tiles, tiles = kApart ? of_a_part * a.splits : of_a_part, step = gridDim.x / 2;
     auto first_part = [&](uint32_t i) { return kApart ? i / of_a_part : 0u; };
     auto last_part = [&](uint32_t i) { return kApart ? i / of_a_part + 1 : a.splits; };
@@ -660,6 +660,8 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
         const uint32_t quarter = warp % 4, mine = a.width / 4, c0 = warp / 4 * mine;   // its columns: c0 .. c0 + mine
         const uint32_t tw = tmem + (quarter * 32u << 16) + c0;
         const uint32_t signal = umma::map_rank(bar_free, 0);
+        // a chunk of the warp's columns (by rows every fourth run of 16 is its group's: row_tile reads what the warp has summed)
+        auto column = [&](uint32_t c) { return END == kEndRow ? tw - c0 + c / 16 * 64 + warp / 4 * 16 + c % 16 : tw + c; };
         // a gated group's warps meet in every chunk of every tile: after a wait that ran out they go on without waits
         constexpr bool kTogether = END == kEndGated;
         Scale scale = {1.0f, 1.0f};
@@ -717,14 +719,14 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
 #pragma unroll 2
                 for (uint32_t c = 0; c < mine; c += kChunk) {
                     float v[kChunk], w[kChunk];
-                    umma::tmem_ld(tw + c, v);
-                    umma::tmem_ld(tw + 256 + c, w);
+                    umma::tmem_ld(column(c), v);
+                    umma::tmem_ld(column(c) + 256, w);
                     umma::tmem_wait_ld(v);
                     umma::tmem_wait_ld(w);
                     // (the second part arrives where the sum goes)
 #pragma unroll
                     for (int i = 0; i < kChunk; ++i) v[i] = __fadd_rn(v[i], w[i]);
-                    umma::tmem_st(tw + 256 + c, v);
+                    umma::tmem_st(column(c) + 256, v);
                 }
                 umma::tmem_wait_st();
                 umma::fence_before_sync();

@@ -137,17 +137,25 @@ inline int64_t entropy_piece(int64_t T, int64_t V) {
     return ((V + pieces - 1) / pieces + 63) / 64 * 64;
 }
 
-// A gradient summed over `kb` blocks of K (a piece of a vocabulary), [M,N]:
-// pairs of CTAs, tiles of `width` rows, and parts of K that are tiles of their
-// own, so that few tiles fill the GPU; none longer than 256 blocks (16384
-// terms), since the tensor cores' sums cut off bits.  The cheapest by plan_of's
-// estimate of a round; joining parts costs their sums' way through memory.
-inline Plan sum_plan(int64_t N, int64_t M, int64_t kb) {
+// The most blocks of K that one accumulator sums where K is tokens or a
+// vocabulary (16384 of them): the tensor cores cut off each addition's last
+// bits, so that a sum of terms of one sign falls short by a part that grows with
+// them (65536 tokens in one accumulator 1.7e-4, 1048576 6.5e-3, in runs of this
+// length 1.4e-5 both).  The runs are added up in FP32, rounded to nearest.
+constexpr int64_t kSumBlocks = 256;
+
+inline uint32_t sum_parts(int64_t kb) { return uint32_t((kb + kSumBlocks - 1) / kSumBlocks); }
+
+// A gradient summed over `kb` blocks of K, [M,N]: pairs of CTAs, tiles of `width`
+// rows (a multiple of `step`), and parts of K that are tiles of their own, so
+// that few tiles fill the GPU.  The cheapest by plan_of's estimate of a round;
+// joining parts costs their sums' way through memory.
+inline Plan sum_plan(int64_t N, int64_t M, int64_t kb, int64_t step = 32) {
     Plan best = {true, 128, 1};
     int64_t least = INT64_MAX;
-    for (int64_t parts = (kb + 255) / 256; parts == (kb + 255) / 256 || (parts <= 32 && kb >= 4 * parts); ++parts) {
+    for (int64_t parts = sum_parts(kb); parts == sum_parts(kb) || (parts <= 32 && kb >= 4 * parts); ++parts) {
         const int64_t join = parts > 1 ? 4000 + parts * M * N * 8 / 3000 : 0, blocks = (kb + parts - 1) / parts;
-        for (int64_t w = 128; w <= 256; w += 32) {
+        for (int64_t w = 128; w <= 256; w += step) {
             const int64_t rounds = ((N + 255) / 256 * ((M + w - 1) / w) * parts + kPairsAtOnce - 1) / kPairsAtOnce;
             const int64_t block = 41 * w / 20 > 300 ? 41 * w / 20 : 300;
             const int64_t cost = 6000 + 21 * w + rounds * (blocks * block + 1500) + join;
@@ -156,6 +164,20 @@ inline Plan sum_plan(int64_t N, int64_t M, int64_t kb) {
     }
     return best;
 }
+
+// A gated product's grad_w [M,N] over `kb` blocks of tokens: the product's plan,
+// with pair_kernel's tiles summed in parts one after the other.  Few tiles go to
+// split_kernel, whose parts are a cluster's CTAs; where there are more tokens than
+// those sum (token_apart), the parts are tiles of their own (sum_plan).  Whole
+// backward, long runs and these: T = 65536, 1024 -> 2 x 2816 1431 and 1434 us; T = 300000,
+// 256 -> 2 x 100 500 and 436; T = 65536, 1279 -> 2 x 1365 1003 and 899.
+inline Plan token_plan(int64_t N, int64_t M, int64_t kb) {
+    Plan p = plan_of(N, M, kb, true, false);
+    if (p.pair) p.splits = sum_parts(kb);
+    return p;
+}
+
+inline bool token_apart(const Plan& p, int64_t kb) { return !p.pair && kb > kSumBlocks * p.splits; }
 
 }  // namespace linear
 }  // namespace mhc

@@ -48,3 +48,40 @@ def test_pieces_are_legal(tmp_path):
 def test_grad_w_by_rows_has_its_tiles():
     for T, I, F in _ends.BY_ROWS:
         assert I % 16 == 0 and -(-2 * F // 256) * -(-I // 256) >= 76
+
+
+TOKENS = """
+#include <cstdio>
+#include "mhc_linear_plan.h"
+int main() {
+    long long N, M, kb;
+    while (std::scanf("%lld %lld %lld", &N, &M, &kb) == 3) {
+        using namespace mhc::linear;
+        const Plan t = token_plan(N, M, kb), p = plan_of(N, M, kb, true, false), s = sum_plan(N, M, kb, 128);
+        std::printf("%d %u %u %d %d %u %u %u %u\\n", int(t.pair), t.width, t.splits, int(token_apart(t, kb)), int(p.pair), p.width, p.splits,
+                    s.width, s.splits);
+    }
+}
+"""
+
+
+def test_sums_over_tokens(tmp_path):
+    """No accumulator of a gated grad_w takes more than 256 blocks; up to there the plan is the product's."""
+    (tmp_path / "tokens.cpp").write_text(TOKENS)
+    exe = str(tmp_path / "tokens")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", _build.CSRC, "-o", exe, str(tmp_path / "tokens.cpp")], check=True)
+    cases = [(N, M, kb) for N in (1, 16, 264, 600, 1000, 1279, 2048, 7168) for M in (2, 48, 320, 1040, 3000, 4200, 28672)
+             for kb in (1, 63, 255, 256, 257, 512, 513, 1024, 2048, 2049, 16384, 65537)]
+    text = "".join("%d %d %d\n" % c for c in cases)
+    out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.split("\n")
+    ways = set()
+    for (N, M, kb), line in zip(cases, out):
+        pair, width, parts, apart, p_pair, p_width, p_parts, s_width, s_parts = (int(v) for v in line.split())
+        assert (pair, width) == (p_pair, p_width)
+        if kb <= 256:
+            assert parts == p_parts and not apart
+        run = -(-kb // (s_parts if apart else parts))
+        assert run <= 256 and not (apart and pair)
+        assert s_width in (128, 256)                 # (an operand's rows along its columns come in panels of 64, two a tile)
+        ways.add((pair, apart, parts > 1))
+    assert ways >= {(1, 0, False), (1, 0, True), (0, 0, True), (0, 1, True)}
