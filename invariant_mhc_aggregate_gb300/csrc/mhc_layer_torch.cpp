@@ -13,6 +13,7 @@
 #include <c10/core/DeviceGuard.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/Exception.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "mhc_layer.h"
@@ -90,11 +91,15 @@ PyObject* pack(std::initializer_list<const at::Tensor*> list) {
     return out;
 }
 
-// No C++ exception leaves a function that the interpreter called.
+// No C++ exception leaves a function that the interpreter called.  Where memory
+// runs out the call is declined: layer.py's own allocation then raises torch's
+// error for that, which a caller may catch (or succeeds).
 template <class F>
 PyObject* guarded(F f) {
     try {
         return f();
+    } catch (const c10::OutOfMemoryError&) {
+        return none();
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
         return nullptr;
