@@ -5,12 +5,13 @@
 #pragma once
 
 #include "mhc_linear.cuh"
+#include "mhc_linear_plan.h"
 
 namespace mhc {
 namespace entropy {
 
 // lse and loss from the units' pairs: THREADS threads a token (a warp, or a
-// block where a token has more groups than 256), thread i takes the groups i,
+// block where a token has more groups than kJoinGroups), thread i takes the groups i,
 // i + THREADS, ... one after the other, a group's units in increasing order,
 // then the threads' pairs meet in a tree; the order depends on V alone.
 // Bound by the loads' latency where tokens are few (T = 8, V = 32768 6.1 us by
@@ -19,6 +20,7 @@ namespace entropy {
 // 102.7), by HBM where they are many (T = 4096, V =
 // 32768 13.3 us, cold).
 constexpr int kJoinThreads = 256;
+constexpr int kJoinGroups = 256;   // of a token that a warp joins; a block where there are more
 constexpr int kJoinBatch = 4;   // groups of a thread whose loads are under way together
 
 // Thread i's groups, of at most MOST units, and the threads' together (THREADS
@@ -84,14 +86,15 @@ join_kernel(const float2* __restrict__ partial, const float* __restrict__ at, co
 // so four entries a thread are under way at a time (one: T = 1, 7168 x 4096 21.4 us of
 // the whole, four 18.8).
 constexpr int kApartBatch = 4;   // entries of a thread whose loads are under way together
+constexpr int kApartUnits = 2;   // of a group: so few entries are in groups of 32, at most as many as one warp joins in join_kernel
+static_assert(linear::kApartEntries < linear::kWideGroups && linear::kApartEntries <= 32 * kJoinGroups);
 
 template <int THREADS>
 static __global__ void __launch_bounds__(THREADS)
 apart_join_kernel(const float* __restrict__ sums, const int64_t* __restrict__ target, float* __restrict__ loss,
-                  float* __restrict__ lse, int64_t T, int64_t V, uint32_t runs, uint32_t of_a_group) {
+                  float* __restrict__ lse, int64_t T, int64_t V, uint32_t runs) {
     pdl_enter();
     extern __shared__ float2 pairs[];
-    __shared__ float2 part[kJoinThreads / 32];
     __shared__ float at;
     const int64_t t = blockIdx.x, units = (V + linear::kEntropyUnit - 1) / linear::kEntropyUnit;
     const int64_t entry = target[t];
@@ -117,11 +120,8 @@ apart_join_kernel(const float* __restrict__ sums, const int64_t* __restrict__ ta
         }
     }
     __syncthreads();
-    const bool wide = (units + of_a_group - 1) / of_a_group > kJoinThreads;
-    if (threadIdx.x >= (wide ? kJoinThreads : 32)) return;
-    auto load = [&](int64_t u) { return pairs[u]; };
-    const float2 of = wide ? join_units<kJoinThreads, 4>(load, units, of_a_group, threadIdx.x, part)
-                           : join_units<32, 4>(load, units, of_a_group, threadIdx.x, part);
+    if (threadIdx.x >= 32) return;
+    const float2 of = join_units<32, kApartUnits>([&](int64_t u) { return pairs[u]; }, units, kApartUnits, threadIdx.x, nullptr);
     if (threadIdx.x == 0) {
         const float all = __fadd_rn(linear::reference(of.x), logf(of.y));
         lse[t] = all;

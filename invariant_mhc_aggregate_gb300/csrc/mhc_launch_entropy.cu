@@ -42,12 +42,6 @@ uint32_t pair_width(int64_t N, int64_t M, int64_t kb, int64_t step) {
     return best;
 }
 
-// Entries of the vocabulary that are summed together before the join: they
-// follow from V alone, so that a token's loss has the same bits in every
-// batch: 64, and 32 where tiles of 64 a thread would leave SMs without one.
-// With few tokens few_kernel writes their units of 16.
-int64_t entropy_group(int64_t V) { return V >= 256 * kPairsAtOnce ? 64 : 32; }
-
 }  // namespace
 
 int64_t entropy_pairs(int64_t T, int64_t V) {
@@ -79,7 +73,7 @@ cudaError_t entropy_fwd_apart(const EntropyCall& c, float* loss, float* lse, flo
     const uint32_t runs = entropy_runs((c.I + 63) / 64);
     const cudaError_t e = apart_sums(c, runs, sums);
     if (e != cudaSuccess) return e;
-    const int64_t units = (c.V + kEntropyUnit - 1) / kEntropyUnit, group = entropy_group(c.V);
+    const int64_t units = (c.V + kEntropyUnit - 1) / kEntropyUnit;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(uint32_t(c.T));
     // more tokens than SMs have few entries each (T = 256, V = 1024 13.0 us with 1024 threads, 11.5 with 256)
@@ -92,7 +86,7 @@ cudaError_t entropy_fwd_apart(const EntropyCall& c, float* loss, float* lse, flo
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, wide ? entropy::apart_join_kernel<1024> : entropy::apart_join_kernel<256>, sums, c.target, loss, lse, c.T, c.V, runs, uint32_t(group / kEntropyUnit));
+    return cudaLaunchKernelEx(&cfg, wide ? entropy::apart_join_kernel<1024> : entropy::apart_join_kernel<256>, sums, c.target, loss, lse, c.T, c.V, runs);
 }
 
 cudaError_t entropy_fwd(const EntropyCall& c, float* loss, float* lse, float2* partial, float* at) {
@@ -115,7 +109,7 @@ cudaError_t entropy_fwd(const EntropyCall& c, float* loss, float* lse, float2* p
     e = few ? launch_few<false, kBF16, kEndEntropy>(a, mp, mq, c.stream)
             : launch_pair_kernel(pair_kernel<false, kBF16, kBothK, false, kEndEntropy>, allowed, a, pairs_of(a), mp, mq, c.stream);
     if (e != cudaSuccess) return e;
-    const bool wide = groups > 256;
+    const bool wide = groups > entropy::kJoinGroups;
     const int64_t per_block = wide ? 1 : entropy::kJoinThreads / 32;
     constexpr int kWide = entropy::kJoinThreads;
     auto* join = few ? (wide ? entropy::join_kernel<kWide, 4> : entropy::join_kernel<32, 4>)

@@ -93,10 +93,20 @@ inline uint32_t few_lanes(int64_t N) {
 // them the two are even (V = 8192: T = 1, I = 4096 20.1, 20.3; T = 64 25.0, 20.9).
 constexpr uint32_t kEntropyRun = 16;
 
+// Entries of the vocabulary that are summed together before the join: they
+// follow from V alone, so that a token's loss has the same bits in every
+// batch: 64, and 32 where tiles of 64 a thread would leave SMs without one.
+// With few tokens few_kernel writes their units of 16.
+constexpr int64_t kWideGroups = 256 * kPairsAtOnce;   // the smallest vocabulary with 64
+
+inline int64_t entropy_group(int64_t V) { return V >= kWideGroups ? 64 : 32; }
+
+constexpr int64_t kApartEntries = 8192;   // the largest vocabulary whose runs are tiles of their own
+
 inline uint32_t entropy_runs(int64_t kb) { return uint32_t((kb + kEntropyRun - 1) / kEntropyRun); }
 
 inline bool entropy_apart(int64_t T, int64_t V, int64_t kb) {
-    return kb > kEntropyRun && V <= 8192 && T <= 512 && T * V <= int64_t(1) << 19;
+    return kb > kEntropyRun && V <= kApartEntries && T <= 512 && T * V <= int64_t(1) << 19;
 }
 
 // few_kernel's lanes for such tiles, and pair_kernel's width (of tokens): the cheapest
