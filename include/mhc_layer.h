@@ -223,8 +223,8 @@ MHC_API int64_t mhc_gated_linear_bwd_workspace(int64_t T, int64_t I, int64_t F, 
 
 /* ---- Cross entropy over a vocabulary -------------------------------------------
  *
- * The cross entropy of the logits z = x w^T with a target each, which are
- * never stored:
+ * The cross entropy of the logits z = x w^T with a target each, which are no
+ * output and not kept for the gradients (those compute them again):
  *
  *   z[t,v]  = sum over i of x[t,i] * w[v,i]                       (FP32)
  *   lse[t]  = log( sum over v of exp(z[t,v]) )
@@ -234,7 +234,10 @@ MHC_API int64_t mhc_gated_linear_bwd_workspace(int64_t T, int64_t I, int64_t F, 
  * int64 [T]; loss and lse FP32 [T].  A token whose target is outside 0 .. V-1
  * (negative, as -100, by custom) is ignored: its loss is 0; its lse is
  * computed all the same.  workspace:
- * mhc_linear_cross_entropy_workspace(...) bytes, 16-byte aligned.
+ * mhc_linear_cross_entropy_workspace(...) bytes, 16-byte aligned: 8 bytes for
+ * every 16 to 64 logits, or, with at most 8192 entries, 512 tokens and 2^19
+ * logits of more than 1024 products each, their FP32 sums over runs of 1024
+ * products (at most 1.4 of the operands' bytes).
  */
 MHC_API mhc_status_t mhc_linear_cross_entropy_fwd(const void* x, const void* w,
                                                   const int64_t* target, float* loss, float* lse,
@@ -255,7 +258,8 @@ MHC_API int64_t mhc_linear_cross_entropy_workspace(int64_t T, int64_t I, int64_t
  *   grad_x[t,i] = cvt( sum over v of cvt(d[t,v]) * w[v,i] )       [T,I]
  *   grad_w[v,i] = cvt( sum over t of cvt(d[t,v]) * x[t,i] )       [V,I]
  *
- * The logits are computed again, by pieces of the vocabulary; cvt(d) is d
+ * The logits are computed again and d is in the workspace by pieces of the
+ * vocabulary (whole with at most 2^27 values, 256 MB); cvt(d) is d
  * rounded to the operands' type after a scaling (one for the whole call, a
  * power of two over the largest |g|, taken out again in FP32), so that
  * binary16 holds small probabilities and a g that all tokens share, as that of

@@ -396,7 +396,7 @@ def gated_linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | Non
 
 class LinearCrossEntropy(torch.autograd.Function):
     """(loss, lse) of the logits x weight^T and their targets; the logits are
-    stored in neither direction, the backward computes them again."""
+    not kept, the backward computes them again."""
 
     @staticmethod
     def forward(ctx, x, weight, target):

@@ -552,11 +552,12 @@ def gated_linear_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.T
 # ---------------------------------------------------------------------------
 
 def linear_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, stream=None):
-    """(loss, lse), FP32 [T], of the logits x weight^T, which are never stored:
-    lse their logsumexp, loss = lse - logit of the target.  x [T,I] and weight
-    [V,I], both bf16 or both f16, with any row stride; target int64 [T].  A
-    token whose target is outside 0 .. V-1 (-100, by custom) is ignored: loss
-    0.  The mean over the others is the caller's division by their number."""
+    """(loss, lse), FP32 [T], of the logits x weight^T, which are not kept (sums
+    of a small vocabulary's pass through the workspace): lse their logsumexp,
+    loss = lse - logit of the target.  x [T,I] and weight [V,I], both bf16 or
+    both f16, with any row stride; target int64 [T].  A token whose target is
+    outside 0 .. V-1 (-100, by custom) is ignored: loss 0.  The mean over the
+    others is the caller's division by their number."""
     if stream is None:
         out = (_fast or _compiled()).linear_cross_entropy(x, weight, target)
         if out is not None:
@@ -582,8 +583,9 @@ def linear_cross_entropy_backward(grad_loss: torch.Tensor | None, x: torch.Tenso
                                   want=(True, True), stream=None):
     """(grad_x, grad_weight) of linear_cross_entropy, from the gradients of loss
     and lse (FP32 [T]; either may be None) and the forward's lse; `want` says
-    which of the two to compute.  The logits are computed again by pieces of
-    the vocabulary; both products read their gradient rounded to the storage
+    which of the two to compute.  The logits are computed again and their
+    gradient is in the workspace by pieces of the vocabulary (whole up to 2^27
+    values, 256 MB); both products read their gradient rounded to the storage
     type (after a scaling, so that f16 holds small probabilities and a gradient
     that all tokens share, as that of a mean, is not rounded)."""
     if stream is None:

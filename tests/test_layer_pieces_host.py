@@ -3,7 +3,7 @@
 import subprocess
 
 import _ends
-from invariant_mhc_aggregate_gb300 import _build
+from invariant_mhc_aggregate_gb300 import _build, layer
 
 PROGRAM = """
 #include <cstdio>
@@ -85,3 +85,22 @@ def test_sums_over_tokens(tmp_path):
         assert s_width in (128, 256)                 # (an operand's rows along its columns come in panels of 64, two a tile)
         ways.add((pair, apart, parts > 1))
     assert ways >= {(1, 0, False), (1, 0, True), (0, 0, True), (0, 1, True)}
+
+
+def test_workspaces_are_what_the_header_says():
+    """8 bytes for 16 to 64 logits, or a small vocabulary's sums; d whole up to 2^27 values, else a piece of it."""
+    _build.build_layer()
+    lib = layer.load()
+    for T in (1, 64, 65, 512, 513, 4096, 100000):
+        for V in (1, 100, 1024, 8192, 8193, 19456, 131072):
+            for I in (64, 1024, 1088, 2048, 7168, 1 << 20):
+                n = lib.mhc_linear_cross_entropy_workspace(T, I, V, I, I, 1)
+                if V <= 8192 and T <= 512 and T * V <= 1 << 19 and I > 1024:
+                    # T V / (T + V) is at most 512 / 1.5, and there are at most I / 1024 + 1 runs
+                    assert n <= 1.4 * 2 * I * (T + V) + 16 and 4 * T * V * -(-I // 1024) <= n <= 4 * T * V * -(-I // 1024) + 16
+                else:
+                    assert n <= 8 * T * -(-V // 16) + 4 * T + 16 and (T <= 64 or n <= 8 * T * -(-V // 32) + 4 * T + 16)
+                d = lib.mhc_linear_cross_entropy_bwd_workspace(T, I, V, I, I, 0, 1, 1)
+                whole = 2 * T * (V + 63)
+                assert d <= max(whole, 4 * T * V * -(-I // 1024) + whole if T * V <= 1 << 19 else 0) + 64
+                assert T * V <= 1 << 27 or d < 2 * T * V
