@@ -90,6 +90,7 @@ few_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUten
     }
     if (warp == kReaders) {
         umma::tmem_alloc<1>(&tmem_base, kColumns);
+        umma::tmem_relinquish<1>();
         if (lane == 0) {
             umma::prefetch_map(&mp);
             umma::prefetch_map(&mq);

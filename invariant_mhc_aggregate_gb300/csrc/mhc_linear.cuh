@@ -344,6 +344,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
     }
     if (warp == kSplitCopy) {
         umma::tmem_alloc<1>(&tmem_base, columns);
+        umma::tmem_relinquish<1>();
         if (lane == 0) {
             umma::prefetch_map(&mp);
             umma::prefetch_map(&mq);
@@ -585,8 +586,9 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
     }
     umma::fence_before_sync();
     __syncthreads();
-    umma::cluster_sync();   // the other CTA's barriers are ready too
+    umma::cluster_sync();   // the other CTA's barriers are ready too, and its tensor memory
     umma::fence_after_sync();
+    if (warp == kCopyP) umma::tmem_relinquish<2>();
     const uint32_t tmem = tmem_base;
     pdl_enter();
     const uint32_t ring = smem_addr(stages), bar_full = smem_addr(full), bar_empty = smem_addr(empty);

@@ -25,9 +25,7 @@ __device__ __forceinline__ float exp_fast(float x) {
 // value's activation is evaluated once, and a warp stores 64 contiguous bytes.
 // T = 4096, 7168 -> 2 x 14336 880 us in short runs (1910 TFLOP/s; the tensor
 // cores), with z 4096 -> 2 x 7168 271 us.  (Gate and up rows in turn on the
-// lanes by small boxes of a 3-D map, paired by shuffles, were as fast, but one
-// call in some 30000 of T = 7550, 3823 -> 2 x 136 never ended, for a reason that
-// was not found; 300000 of these do.)
+// lanes by small boxes of a 3-D map, paired by shuffles, were as fast.)
 // --------------------------------------------------------------------------
 constexpr uint32_t kExchange = 8 * kLanesP * 4;   // bytes of a group
 

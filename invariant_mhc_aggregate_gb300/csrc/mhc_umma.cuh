@@ -41,19 +41,27 @@ constexpr uint32_t instr_desc(uint32_t format, bool a_mn, bool b_mn, uint32_t M,
 // warp of both CTAs.
 template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t columns) {
-    if constexpr (CG == 1) {
+    if constexpr (CG == 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      :
                      : "r"(smem_addr(dst)), "r"(columns)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    } else {
+    else
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
                      :
                      : "r"(smem_addr(dst)), "r"(columns)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-    }
+}
+
+// The right to allocate, given up by the same warps.  With CG = 2 one CTA's word
+// goes for the pair, so both have to have allocated (a cluster_sync between): a
+// peer that came to its allocation after it never got through, and no limit
+// bounds that wait.  One launch in some tens of thousands behind blocks that were
+// still running on one of the two SMs ended so.
+template <int CG>
+__device__ __forceinline__ void tmem_relinquish() {
+    if constexpr (CG == 1) asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    else asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
 
 template <int CG>

@@ -97,3 +97,19 @@ def test_gated_grad_w_at_any_alignment(offset, dtype):
     want, size = u.t() @ x.double(), u.abs().t() @ x.double().abs()
     off = (out.double() - want).abs()
     assert (off <= sums(T, size) + coarse.t() @ x.double().abs() + U[dtype] * want.abs() + TINY[dtype]).all()
+
+
+def test_pairs_behind_blocks_that_still_run():
+    """Thousands of calls without a pause: the logits' gradients' CTA pairs start on SMs where blocks of the launch before them
+    are still running, so that the two CTAs of a pair start apart.  Every call ends, with the same bytes."""
+    T, I, V = 513, 1279, 32003                # (rows off 16 bytes: that launch lays them out again)
+    x, w, target, _, _ = case(T, I, V, HF)
+    target[::3] = -100
+    _, lse = layer.linear_cross_entropy(x, w, target)
+    gl = torch.full((T,), 0.25, device="cuda")
+    want = layer.linear_cross_entropy_backward(gl, x, w, target, lse)
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for _ in range(2000):
+            got = layer.linear_cross_entropy_backward(gl, x, w, target, lse)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

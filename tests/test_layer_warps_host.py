@@ -92,3 +92,15 @@ def test_tensor_memory_is_read_and_written_by_whole_warps():
                 else:
                     together = t.group(2) is not None
     assert functions == 9 and places > 40
+
+
+def test_a_pair_gives_up_its_right_to_allocate_after_both_have():
+    """One CTA's relinquish_alloc_permit.cta_group::2 goes for the pair: the peer's allocation has to be behind it, or it never
+    ends (no limit bounds it).  Between the two stands a barrier of the cluster."""
+    code = "".join(SOURCES.values())
+    alloc, _ = body(code, code.index("void tmem_alloc("))
+    assert "relinquish" not in alloc
+    assert code.count("tmem_alloc<2>(") == 1 and code.count("tmem_relinquish<2>(") == 1 and code.count("tmem_relinquish<1>(") == 2
+    text, _ = body(SOURCES["mhc_linear.cuh"], SOURCES["mhc_linear.cuh"].index("pair_kernel("))
+    first, then, last = (text.index(t) for t in ("tmem_alloc<2>(", "umma::cluster_sync();", "if (warp == kCopyP) umma::tmem_relinquish<2>();"))
+    assert first < then < last < text.index("pdl_enter();")
