@@ -577,6 +577,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
         }
         mbar_init_fence();
     }
+    umma::cluster_sync();   // both CTAs run, and their barriers are ready
     if (warp == kCopyP) {
         umma::tmem_alloc<2>(&tmem_base, kTmemColumns);
         if (lane == 0) {
@@ -586,7 +587,7 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
     }
     umma::fence_before_sync();
     __syncthreads();
-    umma::cluster_sync();   // the other CTA's barriers are ready too, and its tensor memory
+    umma::cluster_sync();   // the other CTA's tensor memory is there too
     umma::fence_after_sync();
     if (warp == kCopyP) umma::tmem_relinquish<2>();
     const uint32_t tmem = tmem_base;
@@ -762,9 +763,10 @@ pair_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUte
         umma::fence_before_sync();
     }
     __syncwarp();
-    umma::cluster_sync();   // neither CTA leaves while the other may still signal it
+    umma::cluster_sync();   // neither CTA's memory is signalled, read or written by the other any more
     umma::fence_after_sync();
     if (warp == kCopyP) umma::tmem_free<2>(tmem, kTmemColumns);
+    umma::cluster_sync();   // neither leaves before both have freed
 }
 
 // Rows of values copied to a row pitch that starts every row on 16 bytes, for

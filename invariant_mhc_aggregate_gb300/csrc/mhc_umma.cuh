@@ -38,7 +38,12 @@ constexpr uint32_t instr_desc(uint32_t format, bool a_mn, bool b_mn, uint32_t M,
 // --------------------------------------------------------------------------
 
 // Whole warp; columns a power of two of at least 32.  With CG = 2 the same
-// warp of both CTAs.
+// warp of both CTAs, and only while both run: the instruction works on both SMs.
+// A CTA whose peer's had gone through before it had started (by 450 ns; 30 is
+// usual) never came out of its own, and no limit bounds that wait: one launch in
+// some tens of thousands where blocks of the launch before still kept one of the
+// SMs busy.  So a cluster_sync stands before the allocation, and one after the
+// freeing, before either CTA leaves.
 template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t columns) {
     if constexpr (CG == 1)
@@ -53,11 +58,8 @@ __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t columns) {
                      : "memory");
 }
 
-// The right to allocate, given up by the same warps.  With CG = 2 one CTA's word
-// goes for the pair, so both have to have allocated (a cluster_sync between): a
-// peer that came to its allocation after it never got through, and no limit
-// bounds that wait.  One launch in some tens of thousands behind blocks that were
-// still running on one of the two SMs ended so.
+// The right to allocate, given up by the same warps; with CG = 2 one CTA's word
+// goes for the pair, so both have to have allocated (a cluster_sync between).
 template <int CG>
 __device__ __forceinline__ void tmem_relinquish() {
     if constexpr (CG == 1) asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -280,10 +282,12 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" : : "r"(bar) : "memory");
 }
 
-// Every thread of every CTA of the cluster.
+// Every thread of every CTA of the cluster; a warp's lanes come to it and leave it together.
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    __syncwarp();
 }
 
 }  // namespace umma

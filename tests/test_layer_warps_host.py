@@ -102,5 +102,19 @@ def test_a_pair_gives_up_its_right_to_allocate_after_both_have():
     assert "relinquish" not in alloc
     assert code.count("tmem_alloc<2>(") == 1 and code.count("tmem_relinquish<2>(") == 1 and code.count("tmem_relinquish<1>(") == 2
     text, _ = body(SOURCES["mhc_linear.cuh"], SOURCES["mhc_linear.cuh"].index("pair_kernel("))
-    first, then, last = (text.index(t) for t in ("tmem_alloc<2>(", "umma::cluster_sync();", "if (warp == kCopyP) umma::tmem_relinquish<2>();"))
-    assert first < then < last < text.index("pdl_enter();")
+    first, last = (text.index(t) for t in ("tmem_alloc<2>(", "if (warp == kCopyP) umma::tmem_relinquish<2>();"))
+    assert first < text.index("umma::cluster_sync();", first) < last < text.index("pdl_enter();")
+
+
+def test_a_pairs_tensor_memory_is_allocated_and_freed_while_both_ctas_run():
+    """tcgen05.alloc and dealloc of cta_group::2 work on both SMs: the kernel's first barrier of the cluster stands before the
+    one, and its last after the other."""
+    code = SOURCES["mhc_linear.cuh"]
+    text, _ = body(code, code.index("pair_kernel("))
+    assert len(re.findall(r"tmem_free<2>\(|tmem_alloc<2>\(", "".join(SOURCES.values()))) == 2
+    first = text.index("umma::cluster_sync();")
+    assert first < text.index("tmem_alloc<2>(") < text.index("umma::cluster_sync();", first + 1) < text.index("pdl_enter();")
+    assert re.search(r"umma::cluster_sync\(\);\s*umma::fence_after_sync\(\);\s*if \(warp == kCopyP\) umma::tmem_free<2>\(tmem, kTmemColumns\);"
+                     r"\s*umma::cluster_sync\(\);\s*$", text)
+    # whole warps at the barrier, and behind it
+    assert re.search(r"void cluster_sync\(\) \{\s*__syncwarp\(\);[^}]*__syncwarp\(\);\s*\}", SOURCES["mhc_umma.cuh"])
