@@ -477,7 +477,7 @@ split_kernel(const __grid_constant__ CUtensorMap mp, const __grid_constant__ CUt
 // the first one holds every other part.  (Sums in registers instead, 64 or
 // 128 columns a thread, spilled: T = 4096, 7168 x 7168 269 to 330 us.)  Bound by
 // the tensor cores and their power: T = 4096, 7168 x 7168 225 us (1870 TFLOP/s)
-// in short runs, with bias, gelu and residual 278 us in long ones.
+// in short runs, with bias, gelu and residual 254 to 259 us in long ones.
 //
 // Warps 0-15 read tensor memory (four warps for each quarter of the lanes, a
 // quarter of the columns each).  Warp 16 copies P, warp 18 copies Q (a block of K

@@ -23,8 +23,9 @@ __device__ __forceinline__ float exp_fast(float x) {
 // are).  The four warps of a group, which hold the lanes of the same columns,
 // put 8 columns of z in shared memory at a time and take it out by pairs: every
 // value's activation is evaluated once, and a warp stores 64 contiguous bytes.
-// T = 4096, 7168 -> 2 x 14336 880 us in short runs (1910 TFLOP/s; the tensor
-// cores), with z 4096 -> 2 x 7168 271 us.  (Gate and up rows in turn on the
+// T = 4096, 7168 -> 2 x 14336 870 to 910 us in short runs (1850 to 1940 TFLOP/s; the
+// tensor cores), 998 in calls one after the other; with z 4096 -> 2 x 7168 261 to 301
+// and 296 us; E4M3 454 and 461 to 469 us.  (Gate and up rows in turn on the
 // lanes by small boxes of a 3-D map, paired by shuffles, were as fast.)
 // --------------------------------------------------------------------------
 constexpr uint32_t kExchange = 8 * kLanesP * 4;   // bytes of a group
@@ -327,8 +328,9 @@ __device__ __forceinline__ void row_tile(const TileArgs& a, const RowHead& h, ui
 // logits' bytes in 16 bits.  A unit of 16 entries has a maximum and a sum of its
 // own, units are joined in increasing order, so that few_kernel, with the
 // vocabulary on the lanes, has the same sums in the same order.  Under the
-// multiplications of the next tile: T = 4096, I = 7168, 65536 entries 1.95 ms in
-// short runs (1970 TFLOP/s), bound by the tensor cores and their power.
+// multiplications of the next tile: T = 4096, I = 7168, 65536 entries 1.91 to
+// 2.05 ms in short runs (1880 to 2010 TFLOP/s), 2.20 in calls one after the
+// other, bound by the tensor cores and their power.
 // --------------------------------------------------------------------------
 constexpr int kEntropyUnit = 16;
 
