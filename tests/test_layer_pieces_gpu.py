@@ -72,6 +72,12 @@ def test_gated_grad_w_by_rows(T, I, F, act, dtype):
 
 
 @pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("T,I,F", [c[:3] for c in _ends.RUNS])
+def test_gated_grad_w_of_runs_of_tokens(T, I, F, dtype):
+    check_gated_backward(T, I, F, "silu", dtype)
+
+
+@pytest.mark.parametrize("dtype", BOTH)
 @pytest.mark.parametrize("offset", [0, 16, 2])
 def test_gated_grad_w_at_any_alignment(offset, dtype):
     """By rows on 32 bytes, with its values on the lanes elsewhere; nothing beside it is written."""

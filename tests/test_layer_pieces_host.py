@@ -85,6 +85,11 @@ def test_sums_over_tokens(tmp_path):
         assert s_width in (128, 256)                 # (an operand's rows along its columns come in panels of 64, two a tile)
         ways.add((pair, apart, parts > 1))
     assert ways >= {(1, 0, False), (1, 0, True), (0, 0, True), (0, 1, True)}
+    cases = [(I, 2 * F, -(-T // 64)) for T, I, F, _ in _ends.RUNS]
+    out = subprocess.run([exe], input="".join("%d %d %d\n" % c for c in cases), capture_output=True, text=True, check=True).stdout.split("\n")
+    got = [tuple(int(v) for v in line.split()) for line in out if line]
+    assert ["apart" if g[3] else "pair" if g[0] and g[2] > 1 else "" for g in got] == [c[3] for c in _ends.RUNS]
+    assert {g[7] for g, c in zip(got, _ends.RUNS) if c[3] == "apart"} == {128, 256}
 
 
 def test_workspaces_are_what_the_header_says():
